@@ -9,10 +9,13 @@ import sys
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
-# translation units: the decode / recurrent-prefill kernels with every C entry
-# point, and the tensor-core chunked prefill
-SRCS = [os.path.join(CSRC, "gdnspec.cu"), os.path.join(CSRC, "gdnprefill_chunked.cu")]
-HEADERS = [os.path.join(ROOT, "include", "gdnspec.h"), os.path.join(CSRC, "gdn_internal.h")]
+# translation units: the decode / recurrent-prefill kernels with the gated-delta
+# layer's C entry points, its tensor-core chunked prefill, the verification and
+# tables between steps, and the state-space layer's step and scan
+SRCS = [os.path.join(CSRC, f) for f in ("gdnspec.cu", "gdnprefill_chunked.cu", "gdnverify.cu", "gdnssm.cu",
+                                        "gdnssm_prefill.cu")]
+HEADERS = [os.path.join(ROOT, "include", "gdnspec.h")] + [
+    os.path.join(CSRC, f) for f in ("gdn_internal.h", "gdn_common.h", "gdnssm.h", "gdnssm_recur.cuh")]
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD_DIR, "libgdnspec.so")
 

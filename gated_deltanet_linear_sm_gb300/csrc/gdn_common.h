@@ -1,0 +1,48 @@
+// Internal to libgdnspec: host and device helpers that the operators around
+// the step share (gdnverify.cu, gdnssm.cu, gdnssm_prefill.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "gdnspec.h"
+
+namespace gdn_common {
+
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+inline bool is_dtype(gdn_dtype t) { return t == GDN_F32 || t == GDN_BF16 || t == GDN_F16; }
+
+// SMs of the current device (asked once per device; 0 if that fails)
+inline int sm_count() {
+    static int sms[64] = {0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    int n = __atomic_load_n(&sms[dev], __ATOMIC_RELAXED);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+        __atomic_store_n(&sms[dev], n, __ATOMIC_RELAXED);
+    }
+    return n;
+}
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr float kSoftplusThreshold = 20.0f;                    // softplus(x) = x above this
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+
+__device__ __forceinline__ void raise(int32_t* status, int flag) {
+    if (status != nullptr) atomicOr(status, flag);
+}
+
+__device__ __forceinline__ float softplus(float x) { return x > kSoftplusThreshold ? x : log1pf(expf(x)); }
+
+// silu(z) = z sigmoid(z); for very negative z the denominator overflows and
+// the fast division returns zero
+__device__ __forceinline__ float silu(float z) { return __fdividef(z, 1.0f + __expf(-z)); }
+
+}  // namespace gdn_common

@@ -51,8 +51,10 @@ extern "C" {
 /* 2: gdn_spec_decode_split takes the state dtype; dims->split accepts GDN_SPLIT_NARROW
    3: dims->flags (formerly reserved): GDN_PRE_INDEX, GDN_PRE_TOKENS, GDN_PRE_STATE
    4: dims->split accepts GDN_SPLIT_HALFK | 1 and | 2, the automatic choice for small
-      FP32 batches */
-#define GDNSPEC_VERSION 4
+      FP32 batches
+   5: gdn_verify_drafts, gdn_step_tables, gdn_conv_prefill, gdn_ssm_prefill, gdn_ssm_decode
+      and GDN_FLAG_NO_TOKEN */
+#define GDNSPEC_VERSION 5
 
 #if defined(__GNUC__)
 #define GDNSPEC_API __attribute__((visibility("default")))
@@ -90,6 +92,8 @@ typedef enum { GDN_F32 = 0, GDN_BF16 = 1, GDN_F16 = 2 } gdn_dtype;
                                   default bound) for the products still in flight ran out too; the
                                   CTA released its tensor memory regardless, since holding it would
                                   block every later kernel on that SM */
+#define GDN_FLAG_NO_TOKEN   64 /* gdn_verify_drafts only: every probability of the row to sample from
+                                  counts as 0, so that no token was emitted */
 
 /*
  * dims->split flag: each warp of the decode step owns 8 of a unit's 128 V
@@ -365,6 +369,246 @@ GDNSPEC_API gdn_status gdn_spec_decode_conv(
     const int32_t* cu_seqlens, const int32_t* spec_token_indx,
     void* out,
     const gdn_dims* dims, float scale, float eps, gdn_dtype state_dtype,
+    int32_t* status_word, gdn_stream_t stream);
+
+/* ---- around the step: verification, tables, the convolution over prompts, and
+ *      the state-space layer ------------------------------------------------------
+ *
+ * These serve the same loop as the entry points above and share their slots,
+ * tables, status bits and conventions: asynchronous on `stream`, no allocation,
+ * no host read of device data, capturable.  The device data of a call (tables,
+ * lengths, slots) is checked on the device and reported through `status_word`;
+ * outputs must not overlap inputs unless a call says so.
+ */
+
+/* Sizes of gdn_verify_drafts. */
+typedef struct {
+    int32_t batch;          /* sequences */
+    int32_t num_tokens;     /* rows of target_probs */
+    int32_t vocab;          /* entries of a row, >= 1 */
+    int32_t max_T;          /* columns of out_tokens: host-known bound on every q_len, 1..32 */
+    /* strides in ELEMENTS; 0 selects the dense default */
+    int64_t target_stride;  /* between rows of target_probs (vocab) */
+    int64_t draft_stride;   /* between drafts of a sequence in draft_probs (vocab) */
+    int64_t draft_seq;      /* between sequences in draft_probs ((max_T - 1) * draft_stride) */
+    int64_t token_stride;   /* between sequences in draft_tokens and accept_u (max_T - 1) */
+} gdn_verify_dims;
+
+/*
+ * gdn_verify_drafts -- which drafted tokens the target model keeps, and the
+ * token that follows them: what sets the num_accepted of the next step.
+ *
+ * Sequence i made q_len_i = cu_seqlens[i+1] - cu_seqlens[i] rows of
+ * target_probs (the target's distribution after each of the step's tokens, the
+ * last sampled token and n = q_len_i - 1 drafts).  With p_t its row t, d_t its
+ * draft t, q_t the drafter's distribution for that draft and u_t = accept_u:
+ *     draft t is kept iff every earlier one was and u_t q_t(d_t) < p_t(d_t);
+ *     a = the number kept;  r = max(p_a - q_a, 0) if a < n, else p_n
+ *         (p_a itself where that leaves nothing);
+ *     the next token is the lowest v with sum_{w <= v} r_w > sample_u_i sum_w r_w.
+ * Without draft_probs q_t is 1 at d_t and 0 elsewhere.  A draft token outside
+ * [0, vocab) is never kept, and its place is sampled from p alone.
+ *
+ *   out_tokens[i]    d_0 .. d_{a-1}, the next token, then -1 up to max_T
+ *   num_accepted[i]  a + 1: the step's tokens that stay, as gdn_spec_decode
+ *                    and gdn_ssm_decode count them (the state after the last
+ *                    kept token is in slot state_indices[i, a])
+ *
+ * Arithmetic: a probability counts as a whole multiple of 2^-52 (rounded to
+ * nearest; below 0 and NaN count as 0, above 1 as 1), so that the sums are
+ * exact and the token does not depend on how a row is split.  The product
+ * u q is formed in 64 bits; sample_u is taken into [0, 1).
+ *
+ *   target_probs   prob_dtype [num_tokens, vocab]
+ *   draft_probs    prob_dtype [batch, max_T - 1, vocab], or NULL
+ *   draft_tokens   int32 [batch, max_T - 1]   (NULL with max_T = 1)
+ *   accept_u       fp32  [batch, max_T - 1], uniform in [0, 1)   (NULL with max_T = 1)
+ *   sample_u       fp32  [batch], uniform in [0, 1)
+ *   cu_seqlens     int32 [batch + 1]
+ *   spec_token_indx int32 [cu_seqlens[batch]] row of every position, or NULL
+ *                  when sequence i's rows are cu_seqlens[i] + t
+ *   out_tokens     int32 [batch, max_T];  num_accepted int32 [batch]
+ *
+ * A sequence with q_len <= 0 gets num_accepted 0 and no tokens; so does one
+ * with bad data (q_len > max_T: GDN_FLAG_QLEN; a row outside [0, num_tokens),
+ * or cu_seqlens out of order with cu_seqlens[batch]: GDN_FLAG_TOKEN_ROW).  A
+ * row to sample from that counts as 0 throughout emits -1 and sets
+ * GDN_FLAG_NO_TOKEN.  Every pointer needs only its element's alignment.
+ */
+GDNSPEC_API gdn_status gdn_verify_drafts(
+    const void* target_probs, const void* draft_probs, const int32_t* draft_tokens,
+    const float* accept_u, const float* sample_u,
+    const int32_t* cu_seqlens, const int32_t* spec_token_indx,
+    int32_t* out_tokens, int32_t* num_accepted,
+    const gdn_verify_dims* dims, gdn_dtype prob_dtype,
+    int32_t* status_word, gdn_stream_t stream);
+
+/* Sizes of gdn_step_tables. */
+typedef struct {
+    int32_t batch;          /* requests of this step */
+    int32_t num_tokens;     /* entries of token_indx: host-known bound on the step's rows */
+    int32_t spec_stride;    /* columns of slot_table and state_indices */
+    int32_t num_requests;   /* rows of slot_table, accepted, conv_table and conv_turn */
+} gdn_tables_dims;
+
+/*
+ * gdn_step_tables -- the tables of one step, from the lengths of its requests:
+ * the offsets, the row gather, the slots and the conv slots that
+ * gdn_spec_decode, gdn_spec_decode_conv, gdn_ssm_decode and gdn_verify_drafts
+ * read.  The requests' rows follow one another in the token batch.  With q_i =
+ * max(q_lens[i], 0), r = request[i] and m_i = "request i is speculative"
+ * (spec[i] != 0, 0 <= r < num_requests, q_i <= spec_stride):
+ *     row_starts[i]  = sum_{j < i} q_j                   (batch + 1 entries)
+ *     cu_seqlens[i]  = sum_{j < i} q_j m_j               (batch + 1 entries)
+ *     token_indx     = the rows of the speculative requests in order, then all
+ *                      other rows in order: its first cu_seqlens[batch] entries
+ *                      are the spec_token_indx of the other calls; entries from
+ *                      row_starts[batch] on are left as they were
+ *     state_indices[i] = m_i ? slot_table[r] : -1 ...
+ *     num_accepted[i]  = m_i ? accepted[r] : 0
+ *     conv_in[i], conv_out[i] = m_i ? conv_table[r, c], conv_table[r, 1 - c] : -1, -1
+ *                      with c = conv_turn[r] & 1; where m_i and q_i > 0,
+ *                      conv_turn[r] <- 1 - c, so that the next step reads the
+ *                      slot that this one writes
+ *
+ *   q_lens       int32 [batch]
+ *   spec         int32 [batch], or NULL (every request is speculative)
+ *   request      int32 [batch] row of the request in the tables below, or NULL
+ *                (row i); negative: none (a padded entry); distinct
+ *   slot_table   int32 [num_requests, spec_stride] the state slots of a request
+ *   accepted     int32 [num_requests] (gdn_verify_drafts' num_accepted)
+ *   conv_table   int32 [num_requests, 2], conv_turn int32 [num_requests]
+ *                (updated), conv_in, conv_out int32 [batch]: all four or none
+ *   row_starts   may be NULL
+ *
+ * A request row >= num_requests sets GDN_FLAG_SLOT_RANGE and a speculative
+ * request with q_i > spec_stride sets GDN_FLAG_QLEN; either counts as not
+ * speculative.  More than num_tokens rows in all set GDN_FLAG_TOKEN_ROW and
+ * give an empty step: every q_i counts as 0 and no request as speculative.
+ */
+GDNSPEC_API gdn_status gdn_step_tables(
+    const int32_t* q_lens, const int32_t* spec, const int32_t* request,
+    const int32_t* slot_table, const int32_t* accepted,
+    const int32_t* conv_table, int32_t* conv_turn,
+    int32_t* cu_seqlens, int32_t* row_starts, int32_t* token_indx,
+    int32_t* state_indices, int32_t* num_accepted, int32_t* conv_in, int32_t* conv_out,
+    const gdn_tables_dims* dims, int32_t* status_word, gdn_stream_t stream);
+
+/*
+ * gdn_conv_prefill -- the depthwise causal convolution of gdn_spec_decode_conv
+ * over whole prompts, or over the next chunk of prompts: it makes the rows
+ * that gdn_prefill, gdn_prefill_chunked and gdn_ssm_prefill read, and seeds the
+ * conv slots of the steps that follow.
+ *
+ * Sequence i is rows cu_seqlens[i] .. cu_seqlens[i+1]-1 of x.  With x_t for
+ * t < 0 the history: rows 1 .. W-1 of conv slot conv_in[i] in time order
+ * (zeros when conv_in[i] < 0):
+ *     y_t[c] = round_bf16( silu( bias[c] + sum_{w<W} weight[c][w] x_{t-W+1+w}[c] ) )
+ * in FP32, and conv slot conv_out[i] (skipped when < 0) gets the last W inputs
+ * (history included) in rows 0 .. W-1, bit for bit; its other rows are left as
+ * they were.  A step after it passes num_accepted = 1; a further chunk of the
+ * prompt passes conv_in[i] = that slot.  conv_in[i] == conv_out[i] updates a
+ * slot in place.
+ *
+ *   x            bf16 [num_tokens, conv_dim], row stride cdims->x_stride
+ *   conv_weight  bf16 [conv_dim, W];  conv_bias bf16 [conv_dim], or NULL
+ *   conv_pool    bf16 [num_conv_slots, state_len, conv_dim], state_len >= W
+ *   conv_in, conv_out int32 [batch];  cu_seqlens int32 [batch + 1]
+ *   y            bf16 [num_tokens, conv_dim], row stride y_stride (0: conv_dim);
+ *                rows of no sequence are left as they were
+ *
+ * cdims->width 1..4.  conv_dim a multiple of 4; x, y, conv_weight, conv_bias
+ * and conv_pool 8-byte aligned; x_stride and y_stride multiples of 4 (16-byte
+ * aligned pointers and multiples of 8 run faster).  Sequences follow one
+ * another: cu_seqlens does not decrease.  No conv_out[j] >= 0 equals another
+ * sequence's conv_in or conv_out.  Bad device data skips the sequence: a conv
+ * slot >= num_conv_slots sets GDN_FLAG_SLOT_RANGE, rows outside
+ * [0, num_tokens) set GDN_FLAG_TOKEN_ROW.
+ */
+GDNSPEC_API gdn_status gdn_conv_prefill(
+    const void* x, const void* conv_weight, const void* conv_bias, void* conv_pool,
+    const int32_t* conv_in, const int32_t* conv_out, const int32_t* cu_seqlens,
+    void* y, int32_t batch, int32_t num_tokens, int32_t conv_dim, int64_t y_stride,
+    const gdn_conv_dims* cdims, int32_t* status_word, gdn_stream_t stream);
+
+/* Sizes of the state-space layer. */
+typedef struct {
+    int32_t batch;        /* sequences */
+    int32_t num_tokens;   /* rows of the token tensors */
+    int32_t H, G;         /* heads, and groups of heads that share B and C; H % G == 0 */
+    int32_t P, N;         /* head dim (a multiple of 64, at most 256) and state dim (64 or 128) */
+    int32_t spec_stride;  /* gdn_ssm_decode: columns of state_indices */
+    int32_t max_T;        /* gdn_ssm_decode: host-known bound on every q_len, 1..8 */
+    int64_t num_slots;    /* slots in state_pool */
+    /* row strides in ELEMENTS, 0 = dense (x, z, out: H*P; B, C: G*N; dt: H) */
+    int64_t x_stride, b_stride, c_stride, dt_stride, z_stride, out_stride;
+    int32_t reserved[2];  /* must be 0 */
+} gdn_ssm_dims;
+
+/*
+ * gdn_ssm_prefill -- a selective state-space layer over whole prompts: the
+ * gated linear recurrence of this library without the delta term, with one
+ * decay per head and token.  Head h uses group g = h / (H / G).  With S the
+ * N x P state of (sequence i, head h), P contiguous:
+ *     d = softplus(dt[r,h] + dt_bias[h])                (as in gdn_spec_decode)
+ *     S <- e^(-exp(A_log[h]) d) S + B[r,g] (d x[r,h])^T
+ *     out[r,h] = round_bf16( (S^T C[r,g] + D[h] x[r,h]) silu(z[r,h]) )
+ * Sequence i is rows cu_seqlens[i] .. cu_seqlens[i+1]-1; it starts from slot
+ * read_slots[i] (the zero state when < 0) and its last state goes to slot
+ * write_slots[i] (no write when < 0; in place when equal), rounded once.
+ *
+ *   x            bf16 [num_tokens, H, P];  B, C bf16 [num_tokens, G, N]
+ *   dt           bf16 [num_tokens, H];  dt_bias bf16 [H];  A_log fp32 [H]
+ *   z            bf16 [num_tokens, H, P], or NULL (no gate);  D fp32 [H], or NULL (0)
+ *   state_pool   state_dtype [num_slots, H, N, P]
+ *   out          bf16 [num_tokens, H, P]; rows of no sequence are left as they were
+ *   workspace    gdn_ssm_prefill_workspace(dims) bytes of device memory, 16-byte
+ *                aligned, used by this call alone until it has run (NULL when that
+ *                is 0); what it holds before and after does not matter
+ *
+ * Within a row the heads (groups) are contiguous; x, B and C may be views into
+ * one packed row.  x, B, C, z, out and state_pool are 16-byte aligned and
+ * x/B/C/z/out strides multiples of 8.  A head dim P > 64 runs as P / 64 column
+ * blocks.  Caller contract and skips as for gdn_prefill.  An infinite or NaN
+ * input gives NaN or infinity in the rows and states that it reaches, and no
+ * other sequence's.
+ */
+GDNSPEC_API gdn_status gdn_ssm_prefill(
+    const void* x, const void* B, const void* C, const void* dt, const void* z,
+    const float* A_log, const void* dt_bias, const float* D,
+    void* state_pool, const int32_t* read_slots, const int32_t* write_slots,
+    const int32_t* cu_seqlens, void* out, void* workspace, int64_t workspace_bytes,
+    const gdn_ssm_dims* dims, gdn_dtype state_dtype,
+    int32_t* status_word, gdn_stream_t stream);
+
+/* Workspace that gdn_ssm_prefill needs for these sizes, in bytes (-1: invalid dims).
+ * Host only; depends on the current device's number of SMs. */
+GDNSPEC_API int64_t gdn_ssm_prefill_workspace(const gdn_ssm_dims* dims);
+
+/*
+ * gdn_ssm_decode -- the state-space layer over one to eight tokens of each
+ * sequence, with the short causal convolution fused in front and the rewind of
+ * gdn_spec_decode_conv: projection rows xbc [num_tokens, conv_dim] (conv_dim =
+ * H P + 2 G N, channels x | B | C) are convolved (silu, never rounded to bf16),
+ * the state starts from slot state_indices[i, max(num_accepted[i]-1, 0)], and
+ * the state after token t goes to slot state_indices[i, t] (skipped when < 0),
+ * rounded once.  A single-token step is spec_stride = max_T = 1.
+ *
+ * The conv slots (history rows, new rows, seeding), the gather, the skips, the
+ * caller contract and the status bits are those of gdn_spec_decode_conv; the
+ * recurrence, dt, z, D and the pool are those of gdn_ssm_prefill.
+ * cdims->x_stride is the row stride of xbc; dims->x_stride, b_stride and
+ * c_stride are not used.  state_pool 16-byte aligned; xbc, conv_weight (W = 4),
+ * conv_bias, conv_pool, z and out 8-byte aligned with xbc/z/out strides
+ * multiples of 4.
+ */
+GDNSPEC_API gdn_status gdn_ssm_decode(
+    const void* xbc, const void* conv_weight, const void* conv_bias, void* conv_pool,
+    const int32_t* conv_in, const int32_t* conv_out, const gdn_conv_dims* cdims,
+    const void* dt, const void* z, const float* A_log, const void* dt_bias, const float* D,
+    void* state_pool, const int32_t* state_indices, const int32_t* num_accepted,
+    const int32_t* cu_seqlens, const int32_t* spec_token_indx, void* out,
+    const gdn_ssm_dims* dims, gdn_dtype state_dtype,
     int32_t* status_word, gdn_stream_t stream);
 
 /*
