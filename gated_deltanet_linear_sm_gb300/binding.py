@@ -23,6 +23,7 @@ GDN_FLAG_QLEN = 4
 GDN_FLAG_TOKEN_ROW = 8
 GDN_FLAG_TIMEOUT = 16
 GDN_FLAG_DRAIN = 32
+GDN_FLAG_NO_TOKEN = 64
 GDN_SPLIT_NARROW = 0x100     # dims.split flag: 8 V columns per warp (small batches)
 GDN_SPLIT_HALFK = 0x200      # dims.split flag (with 2): half of the K rows per warp (small batches)
 GDN_PRE_INDEX = 0x1          # dims.flags: the index tables were not written by the preceding kernel

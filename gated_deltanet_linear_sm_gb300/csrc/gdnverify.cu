@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kVThreads) gdn_verify_kernel(const VerifyParam
             if (lane < p.max_T && !(valid && lane == kept))
                 p.out[static_cast<int64_t>(i) * p.max_T + lane] = lane < kept ? d : -1;
             if (lane == 0) {
-                p.accepted[i] = valid ? kept + 1 : 0;
+                if (valid) p.accepted[i] = kept + 1;
                 if (flag) raise(p.status, flag);
             }
         }

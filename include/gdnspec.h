@@ -429,8 +429,9 @@ typedef struct {
  *                  when sequence i's rows are cu_seqlens[i] + t
  *   out_tokens     int32 [batch, max_T];  num_accepted int32 [batch]
  *
- * A sequence with q_len <= 0 gets num_accepted 0 and no tokens; so does one
- * with bad data (q_len > max_T: GDN_FLAG_QLEN; a row outside [0, num_tokens),
+ * A sequence with q_len <= 0 gets no tokens (-1 throughout) and keeps its
+ * num_accepted, as its states keep theirs; so does one with bad data, which the
+ * step skips too (q_len > max_T: GDN_FLAG_QLEN; a row outside [0, num_tokens),
  * or cu_seqlens out of order with cu_seqlens[batch]: GDN_FLAG_TOKEN_ROW).  A
  * row to sample from that counts as 0 throughout emits -1 and sets
  * GDN_FLAG_NO_TOKEN.  Every pointer needs only its element's alignment.
@@ -570,8 +571,8 @@ typedef struct {
  * one packed row.  x, B, C, z, out and state_pool are 16-byte aligned and
  * x/B/C/z/out strides multiples of 8.  A head dim P > 64 runs as P / 64 column
  * blocks.  Caller contract and skips as for gdn_prefill.  An infinite or NaN
- * input gives NaN or infinity in the rows and states that it reaches, and no
- * other sequence's.
+ * input spoils rows and the last state of its own sequence (rows shortly before
+ * it among them: the products run over tiles of tokens), and no other's.
  */
 GDNSPEC_API gdn_status gdn_ssm_prefill(
     const void* x, const void* B, const void* C, const void* dt, const void* z,
