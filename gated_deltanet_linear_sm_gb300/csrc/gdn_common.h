@@ -31,6 +31,23 @@ inline int sm_count() {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kSoftplusThreshold = 20.0f;                    // softplus(x) = x above this
 
+// Programmatic dependent launch.  A kernel launched with it may start while its
+// predecessor on the stream still runs: it waits (dep_wait) until that has
+// completed before it touches memory, and after that wait it may let its own
+// successor start (dep_launch).  The kernels here that write the tables which
+// every step reads (gdn_verify_drafts, gdn_step_tables) do not call dep_launch,
+// so their successor starts when they have completed: it may then read tables
+// before any wait of its own.
+__device__ __forceinline__ void dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// A plain load: unlike __ldg (which promises that nothing writes the memory
+// while the kernel runs, early starts included) it stays behind dep_wait.
+template <typename T>
+__device__ __forceinline__ T ld(const T* p) {
+    return *p;
+}
+
 __device__ __forceinline__ float to_f(float x) { return x; }
 __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_f(__half x) { return __half2float(x); }

@@ -57,21 +57,21 @@ __device__ __forceinline__ void unpack(const Raw<CV>& raw, float (&x)[CV]) {
 // whether sequence j may run: its rows and conv slots are in range
 __device__ __forceinline__ int conv_flag(const ConvParams& p, int s, int e, int j) {
     if (s < 0 || e > p.num_tokens) return GDN_FLAG_TOKEN_ROW;
-    if (__ldg(p.in + j) >= p.num_slots || __ldg(p.out + j) >= p.num_slots) return GDN_FLAG_SLOT_RANGE;
+    if (ld(p.in + j) >= p.num_slots || ld(p.out + j) >= p.num_slots) return GDN_FLAG_SLOT_RANGE;
     return 0;
 }
 
 template <int CV, int W>
 __global__ void __launch_bounds__(kCThreads) gdn_conv_prefill_kernel(const ConvParams p) {
     constexpr int HN = W > 1 ? W - 1 : 1;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    dep_wait();
+    dep_launch();
     const int cb = blockIdx.x % p.col_blocks;
     const int r0 = static_cast<int>(blockIdx.x / p.col_blocks) * p.run;
     const int r1 = min(p.num_tokens, r0 + p.run);
     if (blockIdx.x == 0) {                          // bad data, reported once
         for (int j = threadIdx.x; j < p.batch; j += kCThreads) {
-            const int s = __ldg(p.cu + j), e = __ldg(p.cu + j + 1);
+            const int s = ld(p.cu + j), e = ld(p.cu + j + 1);
             const int flag = e > s ? conv_flag(p, s, e, j) : 0;
             if (flag) raise(p.status, flag);
         }
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kCThreads) gdn_conv_prefill_kernel(const ConvP
     int j = 0;
     for (int base = 0; base < p.batch; base += kCThreads) {
         const int k = base + threadIdx.x;
-        const int done = __syncthreads_count(k < p.batch && __ldg(p.cu + k + 1) <= r0);
+        const int done = __syncthreads_count(k < p.batch && ld(p.cu + k + 1) <= r0);
         j += done;
         if (done < kCThreads) break;
     }
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kCThreads) gdn_conv_prefill_kernel(const ConvP
 #pragma unroll
         for (int e = 0; e < CV; ++e) {
             float f[4];
-            unpack<4>(__ldg(reinterpret_cast<const uint2*>(p.w + static_cast<int64_t>(c + e) * 4)), f);
+            unpack<4>(ld(reinterpret_cast<const uint2*>(p.w + static_cast<int64_t>(c + e) * 4)), f);
 #pragma unroll
             for (int k = 0; k < 4; ++k) wt[e][k] = f[k];
         }
@@ -104,11 +104,11 @@ __global__ void __launch_bounds__(kCThreads) gdn_conv_prefill_kernel(const ConvP
 #pragma unroll
             for (int k = 0; k < W; ++k) wt[e][k] = __bfloat162float(p.w[static_cast<int64_t>(c + e) * W + k]);
     }
-    if (p.bias) unpack<CV>(__ldg(reinterpret_cast<const Raw<CV>*>(p.bias + c)), bias);
+    if (p.bias) unpack<CV>(ld(reinterpret_cast<const Raw<CV>*>(p.bias + c)), bias);
 
-    auto row_of_x = [&](int64_t r) { return __ldg(reinterpret_cast<const Raw<CV>*>(p.x + r * p.x_stride + c)); };
+    auto row_of_x = [&](int64_t r) { return ld(reinterpret_cast<const Raw<CV>*>(p.x + r * p.x_stride + c)); };
     for (; j < p.batch; ++j) {
-        const int s = __ldg(p.cu + j), e = __ldg(p.cu + j + 1);
+        const int s = ld(p.cu + j), e = ld(p.cu + j + 1);
         if (s >= r1) break;
         if (e <= s || conv_flag(p, s, e, j)) continue;
         const bool first = s >= r0;
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kCThreads) gdn_conv_prefill_kernel(const ConvP
         if (a >= b) continue;
         Raw<CV> win[HN] = {};
         if (W > 1 && first) {
-            const int in = __ldg(p.in + j);
+            const int in = ld(p.in + j);
 #pragma unroll
             for (int k = 0; k < W - 1; ++k)
                 if (in >= 0) win[k] = *reinterpret_cast<const Raw<CV>*>(p.pool + in * p.slot + (k + 1) * static_cast<int64_t>(p.dim) + c);
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kCThreads) gdn_conv_prefill_kernel(const ConvP
             for (int k = 0; k < W - 1; ++k) win[k] = row_of_x(a - (W - 1) + k);
         }
         if (first) {
-            const int out = __ldg(p.out + j);
+            const int out = ld(p.out + j);
             if (out >= 0) {
                 __nv_bfloat16* dst = p.pool + out * p.slot + c;
 #pragma unroll
@@ -234,16 +234,16 @@ __global__ void __launch_bounds__(kRThreads, 4) gdn_ssm_decode_kernel(const Para
     const int unit = static_cast<int>(blockIdx.x / p.blocks);
     const int i = unit / p.H, h = unit - i * p.H;
     const int g = h / p.group;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    dep_wait();
+    dep_launch();
 
     // ---- the work item (every thread finds the same) ----
     const int32_t* slot_row = p.idx + static_cast<int64_t>(i) * p.stride;
-    const int bos = __ldg(p.cu + i);
-    const int eos = __ldg(p.cu + i + 1);
-    const int acc = __ldg(p.num_acc + i);
-    const int total = __ldg(p.cu + p.batch);
-    const long long cin = __ldg(p.conv_in + i), cout = __ldg(p.conv_out + i);
+    const int bos = ld(p.cu + i);
+    const int eos = ld(p.cu + i + 1);
+    const int acc = ld(p.num_acc + i);
+    const int total = ld(p.cu + p.batch);
+    const long long cin = ld(p.conv_in + i), cout = ld(p.conv_out + i);
     if (eos <= bos) return;
     const int n = bos < 0 ? 0 : eos - bos;
     int flag = 0;
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kRThreads, 4) gdn_ssm_decode_kernel(const Para
         if (tid == 0) raise(p.status, flag);
         return;
     }
-    const long long rs = __ldg(slot_row + max(acc - 1, 0));
+    const long long rs = ld(slot_row + max(acc - 1, 0));
     if (rs < 0) return;                             // a padded sequence
     if (rs >= p.num_slots || cin >= p.num_conv_slots || cout >= p.num_conv_slots) {
         if (tid == 0) raise(p.status, GDN_FLAG_SLOT_RANGE);
@@ -271,13 +271,13 @@ __global__ void __launch_bounds__(kRThreads, 4) gdn_ssm_decode_kernel(const Para
     // ---- rows, decays, the gate's quads ----
     int bad = 0;
     if (tid < n) {
-        const int r = p.sti ? __ldg(p.sti + bos + tid) : bos + tid;
+        const int r = p.sti ? ld(p.sti + bos + tid) : bos + tid;
         bad = r < 0 || r >= p.num_tokens;
         s.row[tid] = r;
         if (!bad) {
             const float d = softplus(__bfloat162float(p.dt[r * p.dt_stride + h]) + __bfloat162float(p.dt_bias[h]));
             s.step[tid] = d;
-            s.decay[tid] = expf(-expf(__ldg(p.A_log + h)) * d);
+            s.decay[tid] = expf(-expf(ld(p.A_log + h)) * d);
         }
     }
     if (__syncthreads_or(bad)) {
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kRThreads, 4) gdn_ssm_decode_kernel(const Para
     uint2 zraw = make_uint2(0, 0);
     const int col = h * p.P + pb * kPB;
     if (p.z && to < n)
-        zraw = __ldg(reinterpret_cast<const uint2*>(p.z + s.row[to] * p.z_stride + col + 4 * qo));
+        zraw = ld(reinterpret_cast<const uint2*>(p.z + s.row[to] * p.z_stride + col + 4 * qo));
     // ---- the convolution: quad q of x | B | C, all tokens ----
     if (tid < kQuads) {
         const int W = p.conv_width;
@@ -303,18 +303,18 @@ __global__ void __launch_bounds__(kRThreads, 4) gdn_ssm_decode_kernel(const Para
         for (int k = 0; k < 3; ++k) {
             const int m = k - (4 - W);              // history row m of W - 1
             raw[k] = make_uint2(0, 0);
-            if (m >= 0 && hist) raw[k] = __ldg(reinterpret_cast<const uint2*>(hist + static_cast<int64_t>(m) * p.conv_dim));
+            if (m >= 0 && hist) raw[k] = ld(reinterpret_cast<const uint2*>(hist + static_cast<int64_t>(m) * p.conv_dim));
         }
 #pragma unroll
         for (int t = 0; t < kMaxT; ++t)
-            if (t < n) raw[3 + t] = __ldg(reinterpret_cast<const uint2*>(p.x + s.row[t] * p.x_stride + ch));
+            if (t < n) raw[3 + t] = ld(reinterpret_cast<const uint2*>(p.x + s.row[t] * p.x_stride + ch));
         float wt[4][4], bias[4] = {0.f, 0.f, 0.f, 0.f};  // taps right-aligned: tap 3 is the token itself
 #pragma unroll
         for (int e = 0; e < 4; ++e)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
                 wt[e][k] = k >= 4 - W ? __bfloat162float(p.conv_w[static_cast<int64_t>(ch + e) * W + k - (4 - W)]) : 0.f;
-        if (p.conv_b) unpack4(__ldg(reinterpret_cast<const uint2*>(p.conv_b + ch)), bias);
+        if (p.conv_b) unpack4(ld(reinterpret_cast<const uint2*>(p.conv_b + ch)), bias);
         float f[3][4];
 #pragma unroll
         for (int k = 0; k < 3; ++k) unpack4(raw[k], f[k]);
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kRThreads, 4) gdn_ssm_decode_kernel(const Para
     // ---- the tokens ----
     for (int t = 0; t < n; ++t) {
         token<StateT, N>(S, s, t);
-        const long long ws = __ldg(slot_row + t);
+        const long long ws = ld(slot_row + t);
         if (ws >= 0 && ws < p.num_slots) {
             StateT* dst = static_cast<StateT*>(p.pool) + ws * p.H * tile + at;
 #pragma unroll
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kRThreads, 4) gdn_ssm_decode_kernel(const Para
     }
     __syncthreads();
     if (to < n)
-        write_out(s, to, qo, p.D ? __ldg(p.D + h) : 0.f, p.z != nullptr, zraw,
+        write_out(s, to, qo, p.D ? ld(p.D + h) : 0.f, p.z != nullptr, zraw,
                   p.out + s.row[to] * p.out_stride + col + 4 * qo);
 }
 

@@ -1,103 +1,883 @@
 // libgdnspec: the state-space layer over prompts (gdn_ssm_prefill, whose C
-// entry point and argument checks are in gdnssm.cu).
+// entry point and argument checks are in gdnssm.cu) on the sm_103a tensor cores.
+//
+// Chunked form (Q = 128 tokens; S the N x 64 state block at the chunk start; l_t
+// the running sum of the log2-decays inside the chunk; d_t the step sizes):
+//     y_t = 2^(l_t) S^T C_t + sum_{s <= t} 2^(l_t - l_s) d_s (C_t . B_s) x_s
+//     S  <- 2^(l_last) S + sum_s B_s (2^(l_last - l_s) d_s x_s)^T
+// the token recurrence unrolled over the chunk, the same quantities in exact
+// arithmetic.  Every decay factor is 2^(non-positive), so nothing overflows.
+//
+// One CTA works on a (sequence, head, 64 columns of the head dim), chunk by
+// chunk, with four products of 128 rows (tcgen05.mma, bf16 operands, FP32
+// accumulators in tensor memory):
+//     G  = C B^T          rows t, columns s     128 x 128 x N
+//     Y1 = Pm X           rows t, columns p     128 x  64 x 128, Pm = G with the decays, causal
+//     Y2 = C S            rows t, columns p     128 x  64 x N
+//     dS = B^T Xw         rows n, columns p     128 x  64 x 128, Xw_s = 2^(l_last - l_s) d_s x_s
+// B, C and x are bf16 and exact.  What is computed in FP32 (Pm, S, Xw) enters as
+// a bf16 hi and a bf16 lo part, together within 2^-18 of its value, each part a
+// product of its own in the same accumulator; the state itself stays in FP32
+// registers.  With the hi parts alone an FP32 state would be off by 2^-9.
+//
+// x, B, C and z come by TMA (128-byte swizzle, the operand layout of the tensor
+// cores), so x, B and C are operands as they land; B^T and X as the operand
+// with rows and depth exchanged need no transposed copy.  Pm goes back into the
+// tensor memory that G was in and is multiplied from there.
+//
+// Ten warps: 0-7 the arithmetic on tiles (warp w and w + 4 share the 32 rows
+// that hardware lets them reach, and split the columns), 8 issues copies and
+// products, 9 turns dt into the decay factors of the chunk after next.  They
+// meet at mbarriers only.  dS and G of a chunk do not depend on the state, so
+// the chain from chunk to chunk is the FP32 update of S and the product Y2.
+// Every wait is bounded: on a timeout the CTA sets GDN_FLAG_TIMEOUT, writes no
+// state, waits (bounded) for what it has in flight and releases its tensor
+// memory.
+//
+// With few (sequence, head) pairs the prompts are cut into segments: a first
+// launch computes what each segment adds to the state (dS alone: no G, Pm, Y1,
+// Y2), and the second starts each segment from the initial state and the
+// segments before it, which it combines itself.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "gdn_internal.h"
+#include "gdn_tcgen05.h"
 #include "gdnssm.h"
 #include "gdnssm_recur.cuh"
 
 using namespace gdn_common;
 using namespace gdn_ssm;
+using namespace gdn_tc;
 
 namespace {
 
-// The token recurrence, 8 tokens a round: one CTA of 128 threads per
-// (sequence, head, 64 columns), the state block in FP32 registers.
-template <typename StateT, int N>
-__global__ void __launch_bounds__(kRThreads, 4) gdn_ssm_prefill_kernel(const Params p) {
-    constexpr int R = N / 16;
-    __shared__ Round<N> s;
-    const int tid = threadIdx.x, cg = tid & 7, rg = tid >> 3;
-    const int pb = static_cast<int>(blockIdx.x % p.blocks);
-    const int unit = static_cast<int>(blockIdx.x / p.blocks);
-    const int i = unit / p.H, h = unit - i * p.H;
-    const int g = h / p.group;
-    const int bos = __ldg(p.cu + i);
-    const int eos = __ldg(p.cu + i + 1);
-    const long long rs = __ldg(p.read_slots + i), ws = __ldg(p.write_slots + i);
-    if (eos <= bos) return;
-    int flag = 0;
-    if (bos < 0 || eos > p.num_tokens) flag = GDN_FLAG_TOKEN_ROW;
-    else if (rs >= p.num_slots || ws >= p.num_slots) flag = GDN_FLAG_SLOT_RANGE;
-    if (flag) {
-        if (tid == 0) raise(p.status, flag);
-        return;
+constexpr int kQ = 128;                          // tokens of a chunk
+constexpr int kWarps = 8;                        // on tiles
+constexpr int kSThreads = 32 * (kWarps + 2);
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kXStages = 3;
+
+struct ScanParams {
+    CUtensorMap x, B, C, z;                      // boxes of 64 elements x 128 rows
+    Params p;
+    float* part;                                 // segments: [segment][unit][N][64] what a segment adds
+    float* part_decay;                           // and its log2-decay, [segment][unit]
+    int32_t seg_chunks;                          // chunks of a segment (0: whole sequences)
+    int32_t segs;                                // segments that the launch has room for
+    uint32_t wait_limit;
+};
+
+// ---- shared memory (from a 1024-byte aligned base) ------------------------------
+// Tiles of 128-byte rows, 16-byte unit j of row r at r * 128 + ((j ^ (r & 7)) << 4).
+template <int N>
+struct Lay {
+    static constexpr int kTile = kQ * 128;                      // 128 rows
+    static constexpr int kX = 0;                                // kXStages tiles [s][p]
+    static constexpr int kZ = kX + kXStages * kTile;            // 2 tiles [t][p]: z, then the outputs
+    static constexpr int kB = kZ + 2 * kTile;                   // N / 64 tiles [s][64 n]
+    static constexpr int kC = kB + N / 64 * kTile;              // N / 64 tiles [t][64 n]
+    static constexpr int kXw = kC + N / 64 * kTile;             // hi, lo [s][p]
+    static constexpr int kS = kXw + 2 * kTile;                  // hi, lo [n][p], N rows each
+    static constexpr int kMisc = kS + 2 * N * 128;
+};
+
+// Decay factors of one chunk.  The log2-decays are added up as whole multiples
+// of 2^-32 in 64 bits: after a strong decay an FP32 sum is thousands with steps
+// of 2^-10, and the difference of two neighbours, whose weight is near 1, would
+// be off by as much.
+struct alignas(16) Gates {
+    float l[kQ];       // running sum of the log2-decays,
+    float l_lo[kQ];    // and what rounding it to FP32 left
+    float f[kQ];       // 2^(l at the end of the token's block of 32 - l_t) d_t
+    float e[kQ];       // 2^(l_t)
+    float w[kQ];       // 2^(l_last - l_t) d_t
+    float d[kQ];       // step sizes
+    float total;       // 2^(l_last)
+    float total_log;
+};
+
+struct alignas(16) Misc {
+    Gates gates[2];
+    unsigned long long x_full[kXStages], bc_full, z_full[2];    // copies have landed
+    unsigned long long gates_full[2];
+    unsigned long long g_done, ds_done, y2_done, y1_done;       // products are complete
+    unsigned long long xw_ready, s_ready, p_ready, chunk_done;  // the tile warps have written / read
+    unsigned long long drain;
+    uint32_t tmem;
+    int abort;
+};
+template <int N>
+constexpr int scan_smem() { return Lay<N>::kMisc + static_cast<int>(sizeof(Misc)) + 1024; }
+static_assert(sizeof(Gates) % 16 == 0 && Lay<64>::kMisc % 16 == 0 && Lay<128>::kMisc % 16 == 0, "float4 accesses");
+static_assert(scan_smem<128>() <= 227 * 1024, "shared memory budget");
+
+// tensor-memory columns
+constexpr uint32_t kTG = 0;                      // two G / Pm tiles of 128
+constexpr uint32_t kTY1 = 256, kTY2 = 320;       // Y1; two Y2
+constexpr uint32_t kTdS = 448;
+
+// ---- instructions -----------------------------------------------------------------
+
+// MN-major operand: rows of 64 elements are the depth (K) direction; 8-row groups
+// are 1024 bytes apart, the next 64 rows of the product `mn` bytes
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t mn) {
+    return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | (static_cast<uint64_t>(mn >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
+           (static_cast<uint64_t>(2) << 61);
+}
+constexpr uint32_t kAMn = 1u << 15, kBMn = 1u << 16;            // instruction descriptor: MN-major A, B
+
+// A from tensor memory
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+
+__device__ __forceinline__ void tm_ld32_nowait(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void bar_init(unsigned long long* b, int count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(saddr(b)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(unsigned long long* b) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(saddr(b)) : "memory");
+}
+__device__ __forceinline__ void bar_expect(unsigned long long* b, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(saddr(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, unsigned long long* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(saddr(bar))
+        : "memory");
+}
+
+// bounded wait; gives up early once another warp has
+__device__ __forceinline__ bool wait(unsigned long long* bar, int use, uint32_t limit, const volatile int* abort) {
+    const uint32_t addr = saddr(bar), parity = use & 1;
+    if (limit != 0) return test_parity(addr, parity, limit);
+    for (uint32_t round = 0; round < kSpinLimit / 64; ++round) {
+        if (wait_parity(addr, parity, 64)) return true;
+        if (*abort) return false;
     }
-    const int L = eos - bos;
-    const int64_t tile = static_cast<int64_t>(N) * p.P;
-    const int64_t at = h * tile + static_cast<int64_t>(rg * R) * p.P + pb * kPB;
-    u64 S[R][4] = {};
-    if (rs >= 0) {
-        const StateT* src = static_cast<const StateT*>(p.pool) + rs * p.H * tile + at;
+    return false;
+}
+
+__device__ __forceinline__ uint32_t unit16(int r, int j) { return static_cast<uint32_t>(r * 128 + ((j ^ (r & 7)) << 4)); }
+
+// 32 consecutive elements of a state row <-> FP32
+__device__ __forceinline__ void load_row32(const float* p, float (&x)[32]) {
 #pragma unroll
-        for (int j = 0; j < R; ++j) Row8<StateT>::load(src + static_cast<int64_t>(j) * p.P, cg, S[j]);
-    }
-    const int to = tid >> 4, qo = tid & 15;
-    const int col = h * p.P + pb * kPB;
-    const float rate = -expf(__ldg(p.A_log + h)), bias = __bfloat162float(p.dt_bias[h]);
-    const float D = p.D ? __ldg(p.D + h) : 0.f;
-    for (int c0 = 0; c0 < L; c0 += kMaxT) {
-        const int n = min(kMaxT, L - c0);
-        const int64_t r0 = bos + c0;
-        if (tid < n) {
-            const float d = softplus(__bfloat162float(p.dt[(r0 + tid) * p.dt_stride + h]) + bias);
-            s.step[tid] = d;
-            s.decay[tid] = expf(rate * d);
-        }
-        uint2 zraw = make_uint2(0, 0);
-        if (to < n) {
-            const int64_t r = r0 + to;
-            float f[4];
-            unpack4(__ldg(reinterpret_cast<const uint2*>(p.x + r * p.x_stride + col + 4 * qo)), f);
-            *reinterpret_cast<float4*>(&s.x[to][4 * qo]) = make_float4(f[0], f[1], f[2], f[3]);
-            if (p.z) zraw = __ldg(reinterpret_cast<const uint2*>(p.z + r * p.z_stride + col + 4 * qo));
-            for (int q = qo; q < N / 4; q += 16) {
-                unpack4(__ldg(reinterpret_cast<const uint2*>(p.B + r * p.b_stride + g * N + 4 * q)), f);
-                *reinterpret_cast<float4*>(&s.B[to][4 * q]) = make_float4(f[0], f[1], f[2], f[3]);
-                unpack4(__ldg(reinterpret_cast<const uint2*>(p.C + r * p.c_stride + g * N + 4 * q)), f);
-                *reinterpret_cast<float4*>(&s.C[to][4 * q]) = make_float4(f[0], f[1], f[2], f[3]);
-            }
-        }
-        __syncthreads();
-        for (int t = 0; t < n; ++t) token<StateT, N>(S, s, t);
-        __syncthreads();
-        if (to < n) write_out(s, to, qo, D, p.z != nullptr, zraw, p.out + (r0 + to) * p.out_stride + col + 4 * qo);
-        __syncthreads();
-    }
-    if (ws >= 0) {
-        StateT* dst = static_cast<StateT*>(p.pool) + ws * p.H * tile + at;
+    for (int j = 0; j < 8; ++j) *reinterpret_cast<float4*>(x + 4 * j) = __ldcs(reinterpret_cast<const float4*>(p) + j);
+}
+__device__ __forceinline__ void load_row32(const __nv_bfloat16* p, float (&x)[32]) {
 #pragma unroll
-        for (int j = 0; j < R; ++j) Row8<StateT>::store(dst + static_cast<int64_t>(j) * p.P, cg, S[j]);
+    for (int j = 0; j < 4; ++j) {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p) + j);
+        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = __bfloat1622float2(h[e]);
+            x[8 * j + 2 * e] = f.x;
+            x[8 * j + 2 * e + 1] = f.y;
+        }
+    }
+}
+__device__ __forceinline__ void load_row32(const __half* p, float (&x)[32]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p) + j);
+        const __half2* h = reinterpret_cast<const __half2*>(&v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = __half22float2(h[e]);
+            x[8 * j + 2 * e] = f.x;
+            x[8 * j + 2 * e + 1] = f.y;
+        }
+    }
+}
+__device__ __forceinline__ void store_row32(float* p, const float (&x)[32]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) __stcs(reinterpret_cast<float4*>(p) + j, *reinterpret_cast<const float4*>(x + 4 * j));
+}
+__device__ __forceinline__ void store_row32(__nv_bfloat16* p, const float (&x)[32]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        __stcs(reinterpret_cast<uint4*>(p) + j, make_uint4(pack2(x[8 * j], x[8 * j + 1]), pack2(x[8 * j + 2], x[8 * j + 3]),
+                                                           pack2(x[8 * j + 4], x[8 * j + 5]), pack2(x[8 * j + 6], x[8 * j + 7])));
+}
+__device__ __forceinline__ void store_row32(__half* p, const float (&x)[32]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const __half2 h = __floats2half2_rn(x[8 * j + 2 * e], x[8 * j + 2 * e + 1]);
+            w[e] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        __stcs(reinterpret_cast<uint4*>(p) + j, make_uint4(w[0], w[1], w[2], w[3]));
     }
 }
 
-template <typename StateT>
-cudaError_t launch(const Params& p, int N, cudaStream_t stream) {
+// What this CTA works on.  kind 0: nothing.
+struct Work {
+    int kind, seq, bos, len;                     // rows of the whole sequence
+    int first, chunks;                           // chunks of this CTA
+    int seg, segs;                               // its segment's index in the sequence, and in the launch (its first)
+    bool last;
+};
+
+// The whole-sequence form: sequence = blockIdx / units.  With segments, the
+// launch's segment index is looked up among the sequences' segment counts (one
+// warp, 32 sequences at a time; every warp does the same).
+__device__ Work find_work(const ScanParams& sp, int index, int lane) {
+    const Params& p = sp.p;
+    Work w = {};
+    auto bounds = [&](int i, int& bos, int& eos) {
+        bos = ld(p.cu + i);
+        eos = ld(p.cu + i + 1);
+        if (eos <= bos) return 0;
+        if (bos < 0 || eos > p.num_tokens) return GDN_FLAG_TOKEN_ROW;
+        if (ld(p.read_slots + i) >= p.num_slots || ld(p.write_slots + i) >= p.num_slots) return GDN_FLAG_SLOT_RANGE;
+        return -1;
+    };
+    if (sp.seg_chunks == 0) {
+        int bos, eos;
+        const int f = bounds(index, bos, eos);
+        if (f > 0 && threadIdx.x == 0) raise(p.status, f);
+        if (f != -1) return w;
+        w = {1, index, bos, eos - bos, 0, (eos - bos + kQ - 1) / kQ, 0, 0, true};
+        return w;
+    }
+    int base = 0;
+    for (int i0 = 0; i0 < p.batch; i0 += 32) {
+        const int i = i0 + lane;
+        int bos = 0, eos = 0, n = 0;
+        if (i < p.batch) {
+            const int f = bounds(i, bos, eos);
+            if (f > 0 && blockIdx.x == 0 && threadIdx.x < 32) raise(p.status, f);
+            if (f == -1) n = ((eos - bos + kQ - 1) / kQ + sp.seg_chunks - 1) / sp.seg_chunks;
+        }
+        int upto = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kFull, upto, o);
+            if (lane >= o) upto += y;
+        }
+        const unsigned hit = __ballot_sync(kFull, base + upto > index && base + upto - n <= index);
+        if (hit != 0) {
+            const int src = __ffs(hit) - 1;
+            w.kind = 1;
+            w.seq = i0 + src;
+            w.bos = __shfl_sync(kFull, bos, src);
+            w.len = __shfl_sync(kFull, eos, src) - w.bos;
+            w.segs = __shfl_sync(kFull, base + upto - n, src);
+            w.seg = index - w.segs;
+            w.first = w.seg * sp.seg_chunks;
+            w.chunks = min(sp.seg_chunks, (w.len + kQ - 1) / kQ - w.first);
+            w.last = w.seg + 1 == __shfl_sync(kFull, n, src);
+            return w;
+        }
+        base += __shfl_sync(kFull, upto, 31);
+    }
+    return w;
+}
+
+// kStates: the first launch over segments, which only computes what each adds to the state.
+template <typename StateT, int N, bool kStates>
+__global__ void __launch_bounds__(kSThreads, 1) gdn_ssm_scan_kernel(const __grid_constant__ ScanParams sp) {
+    using L = Lay<N>;
+    const Params& p = sp.p;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char* sm = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
+    Misc& ms = *reinterpret_cast<Misc*>(sm + L::kMisc);
+    const uint32_t sbase = saddr(sm);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int units = p.H * p.blocks;
+    const int unit = static_cast<int>(blockIdx.x % units), index = static_cast<int>(blockIdx.x / units);
+    const int h = unit / p.blocks, pb = unit - h * p.blocks, g = h / p.group;
+    const int col = h * p.P + pb * kPB;
+    dep_wait();
+    dep_launch();
+    const Work wk = find_work(sp, index, lane);
+    if (wk.kind == 0 || (kStates && wk.last)) return;            // (nothing follows the last segment)
+
+    if (warp == kWarps) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(saddr(&ms.tmem)));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    if (tid == 0) {
+        for (int k = 0; k < kXStages; ++k) bar_init(&ms.x_full[k], 1);
+        bar_init(&ms.bc_full, 1);
+        for (int k = 0; k < 2; ++k) {
+            bar_init(&ms.z_full[k], 1);
+            bar_init(&ms.gates_full[k], 1);
+        }
+        bar_init(&ms.g_done, 1);
+        bar_init(&ms.ds_done, 1);
+        bar_init(&ms.y2_done, 1);
+        bar_init(&ms.y1_done, 1);
+        bar_init(&ms.xw_ready, kWarps);
+        bar_init(&ms.s_ready, kWarps);
+        bar_init(&ms.p_ready, kWarps);
+        bar_init(&ms.chunk_done, kWarps);
+        bar_init(&ms.drain, 1);
+        ms.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tm = ms.tmem;
+    const uint32_t limit = sp.wait_limit;
+    const bool gated = p.z != nullptr;
+    volatile int* abort = &ms.abort;
+    const int row0 = wk.bos + wk.first * kQ;                     // first row of this CTA
+    const int left = wk.len - wk.first * kQ;                     // rows from there to the end of the sequence
+    auto rows_of = [&](int c) { return min(kQ, left - c * kQ); };
+    // Phase `use` of a barrier.  A role never waits for a phase that the barrier
+    // may have left behind by two (the parity would stand for the later one): who
+    // completes phase use + 1 waits, itself or through others, for what the
+    // waiter does after phase use.  need_warp: the whole warp takes one answer.
+    bool ok = true;
+    auto need = [&](unsigned long long* bar, int use) {
+        if (ok && !wait(bar, use, limit, abort)) {
+            ok = false;
+            *abort = 1;
+        }
+        return ok;
+    };
+    auto need_warp = [&](unsigned long long* bar, int use) {
+        if (ok && !__all_sync(kFull, wait(bar, use, limit, abort))) {
+            ok = false;
+            *abort = 1;
+        }
+        return ok;
+    };
+
+    if (warp == kWarps) {
+        // ---- copies and products ----
+        if (lane == 0) {
+            auto load_x = [&](int c) {
+                unsigned long long* bar = &ms.x_full[c % kXStages];
+                bar_expect(bar, L::kTile);
+                tma_load(sbase + L::kX + c % kXStages * L::kTile, &sp.x, col, row0 + c * kQ, bar);
+            };
+            auto load_bc = [&](int c) {
+                bar_expect(&ms.bc_full, (kStates ? 1 : 2) * (N / 64) * L::kTile);
+                for (int k = 0; k < N / 64; ++k) {
+                    tma_load(sbase + L::kB + k * L::kTile, &sp.B, g * N + 64 * k, row0 + c * kQ, &ms.bc_full);
+                    if (!kStates) tma_load(sbase + L::kC + k * L::kTile, &sp.C, g * N + 64 * k, row0 + c * kQ, &ms.bc_full);
+                }
+            };
+            auto load_z = [&](int c) {
+                if (kStates || !gated) return;
+                bar_expect(&ms.z_full[c & 1], L::kTile);
+                tma_load(sbase + L::kZ + (c & 1) * L::kTile, &sp.z, col, row0 + c * kQ, &ms.z_full[c & 1]);
+            };
+            load_x(0);
+            load_bc(0);
+            load_z(0);
+            if (wk.chunks > 1) load_x(1);
+            int x_loads = wk.chunks > 1 ? 2 : 1, bc_loads = 1, z_loads = 1;
+            const uint32_t id_g = idesc_bf16(128, 128);
+            const uint32_t id_y1 = idesc_bf16(128, 64) | kBMn;
+            const uint32_t id_ds = idesc_bf16(128, 64) | kAMn | kBMn;
+            for (int c = 0; c < wk.chunks; ++c) {
+                const bool tail = rows_of(c) < kQ;               // its rows past the end are cleared before any product
+                if (!need(&ms.bc_full, c)) break;
+                if (tail && !need(&ms.xw_ready, c)) break;
+                fence_after();
+                if (!kStates) {
+                    const uint32_t dst = tm + kTG + (c & 1) * 128;
+                    for (int ks = 0; ks < N / 16; ++ks) {
+                        const uint32_t o = (ks >> 2) * L::kTile + (ks & 3) * 32;
+                        mma_bf16(dst, desc_sw128(sbase + L::kC + o), desc_sw128(sbase + L::kB + o), id_g, ks > 0);
+                    }
+                    commit(saddr(&ms.g_done));
+                }
+                if (!tail && !need(&ms.xw_ready, c)) break;
+                fence_after();
+                for (int part = 0; part < 2; ++part)
+                    for (int ks = 0; ks < kQ / 16; ++ks)
+                        mma_bf16(tm + kTdS, desc_mn(sbase + L::kB + ks * 2048, L::kTile),
+                                 desc_mn(sbase + L::kXw + part * L::kTile + ks * 2048, L::kTile), id_ds, part + ks > 0);
+                commit(saddr(&ms.ds_done));
+                if (!kStates) {
+                    if (!need(&ms.s_ready, c)) break;
+                    fence_after();
+                    const uint32_t dst = tm + kTY2 + (c & 1) * 64;
+                    for (int part = 0; part < 2; ++part)
+                        for (int ks = 0; ks < N / 16; ++ks)
+                            mma_bf16(dst, desc_sw128(sbase + L::kC + (ks >> 2) * L::kTile + (ks & 3) * 32),
+                                     desc_mn(sbase + L::kS + part * N * 128 + ks * 2048, L::kTile), id_y1, part + ks > 0);
+                    commit(saddr(&ms.y2_done));
+                }
+                // the next copies, each once what it overwrites has been read (x of chunk c - 1
+                // by the outputs, or by the weighing alone, which xw_ready of this chunk follows)
+                if (!kStates && c > 0 && c + 1 < wk.chunks && !need(&ms.chunk_done, c - 1)) break;
+                if (c + 2 < wk.chunks) {
+                    load_x(c + 2);
+                    ++x_loads;
+                }
+                if (c + 1 < wk.chunks) {
+                    load_z(c + 1);
+                    ++z_loads;
+                    if (!kStates && (!need(&ms.g_done, c) || !need(&ms.y2_done, c))) break;
+                    if (!need(&ms.ds_done, c)) break;
+                    load_bc(c + 1);
+                    ++bc_loads;
+                }
+                if (!kStates) {
+                    if (!need(&ms.p_ready, c)) break;
+                    fence_after();
+                    const uint32_t a = tm + kTG + (c & 1) * 128;
+                    for (int part = 0; part < 2; ++part)
+                        for (int ks = 0; ks < kQ / 16; ++ks)
+                            mma_bf16_ts(tm + kTY1, a + (ks >> 2) * 64 + part * 32 + (ks & 3) * 8,
+                                        desc_mn(sbase + L::kX + c % kXStages * L::kTile + ks * 2048, L::kTile), id_y1,
+                                        part + ks > 0);
+                    commit(saddr(&ms.y1_done));
+                }
+            }
+            // what is in flight, with the default bound: every product issued and every copy
+            // (all long complete, unless some warp gave up)
+            commit(saddr(&ms.drain));
+            bool drained = wait_parity(saddr(&ms.drain), 0, kSpinLimit);
+            for (int k = 0; k < kXStages; ++k) {
+                const int n = (x_loads - k + kXStages - 1) / kXStages;       // copies into this stage
+                if (n > 0) drained &= wait_parity(saddr(&ms.x_full[k]), (n - 1) & 1, kSpinLimit);
+            }
+            drained &= wait_parity(saddr(&ms.bc_full), (bc_loads - 1) & 1, kSpinLimit);
+            if (!kStates && gated)
+                for (int k = 0; k < 2; ++k) {
+                    const int n = (z_loads - k + 1) / 2;
+                    if (n > 0) drained &= wait_parity(saddr(&ms.z_full[k]), (n - 1) & 1, kSpinLimit);
+                }
+            if (!drained) raise(p.status, GDN_FLAG_DRAIN);
+        }
+        __syncwarp();
+    } else if (warp == kWarps + 1) {
+        // ---- decay factors: four tokens a lane ----
+        const float rate = -expf(ld(p.A_log + h)) * kLog2e, bias = __bfloat162float(p.dt_bias[h]);
+        __nv_bfloat16 raw[4];
+        auto fetch = [&](int c) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int t = 4 * lane + k;
+                if (t < rows_of(c)) raw[k] = p.dt[(static_cast<int64_t>(row0) + c * kQ + t) * p.dt_stride + h];
+            }
+        };
+        fetch(0);
+        for (int c = 0; c < wk.chunks; ++c) {
+            const int n = rows_of(c);
+            float d[4];
+            long long la[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                d[k] = 4 * lane + k < n ? softplus(__bfloat162float(raw[k]) + bias) : 0.f;
+                la[k] = __float2ll_rn(fmaxf(rate * d[k], -1048576.0f) * 4294967296.0f);   // 2^-(2^20) is 0 as it is
+            }
+            if (c + 1 < wk.chunks) fetch(c + 1);
+            // l: sums up to and with a token; r: sums behind it
+            long long l[4], up = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) l[k] = up += la[k];
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long a = __shfl_up_sync(kFull, up, o);
+                if (lane >= o) up += a;
+            }
+            const long long before = up - l[3];
+            const long long all = __shfl_sync(kFull, up, 31), block_end = __shfl_sync(kFull, up, lane | 7);
+            auto real = [](long long v) { return __ll2float_rn(v) * (1.0f / 4294967296.0f); };
+            float hi[4], lo[4], f[4], e[4], w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                l[k] += before;
+                const float units_hi = __ll2float_rn(l[k]);
+                hi[k] = units_hi * (1.0f / 4294967296.0f);
+                lo[k] = real(l[k] - __float2ll_rn(units_hi));
+                f[k] = exp2f(real(block_end - l[k])) * d[k];
+                e[k] = exp2f(hi[k]);
+                w[k] = exp2f(real(all - l[k])) * d[k];
+            }
+            if (c >= 2 && !need_warp(&ms.chunk_done, c - 2)) break;   // the buffer's last readers
+            Gates& gt = ms.gates[c & 1];
+            *reinterpret_cast<float4*>(gt.l + 4 * lane) = make_float4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<float4*>(gt.l_lo + 4 * lane) = make_float4(lo[0], lo[1], lo[2], lo[3]);
+            *reinterpret_cast<float4*>(gt.f + 4 * lane) = make_float4(f[0], f[1], f[2], f[3]);
+            *reinterpret_cast<float4*>(gt.e + 4 * lane) = make_float4(e[0], e[1], e[2], e[3]);
+            *reinterpret_cast<float4*>(gt.w + 4 * lane) = make_float4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<float4*>(gt.d + 4 * lane) = make_float4(d[0], d[1], d[2], d[3]);
+            if (lane == 0) {
+                gt.total = exp2f(real(all));
+                gt.total_log = real(all);
+            }
+            __syncwarp();
+            if (lane == 0) bar_arrive(&ms.gates_full[c & 1]);
+        }
+    } else {
+        // ---- tiles ----
+        const int quad = warp & 3, hh = warp >> 2;
+        const int row = quad * 32 + lane;                        // token t or s, or state row n: this thread's lane
+        const uint32_t lanes = tm + (static_cast<uint32_t>(quad * 32) << 16);
+        const bool state_row = row < N;                          // whole warps
+        const float D = p.D ? ld(p.D + h) : 0.f;
+        alignas(16) float S[32];                                 // state row `row`, columns 32 hh ..
+#pragma unroll
+        for (int j = 0; j < 32; ++j) S[j] = 0.f;
+        float run_log = 0.f;
+        if (!kStates && state_row) {
+            const long long rs = ld(p.read_slots + wk.seq);
+            if (rs >= 0)
+                load_row32(static_cast<const StateT*>(p.pool) + ((rs * p.H + h) * N + row) * static_cast<int64_t>(p.P) + pb * kPB +
+                               32 * hh,
+                           S);
+            // segments: what lies before this one
+            for (int k = 0; k < wk.seg; ++k) {
+                const int64_t at = static_cast<int64_t>(wk.segs + k) * units + unit;
+                const float a = exp2f(sp.part_decay[at]);
+                alignas(16) float x[32];
+                load_row32(sp.part + (at * N + row) * kPB + 32 * hh, x);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) S[j] = fmaf(a, S[j], x[j]);
+            }
+        }
+        // Xw of chunk c, and the rows past the sequence's end cleared
+        auto weigh = [&](int c) {
+            if (!need_warp(&ms.gates_full[c & 1], c >> 1) || !need_warp(&ms.x_full[c % kXStages], c / kXStages)) return;
+            const int n = rows_of(c);
+            unsigned char* X = sm + L::kX + c % kXStages * L::kTile;
+            const float w = ms.gates[c & 1].w[row];
+            if (n < kQ) {
+                if (!need_warp(&ms.bc_full, c)) return;
+                if (row >= n) {
+                    const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(X + unit16(row, 4 * hh + j)) = zero;
+#pragma unroll
+                    for (int j = 0; j < N / 16; ++j) {           // this half of the row's N / 8 units
+                        const int u = hh * (N / 16) + j;
+                        *reinterpret_cast<uint4*>(sm + L::kB + (u >> 3) * L::kTile + unit16(row, u & 7)) = zero;
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t at = unit16(row, 4 * hh + j);
+                const uint4 v = *reinterpret_cast<const uint4*>(X + at);
+                const __nv_bfloat162* hx = reinterpret_cast<const __nv_bfloat162*>(&v);
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = __bfloat1622float2(hx[e]);
+                    x[2 * e] = f.x * w;
+                    x[2 * e + 1] = f.y * w;
+                }
+                uint4 hi, lo;
+                split8(x, hi, lo);
+                *reinterpret_cast<uint4*>(sm + L::kXw + at) = hi;
+                *reinterpret_cast<uint4*>(sm + L::kXw + L::kTile + at) = lo;
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&ms.xw_ready);
+        };
+        // the state's hi and lo images for chunk c
+        auto image = [&]() {
+            if (state_row) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint4 hi, lo;
+                    split8(S + 8 * j, hi, lo);
+                    *reinterpret_cast<uint4*>(sm + L::kS + unit16(row, 4 * hh + j)) = hi;
+                    *reinterpret_cast<uint4*>(sm + L::kS + N * 128 + unit16(row, 4 * hh + j)) = lo;
+                }
+            }
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&ms.s_ready);
+        };
+        weigh(0);
+        if (!kStates && ok) image();
+        for (int c = 0; c < wk.chunks && ok; ++c) {
+            const int n = rows_of(c);
+            const Gates& gt = ms.gates[c & 1];
+            if (!kStates) {
+                // Pm = G with the decays, causal, hi and lo, into the columns that this warp read
+                if (!need_warp(&ms.g_done, c)) break;
+                fence_after();
+                const uint32_t G = lanes + kTG + (c & 1) * 128 + 64 * hh;
+                uint32_t raw[2][32];
+                if (2 * hh <= quad) tm_ld32_nowait(G, raw[0]);
+                if (2 * hh + 1 <= quad) tm_ld32_nowait(G + 32, raw[1]);
+                tm_wait_ld();
+                const float lt = gt.l[row], lt_lo = gt.l_lo[row];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const int j = 2 * hh + b;                    // block of 32 columns s
+                    uint32_t hi[16], lo[16];
+                    if (j > quad) {
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) hi[k] = lo[k] = 0;
+                    } else if (j < quad) {
+                        const float e = exp2f((lt - gt.l[32 * j + 31]) + (lt_lo - gt.l_lo[32 * j + 31]));
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float4 f = *reinterpret_cast<const float4*>(gt.f + 32 * j + 4 * k);
+                            split2(__uint_as_float(raw[b][4 * k]) * (e * f.x), __uint_as_float(raw[b][4 * k + 1]) * (e * f.y),
+                                   hi[2 * k], lo[2 * k]);
+                            split2(__uint_as_float(raw[b][4 * k + 2]) * (e * f.z), __uint_as_float(raw[b][4 * k + 3]) * (e * f.w),
+                                   hi[2 * k + 1], lo[2 * k + 1]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const float4 l4 = *reinterpret_cast<const float4*>(gt.l + 32 * j + 4 * k);
+                            const float4 d4 = *reinterpret_cast<const float4*>(gt.d + 32 * j + 4 * k);
+                            const float4 m4 = *reinterpret_cast<const float4*>(gt.l_lo + 32 * j + 4 * k);
+                            const float ls[4] = {l4.x, l4.y, l4.z, l4.w}, ds[4] = {d4.x, d4.y, d4.z, d4.w};
+                            const float ms_lo[4] = {m4.x, m4.y, m4.z, m4.w};
+                            float v[4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                v[q] = 4 * k + q <= lane ? __uint_as_float(raw[b][4 * k + q]) * (exp2f((lt - ls[q]) + (lt_lo - ms_lo[q])) * ds[q]) : 0.f;
+                            split2(v[0], v[1], hi[2 * k], lo[2 * k]);
+                            split2(v[2], v[3], hi[2 * k + 1], lo[2 * k + 1]);
+                        }
+                    }
+                    tm_st16(G + 16 * b, hi);
+                    tm_st16(G + 32 + 16 * b, lo);
+                }
+                tm_wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&ms.p_ready);
+            }
+            // the state after this chunk
+            if (!need_warp(&ms.ds_done, c)) break;
+            fence_after();
+            const float a = gt.total;
+            run_log += gt.total_log;
+            if (state_row) {
+                uint32_t x[32];
+                tm_ld32_nowait(lanes + kTdS + 32 * hh, x);
+                tm_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) S[j] = fmaf(a, S[j], __uint_as_float(x[j]));
+            }
+            fence_before();
+            const float et = gt.e[row];
+            if (c + 1 < wk.chunks) {
+                weigh(c + 1);
+                if (!kStates) {
+                    if (!need_warp(&ms.y2_done, c)) break;            // the images may be overwritten
+                    image();
+                }
+            }
+            if (!kStates) {
+                // the outputs: (2^(l_t) Y2 + Y1 + D x) silu(z)
+                // (with a chunk to come y2_done has been waited for above, and may be a phase on)
+                if (c + 1 == wk.chunks && !need_warp(&ms.y2_done, c)) break;
+                if (!need_warp(&ms.y1_done, c)) break;
+                if (gated && !need_warp(&ms.z_full[c & 1], c >> 1)) break;
+                fence_after();
+                uint32_t y1[32], y2[32];
+                tm_ld32_nowait(lanes + kTY1 + 32 * hh, y1);
+                tm_ld32_nowait(lanes + kTY2 + (c & 1) * 64 + 32 * hh, y2);
+                tm_wait_ld();
+                const unsigned char* X = sm + L::kX + c % kXStages * L::kTile;
+                unsigned char* Z = sm + L::kZ + (c & 1) * L::kTile;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t at = unit16(row, 4 * hh + j);
+                    const uint4 xv = *reinterpret_cast<const uint4*>(X + at);
+                    const __nv_bfloat162* hx = reinterpret_cast<const __nv_bfloat162*>(&xv);
+                    float o[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = __bfloat1622float2(hx[e]);
+                        const int k = 8 * j + 2 * e;
+                        o[2 * e] = fmaf(D, f.x, fmaf(et, __uint_as_float(y2[k]), __uint_as_float(y1[k])));
+                        o[2 * e + 1] = fmaf(D, f.y, fmaf(et, __uint_as_float(y2[k + 1]), __uint_as_float(y1[k + 1])));
+                    }
+                    if (gated) {
+                        const uint4 zv = *reinterpret_cast<const uint4*>(Z + at);
+                        const __nv_bfloat162* hz = reinterpret_cast<const __nv_bfloat162*>(&zv);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 f = __bfloat1622float2(hz[e]);
+                            o[2 * e] *= silu(f.x);
+                            o[2 * e + 1] *= silu(f.y);
+                        }
+                    }
+                    *reinterpret_cast<uint4*>(Z + at) =
+                        make_uint4(pack2(o[0], o[1]), pack2(o[2], o[3]), pack2(o[4], o[5]), pack2(o[6], o[7]));
+                }
+                fence_before();
+                __syncwarp();
+                // rows of this warp to memory: 64 bytes of 8 rows an access
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int t = 32 * quad + 8 * k + (lane >> 2), u = 4 * hh + (lane & 3);
+                    const uint4 v = *reinterpret_cast<const uint4*>(Z + unit16(t, u));
+                    if (t < n)
+                        *reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(row0) + c * kQ + t) * p.out_stride + col + 8 * u) = v;
+                }
+            }
+            fence_async_smem();                                  // before the next copies overwrite what was read
+            __syncwarp();
+            if (lane == 0) bar_arrive(&ms.chunk_done);
+        }
+        // what this CTA leaves, unless a warp gave up: its segment's part, or the sequence's last
+        // state, rounded once
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
+        if (*abort == 0 && state_row) {
+            if (kStates) {
+                const int64_t at = static_cast<int64_t>(index) * units + unit;
+                store_row32(sp.part + (at * N + row) * kPB + 32 * hh, S);
+                if (row == 0 && hh == 0) sp.part_decay[at] = run_log;
+            } else if (wk.last) {
+                const long long ws = ld(p.write_slots + wk.seq);
+                if (ws >= 0)
+                    store_row32(static_cast<StateT*>(p.pool) + ((ws * p.H + h) * N + row) * static_cast<int64_t>(p.P) + pb * kPB +
+                                    32 * hh,
+                                S);
+            }
+        }
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (tid == 0 && *abort != 0) raise(p.status, GDN_FLAG_TIMEOUT);
+    if (warp == kWarps) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm));
+}
+
+// ---- host side ----------------------------------------------------------------------
+
+// rows x cols bf16, rows `stride` elements apart, read in boxes of 64 x 128
+bool encode_map(CUtensorMap& map, const void* base, int64_t cols, int64_t rows, int64_t stride) {
+    using Encode = PFN_cuTensorMapEncodeTiled_v12000;
+    static const Encode encode = [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            fn = nullptr;
+        return reinterpret_cast<Encode>(fn);
+    }();
+    if (encode == nullptr) return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(stride) * 2};
+    const cuuint32_t box[2] = {64, kQ};
+    const cuuint32_t estr[2] = {1, 1};
+    return encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename StateT, int N, bool kStates>
+cudaError_t launch_kernel(const ScanParams& sp, int64_t ctas, cudaStream_t stream) {
+    auto kernel = gdn_ssm_scan_kernel<StateT, N, kStates>;
+    static bool done[64] = {false};                              // shared-memory opt-in, once per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64 || !__atomic_load_n(&done[dev], __ATOMIC_ACQUIRE)) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, scan_smem<N>());
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) __atomic_store_n(&done[dev], true, __ATOMIC_RELEASE);
+    }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(static_cast<int64_t>(p.batch) * p.H * p.blocks), 1, 1);
-    cfg.blockDim = dim3(kRThreads, 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
+    cfg.blockDim = dim3(kSThreads, 1, 1);
+    cfg.dynamicSmemBytes = scan_smem<N>();
     cfg.stream = stream;
-    return N == 64 ? cudaLaunchKernelEx(&cfg, gdn_ssm_prefill_kernel<StateT, 64>, p)
-                   : cudaLaunchKernelEx(&cfg, gdn_ssm_prefill_kernel<StateT, 128>, p);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, sp);
+}
+
+// Chunks of a segment, 0 for whole sequences.
+int segment_chunks(int batch, int num_tokens, int units) {
+    (void)batch, (void)num_tokens, (void)units;
+    return 0;
+}
+
+int64_t segment_room(int batch, int num_tokens, int chunks) {
+    return static_cast<int64_t>(num_tokens) / (static_cast<int64_t>(chunks) * kQ) + batch;
+}
+
+template <typename StateT, int N>
+cudaError_t launch(ScanParams& sp, int units, void* workspace, cudaStream_t stream) {
+    const Params& p = sp.p;
+    sp.seg_chunks = segment_chunks(p.batch, p.num_tokens, units);
+    if (sp.seg_chunks == 0) {
+        sp.segs = p.batch;
+        return launch_kernel<StateT, N, false>(sp, static_cast<int64_t>(p.batch) * units, stream);
+    }
+    const int64_t room = segment_room(p.batch, p.num_tokens, sp.seg_chunks);
+    if (room * units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    sp.segs = static_cast<int32_t>(room);
+    sp.part = static_cast<float*>(workspace);
+    sp.part_decay = sp.part + room * units * N * kPB;
+    const cudaError_t e = launch_kernel<StateT, N, true>(sp, room * units, stream);
+    return e != cudaSuccess ? e : launch_kernel<StateT, N, false>(sp, room * units, stream);
+}
+
+template <int N>
+cudaError_t launch_n(ScanParams& sp, gdn_dtype t, int units, void* ws, cudaStream_t s) {
+    return t == GDN_F32    ? launch<float, N>(sp, units, ws, s)
+           : t == GDN_BF16 ? launch<__nv_bfloat16, N>(sp, units, ws, s)
+                           : launch<__half, N>(sp, units, ws, s);
 }
 
 }  // namespace
 
 namespace gdn_ssm {
 
-int64_t prefill_workspace(int, int, int, int) { return 0; }
+int64_t prefill_workspace(int batch, int num_tokens, int units, int N) {
+    const int chunks = segment_chunks(batch, num_tokens, units);
+    return chunks == 0 ? 0 : segment_room(batch, num_tokens, chunks) * units * (static_cast<int64_t>(N) * kPB + 1) * 4;
+}
 
-cudaError_t launch_prefill(const Params& p, int N, gdn_dtype state_dtype, void*, cudaStream_t stream) {
-    return state_dtype == GDN_F32    ? launch<float>(p, N, stream)
-           : state_dtype == GDN_BF16 ? launch<__nv_bfloat16>(p, N, stream)
-                                     : launch<__half>(p, N, stream);
+cudaError_t launch_prefill(const Params& p, int N, gdn_dtype state_dtype, void* workspace, cudaStream_t stream) {
+    ScanParams sp = {};
+    sp.p = p;
+    sp.wait_limit = __atomic_load_n(&gdn_internal::g_wait_limit, __ATOMIC_RELAXED);
+    const int64_t HP = static_cast<int64_t>(p.H) * p.P, GN = static_cast<int64_t>(p.G) * N;
+    if (!encode_map(sp.x, p.x, HP, p.num_tokens, p.x_stride) || !encode_map(sp.B, p.B, GN, p.num_tokens, p.b_stride) ||
+        !encode_map(sp.C, p.C, GN, p.num_tokens, p.c_stride) ||
+        (p.z && !encode_map(sp.z, p.z, HP, p.num_tokens, p.z_stride)))
+        return cudaErrorInvalidValue;
+    const int units = p.H * p.blocks;
+    return N == 64 ? launch_n<64>(sp, state_dtype, units, workspace, stream)
+                   : launch_n<128>(sp, state_dtype, units, workspace, stream);
 }
 
 }  // namespace gdn_ssm

@@ -142,7 +142,7 @@ __device__ __forceinline__ void token(u64 (&S)[N / 16][4], Round<N>& s, int t) {
         xs[2 * e] = pk2(d * v.x, d * v.y);
         xs[2 * e + 1] = pk2(d * v.z, d * v.w);
     }
-    float b[R], c[R];
+    alignas(16) float b[R], c[R];
 #pragma unroll
     for (int j = 0; j < R; j += 4) {
         *reinterpret_cast<float4*>(b + j) = *reinterpret_cast<const float4*>(&s.B[t][rg * R + j]);

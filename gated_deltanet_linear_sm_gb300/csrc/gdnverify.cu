@@ -65,7 +65,7 @@ template <typename T>
 struct Vec {
     static constexpr int E = 16 / sizeof(T);
     __device__ static void load(const T* p, float (&x)[E]) {
-        const uint4 raw = __ldg(reinterpret_cast<const uint4*>(p));
+        const uint4 raw = ld(reinterpret_cast<const uint4*>(p));
         const T* e = reinterpret_cast<const T*>(&raw);
 #pragma unroll
         for (int k = 0; k < E; ++k) x[k] = to_f(e[k]);
@@ -99,13 +99,12 @@ __global__ void __launch_bounds__(kVThreads) gdn_verify_kernel(const VerifyParam
     const T* draft = static_cast<const T*>(p.draft);
     // every CTA of the cluster runs before one writes into another's memory (waited for below)
     asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    dep_wait();
 
     // ---- which drafts stay ----
     if (warp == 0) {
-        const int bos = __ldg(p.cu + i);
-        const int eos = __ldg(p.cu + i + 1);
+        const int bos = ld(p.cu + i);
+        const int eos = ld(p.cu + i + 1);
         const int n = (eos > bos && bos >= 0) ? eos - bos : 0;
         int flag = 0;
         int64_t row = 0;
@@ -114,9 +113,9 @@ __global__ void __launch_bounds__(kVThreads) gdn_verify_kernel(const VerifyParam
         } else if (n > p.max_T) {
             flag = GDN_FLAG_QLEN;
         } else if (n > 0) {
-            bool bad = eos > __ldg(p.cu + p.batch);
+            bool bad = eos > ld(p.cu + p.batch);
             if (!bad && lane < n) {
-                row = p.sti ? __ldg(p.sti + bos + lane) : bos + lane;
+                row = p.sti ? ld(p.sti + bos + lane) : bos + lane;
                 bad = row < 0 || row >= p.num_tokens;
             }
             if (__any_sync(kFull, bad)) flag = GDN_FLAG_TOKEN_ROW;
@@ -125,13 +124,13 @@ __global__ void __launch_bounds__(kVThreads) gdn_verify_kernel(const VerifyParam
         int d = -1;
         bool keep = false, in_range = false;
         if (valid && lane < n - 1) {
-            d = __ldg(p.tokens + i * p.token_stride + lane);
+            d = ld(p.tokens + i * p.token_stride + lane);
             in_range = d >= 0 && d < p.vocab;
             if (in_range) {
                 const float pd = clamp01(to_f(target[row * p.target_stride + d]));
                 const float qd =
                     draft ? clamp01(to_f(draft[i * p.draft_seq + lane * p.draft_stride + d])) : 1.0f;
-                const double u = __ldg(p.accept_u + i * p.token_stride + lane);
+                const double u = ld(p.accept_u + i * p.token_stride + lane);
                 keep = u * static_cast<double>(qd) < static_cast<double>(pd);   // the product of two floats is exact
             }
         }
@@ -232,7 +231,7 @@ __global__ void __launch_bounds__(kVThreads) gdn_verify_kernel(const VerifyParam
         }
         return;
     }
-    const double x = fmax(static_cast<double>(__ldg(p.sample_u + i)) * static_cast<double>(total), 0.0);   // NaN -> 0
+    const double x = fmax(static_cast<double>(ld(p.sample_u + i)) * static_cast<double>(total), 0.0);   // NaN -> 0
     u64 level = x < static_cast<double>(total) ? static_cast<u64>(x) : total - 1;
     if (level >= total) level = total - 1;
     const u64* sums = whole ? s.cta_p : s.cta_rest;
@@ -343,14 +342,14 @@ struct Request {
 
 __device__ __forceinline__ Request request_at(const TablesParams& p, int i) {
     Request v;
-    v.q = max(__ldg(p.q_lens + i), 0);
-    v.r = p.request ? __ldg(p.request + i) : i;
+    v.q = max(ld(p.q_lens + i), 0);
+    v.r = p.request ? ld(p.request + i) : i;
     v.flag = 0;
     if (v.r >= p.num_requests) {
         v.flag = GDN_FLAG_SLOT_RANGE;
         v.r = -1;
     }
-    v.mine = (p.spec == nullptr || __ldg(p.spec + i) != 0) && v.r >= 0;
+    v.mine = (p.spec == nullptr || ld(p.spec + i) != 0) && v.r >= 0;
     if (v.mine && v.q > p.stride) {
         v.flag |= GDN_FLAG_QLEN;
         v.mine = false;
@@ -364,8 +363,7 @@ __global__ void __launch_bounds__(kTThreads) gdn_step_tables_kernel(const Tables
     __shared__ bool is_mine[kTile];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int i0 = blockIdx.x * kTile, i1 = min(p.batch, i0 + kTile);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    dep_wait();
 
     // rows and speculative rows before the tile, and of all requests
     long long sums[4] = {0, 0, 0, 0};
@@ -432,14 +430,14 @@ __global__ void __launch_bounds__(kTThreads) gdn_step_tables_kernel(const Tables
         const int i = i0 + k;
         p.cu[i] = spec_start[k];
         if (p.starts) p.starts[i] = start[k];
-        const int r = p.request ? __ldg(p.request + i) : i;
-        p.acc[i] = is_mine[k] ? __ldg(p.accepted + r) : 0;
+        const int r = p.request ? ld(p.request + i) : i;
+        p.acc[i] = is_mine[k] ? ld(p.accepted + r) : 0;
         if (p.conv_table) {
             int in = -1, out = -1;
             if (is_mine[k]) {
                 const int c = p.conv_turn[r] & 1;
-                in = __ldg(p.conv_table + 2 * static_cast<int64_t>(r) + c);
-                out = __ldg(p.conv_table + 2 * static_cast<int64_t>(r) + 1 - c);
+                in = ld(p.conv_table + 2 * static_cast<int64_t>(r) + c);
+                out = ld(p.conv_table + 2 * static_cast<int64_t>(r) + 1 - c);
                 if (start[k + 1] > start[k]) p.conv_turn[r] = 1 - c;
             }
             p.conv_in[i] = in;
@@ -453,9 +451,9 @@ __global__ void __launch_bounds__(kTThreads) gdn_step_tables_kernel(const Tables
     const int cells = (i1 - i0) * p.stride;
     for (int e = tid; e < cells; e += kTThreads) {
         const int k = e / p.stride;
-        const int r = p.request ? __ldg(p.request + i0 + k) : i0 + k;
+        const int r = p.request ? ld(p.request + i0 + k) : i0 + k;
         p.idx[static_cast<int64_t>(i0) * p.stride + e] =
-            is_mine[k] ? __ldg(p.slots + static_cast<int64_t>(r) * p.stride + (e - k * p.stride)) : -1;
+            is_mine[k] ? ld(p.slots + static_cast<int64_t>(r) * p.stride + (e - k * p.stride)) : -1;
     }
     // the rows: speculative ones first
     for (int row = start[0] + tid; row < start[i1 - i0]; row += kTThreads) {
