@@ -274,6 +274,7 @@ __global__ void __launch_bounds__(kRThreads, 4) gdn_ssm_decode_kernel(const Para
         const int r = p.sti ? ld(p.sti + bos + tid) : bos + tid;
         bad = r < 0 || r >= p.num_tokens;
         s.row[tid] = r;
+        s.slot[tid] = ld(slot_row + tid);
         if (!bad) {
             const float d = softplus(__bfloat162float(p.dt[r * p.dt_stride + h]) + __bfloat162float(p.dt_bias[h]));
             s.step[tid] = d;
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(kRThreads, 4) gdn_ssm_decode_kernel(const Para
     // ---- the tokens ----
     for (int t = 0; t < n; ++t) {
         token<StateT, N>(S, s, t);
-        const long long ws = ld(slot_row + t);
+        const long long ws = s.slot[t];
         if (ws >= 0 && ws < p.num_slots) {
             StateT* dst = static_cast<StateT*>(p.pool) + ws * p.H * tile + at;
 #pragma unroll

@@ -12,7 +12,8 @@
 // chunk, with four products of 128 rows (tcgen05.mma, bf16 operands, FP32
 // accumulators in tensor memory):
 //     G  = C B^T          rows t, columns s     128 x 128 x N
-//     Y1 = Pm X           rows t, columns p     128 x  64 x 128, Pm = G with the decays, causal
+//     Y1 = Pm X           rows t, columns p     128 x  64 x 128, Pm = G with the decays, causal,
+//                                               and D on its diagonal
 //     Y2 = C S            rows t, columns p     128 x  64 x N
 //     dS = B^T Xw         rows n, columns p     128 x  64 x 128, Xw_s = 2^(l_last - l_s) d_s x_s
 // B, C and x are bf16 and exact.  What is computed in FP32 (Pm, S, Xw) enters as
@@ -25,11 +26,14 @@
 // with rows and depth exchanged need no transposed copy.  Pm goes back into the
 // tensor memory that G was in and is multiplied from there.
 //
-// Ten warps: 0-7 the arithmetic on tiles (warp w and w + 4 share the 32 rows
-// that hardware lets them reach, and split the columns), 8 issues copies and
-// products, 9 turns dt into the decay factors of the chunk after next.  They
-// meet at mbarriers only.  dS and G of a chunk do not depend on the state, so
-// the chain from chunk to chunk is the FP32 update of S and the product Y2.
+// Eighteen warps.  0-7 keep the state: they weigh x, update S, write its images
+// and finish the outputs; 8 issues copies and products; 9 turns dt into the decay
+// factors of the chunk after next; 10-17 turn G into Pm, up to a chunk ahead of
+// the others, since G does not depend on the state.  (Two warps share the 32 rows
+// of tensor memory that the hardware lets them reach, and split the columns.)
+// They meet at mbarriers only.  dS of a chunk does not depend on the state either,
+// so the chain from chunk to chunk is the FP32 update of S and the product Y2.
+// Arithmetic runs on pairs of columns (fma.rn.f32x2).
 // Every wait is bounded: on a timeout the CTA sets GDN_FLAG_TIMEOUT, writes no
 // state, waits (bounded) for what it has in flight and releases its tensor
 // memory.
@@ -53,8 +57,9 @@ using namespace gdn_tc;
 namespace {
 
 constexpr int kQ = 128;                          // tokens of a chunk
-constexpr int kWarps = 8;                        // on tiles
-constexpr int kSThreads = 32 * (kWarps + 2);
+constexpr int kWarps = 8;                        // that keep the state; as many make Pm
+constexpr int kSThreads = 32 * (2 * kWarps + 2);
+constexpr int kStatesThreads = 32 * (kWarps + 2);
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kXStages = 3;
 
@@ -147,14 +152,19 @@ __device__ __forceinline__ void tm_ld32_nowait(uint32_t taddr, uint32_t (&r)[32]
           "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
 }
+__device__ __forceinline__ void tm_ld16_nowait(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
 __device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-        : "memory");
+__device__ __forceinline__ void tm_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
 }
 
 __device__ __forceinline__ void bar_init(unsigned long long* b, int count) {
@@ -184,60 +194,84 @@ __device__ __forceinline__ bool wait(unsigned long long* bar, int use, uint32_t 
     return false;
 }
 
+// 2^x and 1 / x as single instructions (results and inputs below 2^-126 become 0)
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ u64 dup2(float x) { return pk2(x, x); }
+__device__ __forceinline__ u64 raw2(uint32_t a, uint32_t b) { return (static_cast<u64>(b) << 32) | a; }
+// the two bf16 of a word as a pair of floats
+__device__ __forceinline__ u64 widen(uint32_t w) { return raw2(w << 16, w & 0xffff0000u); }
+// x as bf16 hi and lo words: lo = bf16(x - hi), the difference exact
+__device__ __forceinline__ void split_pair(u64 x, uint32_t& hi, uint32_t& lo) {
+    hi = pack2(lo2(x), hi2(x));
+    const u64 r = ffma2(widen(hi), dup2(-1.0f), x);
+    lo = pack2(lo2(r), hi2(r));
+}
+__device__ __forceinline__ void split_quads(const u64* x, uint4& hi, uint4& lo) {
+    split_pair(x[0], hi.x, lo.x);
+    split_pair(x[1], hi.y, lo.y);
+    split_pair(x[2], hi.z, lo.z);
+    split_pair(x[3], hi.w, lo.w);
+}
+// o * silu(z) for a pair, z in bf16: z / (1 + 2^(-z log2 e))
+__device__ __forceinline__ u64 gate_pair(u64 o, uint32_t zw) {
+    const u64 z = widen(zw);
+    const u64 t = fmul2(z, dup2(-kLog2e));
+    const u64 den = raw2(__float_as_uint(1.0f + ex2(lo2(t))), __float_as_uint(1.0f + ex2(hi2(t))));
+    return fmul2(o, fmul2(z, pk2(rcp(lo2(den)), rcp(hi2(den)))));
+}
+
 __device__ __forceinline__ uint32_t unit16(int r, int j) { return static_cast<uint32_t>(r * 128 + ((j ^ (r & 7)) << 4)); }
 
-// 32 consecutive elements of a state row <-> FP32
-__device__ __forceinline__ void load_row32(const float* p, float (&x)[32]) {
+// 32 consecutive elements of a state row <-> pairs of FP32
+__device__ __forceinline__ void load_row32(const float* p, u64 (&x)[16]) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) *reinterpret_cast<float4*>(x + 4 * j) = __ldcs(reinterpret_cast<const float4*>(p) + j);
+    for (int j = 0; j < 8; ++j) {
+        const float4 v = __ldcs(reinterpret_cast<const float4*>(p) + j);
+        x[2 * j] = pk2(v.x, v.y);
+        x[2 * j + 1] = pk2(v.z, v.w);
+    }
 }
-__device__ __forceinline__ void load_row32(const __nv_bfloat16* p, float (&x)[32]) {
+__device__ __forceinline__ u64 to_pair(uint32_t w, __nv_bfloat16) { return widen(w); }
+__device__ __forceinline__ u64 to_pair(uint32_t w, __half) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    return pk2(f.x, f.y);
+}
+__device__ __forceinline__ uint32_t from_pair(u64 x, __nv_bfloat16) { return pack2(lo2(x), hi2(x)); }
+__device__ __forceinline__ uint32_t from_pair(u64 x, __half) {
+    const __half2 h = __floats2half2_rn(lo2(x), hi2(x));
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <typename T>
+__device__ __forceinline__ void load_row32(const T* p, u64 (&x)[16]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p) + j);
-        const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 f = __bfloat1622float2(h[e]);
-            x[8 * j + 2 * e] = f.x;
-            x[8 * j + 2 * e + 1] = f.y;
-        }
+        x[4 * j] = to_pair(v.x, T());
+        x[4 * j + 1] = to_pair(v.y, T());
+        x[4 * j + 2] = to_pair(v.z, T());
+        x[4 * j + 3] = to_pair(v.w, T());
     }
 }
-__device__ __forceinline__ void load_row32(const __half* p, float (&x)[32]) {
+__device__ __forceinline__ void store_row32(float* p, const u64 (&x)[16]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p) + j);
-        const __half2* h = reinterpret_cast<const __half2*>(&v);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float2 f = __half22float2(h[e]);
-            x[8 * j + 2 * e] = f.x;
-            x[8 * j + 2 * e + 1] = f.y;
-        }
-    }
+    for (int j = 0; j < 8; ++j)
+        __stcs(reinterpret_cast<float4*>(p) + j, make_float4(lo2(x[2 * j]), hi2(x[2 * j]), lo2(x[2 * j + 1]), hi2(x[2 * j + 1])));
 }
-__device__ __forceinline__ void store_row32(float* p, const float (&x)[32]) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) __stcs(reinterpret_cast<float4*>(p) + j, *reinterpret_cast<const float4*>(x + 4 * j));
-}
-__device__ __forceinline__ void store_row32(__nv_bfloat16* p, const float (&x)[32]) {
+template <typename T>
+__device__ __forceinline__ void store_row32(T* p, const u64 (&x)[16]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        __stcs(reinterpret_cast<uint4*>(p) + j, make_uint4(pack2(x[8 * j], x[8 * j + 1]), pack2(x[8 * j + 2], x[8 * j + 3]),
-                                                           pack2(x[8 * j + 4], x[8 * j + 5]), pack2(x[8 * j + 6], x[8 * j + 7])));
-}
-__device__ __forceinline__ void store_row32(__half* p, const float (&x)[32]) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        uint32_t w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const __half2 h = __floats2half2_rn(x[8 * j + 2 * e], x[8 * j + 2 * e + 1]);
-            w[e] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-        __stcs(reinterpret_cast<uint4*>(p) + j, make_uint4(w[0], w[1], w[2], w[3]));
-    }
+        __stcs(reinterpret_cast<uint4*>(p) + j, make_uint4(from_pair(x[4 * j], T()), from_pair(x[4 * j + 1], T()),
+                                                           from_pair(x[4 * j + 2], T()), from_pair(x[4 * j + 3], T())));
 }
 
 // What this CTA works on.  kind 0: nothing.
@@ -306,7 +340,7 @@ __device__ Work find_work(const ScanParams& sp, int index, int lane) {
 
 // kStates: the first launch over segments, which only computes what each adds to the state.
 template <typename StateT, int N, bool kStates>
-__global__ void __launch_bounds__(kSThreads, 1) gdn_ssm_scan_kernel(const __grid_constant__ ScanParams sp) {
+__global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_ssm_scan_kernel(const __grid_constant__ ScanParams sp) {
     using L = Lay<N>;
     const Params& p = sp.p;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -434,9 +468,10 @@ __global__ void __launch_bounds__(kSThreads, 1) gdn_ssm_scan_kernel(const __grid
                                      desc_mn(sbase + L::kS + part * N * 128 + ks * 2048, L::kTile), id_y1, part + ks > 0);
                     commit(saddr(&ms.y2_done));
                 }
-                // the next copies, each once what it overwrites has been read (x of chunk c - 1
-                // by the outputs, or by the weighing alone, which xw_ready of this chunk follows)
-                if (!kStates && c > 0 && c + 1 < wk.chunks && !need(&ms.chunk_done, c - 1)) break;
+                // The outputs of chunk c - 1 have been read: z's buffer, x's stage and Y1 may be
+                // overwritten.  (Without outputs x is read by the weighing alone, which xw_ready
+                // of this chunk follows.)
+                if (!kStates && c > 0 && !need(&ms.chunk_done, c - 1)) break;
                 if (c + 2 < wk.chunks) {
                     load_x(c + 2);
                     ++x_loads;
@@ -538,16 +573,15 @@ __global__ void __launch_bounds__(kSThreads, 1) gdn_ssm_scan_kernel(const __grid
             __syncwarp();
             if (lane == 0) bar_arrive(&ms.gates_full[c & 1]);
         }
-    } else {
-        // ---- tiles ----
+    } else if (warp < kWarps) {
+        // ---- the state, and the outputs ----
         const int quad = warp & 3, hh = warp >> 2;
         const int row = quad * 32 + lane;                        // token t or s, or state row n: this thread's lane
         const uint32_t lanes = tm + (static_cast<uint32_t>(quad * 32) << 16);
         const bool state_row = row < N;                          // whole warps
-        const float D = p.D ? ld(p.D + h) : 0.f;
-        alignas(16) float S[32];                                 // state row `row`, columns 32 hh ..
+        u64 S[16];                                               // state row `row`, columns 32 hh ..
 #pragma unroll
-        for (int j = 0; j < 32; ++j) S[j] = 0.f;
+        for (int j = 0; j < 16; ++j) S[j] = 0;
         float run_log = 0.f;
         if (!kStates && state_row) {
             const long long rs = ld(p.read_slots + wk.seq);
@@ -558,11 +592,11 @@ __global__ void __launch_bounds__(kSThreads, 1) gdn_ssm_scan_kernel(const __grid
             // segments: what lies before this one
             for (int k = 0; k < wk.seg; ++k) {
                 const int64_t at = static_cast<int64_t>(wk.segs + k) * units + unit;
-                const float a = exp2f(sp.part_decay[at]);
-                alignas(16) float x[32];
+                const u64 a2 = dup2(exp2f(ld(sp.part_decay + at)));
+                u64 x[16];
                 load_row32(sp.part + (at * N + row) * kPB + 32 * hh, x);
 #pragma unroll
-                for (int j = 0; j < 32; ++j) S[j] = fmaf(a, S[j], x[j]);
+                for (int j = 0; j < 16; ++j) S[j] = ffma2(a2, S[j], x[j]);
             }
         }
         // Xw of chunk c, and the rows past the sequence's end cleared
@@ -570,7 +604,7 @@ __global__ void __launch_bounds__(kSThreads, 1) gdn_ssm_scan_kernel(const __grid
             if (!need_warp(&ms.gates_full[c & 1], c >> 1) || !need_warp(&ms.x_full[c % kXStages], c / kXStages)) return;
             const int n = rows_of(c);
             unsigned char* X = sm + L::kX + c % kXStages * L::kTile;
-            const float w = ms.gates[c & 1].w[row];
+            const u64 w2 = dup2(ms.gates[c & 1].w[row]);
             if (n < kQ) {
                 if (!need_warp(&ms.bc_full, c)) return;
                 if (row >= n) {
@@ -588,16 +622,9 @@ __global__ void __launch_bounds__(kSThreads, 1) gdn_ssm_scan_kernel(const __grid
             for (int j = 0; j < 4; ++j) {
                 const uint32_t at = unit16(row, 4 * hh + j);
                 const uint4 v = *reinterpret_cast<const uint4*>(X + at);
-                const __nv_bfloat162* hx = reinterpret_cast<const __nv_bfloat162*>(&v);
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 f = __bfloat1622float2(hx[e]);
-                    x[2 * e] = f.x * w;
-                    x[2 * e + 1] = f.y * w;
-                }
+                const u64 x[4] = {fmul2(widen(v.x), w2), fmul2(widen(v.y), w2), fmul2(widen(v.z), w2), fmul2(widen(v.w), w2)};
                 uint4 hi, lo;
-                split8(x, hi, lo);
+                split_quads(x, hi, lo);
                 *reinterpret_cast<uint4*>(sm + L::kXw + at) = hi;
                 *reinterpret_cast<uint4*>(sm + L::kXw + L::kTile + at) = lo;
             }
@@ -605,13 +632,13 @@ __global__ void __launch_bounds__(kSThreads, 1) gdn_ssm_scan_kernel(const __grid
             __syncwarp();
             if (lane == 0) bar_arrive(&ms.xw_ready);
         };
-        // the state's hi and lo images for chunk c
+        // the state's hi and lo images for the next chunk
         auto image = [&]() {
             if (state_row) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     uint4 hi, lo;
-                    split8(S + 8 * j, hi, lo);
+                    split_quads(S + 4 * j, hi, lo);
                     *reinterpret_cast<uint4*>(sm + L::kS + unit16(row, 4 * hh + j)) = hi;
                     *reinterpret_cast<uint4*>(sm + L::kS + N * 128 + unit16(row, 4 * hh + j)) = lo;
                 }
@@ -625,116 +652,60 @@ __global__ void __launch_bounds__(kSThreads, 1) gdn_ssm_scan_kernel(const __grid
         for (int c = 0; c < wk.chunks && ok; ++c) {
             const int n = rows_of(c);
             const Gates& gt = ms.gates[c & 1];
-            if (!kStates) {
-                // Pm = G with the decays, causal, hi and lo, into the columns that this warp read
-                if (!need_warp(&ms.g_done, c)) break;
-                fence_after();
-                const uint32_t G = lanes + kTG + (c & 1) * 128 + 64 * hh;
-                uint32_t raw[2][32];
-                if (2 * hh <= quad) tm_ld32_nowait(G, raw[0]);
-                if (2 * hh + 1 <= quad) tm_ld32_nowait(G + 32, raw[1]);
-                tm_wait_ld();
-                const float lt = gt.l[row], lt_lo = gt.l_lo[row];
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const int j = 2 * hh + b;                    // block of 32 columns s
-                    uint32_t hi[16], lo[16];
-                    if (j > quad) {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) hi[k] = lo[k] = 0;
-                    } else if (j < quad) {
-                        const float e = exp2f((lt - gt.l[32 * j + 31]) + (lt_lo - gt.l_lo[32 * j + 31]));
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float4 f = *reinterpret_cast<const float4*>(gt.f + 32 * j + 4 * k);
-                            split2(__uint_as_float(raw[b][4 * k]) * (e * f.x), __uint_as_float(raw[b][4 * k + 1]) * (e * f.y),
-                                   hi[2 * k], lo[2 * k]);
-                            split2(__uint_as_float(raw[b][4 * k + 2]) * (e * f.z), __uint_as_float(raw[b][4 * k + 3]) * (e * f.w),
-                                   hi[2 * k + 1], lo[2 * k + 1]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const float4 l4 = *reinterpret_cast<const float4*>(gt.l + 32 * j + 4 * k);
-                            const float4 d4 = *reinterpret_cast<const float4*>(gt.d + 32 * j + 4 * k);
-                            const float4 m4 = *reinterpret_cast<const float4*>(gt.l_lo + 32 * j + 4 * k);
-                            const float ls[4] = {l4.x, l4.y, l4.z, l4.w}, ds[4] = {d4.x, d4.y, d4.z, d4.w};
-                            const float ms_lo[4] = {m4.x, m4.y, m4.z, m4.w};
-                            float v[4];
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                v[q] = 4 * k + q <= lane ? __uint_as_float(raw[b][4 * k + q]) * (exp2f((lt - ls[q]) + (lt_lo - ms_lo[q])) * ds[q]) : 0.f;
-                            split2(v[0], v[1], hi[2 * k], lo[2 * k]);
-                            split2(v[2], v[3], hi[2 * k + 1], lo[2 * k + 1]);
-                        }
-                    }
-                    tm_st16(G + 16 * b, hi);
-                    tm_st16(G + 32 + 16 * b, lo);
-                }
-                tm_wait_st();
-                fence_before();
-                __syncwarp();
-                if (lane == 0) bar_arrive(&ms.p_ready);
-            }
             // the state after this chunk
             if (!need_warp(&ms.ds_done, c)) break;
             fence_after();
-            const float a = gt.total;
             run_log += gt.total_log;
             if (state_row) {
                 uint32_t x[32];
                 tm_ld32_nowait(lanes + kTdS + 32 * hh, x);
+                const u64 a2 = dup2(gt.total);
                 tm_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 32; ++j) S[j] = fmaf(a, S[j], __uint_as_float(x[j]));
+                for (int j = 0; j < 16; ++j) S[j] = ffma2(a2, S[j], raw2(x[2 * j], x[2 * j + 1]));
             }
             fence_before();
-            const float et = gt.e[row];
+            const u64 et2 = dup2(gt.e[row]);
             if (c + 1 < wk.chunks) {
                 weigh(c + 1);
                 if (!kStates) {
-                    if (!need_warp(&ms.y2_done, c)) break;            // the images may be overwritten
+                    if (!need_warp(&ms.y2_done, c)) break;       // the images may be overwritten
                     image();
                 }
             }
             if (!kStates) {
-                // the outputs: (2^(l_t) Y2 + Y1 + D x) silu(z)
+                // the outputs: (2^(l_t) Y2 + Y1) silu(z)
                 // (with a chunk to come y2_done has been waited for above, and may be a phase on)
                 if (c + 1 == wk.chunks && !need_warp(&ms.y2_done, c)) break;
                 if (!need_warp(&ms.y1_done, c)) break;
                 if (gated && !need_warp(&ms.z_full[c & 1], c >> 1)) break;
                 fence_after();
-                uint32_t y1[32], y2[32];
-                tm_ld32_nowait(lanes + kTY1 + 32 * hh, y1);
-                tm_ld32_nowait(lanes + kTY2 + (c & 1) * 64 + 32 * hh, y2);
-                tm_wait_ld();
-                const unsigned char* X = sm + L::kX + c % kXStages * L::kTile;
                 unsigned char* Z = sm + L::kZ + (c & 1) * L::kTile;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t at = unit16(row, 4 * hh + j);
-                    const uint4 xv = *reinterpret_cast<const uint4*>(X + at);
-                    const __nv_bfloat162* hx = reinterpret_cast<const __nv_bfloat162*>(&xv);
-                    float o[8];
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t y1[16], y2[16];
+                    tm_ld16_nowait(lanes + kTY1 + 32 * hh + 16 * half, y1);
+                    tm_ld16_nowait(lanes + kTY2 + (c & 1) * 64 + 32 * hh + 16 * half, y2);
+                    tm_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 f = __bfloat1622float2(hx[e]);
-                        const int k = 8 * j + 2 * e;
-                        o[2 * e] = fmaf(D, f.x, fmaf(et, __uint_as_float(y2[k]), __uint_as_float(y1[k])));
-                        o[2 * e + 1] = fmaf(D, f.y, fmaf(et, __uint_as_float(y2[k + 1]), __uint_as_float(y1[k + 1])));
-                    }
-                    if (gated) {
-                        const uint4 zv = *reinterpret_cast<const uint4*>(Z + at);
-                        const __nv_bfloat162* hz = reinterpret_cast<const __nv_bfloat162*>(&zv);
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t at = unit16(row, 4 * hh + 2 * half + j);
+                        u64 o[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float2 f = __bfloat1622float2(hz[e]);
-                            o[2 * e] *= silu(f.x);
-                            o[2 * e + 1] *= silu(f.y);
+                            const int k = 8 * j + 2 * e;
+                            o[e] = ffma2(et2, raw2(y2[k], y2[k + 1]), raw2(y1[k], y1[k + 1]));
                         }
+                        if (gated) {
+                            const uint4 z = *reinterpret_cast<const uint4*>(Z + at);
+                            o[0] = gate_pair(o[0], z.x);
+                            o[1] = gate_pair(o[1], z.y);
+                            o[2] = gate_pair(o[2], z.z);
+                            o[3] = gate_pair(o[3], z.w);
+                        }
+                        *reinterpret_cast<uint4*>(Z + at) = make_uint4(pack2(lo2(o[0]), hi2(o[0])), pack2(lo2(o[1]), hi2(o[1])),
+                                                                       pack2(lo2(o[2]), hi2(o[2])), pack2(lo2(o[3]), hi2(o[3])));
                     }
-                    *reinterpret_cast<uint4*>(Z + at) =
-                        make_uint4(pack2(o[0], o[1]), pack2(o[2], o[3]), pack2(o[4], o[5]), pack2(o[6], o[7]));
                 }
                 fence_before();
                 __syncwarp();
@@ -766,6 +737,68 @@ __global__ void __launch_bounds__(kSThreads, 1) gdn_ssm_scan_kernel(const __grid
                                     32 * hh,
                                 S);
             }
+        }
+    } else if constexpr (!kStates) {
+        // ---- Pm = G with the decays, causal, hi and lo, into the columns that the warp read ----
+        const int quad = warp & 3, hh = (warp - kWarps - 2) >> 2;
+        const int row = quad * 32 + lane;
+        const float D = p.D ? ld(p.D + h) : 0.f;
+        for (int c = 0; c < wk.chunks; ++c) {
+            if (!need_warp(&ms.gates_full[c & 1], c >> 1) || !need_warp(&ms.g_done, c)) break;
+            fence_after();
+            const Gates& gt = ms.gates[c & 1];
+            const uint32_t G = tm + (static_cast<uint32_t>(quad * 32) << 16) + kTG + (c & 1) * 128 + 64 * hh;
+            uint32_t raw[2][32];
+            if (2 * hh <= quad) tm_ld32_nowait(G, raw[0]);
+            if (2 * hh + 1 <= quad) tm_ld32_nowait(G + 32, raw[1]);
+            const float lt = gt.l[row], lt_lo = gt.l_lo[row];
+            tm_wait_ld();
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                // 16 columns s0 .., half of the block j of 32
+                const int j = 2 * hh + (b >> 1), s0 = 16 * (b & 1);
+                const uint32_t* r = raw[b >> 1] + s0;
+                uint32_t hi[8], lo[8];
+                if (j > quad) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) hi[k] = lo[k] = 0;
+                } else if (j < quad) {
+                    // 2^(l_t - l_s) d_s through the end of the block of s: both factors at most 1 (times d_s)
+                    const u64 e2 = dup2(ex2((lt - gt.l[32 * j + 31]) + (lt_lo - gt.l_lo[32 * j + 31])));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(gt.f + 32 * j + s0 + 4 * k);
+                        split_pair(fmul2(raw2(r[4 * k], r[4 * k + 1]), fmul2(e2, f.x)), hi[2 * k], lo[2 * k]);
+                        split_pair(fmul2(raw2(r[4 * k + 2], r[4 * k + 3]), fmul2(e2, f.y)), hi[2 * k + 1], lo[2 * k + 1]);
+                    }
+                } else {
+                    const u64 lt2 = dup2(lt), lo_t2 = dup2(lt_lo), neg = dup2(-1.0f);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const ulonglong2 ls = *reinterpret_cast<const ulonglong2*>(gt.l + 32 * j + s0 + 4 * k);
+                        const ulonglong2 lo_s = *reinterpret_cast<const ulonglong2*>(gt.l_lo + 32 * j + s0 + 4 * k);
+                        const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(gt.d + 32 * j + s0 + 4 * k);
+                        const u64 l_s[2] = {ls.x, ls.y}, l_o[2] = {lo_s.x, lo_s.y}, d_s[2] = {d.x, d.y};
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const int at = 4 * k + 2 * q, s = s0 + at;
+                            const u64 x = ffma2(l_s[q], neg, lt2), y = ffma2(l_o[q], neg, lo_t2);
+                            const float x0 = ex2(lo2(x) + lo2(y)), x1 = ex2(hi2(x) + hi2(y));   // (unused beyond the diagonal)
+                            const u64 v = fmul2(raw2(r[at], r[at + 1]), fmul2(pk2(x0, x1), d_s[q]));
+                            float v0 = lo2(v) + (s == lane ? D : 0.f), v1 = hi2(v) + (s + 1 == lane ? D : 0.f);
+                            v0 = s <= lane ? v0 : 0.f;
+                            v1 = s + 1 <= lane ? v1 : 0.f;
+                            split_pair(pk2(v0, v1), hi[2 * k + q], lo[2 * k + q]);
+                        }
+                    }
+                }
+                tm_st8(G + 8 * b, hi);
+                tm_st8(G + 32 + 8 * b, lo);
+            }
+            tm_wait_st();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&ms.p_ready);
         }
     }
     fence_before();
@@ -812,7 +845,7 @@ cudaError_t launch_kernel(const ScanParams& sp, int64_t ctas, cudaStream_t strea
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
-    cfg.blockDim = dim3(kSThreads, 1, 1);
+    cfg.blockDim = dim3(kStates ? kStatesThreads : kSThreads, 1, 1);
     cfg.dynamicSmemBytes = scan_smem<N>();
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];

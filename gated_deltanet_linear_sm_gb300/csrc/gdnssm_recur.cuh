@@ -126,6 +126,7 @@ struct alignas(16) Round {
     float y[kMaxT][4][64];
     float decay[kMaxT], step[kMaxT];
     int row[kMaxT];
+    int slot[kMaxT];     // the step: slot that takes the state after the token
 };
 
 // Token t: the update of this thread's rows, and the warp's part of y.
