@@ -183,12 +183,31 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
         : "memory");
 }
 
-// bounded wait; gives up early once another warp has
+// Bounded wait for phase `use` of a barrier: blocking polls up to the default
+// bound, or non-blocking ones up to one set by gdn_set_wait_limit; gives up early
+// once another warp has.  (Kept small: there are some twenty of them, and with
+// the polls unrolled the kernel waited for its own instructions.)
+__device__ __forceinline__ bool poll(uint32_t addr, uint32_t parity, bool blocking) {
+    uint32_t done;
+    if (blocking)
+        asm volatile(
+            "{\n\t.reg .pred P;\n\tmbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2;\n\tselp.u32 %0, 1, 0, P;\n\t}"
+            : "=r"(done)
+            : "r"(addr), "r"(parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred P;\n\tmbarrier.test_wait.parity.shared::cta.b64 P, [%1], %2;\n\tselp.u32 %0, 1, 0, P;\n\t}"
+            : "=r"(done)
+            : "r"(addr), "r"(parity)
+            : "memory");
+    return done != 0;
+}
 __device__ __forceinline__ bool wait(unsigned long long* bar, int use, uint32_t limit, const volatile int* abort) {
-    const uint32_t addr = saddr(bar), parity = use & 1;
-    if (limit != 0) return test_parity(addr, parity, limit);
-    for (uint32_t round = 0; round < kSpinLimit / 64; ++round) {
-        if (wait_parity(addr, parity, 64)) return true;
+    const uint32_t addr = saddr(bar), parity = use & 1, most = limit ? limit : kSpinLimit;
+#pragma unroll 1
+    for (uint32_t n = 0; n < most; ++n) {
+        if (poll(addr, parity, limit == 0)) return true;
         if (*abort) return false;
     }
     return false;
@@ -499,16 +518,19 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
             // what is in flight, with the default bound: every product issued and every copy
             // (all long complete, unless some warp gave up)
             commit(saddr(&ms.drain));
-            bool drained = wait_parity(saddr(&ms.drain), 0, kSpinLimit);
+            const int never = 0;
+            bool drained = wait(&ms.drain, 0, 0, &never);
+#pragma unroll 1
             for (int k = 0; k < kXStages; ++k) {
                 const int n = (x_loads - k + kXStages - 1) / kXStages;       // copies into this stage
-                if (n > 0) drained &= wait_parity(saddr(&ms.x_full[k]), (n - 1) & 1, kSpinLimit);
+                if (n > 0) drained &= wait(&ms.x_full[k], n - 1, 0, &never);
             }
-            drained &= wait_parity(saddr(&ms.bc_full), (bc_loads - 1) & 1, kSpinLimit);
+            drained &= wait(&ms.bc_full, bc_loads - 1, 0, &never);
             if (!kStates && gated)
+#pragma unroll 1
                 for (int k = 0; k < 2; ++k) {
                     const int n = (z_loads - k + 1) / 2;
-                    if (n > 0) drained &= wait_parity(saddr(&ms.z_full[k]), (n - 1) & 1, kSpinLimit);
+                    if (n > 0) drained &= wait(&ms.z_full[k], n - 1, 0, &never);
                 }
             if (!drained) raise(p.status, GDN_FLAG_DRAIN);
         }
