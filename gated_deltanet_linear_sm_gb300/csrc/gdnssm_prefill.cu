@@ -26,10 +26,10 @@
 // with rows and depth exchanged need no transposed copy.  Pm goes back into the
 // tensor memory that G was in and is multiplied from there.
 //
-// Eighteen warps.  0-7 keep the state: they weigh x, update S, write its images
+// Nineteen warps.  0-7 keep the state: they weigh x, update S, write its images
 // and finish the outputs; 8 issues copies and products; 9 turns dt into the decay
 // factors of the chunk after next; 10-17 turn G into Pm, up to a chunk ahead of
-// the others, since G does not depend on the state.  (Two warps share the 32 rows
+// the others, since G does not depend on the state; 18 stores the outputs.  (Two warps share the 32 rows
 // of tensor memory that the hardware lets them reach, and split the columns.)
 // They meet at mbarriers only.  dS of a chunk does not depend on the state either,
 // so the chain from chunk to chunk is the FP32 update of S and the product Y2.
@@ -58,13 +58,13 @@ namespace {
 
 constexpr int kQ = 128;                          // tokens of a chunk
 constexpr int kWarps = 8;                        // that keep the state; as many make Pm
-constexpr int kSThreads = 32 * (2 * kWarps + 2);
+constexpr int kSThreads = 32 * (2 * kWarps + 3);
 constexpr int kStatesThreads = 32 * (kWarps + 2);
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kXStages = 3;
 
 struct ScanParams {
-    CUtensorMap x, B, C, z;                      // boxes of 64 elements x 128 rows
+    CUtensorMap x, B, C, z, out;                 // boxes of 64 elements x 128 rows
     Params p;
     float* part;                                 // segments: [segment][unit][N][64] what a segment adds
     float* part_decay;                           // and its log2-decay, [segment][unit]
@@ -107,7 +107,8 @@ struct alignas(16) Misc {
     unsigned long long x_full[kXStages], bc_full, z_full[2];    // copies have landed
     unsigned long long gates_full[2];
     unsigned long long g_done, ds_done, y2_done, y1_done;       // products are complete
-    unsigned long long xw_ready, s_ready, p_ready, chunk_done;  // the tile warps have written / read
+    unsigned long long ready, p_ready, chunk_done[2];           // the tile warps have written / read
+    unsigned long long z_free[2];                               // the outputs have left their buffer
     unsigned long long drain;
     uint32_t tmem;
     int abort;
@@ -386,15 +387,15 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
         for (int k = 0; k < 2; ++k) {
             bar_init(&ms.z_full[k], 1);
             bar_init(&ms.gates_full[k], 1);
+            bar_init(&ms.z_free[k], 1);
+            bar_init(&ms.chunk_done[k], kWarps);
         }
         bar_init(&ms.g_done, 1);
         bar_init(&ms.ds_done, 1);
         bar_init(&ms.y2_done, 1);
         bar_init(&ms.y1_done, 1);
-        bar_init(&ms.xw_ready, kWarps);
-        bar_init(&ms.s_ready, kWarps);
+        bar_init(&ms.ready, kWarps);
         bar_init(&ms.p_ready, kWarps);
-        bar_init(&ms.chunk_done, kWarps);
         bar_init(&ms.drain, 1);
         ms.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -445,13 +446,12 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
                 }
             };
             auto load_z = [&](int c) {
-                if (kStates || !gated) return;
                 bar_expect(&ms.z_full[c & 1], L::kTile);
                 tma_load(sbase + L::kZ + (c & 1) * L::kTile, &sp.z, col, row0 + c * kQ, &ms.z_full[c & 1]);
             };
             load_x(0);
             load_bc(0);
-            load_z(0);
+            if (!kStates && gated) load_z(0);
             if (wk.chunks > 1) load_x(1);
             int x_loads = wk.chunks > 1 ? 2 : 1, bc_loads = 1, z_loads = 1;
             const uint32_t id_g = idesc_bf16(128, 128);
@@ -460,7 +460,7 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
             for (int c = 0; c < wk.chunks; ++c) {
                 const bool tail = rows_of(c) < kQ;               // its rows past the end are cleared before any product
                 if (!need(&ms.bc_full, c)) break;
-                if (tail && !need(&ms.xw_ready, c)) break;
+                if (tail && !need(&ms.ready, c)) break;
                 fence_after();
                 if (!kStates) {
                     const uint32_t dst = tm + kTG + (c & 1) * 128;
@@ -470,7 +470,7 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
                     }
                     commit(saddr(&ms.g_done));
                 }
-                if (!tail && !need(&ms.xw_ready, c)) break;
+                if (!tail && !need(&ms.ready, c)) break;
                 fence_after();
                 for (int part = 0; part < 2; ++part)
                     for (int ks = 0; ks < kQ / 16; ++ks)
@@ -478,8 +478,6 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
                                  desc_mn(sbase + L::kXw + part * L::kTile + ks * 2048, L::kTile), id_ds, part + ks > 0);
                 commit(saddr(&ms.ds_done));
                 if (!kStates) {
-                    if (!need(&ms.s_ready, c)) break;
-                    fence_after();
                     const uint32_t dst = tm + kTY2 + (c & 1) * 64;
                     for (int part = 0; part < 2; ++part)
                         for (int ks = 0; ks < N / 16; ++ks)
@@ -487,17 +485,19 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
                                      desc_mn(sbase + L::kS + part * N * 128 + ks * 2048, L::kTile), id_y1, part + ks > 0);
                     commit(saddr(&ms.y2_done));
                 }
-                // The outputs of chunk c - 1 have been read: z's buffer, x's stage and Y1 may be
-                // overwritten.  (Without outputs x is read by the weighing alone, which xw_ready
-                // of this chunk follows.)
-                if (!kStates && c > 0 && !need(&ms.chunk_done, c - 1)) break;
+                // The outputs of chunk c - 1 are made: x's stage and Y1 may be overwritten.  (Without
+                // outputs x is read by the weighing alone, which `ready` of this chunk follows.)
+                if (!kStates && c > 0 && !need(&ms.chunk_done[(c - 1) & 1], (c - 1) >> 1)) break;
                 if (c + 2 < wk.chunks) {
                     load_x(c + 2);
                     ++x_loads;
                 }
                 if (c + 1 < wk.chunks) {
-                    load_z(c + 1);
-                    ++z_loads;
+                    if (!kStates && gated) {
+                        if (c > 0 && !need(&ms.z_free[(c + 1) & 1], (c - 1) >> 1)) break;
+                        load_z(c + 1);
+                        ++z_loads;
+                    }
                     if (!kStates && (!need(&ms.g_done, c) || !need(&ms.y2_done, c))) break;
                     if (!need(&ms.ds_done, c)) break;
                     load_bc(c + 1);
@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
                 e[k] = exp2f(hi[k]);
                 w[k] = exp2f(real(all - l[k])) * d[k];
             }
-            if (c >= 2 && !need_warp(&ms.chunk_done, c - 2)) break;   // the buffer's last readers
+            if (c >= 2 && !need_warp(&ms.chunk_done[c & 1], (c - 2) >> 1)) break;   // the buffer's last readers
             Gates& gt = ms.gates[c & 1];
             *reinterpret_cast<float4*>(gt.l + 4 * lane) = make_float4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<float4*>(gt.l_lo + 4 * lane) = make_float4(lo[0], lo[1], lo[2], lo[3]);
@@ -650,9 +650,6 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
                 *reinterpret_cast<uint4*>(sm + L::kXw + at) = hi;
                 *reinterpret_cast<uint4*>(sm + L::kXw + L::kTile + at) = lo;
             }
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) bar_arrive(&ms.xw_ready);
         };
         // the state's hi and lo images for the next chunk
         auto image = [&]() {
@@ -665,12 +662,15 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
                     *reinterpret_cast<uint4*>(sm + L::kS + N * 128 + unit16(row, 4 * hh + j)) = lo;
                 }
             }
+        };
+        auto publish = [&]() {
             fence_async_smem();
             __syncwarp();
-            if (lane == 0) bar_arrive(&ms.s_ready);
+            if (lane == 0) bar_arrive(&ms.ready);
         };
         weigh(0);
-        if (!kStates && ok) image();
+        if (!kStates) image();
+        if (ok) publish();
         for (int c = 0; c < wk.chunks && ok; ++c) {
             const int n = rows_of(c);
             const Gates& gt = ms.gates[c & 1];
@@ -694,13 +694,16 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
                     if (!need_warp(&ms.y2_done, c)) break;       // the images may be overwritten
                     image();
                 }
+                if (!ok) break;
+                publish();
             }
             if (!kStates) {
                 // the outputs: (2^(l_t) Y2 + Y1) silu(z)
                 // (with a chunk to come y2_done has been waited for above, and may be a phase on)
                 if (c + 1 == wk.chunks && !need_warp(&ms.y2_done, c)) break;
                 if (!need_warp(&ms.y1_done, c)) break;
-                if (gated && !need_warp(&ms.z_full[c & 1], c >> 1)) break;
+                // z has landed; without it the buffer's last outputs have left
+                if (gated ? !need_warp(&ms.z_full[c & 1], c >> 1) : c >= 2 && !need_warp(&ms.z_free[c & 1], (c - 2) >> 1)) break;
                 fence_after();
                 unsigned char* Z = sm + L::kZ + (c & 1) * L::kTile;
 #pragma unroll
@@ -730,19 +733,10 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
                     }
                 }
                 fence_before();
-                __syncwarp();
-                // rows of this warp to memory: 64 bytes of 8 rows an access
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int t = 32 * quad + 8 * k + (lane >> 2), u = 4 * hh + (lane & 3);
-                    const uint4 v = *reinterpret_cast<const uint4*>(Z + unit16(t, u));
-                    if (t < n)
-                        *reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(row0) + c * kQ + t) * p.out_stride + col + 8 * u) = v;
-                }
             }
-            fence_async_smem();                                  // before the next copies overwrite what was read
+            fence_async_smem();
             __syncwarp();
-            if (lane == 0) bar_arrive(&ms.chunk_done);
+            if (lane == 0) bar_arrive(&ms.chunk_done[c & 1]);
         }
         // what this CTA leaves, unless a warp gave up: its segment's part, or the sequence's last
         // state, rounded once
@@ -760,7 +754,36 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
                                 S);
             }
         }
-    } else if constexpr (!kStates) {
+    } else if (kStates) {
+        // (not launched)
+    } else if (warp == 2 * kWarps + 2) {
+        // ---- the outputs to memory: whole tiles by TMA (it is not the state's warps that store: their
+        //      proxy fences would wait for the stores), the last rows of a sequence one by one ----
+        for (int c = 0; c < wk.chunks; ++c) {
+            if (!need_warp(&ms.chunk_done[c & 1], c >> 1)) break;
+            const int n = rows_of(c);
+            if (n == kQ) {
+                if (lane == 0) {
+                    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                                     reinterpret_cast<uint64_t>(&sp.out)),
+                                 "r"(sbase + L::kZ + (c & 1) * L::kTile), "r"(col), "r"(row0 + c * kQ)
+                                 : "memory");
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                }
+            } else {
+                const unsigned char* Z = sm + L::kZ + (c & 1) * L::kTile;
+                for (int t = lane >> 3; t < n; t += 4)
+                    *reinterpret_cast<uint4*>(p.out + (static_cast<int64_t>(row0) + c * kQ + t) * p.out_stride + col +
+                                              8 * (lane & 7)) = *reinterpret_cast<const uint4*>(Z + unit16(t, lane & 7));
+                fence_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) bar_arrive(&ms.z_free[c & 1]);
+        }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
+    } else {
         // ---- Pm = G with the decays, causal, hi and lo, into the columns that the warp read ----
         const int quad = warp & 3, hh = (warp - kWarps - 2) >> 2;
         const int row = quad * 32 + lane;
@@ -928,7 +951,7 @@ cudaError_t launch_prefill(const Params& p, int N, gdn_dtype state_dtype, void* 
     const int64_t HP = static_cast<int64_t>(p.H) * p.P, GN = static_cast<int64_t>(p.G) * N;
     if (!encode_map(sp.x, p.x, HP, p.num_tokens, p.x_stride) || !encode_map(sp.B, p.B, GN, p.num_tokens, p.b_stride) ||
         !encode_map(sp.C, p.C, GN, p.num_tokens, p.c_stride) ||
-        (p.z && !encode_map(sp.z, p.z, HP, p.num_tokens, p.z_stride)))
+        (p.z && !encode_map(sp.z, p.z, HP, p.num_tokens, p.z_stride)) || !encode_map(sp.out, p.out, HP, p.num_tokens, p.out_stride))
         return cudaErrorInvalidValue;
     const int units = p.H * p.blocks;
     return N == 64 ? launch_n<64>(sp, state_dtype, units, workspace, stream)
