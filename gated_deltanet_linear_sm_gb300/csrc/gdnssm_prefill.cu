@@ -26,11 +26,12 @@
 // with rows and depth exchanged need no transposed copy.  Pm goes back into the
 // tensor memory that G was in and is multiplied from there.
 //
-// Nineteen warps.  0-7 keep the state: they weigh x, update S, write its images
-// and finish the outputs; 8 issues copies and products; 9 turns dt into the decay
-// factors of the chunk after next; 10-17 turn G into Pm, up to a chunk ahead of
-// the others, since G does not depend on the state; 18 stores the outputs.  (Two warps share the 32 rows
-// of tensor memory that the hardware lets them reach, and split the columns.)
+// Twenty warps.  0-7 keep the state: they weigh x, update S, write its images and
+// finish the outputs; 12-19 turn G into Pm, up to a chunk ahead of the others,
+// since G does not depend on the state; one warp each issues the products, issues
+// the copies, turns dt into decay factors some chunks ahead, and stores the
+// outputs.  (Two warps share the 32 rows of tensor memory that the hardware lets
+// them reach, and split the columns.)
 // They meet at mbarriers only.  dS of a chunk does not depend on the state either,
 // so the chain from chunk to chunk is the FP32 update of S and the product Y2.
 // Arithmetic runs on pairs of columns (fma.rn.f32x2).
@@ -58,8 +59,11 @@ namespace {
 
 constexpr int kQ = 128;                          // tokens of a chunk
 constexpr int kWarps = 8;                        // that keep the state; as many make Pm
-constexpr int kSThreads = 32 * (2 * kWarps + 3);
-constexpr int kStatesThreads = 32 * (kWarps + 2);
+constexpr int kMma = kWarps, kLoad = kWarps + 1, kGate = kWarps + 2, kStore = kWarps + 3;   // and a warp each
+constexpr int kPm = kWarps + 4;                  // the first that makes Pm (a multiple of 4)
+constexpr int kSThreads = 32 * (2 * kWarps + 4);
+constexpr int kStatesThreads = 32 * (kWarps + 3);
+constexpr int kGates = 3;                        // chunks whose decay factors are held
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kXStages = 3;
 
@@ -103,9 +107,9 @@ struct alignas(16) Gates {
 };
 
 struct alignas(16) Misc {
-    Gates gates[2];
+    Gates gates[kGates];
     unsigned long long x_full[kXStages], bc_full, z_full[2];    // copies have landed
-    unsigned long long gates_full[2];
+    unsigned long long gates_full[kGates];
     unsigned long long g_done, ds_done, y2_done, y1_done;       // products are complete
     unsigned long long ready, p_ready, chunk_done[2];           // the tile warps have written / read
     unsigned long long z_free[2];                               // the outputs have left their buffer
@@ -377,16 +381,16 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
     const Work wk = find_work(sp, index, lane);
     if (wk.kind == 0 || (kStates && wk.last)) return;            // (nothing follows the last segment)
 
-    if (warp == kWarps) {
+    if (warp == kMma) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(saddr(&ms.tmem)));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     if (tid == 0) {
         for (int k = 0; k < kXStages; ++k) bar_init(&ms.x_full[k], 1);
+        for (int k = 0; k < kGates; ++k) bar_init(&ms.gates_full[k], 1);
         bar_init(&ms.bc_full, 1);
         for (int k = 0; k < 2; ++k) {
             bar_init(&ms.z_full[k], 1);
-            bar_init(&ms.gates_full[k], 1);
             bar_init(&ms.z_free[k], 1);
             bar_init(&ms.chunk_done[k], kWarps);
         }
@@ -430,8 +434,72 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
         return ok;
     };
 
-    if (warp == kWarps) {
-        // ---- copies and products ----
+    if (warp == kMma) {
+        // ---- products ----
+        if (lane == 0) {
+            constexpr uint32_t id_g = (1u << 4) | (1u << 7) | (1u << 10) | (128u >> 3 << 17) | (128u >> 4 << 24);
+            constexpr uint32_t id_y = (1u << 4) | (1u << 7) | (1u << 10) | (64u >> 3 << 17) | (128u >> 4 << 24) | kBMn;
+            constexpr uint32_t id_ds = id_y | kAMn;
+            // operands as their descriptors, formed once; a step along the depth adds its bytes / 16
+            const uint64_t c_km = desc_sw128(sbase + L::kC), b_km = desc_sw128(sbase + L::kB);
+            const uint64_t b_mn = desc_mn(sbase + L::kB, L::kTile), xw_mn = desc_mn(sbase + L::kXw, L::kTile);
+            const uint64_t s_mn = desc_mn(sbase + L::kS, L::kTile), x_mn0 = desc_mn(sbase + L::kX, L::kTile);
+            for (int c = 0; c < wk.chunks; ++c) {
+                const bool tail = rows_of(c) < kQ;               // its rows past the end are cleared before any product
+                if (!need(&ms.bc_full, c)) break;
+                if (tail && !need(&ms.ready, c)) break;
+                fence_after();
+                if (!kStates) {
+                    const uint32_t dst = tm + kTG + (c & 1) * 128;
+#pragma unroll
+                    for (int ks = 0; ks < N / 16; ++ks) {
+                        constexpr int unit = L::kTile / 16;
+                        const uint64_t o = (ks >> 2) * unit + (ks & 3) * 2;
+                        mma_bf16(dst, c_km + o, b_km + o, id_g, ks > 0);
+                    }
+                    commit(saddr(&ms.g_done));
+                }
+                if (!tail && !need(&ms.ready, c)) break;
+                fence_after();
+#pragma unroll
+                for (int part = 0; part < 2; ++part)
+#pragma unroll
+                    for (int ks = 0; ks < kQ / 16; ++ks)
+                        mma_bf16(tm + kTdS, b_mn + ks * 128, xw_mn + part * (L::kTile / 16) + ks * 128, id_ds, part + ks > 0);
+                commit(saddr(&ms.ds_done));
+                if (!kStates) {
+                    const uint32_t dst = tm + kTY2 + (c & 1) * 64;
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int ks = 0; ks < N / 16; ++ks)
+                            mma_bf16(dst, c_km + (ks >> 2) * (L::kTile / 16) + (ks & 3) * 2, s_mn + part * N * 8 + ks * 128, id_y,
+                                     part + ks > 0);
+                    commit(saddr(&ms.y2_done));
+                    // Y1 has been read
+                    if (c > 0 && !need(&ms.chunk_done[(c - 1) & 1], (c - 1) >> 1)) break;
+                    if (!need(&ms.p_ready, c)) break;
+                    fence_after();
+                    const uint32_t a = tm + kTG + (c & 1) * 128;
+                    const uint64_t x_mn = x_mn0 + c % kXStages * (L::kTile / 16);
+#pragma unroll
+                    for (int part = 0; part < 2; ++part)
+#pragma unroll
+                        for (int ks = 0; ks < kQ / 16; ++ks)
+                            mma_bf16_ts(tm + kTY1, a + (ks >> 2) * 64 + part * 32 + (ks & 3) * 8, x_mn + ks * 128, id_y,
+                                        part + ks > 0);
+                    commit(saddr(&ms.y1_done));
+                }
+            }
+            // every product issued has to finish before tensor memory goes (with the default
+            // bound; long complete, unless some warp gave up)
+            commit(saddr(&ms.drain));
+            const int never = 0;
+            if (!wait(&ms.drain, 0, 0, &never)) raise(p.status, GDN_FLAG_DRAIN);
+        }
+        __syncwarp();
+    } else if (warp == kLoad) {
+        // ---- copies, each once what it overwrites has been read ----
         if (lane == 0) {
             auto load_x = [&](int c) {
                 unsigned long long* bar = &ms.x_full[c % kXStages];
@@ -440,6 +508,7 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
             };
             auto load_bc = [&](int c) {
                 bar_expect(&ms.bc_full, (kStates ? 1 : 2) * (N / 64) * L::kTile);
+#pragma unroll
                 for (int k = 0; k < N / 64; ++k) {
                     tma_load(sbase + L::kB + k * L::kTile, &sp.B, g * N + 64 * k, row0 + c * kQ, &ms.bc_full);
                     if (!kStates) tma_load(sbase + L::kC + k * L::kTile, &sp.C, g * N + 64 * k, row0 + c * kQ, &ms.bc_full);
@@ -449,93 +518,46 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
                 bar_expect(&ms.z_full[c & 1], L::kTile);
                 tma_load(sbase + L::kZ + (c & 1) * L::kTile, &sp.z, col, row0 + c * kQ, &ms.z_full[c & 1]);
             };
-            load_x(0);
             load_bc(0);
-            if (!kStates && gated) load_z(0);
+            load_x(0);
             if (wk.chunks > 1) load_x(1);
+            if (!kStates && gated) load_z(0);
             int x_loads = wk.chunks > 1 ? 2 : 1, bc_loads = 1, z_loads = 1;
-            const uint32_t id_g = idesc_bf16(128, 128);
-            const uint32_t id_y1 = idesc_bf16(128, 64) | kBMn;
-            const uint32_t id_ds = idesc_bf16(128, 64) | kAMn | kBMn;
-            for (int c = 0; c < wk.chunks; ++c) {
-                const bool tail = rows_of(c) < kQ;               // its rows past the end are cleared before any product
-                if (!need(&ms.bc_full, c)) break;
-                if (tail && !need(&ms.ready, c)) break;
-                fence_after();
-                if (!kStates) {
-                    const uint32_t dst = tm + kTG + (c & 1) * 128;
-                    for (int ks = 0; ks < N / 16; ++ks) {
-                        const uint32_t o = (ks >> 2) * L::kTile + (ks & 3) * 32;
-                        mma_bf16(dst, desc_sw128(sbase + L::kC + o), desc_sw128(sbase + L::kB + o), id_g, ks > 0);
-                    }
-                    commit(saddr(&ms.g_done));
-                }
-                if (!tail && !need(&ms.ready, c)) break;
-                fence_after();
-                for (int part = 0; part < 2; ++part)
-                    for (int ks = 0; ks < kQ / 16; ++ks)
-                        mma_bf16(tm + kTdS, desc_mn(sbase + L::kB + ks * 2048, L::kTile),
-                                 desc_mn(sbase + L::kXw + part * L::kTile + ks * 2048, L::kTile), id_ds, part + ks > 0);
-                commit(saddr(&ms.ds_done));
-                if (!kStates) {
-                    const uint32_t dst = tm + kTY2 + (c & 1) * 64;
-                    for (int part = 0; part < 2; ++part)
-                        for (int ks = 0; ks < N / 16; ++ks)
-                            mma_bf16(dst, desc_sw128(sbase + L::kC + (ks >> 2) * L::kTile + (ks & 3) * 32),
-                                     desc_mn(sbase + L::kS + part * N * 128 + ks * 2048, L::kTile), id_y1, part + ks > 0);
-                    commit(saddr(&ms.y2_done));
-                }
-                // The outputs of chunk c - 1 are made: x's stage and Y1 may be overwritten.  (Without
-                // outputs x is read by the weighing alone, which `ready` of this chunk follows.)
-                if (!kStates && c > 0 && !need(&ms.chunk_done[(c - 1) & 1], (c - 1) >> 1)) break;
-                if (c + 2 < wk.chunks) {
+            for (int c = 0; c + 1 < wk.chunks; ++c) {
+                if (c + 2 < wk.chunks) {                         // into the stage of chunk c - 1
+                    if (c > 0 && !need(&ms.chunk_done[(c - 1) & 1], (c - 1) >> 1)) break;
                     load_x(c + 2);
                     ++x_loads;
                 }
-                if (c + 1 < wk.chunks) {
-                    if (!kStates && gated) {
-                        if (c > 0 && !need(&ms.z_free[(c + 1) & 1], (c - 1) >> 1)) break;
-                        load_z(c + 1);
-                        ++z_loads;
-                    }
-                    if (!kStates && (!need(&ms.g_done, c) || !need(&ms.y2_done, c))) break;
-                    if (!need(&ms.ds_done, c)) break;
-                    load_bc(c + 1);
-                    ++bc_loads;
-                }
-                if (!kStates) {
-                    if (!need(&ms.p_ready, c)) break;
-                    fence_after();
-                    const uint32_t a = tm + kTG + (c & 1) * 128;
-                    for (int part = 0; part < 2; ++part)
-                        for (int ks = 0; ks < kQ / 16; ++ks)
-                            mma_bf16_ts(tm + kTY1, a + (ks >> 2) * 64 + part * 32 + (ks & 3) * 8,
-                                        desc_mn(sbase + L::kX + c % kXStages * L::kTile + ks * 2048, L::kTile), id_y1,
-                                        part + ks > 0);
-                    commit(saddr(&ms.y1_done));
+                if (!kStates && (!need(&ms.g_done, c) || !need(&ms.y2_done, c))) break;
+                if (!need(&ms.ds_done, c)) break;
+                load_bc(c + 1);
+                ++bc_loads;
+                if (!kStates && gated) {
+                    if (c > 0 && !need(&ms.z_free[(c + 1) & 1], (c - 1) >> 1)) break;
+                    load_z(c + 1);
+                    ++z_loads;
                 }
             }
-            // what is in flight, with the default bound: every product issued and every copy
-            // (all long complete, unless some warp gave up)
-            commit(saddr(&ms.drain));
+            // and every copy before shared memory goes
             const int never = 0;
-            bool drained = wait(&ms.drain, 0, 0, &never);
+            bool landed = true;
 #pragma unroll 1
             for (int k = 0; k < kXStages; ++k) {
                 const int n = (x_loads - k + kXStages - 1) / kXStages;       // copies into this stage
-                if (n > 0) drained &= wait(&ms.x_full[k], n - 1, 0, &never);
+                if (n > 0) landed &= wait(&ms.x_full[k], n - 1, 0, &never);
             }
-            drained &= wait(&ms.bc_full, bc_loads - 1, 0, &never);
+            landed &= wait(&ms.bc_full, bc_loads - 1, 0, &never);
             if (!kStates && gated)
 #pragma unroll 1
                 for (int k = 0; k < 2; ++k) {
                     const int n = (z_loads - k + 1) / 2;
-                    if (n > 0) drained &= wait(&ms.z_full[k], n - 1, 0, &never);
+                    if (n > 0) landed &= wait(&ms.z_full[k], n - 1, 0, &never);
                 }
-            if (!drained) raise(p.status, GDN_FLAG_DRAIN);
+            if (!landed) raise(p.status, GDN_FLAG_DRAIN);
         }
         __syncwarp();
-    } else if (warp == kWarps + 1) {
+    } else if (warp == kGate) {
         // ---- decay factors: four tokens a lane ----
         const float rate = -expf(ld(p.A_log + h)) * kLog2e, bias = __bfloat162float(p.dt_bias[h]);
         __nv_bfloat16 raw[4];
@@ -580,8 +602,8 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
                 e[k] = exp2f(hi[k]);
                 w[k] = exp2f(real(all - l[k])) * d[k];
             }
-            if (c >= 2 && !need_warp(&ms.chunk_done[c & 1], (c - 2) >> 1)) break;   // the buffer's last readers
-            Gates& gt = ms.gates[c & 1];
+            if (c >= kGates && !need_warp(&ms.chunk_done[(c - kGates) & 1], (c - kGates) >> 1)) break;   // the buffer's last readers
+            Gates& gt = ms.gates[c % kGates];
             *reinterpret_cast<float4*>(gt.l + 4 * lane) = make_float4(hi[0], hi[1], hi[2], hi[3]);
             *reinterpret_cast<float4*>(gt.l_lo + 4 * lane) = make_float4(lo[0], lo[1], lo[2], lo[3]);
             *reinterpret_cast<float4*>(gt.f + 4 * lane) = make_float4(f[0], f[1], f[2], f[3]);
@@ -593,7 +615,7 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
                 gt.total_log = real(all);
             }
             __syncwarp();
-            if (lane == 0) bar_arrive(&ms.gates_full[c & 1]);
+            if (lane == 0) bar_arrive(&ms.gates_full[c % kGates]);
         }
     } else if (warp < kWarps) {
         // ---- the state, and the outputs ----
@@ -623,10 +645,10 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
         }
         // Xw of chunk c, and the rows past the sequence's end cleared
         auto weigh = [&](int c) {
-            if (!need_warp(&ms.gates_full[c & 1], c >> 1) || !need_warp(&ms.x_full[c % kXStages], c / kXStages)) return;
+            if (!need_warp(&ms.gates_full[c % kGates], c / kGates) || !need_warp(&ms.x_full[c % kXStages], c / kXStages)) return;
             const int n = rows_of(c);
             unsigned char* X = sm + L::kX + c % kXStages * L::kTile;
-            const u64 w2 = dup2(ms.gates[c & 1].w[row]);
+            const u64 w2 = dup2(ms.gates[c % kGates].w[row]);
             if (n < kQ) {
                 if (!need_warp(&ms.bc_full, c)) return;
                 if (row >= n) {
@@ -673,7 +695,7 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
         if (ok) publish();
         for (int c = 0; c < wk.chunks && ok; ++c) {
             const int n = rows_of(c);
-            const Gates& gt = ms.gates[c & 1];
+            const Gates& gt = ms.gates[c % kGates];
             // the state after this chunk
             if (!need_warp(&ms.ds_done, c)) break;
             fence_after();
@@ -756,7 +778,7 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
         }
     } else if (kStates) {
         // (not launched)
-    } else if (warp == 2 * kWarps + 2) {
+    } else if (warp == kStore) {
         // ---- the outputs to memory: whole tiles by TMA (it is not the state's warps that store: their
         //      proxy fences would wait for the stores), the last rows of a sequence one by one ----
         for (int c = 0; c < wk.chunks; ++c) {
@@ -785,13 +807,13 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
         __syncwarp();
     } else {
         // ---- Pm = G with the decays, causal, hi and lo, into the columns that the warp read ----
-        const int quad = warp & 3, hh = (warp - kWarps - 2) >> 2;
+        const int quad = warp & 3, hh = (warp - kPm) >> 2;
         const int row = quad * 32 + lane;
         const float D = p.D ? ld(p.D + h) : 0.f;
         for (int c = 0; c < wk.chunks; ++c) {
-            if (!need_warp(&ms.gates_full[c & 1], c >> 1) || !need_warp(&ms.g_done, c)) break;
+            if (!need_warp(&ms.gates_full[c % kGates], c / kGates) || !need_warp(&ms.g_done, c)) break;
             fence_after();
-            const Gates& gt = ms.gates[c & 1];
+            const Gates& gt = ms.gates[c % kGates];
             const uint32_t G = tm + (static_cast<uint32_t>(quad * 32) << 16) + kTG + (c & 1) * 128 + 64 * hh;
             uint32_t raw[2][32];
             if (2 * hh <= quad) tm_ld32_nowait(G, raw[0]);
@@ -850,7 +872,7 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
     __syncthreads();
     fence_after();
     if (tid == 0 && *abort != 0) raise(p.status, GDN_FLAG_TIMEOUT);
-    if (warp == kWarps) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm));
+    if (warp == kMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm));
 }
 
 // ---- host side ----------------------------------------------------------------------
