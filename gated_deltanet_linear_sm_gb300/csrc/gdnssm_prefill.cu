@@ -46,6 +46,9 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
+#include <cmath>
+
 #include "gdn_internal.h"
 #include "gdn_tcgen05.h"
 #include "gdnssm.h"
@@ -923,10 +926,27 @@ cudaError_t launch_kernel(const ScanParams& sp, int64_t ctas, cudaStream_t strea
     return cudaLaunchKernelEx(&cfg, kernel, sp);
 }
 
-// Chunks of a segment, 0 for whole sequences.
+// Chunks of a segment, 0 for whole sequences: whichever an estimate of the time,
+// in chunk times, says is shorter.  The host knows the rows and the sequences but
+// not their lengths; with several it takes the longest for twice the mean.  A
+// CTA costs kStart chunk times beside its chunks (its first copies, the state),
+// and the first launch over segments kFirst of the second.
 int segment_chunks(int batch, int num_tokens, int units) {
-    (void)batch, (void)num_tokens, (void)units;
-    return 0;
+    constexpr double kStart = 2.0, kFirst = 0.35;
+    const int sms = sm_count() ? sm_count() : 148;
+    const int64_t chunks = (static_cast<int64_t>(num_tokens) + kQ - 1) / kQ;
+    const double mean = static_cast<double>(chunks) / batch, longest = batch > 1 ? 2 * mean : mean;
+    double best = std::max(longest + kStart, std::ceil(static_cast<double>(batch) * units / sms) * (mean + kStart));
+    int take = 0;
+    for (int k = 1; k < longest && k <= 512; ++k) {
+        const double ctas = (static_cast<double>(chunks) / k + (batch > 1 ? 0.5 * batch : 0.0)) * units;
+        const double cost = (1 + kFirst) * std::ceil(std::ceil(ctas) / sms) * (k + kStart);
+        if (cost < best) {
+            best = cost;
+            take = k;
+        }
+    }
+    return take;
 }
 
 int64_t segment_room(int batch, int num_tokens, int chunks) {
