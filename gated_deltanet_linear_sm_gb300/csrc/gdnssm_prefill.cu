@@ -117,6 +117,8 @@ struct alignas(16) Misc {
     unsigned long long ready, p_ready, chunk_done[2];           // the tile warps have written / read
     unsigned long long z_free[2];                               // the outputs have left their buffer
     unsigned long long drain;
+    long long log_decay[kQ];                                    // the gate warp's own
+    float step[kQ];
     uint32_t tmem;
     int abort;
 };
@@ -489,7 +491,7 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
                     for (int part = 0; part < 2; ++part)
 #pragma unroll
                         for (int ks = 0; ks < kQ / 16; ++ks)
-                            mma_bf16_ts(tm + kTY1, a + (ks >> 2) * 64 + part * 32 + (ks & 3) * 8, x_mn + ks * 128, id_y,
+                            mma_bf16_ts(tm + kTY1, a + ks * 16 + part * 8, x_mn + ks * 128, id_y,
                                         part + ks > 0);
                     commit(saddr(&ms.y1_done));
                 }
@@ -561,31 +563,37 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
         }
         __syncwarp();
     } else if (warp == kGate) {
-        // ---- decay factors: four tokens a lane ----
+        // ---- decay factors ----
         const float rate = -expf(ld(p.A_log + h)) * kLog2e, bias = __bfloat162float(p.dt_bias[h]);
-        __nv_bfloat16 raw[4];
+        __nv_bfloat16 raw[4];                                    // dt of tokens lane, lane + 32, ..
         auto fetch = [&](int c) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int t = 4 * lane + k;
+                const int t = 32 * k + lane;
                 if (t < rows_of(c)) raw[k] = p.dt[(static_cast<int64_t>(row0) + c * kQ + t) * p.dt_stride + h];
             }
         };
         fetch(0);
         for (int c = 0; c < wk.chunks; ++c) {
             const int n = rows_of(c);
-            float d[4];
-            long long la[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                d[k] = 4 * lane + k < n ? softplus(__bfloat162float(raw[k]) + bias) : 0.f;
-                la[k] = __float2ll_rn(fmaxf(rate * d[k], -1048576.0f) * 4294967296.0f);   // 2^-(2^20) is 0 as it is
+            __syncwarp();
+#pragma unroll 1
+            for (int t = lane; t < kQ; t += 32) {
+                const float d = t < n ? softplus(__bfloat162float(raw[0]) + bias) : 0.f;
+                ms.step[t] = d;
+                ms.log_decay[t] = __float2ll_rn(fmaxf(rate * d, -1048576.0f) * 4294967296.0f);   // 2^-(2^20) is 0 as it is
+                raw[0] = raw[1];
+                raw[1] = raw[2];
+                raw[2] = raw[3];
             }
             if (c + 1 < wk.chunks) fetch(c + 1);
-            // l: sums up to and with a token; r: sums behind it
-            long long l[4], up = 0;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) l[k] = up += la[k];
+            __syncwarp();
+            // four tokens a lane; l: sums up to and with a token
+            const float4 dv = *reinterpret_cast<const float4*>(ms.step + 4 * lane);
+            const float d[4] = {dv.x, dv.y, dv.z, dv.w};
+            const longlong2 la0 = *reinterpret_cast<const longlong2*>(ms.log_decay + 4 * lane);
+            const longlong2 la1 = *reinterpret_cast<const longlong2*>(ms.log_decay + 4 * lane + 2);
+            long long l[4] = {la0.x, la0.x + la0.y, la0.x + la0.y + la1.x, la0.x + la0.y + la1.x + la1.y}, up = l[3];
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const long long a = __shfl_up_sync(kFull, up, o);
@@ -601,9 +609,9 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
                 const float units_hi = __ll2float_rn(l[k]);
                 hi[k] = units_hi * (1.0f / 4294967296.0f);
                 lo[k] = real(l[k] - __float2ll_rn(units_hi));
-                f[k] = exp2f(real(block_end - l[k])) * d[k];
-                e[k] = exp2f(hi[k]);
-                w[k] = exp2f(real(all - l[k])) * d[k];
+                f[k] = ex2(real(block_end - l[k])) * d[k];
+                e[k] = ex2(hi[k]);
+                w[k] = ex2(real(all - l[k])) * d[k];
             }
             if (c >= kGates && !need_warp(&ms.chunk_done[(c - kGates) & 1], (c - kGates) >> 1)) break;   // the buffer's last readers
             Gates& gt = ms.gates[c % kGates];
@@ -614,7 +622,7 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
             *reinterpret_cast<float4*>(gt.w + 4 * lane) = make_float4(w[0], w[1], w[2], w[3]);
             *reinterpret_cast<float4*>(gt.d + 4 * lane) = make_float4(d[0], d[1], d[2], d[3]);
             if (lane == 0) {
-                gt.total = exp2f(real(all));
+                gt.total = ex2(real(all));
                 gt.total_log = real(all);
             }
             __syncwarp();
@@ -731,7 +739,7 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
                 if (gated ? !need_warp(&ms.z_full[c & 1], c >> 1) : c >= 2 && !need_warp(&ms.z_free[c & 1], (c - 2) >> 1)) break;
                 fence_after();
                 unsigned char* Z = sm + L::kZ + (c & 1) * L::kTile;
-#pragma unroll
+#pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
                     uint32_t y1[16], y2[16];
                     tm_ld16_nowait(lanes + kTY1 + 32 * hh + 16 * half, y1);
@@ -817,53 +825,53 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
             if (!need_warp(&ms.gates_full[c % kGates], c / kGates) || !need_warp(&ms.g_done, c)) break;
             fence_after();
             const Gates& gt = ms.gates[c % kGates];
-            const uint32_t G = tm + (static_cast<uint32_t>(quad * 32) << 16) + kTG + (c & 1) * 128 + 64 * hh;
-            uint32_t raw[2][32];
-            if (2 * hh <= quad) tm_ld32_nowait(G, raw[0]);
-            if (2 * hh + 1 <= quad) tm_ld32_nowait(G + 32, raw[1]);
+            const uint32_t G = tm + (static_cast<uint32_t>(quad * 32) << 16) + kTG + (c & 1) * 128 + 16 * hh;
             const float lt = gt.l[row], lt_lo = gt.l_lo[row];
-            tm_wait_ld();
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
-                // 16 columns s0 .., half of the block j of 32
-                const int j = 2 * hh + (b >> 1), s0 = 16 * (b & 1);
-                const uint32_t* r = raw[b >> 1] + s0;
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {                        // this warp's 16 columns s of block j of 32
+                const int s0 = 32 * j + 16 * hh;
                 uint32_t hi[8], lo[8];
                 if (j > quad) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) hi[k] = lo[k] = 0;
-                } else if (j < quad) {
-                    // 2^(l_t - l_s) d_s through the end of the block of s: both factors at most 1 (times d_s)
-                    const u64 e2 = dup2(ex2((lt - gt.l[32 * j + 31]) + (lt_lo - gt.l_lo[32 * j + 31])));
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(gt.f + 32 * j + s0 + 4 * k);
-                        split_pair(fmul2(raw2(r[4 * k], r[4 * k + 1]), fmul2(e2, f.x)), hi[2 * k], lo[2 * k]);
-                        split_pair(fmul2(raw2(r[4 * k + 2], r[4 * k + 3]), fmul2(e2, f.y)), hi[2 * k + 1], lo[2 * k + 1]);
-                    }
                 } else {
-                    const u64 lt2 = dup2(lt), lo_t2 = dup2(lt_lo), neg = dup2(-1.0f);
+                    uint32_t r[16];
+                    tm_ld16_nowait(G + 32 * j, r);
+                    tm_wait_ld();
+                    if (j < quad) {
+                        // 2^(l_t - l_s) d_s through the end of the block of s: both factors at most 1 (times d_s)
+                        const u64 e2 = dup2(ex2((lt - gt.l[32 * j + 31]) + (lt_lo - gt.l_lo[32 * j + 31])));
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const ulonglong2 ls = *reinterpret_cast<const ulonglong2*>(gt.l + 32 * j + s0 + 4 * k);
-                        const ulonglong2 lo_s = *reinterpret_cast<const ulonglong2*>(gt.l_lo + 32 * j + s0 + 4 * k);
-                        const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(gt.d + 32 * j + s0 + 4 * k);
-                        const u64 l_s[2] = {ls.x, ls.y}, l_o[2] = {lo_s.x, lo_s.y}, d_s[2] = {d.x, d.y};
+                        for (int k = 0; k < 4; ++k) {
+                            const ulonglong2 f = *reinterpret_cast<const ulonglong2*>(gt.f + s0 + 4 * k);
+                            split_pair(fmul2(raw2(r[4 * k], r[4 * k + 1]), fmul2(e2, f.x)), hi[2 * k], lo[2 * k]);
+                            split_pair(fmul2(raw2(r[4 * k + 2], r[4 * k + 3]), fmul2(e2, f.y)), hi[2 * k + 1], lo[2 * k + 1]);
+                        }
+                    } else {
+                        const u64 lt2 = dup2(lt), lo_t2 = dup2(lt_lo), neg = dup2(-1.0f);
+                        const int last = lane - 16 * hh;         // columns up to this one count; it is the diagonal
 #pragma unroll
-                        for (int q = 0; q < 2; ++q) {
-                            const int at = 4 * k + 2 * q, s = s0 + at;
-                            const u64 x = ffma2(l_s[q], neg, lt2), y = ffma2(l_o[q], neg, lo_t2);
-                            const float x0 = ex2(lo2(x) + lo2(y)), x1 = ex2(hi2(x) + hi2(y));   // (unused beyond the diagonal)
-                            const u64 v = fmul2(raw2(r[at], r[at + 1]), fmul2(pk2(x0, x1), d_s[q]));
-                            float v0 = lo2(v) + (s == lane ? D : 0.f), v1 = hi2(v) + (s + 1 == lane ? D : 0.f);
-                            v0 = s <= lane ? v0 : 0.f;
-                            v1 = s + 1 <= lane ? v1 : 0.f;
-                            split_pair(pk2(v0, v1), hi[2 * k + q], lo[2 * k + q]);
+                        for (int k = 0; k < 4; ++k) {
+                            const ulonglong2 ls = *reinterpret_cast<const ulonglong2*>(gt.l + s0 + 4 * k);
+                            const ulonglong2 lo_s = *reinterpret_cast<const ulonglong2*>(gt.l_lo + s0 + 4 * k);
+                            const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(gt.d + s0 + 4 * k);
+                            const u64 l_s[2] = {ls.x, ls.y}, l_o[2] = {lo_s.x, lo_s.y}, d_s[2] = {d.x, d.y};
+#pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                const int s = 4 * k + 2 * q;
+                                const u64 x = ffma2(l_s[q], neg, lt2), y = ffma2(l_o[q], neg, lo_t2);
+                                const float x0 = ex2(lo2(x) + lo2(y)), x1 = ex2(hi2(x) + hi2(y));   // (unused beyond the diagonal)
+                                const u64 v = fmul2(raw2(r[s], r[s + 1]), fmul2(pk2(x0, x1), d_s[q]));
+                                float v0 = lo2(v) + (s == last ? D : 0.f), v1 = hi2(v) + (s + 1 == last ? D : 0.f);
+                                v0 = s <= last ? v0 : 0.f;
+                                v1 = s + 1 <= last ? v1 : 0.f;
+                                split_pair(pk2(v0, v1), hi[2 * k + q], lo[2 * k + q]);
+                            }
                         }
                     }
                 }
-                tm_st8(G + 8 * b, hi);
-                tm_st8(G + 32 + 8 * b, lo);
+                tm_st8(G + 32 * j, hi);
+                tm_st8(G + 32 * j + 8, lo);
             }
             tm_wait_st();
             fence_before();
