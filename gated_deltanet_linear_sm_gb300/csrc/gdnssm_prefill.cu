@@ -128,9 +128,9 @@ static_assert(sizeof(Gates) % 16 == 0 && Lay<64>::kMisc % 16 == 0 && Lay<128>::k
 static_assert(scan_smem<128>() <= 227 * 1024, "shared memory budget");
 
 // tensor-memory columns
-constexpr uint32_t kTG = 0;                      // two G / Pm tiles of 128
-constexpr uint32_t kTY1 = 256, kTY2 = 320;       // Y1; two Y2
-constexpr uint32_t kTdS = 448;
+constexpr uint32_t kTG = 0;                      // G, then Pm in its place
+constexpr uint32_t kTY1 = 128;                   // two Y1 of 64
+constexpr uint32_t kTY2 = 256, kTdS = 384;       // Y2 and dS, the hi and the lo part's product side by side
 
 // ---- instructions -----------------------------------------------------------------
 
@@ -233,6 +233,11 @@ __device__ __forceinline__ float rcp(float x) {
     float y;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+    u64 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 __device__ __forceinline__ u64 dup2(float x) { return pk2(x, x); }
 __device__ __forceinline__ u64 raw2(uint32_t a, uint32_t b) { return (static_cast<u64>(b) << 32) | a; }
@@ -443,56 +448,49 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
         // ---- products ----
         if (lane == 0) {
             constexpr uint32_t id_g = (1u << 4) | (1u << 7) | (1u << 10) | (128u >> 3 << 17) | (128u >> 4 << 24);
-            constexpr uint32_t id_y = (1u << 4) | (1u << 7) | (1u << 10) | (64u >> 3 << 17) | (128u >> 4 << 24) | kBMn;
-            constexpr uint32_t id_ds = id_y | kAMn;
-            // operands as their descriptors, formed once; a step along the depth adds its bytes / 16
+            constexpr uint32_t id_y2 = id_g | kBMn, id_ds = id_g | kAMn | kBMn;
+            constexpr uint32_t id_y1 = (1u << 4) | (1u << 7) | (1u << 10) | (64u >> 3 << 17) | (128u >> 4 << 24) | kBMn;
+            // operands as their descriptors, formed once; a step along the depth adds its bytes / 16.
+            // The hi and lo tiles of Xw and of S are one operand of 128 columns: a product of 64 takes as long.
             const uint64_t c_km = desc_sw128(sbase + L::kC), b_km = desc_sw128(sbase + L::kB);
             const uint64_t b_mn = desc_mn(sbase + L::kB, L::kTile), xw_mn = desc_mn(sbase + L::kXw, L::kTile);
-            const uint64_t s_mn = desc_mn(sbase + L::kS, L::kTile), x_mn0 = desc_mn(sbase + L::kX, L::kTile);
+            const uint64_t s_mn = desc_mn(sbase + L::kS, N * 128), x_mn0 = desc_mn(sbase + L::kX, L::kTile);
             for (int c = 0; c < wk.chunks; ++c) {
                 const bool tail = rows_of(c) < kQ;               // its rows past the end are cleared before any product
                 if (!need(&ms.bc_full, c)) break;
                 if (tail && !need(&ms.ready, c)) break;
                 fence_after();
                 if (!kStates) {
-                    const uint32_t dst = tm + kTG + (c & 1) * 128;
+                    if (c > 0 && !need(&ms.y1_done, c - 1)) break;               // Pm has been used
 #pragma unroll
                     for (int ks = 0; ks < N / 16; ++ks) {
-                        constexpr int unit = L::kTile / 16;
-                        const uint64_t o = (ks >> 2) * unit + (ks & 3) * 2;
-                        mma_bf16(dst, c_km + o, b_km + o, id_g, ks > 0);
+                        const uint64_t o = (ks >> 2) * (L::kTile / 16) + (ks & 3) * 2;
+                        mma_bf16(tm + kTG, c_km + o, b_km + o, id_g, ks > 0);
                     }
                     commit(saddr(&ms.g_done));
                 }
                 if (!tail && !need(&ms.ready, c)) break;
                 fence_after();
 #pragma unroll
-                for (int part = 0; part < 2; ++part)
-#pragma unroll
-                    for (int ks = 0; ks < kQ / 16; ++ks)
-                        mma_bf16(tm + kTdS, b_mn + ks * 128, xw_mn + part * (L::kTile / 16) + ks * 128, id_ds, part + ks > 0);
+                for (int ks = 0; ks < kQ / 16; ++ks)
+                    mma_bf16(tm + kTdS, b_mn + ks * 128, xw_mn + ks * 128, id_ds, ks > 0);
                 commit(saddr(&ms.ds_done));
                 if (!kStates) {
-                    const uint32_t dst = tm + kTY2 + (c & 1) * 64;
-#pragma unroll
-                    for (int part = 0; part < 2; ++part)
-#pragma unroll
-                        for (int ks = 0; ks < N / 16; ++ks)
-                            mma_bf16(dst, c_km + (ks >> 2) * (L::kTile / 16) + (ks & 3) * 2, s_mn + part * N * 8 + ks * 128, id_y,
-                                     part + ks > 0);
-                    commit(saddr(&ms.y2_done));
-                    // Y1 has been read
+                    // the outputs of chunk c - 1 are made: Y2 has been read (so has Y1 of c - 2, before `ready`)
                     if (c > 0 && !need(&ms.chunk_done[(c - 1) & 1], (c - 1) >> 1)) break;
+                    fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < N / 16; ++ks)
+                        mma_bf16(tm + kTY2, c_km + (ks >> 2) * (L::kTile / 16) + (ks & 3) * 2, s_mn + ks * 128, id_y2, ks > 0);
+                    commit(saddr(&ms.y2_done));
                     if (!need(&ms.p_ready, c)) break;
                     fence_after();
-                    const uint32_t a = tm + kTG + (c & 1) * 128;
                     const uint64_t x_mn = x_mn0 + c % kXStages * (L::kTile / 16);
 #pragma unroll
                     for (int part = 0; part < 2; ++part)
 #pragma unroll
                         for (int ks = 0; ks < kQ / 16; ++ks)
-                            mma_bf16_ts(tm + kTY1, a + ks * 16 + part * 8, x_mn + ks * 128, id_y,
-                                        part + ks > 0);
+                            mma_bf16_ts(tm + kTY1 + (c & 1) * 64, tm + kTG + ks * 16 + part * 8, x_mn + ks * 128, id_y1, part + ks > 0);
                     commit(saddr(&ms.y1_done));
                 }
             }
@@ -712,12 +710,17 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
             fence_after();
             run_log += gt.total_log;
             if (state_row) {
-                uint32_t x[32];
-                tm_ld32_nowait(lanes + kTdS + 32 * hh, x);
                 const u64 a2 = dup2(gt.total);
-                tm_wait_ld();
 #pragma unroll
-                for (int j = 0; j < 16; ++j) S[j] = ffma2(a2, S[j], raw2(x[2 * j], x[2 * j + 1]));
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t x[16], y[16];
+                    tm_ld16_nowait(lanes + kTdS + 32 * hh + 16 * half, x);
+                    tm_ld16_nowait(lanes + kTdS + 64 + 32 * hh + 16 * half, y);
+                    tm_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        S[8 * half + j] = ffma2(a2, S[8 * half + j], add2(raw2(x[2 * j], x[2 * j + 1]), raw2(y[2 * j], y[2 * j + 1])));
+                }
             }
             fence_before();
             const u64 et2 = dup2(gt.e[row]);
@@ -741,9 +744,10 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
                 unsigned char* Z = sm + L::kZ + (c & 1) * L::kTile;
 #pragma unroll 1
                 for (int half = 0; half < 2; ++half) {
-                    uint32_t y1[16], y2[16];
-                    tm_ld16_nowait(lanes + kTY1 + 32 * hh + 16 * half, y1);
-                    tm_ld16_nowait(lanes + kTY2 + (c & 1) * 64 + 32 * hh + 16 * half, y2);
+                    uint32_t y1[16], y2[16], y3[16];
+                    tm_ld16_nowait(lanes + kTY1 + (c & 1) * 64 + 32 * hh + 16 * half, y1);
+                    tm_ld16_nowait(lanes + kTY2 + 32 * hh + 16 * half, y2);
+                    tm_ld16_nowait(lanes + kTY2 + 64 + 32 * hh + 16 * half, y3);
                     tm_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
@@ -752,7 +756,7 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int k = 8 * j + 2 * e;
-                            o[e] = ffma2(et2, raw2(y2[k], y2[k + 1]), raw2(y1[k], y1[k + 1]));
+                            o[e] = ffma2(et2, add2(raw2(y2[k], y2[k + 1]), raw2(y3[k], y3[k + 1])), raw2(y1[k], y1[k + 1]));
                         }
                         if (gated) {
                             const uint4 z = *reinterpret_cast<const uint4*>(Z + at);
@@ -825,7 +829,7 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
             if (!need_warp(&ms.gates_full[c % kGates], c / kGates) || !need_warp(&ms.g_done, c)) break;
             fence_after();
             const Gates& gt = ms.gates[c % kGates];
-            const uint32_t G = tm + (static_cast<uint32_t>(quad * 32) << 16) + kTG + (c & 1) * 128 + 16 * hh;
+            const uint32_t G = tm + (static_cast<uint32_t>(quad * 32) << 16) + kTG + 16 * hh;
             const float lt = gt.l[row], lt_lo = gt.l_lo[row];
 #pragma unroll 1
             for (int j = 0; j < 4; ++j) {                        // this warp's 16 columns s of block j of 32
