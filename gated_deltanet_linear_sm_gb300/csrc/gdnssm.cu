@@ -15,8 +15,8 @@ namespace {
 //
 // A thread owns 8 (or 4) neighbouring channels of a run of rows and slides a
 // window of the last W - 1 inputs, in FP32 registers, along them: x is read
-// once (W - 1 rows a run twice) and y written once, in 16-byte accesses, with 8
-// rows of loads in flight.  Rows are cut into runs of the whole token batch,
+// once (W - 1 rows a run twice) and y written once, in 16-byte accesses, with 4
+// rows of loads ahead of the arithmetic, which runs on pairs of channels.  Rows are cut into runs of the whole token batch,
 // not of a sequence, so ragged prompts fill the GPU evenly; a run that crosses
 // the start of a sequence takes its window from the conv slot instead.  The
 // first W - 1 rows of a sequence always belong to the run that holds its first
@@ -44,14 +44,10 @@ template <int CV>
 using Raw = std::conditional_t<CV == 8, uint4, uint2>;
 
 template <int CV>
-__device__ __forceinline__ void unpack(const Raw<CV>& raw, float (&x)[CV]) {
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&raw);
+__device__ __forceinline__ void widen_all(const Raw<CV>& raw, u64 (&x)[CV / 2]) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(&raw);
 #pragma unroll
-    for (int e = 0; e < CV / 2; ++e) {
-        const float2 f = __bfloat1622float2(h[e]);
-        x[2 * e] = f.x;
-        x[2 * e + 1] = f.y;
-    }
+    for (int e = 0; e < CV / 2; ++e) x[e] = widen(w[e]);
 }
 
 // whether sequence j may run: its rows and conv slots are in range
@@ -62,7 +58,7 @@ __device__ __forceinline__ int conv_flag(const ConvParams& p, int s, int e, int 
 }
 
 template <int CV, int W>
-__global__ void __launch_bounds__(kCThreads) gdn_conv_prefill_kernel(const ConvParams p) {
+__global__ void __launch_bounds__(kCThreads, 4) gdn_conv_prefill_kernel(const ConvParams p) {
     constexpr int HN = W > 1 ? W - 1 : 1;
     dep_wait();
     dep_launch();
@@ -87,24 +83,32 @@ __global__ void __launch_bounds__(kCThreads) gdn_conv_prefill_kernel(const ConvP
     const int c = (cb * kCThreads + threadIdx.x) * CV;
     if (c >= p.dim) return;
 
-    float wt[CV][W], bias[CV];
+    u64 wt2[CV / 2][W], bias2[CV / 2];              // pairs of channels
+    {
+        float wt[CV][W], bias[CV];
 #pragma unroll
-    for (int e = 0; e < CV; ++e) bias[e] = 0.f;
-    if constexpr (W == 4) {                         // CV channels' taps: CV 8-byte words
+        for (int e = 0; e < CV; ++e) bias[e] = 0.f;
+        if constexpr (W == 4) {                     // CV channels' taps: CV 8-byte words
 #pragma unroll
-        for (int e = 0; e < CV; ++e) {
-            float f[4];
-            unpack<4>(ld(reinterpret_cast<const uint2*>(p.w + static_cast<int64_t>(c + e) * 4)), f);
+            for (int e = 0; e < CV; ++e)
+                unpack4(ld(reinterpret_cast<const uint2*>(p.w + static_cast<int64_t>(c + e) * 4)), wt[e]);
+        } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) wt[e][k] = f[k];
+            for (int e = 0; e < CV; ++e)
+#pragma unroll
+                for (int k = 0; k < W; ++k) wt[e][k] = __bfloat162float(p.w[static_cast<int64_t>(c + e) * W + k]);
         }
-    } else {
+        if (p.bias) {
 #pragma unroll
-        for (int e = 0; e < CV; ++e)
+            for (int e = 0; e < CV; ++e) bias[e] = __bfloat162float(p.bias[c + e]);
+        }
 #pragma unroll
-            for (int k = 0; k < W; ++k) wt[e][k] = __bfloat162float(p.w[static_cast<int64_t>(c + e) * W + k]);
+        for (int e = 0; e < CV / 2; ++e) {
+            bias2[e] = pk2(bias[2 * e], bias[2 * e + 1]);
+#pragma unroll
+            for (int k = 0; k < W; ++k) wt2[e][k] = pk2(wt[2 * e][k], wt[2 * e + 1][k]);
+        }
     }
-    if (p.bias) unpack<CV>(ld(reinterpret_cast<const Raw<CV>*>(p.bias + c)), bias);
 
     auto row_of_x = [&](int64_t r) { return ld(reinterpret_cast<const Raw<CV>*>(p.x + r * p.x_stride + c)); };
     for (; j < p.batch; ++j) {
@@ -145,39 +149,45 @@ __global__ void __launch_bounds__(kCThreads) gdn_conv_prefill_kernel(const ConvP
                 }
             }
         }
-        float f[HN][CV];
+        // pairs of channels: each tap is one instruction a pair
+        u64 f[HN][CV / 2];
 #pragma unroll
-        for (int k = 0; k < W - 1; ++k) unpack<CV>(win[k], f[k]);
-        constexpr int U = 8;
+        for (int k = 0; k < W - 1; ++k) widen_all<CV>(win[k], f[k]);
+        constexpr int U = 4;                        // rows of loads in flight, twice
+        Raw<CV> next[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (a + u < b) next[u] = row_of_x(a + u);
         for (int r = a; r < b; r += U) {
             Raw<CV> raw[U];
 #pragma unroll
+            for (int u = 0; u < U; ++u) raw[u] = next[u];
+#pragma unroll
             for (int u = 0; u < U; ++u)
-                if (r + u < b) raw[u] = row_of_x(r + u);
+                if (r + U + u < b) next[u] = row_of_x(r + U + u);
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (r + u >= b) break;
-                float v[CV], y[CV];
-                unpack<CV>(raw[u], v);
+                u64 v[CV / 2];
+                widen_all<CV>(raw[u], v);
+                Raw<CV> o;
+                uint32_t* ow = reinterpret_cast<uint32_t*>(&o);
 #pragma unroll
-                for (int e2 = 0; e2 < CV; ++e2) {
-                    float acc = bias[e2];
+                for (int e2 = 0; e2 < CV / 2; ++e2) {
+                    u64 acc = bias2[e2];
 #pragma unroll
-                    for (int k = 0; k < W - 1; ++k) acc = fmaf(wt[e2][k], f[k][e2], acc);
-                    y[e2] = silu(fmaf(wt[e2][W - 1], v[e2], acc));
+                    for (int k = 0; k < W - 1; ++k) acc = ffma2(wt2[e2][k], f[k][e2], acc);
+                    acc = silu2(ffma2(wt2[e2][W - 1], v[e2], acc));
+                    ow[e2] = pack2(lo2(acc), hi2(acc));
                 }
 #pragma unroll
                 for (int k = 0; k + 1 < W - 1; ++k)
 #pragma unroll
-                    for (int e2 = 0; e2 < CV; ++e2) f[k][e2] = f[k + 1][e2];
+                    for (int e2 = 0; e2 < CV / 2; ++e2) f[k][e2] = f[k + 1][e2];
                 if constexpr (W > 1) {
 #pragma unroll
-                    for (int e2 = 0; e2 < CV; ++e2) f[W - 2][e2] = v[e2];
+                    for (int e2 = 0; e2 < CV / 2; ++e2) f[W - 2][e2] = v[e2];
                 }
-                Raw<CV> o;
-                uint32_t* ow = reinterpret_cast<uint32_t*>(&o);
-#pragma unroll
-                for (int e2 = 0; e2 < CV / 2; ++e2) ow[e2] = pack2(y[2 * e2], y[2 * e2 + 1]);
                 *reinterpret_cast<Raw<CV>*>(p.y + (r + u) * p.y_stride + c) = o;
             }
         }
@@ -227,7 +237,7 @@ template <typename StateT, int N>
 __global__ void __launch_bounds__(kRThreads, 4) gdn_ssm_decode_kernel(const Params p) {
     constexpr int R = N / 16;
     constexpr int kQuads = 16 + N / 2;              // channel quads of x, B and C
-    static_assert(kQuads <= kRThreads, "one thread a quad");
+    static_assert(kQuads + kMaxT <= kRThreads, "one thread a quad, and one a token");
     __shared__ Round<N> s;
     const int tid = threadIdx.x, cg = tid & 7, rg = tid >> 3;
     const int pb = static_cast<int>(blockIdx.x % p.blocks);
@@ -268,36 +278,27 @@ __global__ void __launch_bounds__(kRThreads, 4) gdn_ssm_decode_kernel(const Para
 #pragma unroll
         for (int j = 0; j < R; ++j) Row8<StateT>::load(src + static_cast<int64_t>(j) * p.P, cg, S[j]);
     }
-    // ---- rows, decays, the gate's quads ----
+    // ---- rows, decays, the gate's quads: every thread finds the rows it needs, so that the
+    //      projection's rows are on their way together with the state ----
     int bad = 0;
-    if (tid < n) {
-        const int r = p.sti ? ld(p.sti + bos + tid) : bos + tid;
-        bad = r < 0 || r >= p.num_tokens;
-        s.row[tid] = r;
-        s.slot[tid] = ld(slot_row + tid);
-        if (!bad) {
-            const float d = softplus(__bfloat162float(p.dt[r * p.dt_stride + h]) + __bfloat162float(p.dt_bias[h]));
-            s.step[tid] = d;
-            s.decay[tid] = expf(-expf(ld(p.A_log + h)) * d);
-        }
-    }
-    if (__syncthreads_or(bad)) {
-        if (tid == 0) raise(p.status, GDN_FLAG_TOKEN_ROW);
-        return;
-    }
+    auto row_at = [&](int t) {
+        const int r = p.sti ? ld(p.sti + bos + t) : bos + t;
+        if (r >= 0 && r < p.num_tokens) return r;
+        bad = 1;
+        return 0;                                   // (no row exists only where bad data is reported anyway)
+    };
     const int to = tid >> 4, qo = tid & 15;         // the token and column quad this thread writes out
-    uint2 zraw = make_uint2(0, 0);
     const int col = h * p.P + pb * kPB;
-    if (p.z && to < n)
-        zraw = ld(reinterpret_cast<const uint2*>(p.z + s.row[to] * p.z_stride + col + 4 * qo));
-    // ---- the convolution: quad q of x | B | C, all tokens ----
+    uint2 zraw = make_uint2(0, 0);
+    if (p.z && to < n) zraw = ld(reinterpret_cast<const uint2*>(p.z + row_at(to) * p.z_stride + col + 4 * qo));
+    // quad q of x | B | C, all tokens
+    const int W = p.conv_width;
+    const int HP = p.H * p.P;
+    const int ch = tid < 16           ? col + 4 * tid
+                   : tid < 16 + N / 4 ? HP + g * N + 4 * (tid - 16)
+                                      : HP + p.G * N + g * N + 4 * (tid - 16 - N / 4);
+    uint2 raw[kMaxT + 3];                           // history (the last 3 before the step), then the step's rows
     if (tid < kQuads) {
-        const int W = p.conv_width;
-        const int HP = p.H * p.P;
-        const int ch = tid < 16           ? col + 4 * tid
-                       : tid < 16 + N / 4 ? HP + g * N + 4 * (tid - 16)
-                                          : HP + p.G * N + g * N + 4 * (tid - 16 - N / 4);
-        uint2 raw[kMaxT + 3];                       // history (the last 3 before the step), then the step's rows
         const __nv_bfloat16* hist =
             cin < 0 ? nullptr : p.conv_pool + (cin * p.conv_state_len + max(acc, 1)) * static_cast<int64_t>(p.conv_dim) + ch;
 #pragma unroll
@@ -308,49 +309,64 @@ __global__ void __launch_bounds__(kRThreads, 4) gdn_ssm_decode_kernel(const Para
         }
 #pragma unroll
         for (int t = 0; t < kMaxT; ++t)
-            if (t < n) raw[3 + t] = ld(reinterpret_cast<const uint2*>(p.x + s.row[t] * p.x_stride + ch));
-        float wt[4][4], bias[4] = {0.f, 0.f, 0.f, 0.f};  // taps right-aligned: tap 3 is the token itself
+            if (t < n) raw[3 + t] = ld(reinterpret_cast<const uint2*>(p.x + row_at(t) * p.x_stride + ch));
+    } else if (tid - kQuads < n) {                  // (the threads behind the quads: at least 48)
+        const int t = tid - kQuads, r = row_at(t);
+        s.row[t] = r;
+        s.slot[t] = ld(slot_row + t);
+        const float d = softplus(__bfloat162float(p.dt[r * p.dt_stride + h]) + __bfloat162float(p.dt_bias[h]));
+        s.step[t] = d;
+        s.decay[t] = expf(-expf(ld(p.A_log + h)) * d);
+    }
+    // ---- the convolution ----
+    if (tid < kQuads) {
+        u64 wt2[2][4], bias2[2] = {0, 0};           // taps right-aligned: tap 3 is the token itself
+        {
+            float wt[4][4], b4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < 4; ++e)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                wt[e][k] = k >= 4 - W ? __bfloat162float(p.conv_w[static_cast<int64_t>(ch + e) * W + k - (4 - W)]) : 0.f;
-        if (p.conv_b) unpack4(ld(reinterpret_cast<const uint2*>(p.conv_b + ch)), bias);
-        float f[3][4];
+                for (int k = 0; k < 4; ++k)
+                    wt[e][k] = k >= 4 - W ? __bfloat162float(p.conv_w[static_cast<int64_t>(ch + e) * W + k - (4 - W)]) : 0.f;
+            if (p.conv_b) unpack4(ld(reinterpret_cast<const uint2*>(p.conv_b + ch)), b4);
 #pragma unroll
-        for (int k = 0; k < 3; ++k) unpack4(raw[k], f[k]);
+            for (int e = 0; e < 2; ++e) {
+                bias2[e] = pk2(b4[2 * e], b4[2 * e + 1]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) wt2[e][k] = pk2(wt[2 * e][k], wt[2 * e + 1][k]);
+            }
+        }
         float* dst = tid < 16 ? &s.x[0][4 * tid] : tid < 16 + N / 4 ? &s.B[0][4 * (tid - 16)] : &s.C[0][4 * (tid - 16 - N / 4)];
         const int pitch = tid < 16 ? 64 : N;
 #pragma unroll
         for (int t = 0; t < kMaxT; ++t) {
             if (t >= n) break;
-            float v[4], y[4];
-            unpack4(raw[3 + t], v);
+            u64 y[2];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float a = bias[e];
+            for (int e = 0; e < 2; ++e) {
+                y[e] = bias2[e];
 #pragma unroll
-                for (int k = 0; k < 3; ++k)         // a tap that the width lacks reads no row, so adds nothing
-                    if (k >= 4 - W) a = fmaf(wt[e][k], f[k][e], a);
-                y[e] = silu(fmaf(wt[e][3], v[e], a));
-                f[0][e] = f[1][e];
-                f[1][e] = f[2][e];
-                f[2][e] = v[e];
+                for (int k = 0; k < 4; ++k)         // a tap that the width lacks reads no row, so adds nothing
+                    if (k >= 4 - W) y[e] = ffma2(wt2[e][k], widen(e ? raw[t + k].y : raw[t + k].x), y[e]);
+                y[e] = silu2(y[e]);
             }
-            *reinterpret_cast<float4*>(dst + t * pitch) = make_float4(y[0], y[1], y[2], y[3]);
-        }
-        // the new conv slot: the history, then this step's rows; a group's B and C once
-        if (cout >= 0 && (tid < 16 || (h % p.group == 0 && pb == 0))) {
-            __nv_bfloat16* o = p.conv_pool + cout * p.conv_state_len * static_cast<int64_t>(p.conv_dim) + ch;
-#pragma unroll
-            for (int k = 0; k < 3; ++k)
-                if (k >= 4 - W) *reinterpret_cast<uint2*>(o + static_cast<int64_t>(k - (4 - W)) * p.conv_dim) = raw[k];
-#pragma unroll
-            for (int t = 0; t < kMaxT; ++t)
-                if (t < n) *reinterpret_cast<uint2*>(o + static_cast<int64_t>(W - 1 + t) * p.conv_dim) = raw[3 + t];
+            *reinterpret_cast<float4*>(dst + t * pitch) = make_float4(lo2(y[0]), hi2(y[0]), lo2(y[1]), hi2(y[1]));
         }
     }
-    __syncthreads();
+    if (__syncthreads_or(bad)) {
+        if (tid == 0) raise(p.status, GDN_FLAG_TOKEN_ROW);
+        return;
+    }
+    // the new conv slot: the history, then this step's rows; a group's B and C once
+    if (cout >= 0 && tid < kQuads && (tid < 16 || (h % p.group == 0 && pb == 0))) {
+        __nv_bfloat16* o = p.conv_pool + cout * p.conv_state_len * static_cast<int64_t>(p.conv_dim) + ch;
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+            if (k >= 4 - W) *reinterpret_cast<uint2*>(o + static_cast<int64_t>(k - (4 - W)) * p.conv_dim) = raw[k];
+#pragma unroll
+        for (int t = 0; t < kMaxT; ++t)
+            if (t < n) *reinterpret_cast<uint2*>(o + static_cast<int64_t>(W - 1 + t) * p.conv_dim) = raw[3 + t];
+    }
     // ---- the tokens ----
     for (int t = 0; t < n; ++t) {
         token<StateT, N>(S, s, t);

@@ -67,7 +67,6 @@ constexpr int kPm = kWarps + 4;                  // the first that makes Pm (a m
 constexpr int kSThreads = 32 * (2 * kWarps + 4);
 constexpr int kStatesThreads = 32 * (kWarps + 3);
 constexpr int kGates = 3;                        // chunks whose decay factors are held
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kXStages = 3;
 
 struct ScanParams {
@@ -223,26 +222,6 @@ __device__ __forceinline__ bool wait(unsigned long long* bar, int use, uint32_t 
     return false;
 }
 
-// 2^x and 1 / x as single instructions (results and inputs below 2^-126 become 0)
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float rcp(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ u64 add2(u64 a, u64 b) {
-    u64 d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ u64 dup2(float x) { return pk2(x, x); }
-__device__ __forceinline__ u64 raw2(uint32_t a, uint32_t b) { return (static_cast<u64>(b) << 32) | a; }
-// the two bf16 of a word as a pair of floats
-__device__ __forceinline__ u64 widen(uint32_t w) { return raw2(w << 16, w & 0xffff0000u); }
 // x as bf16 hi and lo words: lo = bf16(x - hi), the difference exact
 __device__ __forceinline__ void split_pair(u64 x, uint32_t& hi, uint32_t& lo) {
     hi = pack2(lo2(x), hi2(x));
@@ -255,13 +234,7 @@ __device__ __forceinline__ void split_quads(const u64* x, uint4& hi, uint4& lo) 
     split_pair(x[2], hi.z, lo.z);
     split_pair(x[3], hi.w, lo.w);
 }
-// o * silu(z) for a pair, z in bf16: z / (1 + 2^(-z log2 e))
-__device__ __forceinline__ u64 gate_pair(u64 o, uint32_t zw) {
-    const u64 z = widen(zw);
-    const u64 t = fmul2(z, dup2(-kLog2e));
-    const u64 den = raw2(__float_as_uint(1.0f + ex2(lo2(t))), __float_as_uint(1.0f + ex2(hi2(t))));
-    return fmul2(o, fmul2(z, pk2(rcp(lo2(den)), rcp(hi2(den)))));
-}
+__device__ __forceinline__ u64 gate_pair(u64 o, uint32_t zw) { return fmul2(o, silu2(widen(zw))); }
 
 __device__ __forceinline__ uint32_t unit16(int r, int j) { return static_cast<uint32_t>(r * 128 + ((j ^ (r & 7)) << 4)); }
 

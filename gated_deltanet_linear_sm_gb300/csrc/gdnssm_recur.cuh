@@ -47,6 +47,35 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+__device__ __forceinline__ u64 add2(u64 a, u64 b) {
+    u64 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ u64 dup2(float x) { return pk2(x, x); }
+__device__ __forceinline__ u64 raw2(uint32_t a, uint32_t b) { return (static_cast<u64>(b) << 32) | a; }
+// the two bf16 of a word as a pair of floats
+__device__ __forceinline__ u64 widen(uint32_t w) { return raw2(w << 16, w & 0xffff0000u); }
+
+// 2^x and 1 / x as single instructions (results and inputs below 2^-126 become 0)
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+// silu(z) for a pair: z / (1 + 2^(-z log2 e))
+__device__ __forceinline__ u64 silu2(u64 z) {
+    const u64 t = fmul2(z, dup2(-kLog2e));
+    const u64 den = add2(pk2(ex2(lo2(t)), ex2(hi2(t))), dup2(1.0f));
+    return fmul2(z, pk2(rcp(lo2(den)), rcp(hi2(den))));
+}
+
 // first column of quad e (0 or 1) of column group cg
 template <typename StateT>
 __device__ __forceinline__ constexpr int quad_col(int cg, int e) {

@@ -22,7 +22,11 @@ namespace {
 // A probability is held as a whole multiple of 2^-52 in 64 bits, so the sums
 // are exact: the token depends neither on the order of the additions nor on
 // the number of CTAs, and no floating-point prefix sum has to be reproduced.
-// The row's bytes bound large batches, the chain of dependent loads small ones.
+// The integers are not made entry by entry (the conversion of a float to 64 bits
+// runs on a slow pipe: it held this kernel to a tenth of the memory's rate) but
+// as three sums of 22, 22 and 8 bits that floating-point additions of a constant
+// leave in the low bits of a float (Sums below).  The row's bytes bound large
+// batches, the chain of dependent loads small ones.
 
 constexpr int kVThreads = 512;
 constexpr int kVWarps = kVThreads / 32;
@@ -78,9 +82,33 @@ __device__ __forceinline__ u64 warp_sum(u64 x) {
     return x;
 }
 
+// The sum of fixed(p) over up to 256 entries.  Adding 2 to p in [0, 1] rounds it
+// to a multiple h of 2^-22, whose integer the float's low bits hold; p - h is
+// exact and at most 2^-23, so adding 1.5 * 2^-21 gives its multiple m of 2^-44 in
+// the same way, and 1.5 * 2^-29 the rest's nearest multiple l of 2^-52 (to even).
+// p = h + m + l then rounds as fixed(p) does.
+struct Sums {
+    uint32_t h = 0, m = 0, l = 0;
+    static constexpr float kH = 2.0f, kM = 1.5f / (1 << 21), kL = 1.5f / (1 << 29);
+    __device__ __forceinline__ void add(float p) {
+        const float t = p + kH, r = p - (t - kH);
+        const float u = r + kM, q = r - (u - kM);
+        h += __float_as_uint(t);
+        m += __float_as_uint(u);
+        l += __float_as_uint(q + kL);
+    }
+    // what `count` added entries sum to (32-bit sums of the parts fit: 256 * 2^22)
+    __device__ __forceinline__ long long value(uint32_t count) const {
+        const uint32_t hh = h - count * __float_as_uint(kH);
+        const int32_t mm = static_cast<int32_t>(m - count * __float_as_uint(kM));
+        const int32_t ll = static_cast<int32_t>(l - count * __float_as_uint(kL));
+        return (static_cast<long long>(hh) << 30) + static_cast<long long>(mm) * 256 + ll;
+    }
+};
+
 struct VerifySmem {
-    u64 warp_rest[kVWarps], warp_p[kVWarps];       // sums of each warp's piece
-    u64 cta_rest[kMaxCluster], cta_p[kMaxCluster]; // and of each CTA's, written by its owner
+    u64 warp_sum[kVWarps];                         // of each warp's piece
+    u64 cta_sum[2][kMaxCluster];                   // and of each CTA's, written by its owner (two attempts)
     u64 scan[kVWarps];
     int kept, take, d, valid;                      // the decision on the drafts
     int64_t row;                                   // row to sample from
@@ -162,67 +190,96 @@ __global__ void __launch_bounds__(kVThreads) gdn_verify_kernel(const VerifyParam
     }
 
     // ---- the sums of the row's pieces ----
-    const int take = s.take, d = s.d, V = p.vocab;
+    int take = s.take;
+    const int d = s.d, V = p.vocab;
     const T* prow = target + s.row * p.target_stride;
-    const T* qrow = take == 2 ? draft + i * p.draft_seq + s.kept * p.draft_stride : nullptr;
+    const T* qrow = take == 2 ? draft + i * p.draft_seq + s.kept * p.draft_stride : prow;
     // vector v covers entries v E - mis .. v E - mis + E - 1; only those inside the row are read
     const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(prow) / sizeof(T)) % E);
-    const bool qvec = take == 2 && static_cast<int>((reinterpret_cast<uintptr_t>(qrow) / sizeof(T)) % E) == mis;
+    const bool qvec = static_cast<int>((reinterpret_cast<uintptr_t>(qrow) / sizeof(T)) % E) == mis;
     const int NV = static_cast<int>((static_cast<int64_t>(mis) + V + E - 1) / E);
     const int per = (NV + CL * kVWarps - 1) / (CL * kVWarps);
     const int v0 = min(NV, (rank * kVWarps + warp) * per), v1 = min(NV, v0 + per);
-    u64 sum_rest = 0, sum_p = 0;
-    auto add = [&](float pe, float qe, int e) {
-        const u64 P = fixed(pe);
-        sum_p += P;
-        sum_rest += rest(take, P, take == 2 ? fixed(qe) : 0, e == d);
-    };
+
+    // entries count as p (take 0), as p but for entry d (1), or as max(p - q, 0) (2):
+    // fixed(p) > fixed(q) only where p > q, so the last is a difference of two sums
+    auto piece = [&](int how) {
+        long long sum = 0;
+        for (int base = v0 + lane; base < v1; base += 32 * (256 / E)) {
+            Sums P, Q;
+            uint32_t n = 0;
+            const int stop = min(v1, base + 32 * (256 / E));
+            if (how == 2) {
+#pragma unroll 2
+                for (int v = base; v < stop; v += 32) {
+                    const int e0 = v * E - mis;
+                    float pe[E], qe[E];
+                    if (e0 >= 0 && e0 + E <= V) {
+                        Vec<T>::load(prow + e0, pe);
+                        if (qvec) {
+                            Vec<T>::load(qrow + e0, qe);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < E; ++k) qe[k] = to_f(qrow[e0 + k]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < E; ++k) {
+                            const bool in = e0 + k >= 0 && e0 + k < V;
+                            pe[k] = in ? to_f(prow[e0 + k]) : 0.f;
+                            qe[k] = in ? to_f(qrow[e0 + k]) : 0.f;
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < E; ++k) {
+                        const float a = clamp01(pe[k]), b = clamp01(qe[k]);
+                        P.add(a > b ? a : 0.f);
+                        Q.add(a > b ? b : 0.f);
+                    }
+                    n += E;
+                }
+            } else {
 #pragma unroll 4
-    for (int v = v0 + lane; v < v1; v += 32) {
-        const int e0 = v * E - mis;
-        if (e0 >= 0 && e0 + E <= V) {
-            float pe[E], qe[E];
-            Vec<T>::load(prow + e0, pe);
-            if (qvec) {
-                Vec<T>::load(qrow + e0, qe);
-            } else if (take == 2) {
+                for (int v = base; v < stop; v += 32) {
+                    const int e0 = v * E - mis;
+                    float pe[E];
+                    if (e0 >= 0 && e0 + E <= V) {
+                        Vec<T>::load(prow + e0, pe);
+                    } else {
 #pragma unroll
-                for (int k = 0; k < E; ++k) qe[k] = to_f(qrow[e0 + k]);
+                        for (int k = 0; k < E; ++k) pe[k] = e0 + k >= 0 && e0 + k < V ? to_f(prow[e0 + k]) : 0.f;
+                    }
+#pragma unroll
+                    for (int k = 0; k < E; ++k) P.add(clamp01(pe[k]));
+                    n += E;
+                }
             }
-#pragma unroll
-            for (int k = 0; k < E; ++k) add(pe[k], qe[k], e0 + k);
-        } else {
-            for (int e = max(e0, 0); e < min(e0 + E, V); ++e) add(to_f(prow[e]), take == 2 ? to_f(qrow[e]) : 0.f, e);
+            sum += P.value(n) - (how == 2 ? Q.value(n) : 0);
         }
-    }
-    sum_rest = warp_sum(sum_rest);
-    sum_p = warp_sum(sum_p);
-    if (lane == 0) {
-        s.warp_rest[warp] = sum_rest;
-        s.warp_p[warp] = sum_p;
-    }
-    __syncthreads();
-    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-    if (tid < CL) {
-        u64 a = 0, b = 0;
-        for (int w = 0; w < kVWarps; ++w) {
-            a += s.warp_rest[w];
-            b += s.warp_p[w];
+        u64 total = warp_sum(static_cast<u64>(sum));
+        if (how == 1 && d >= v0 * E - mis && d < v1 * E - mis) total -= fixed(to_f(prow[d]));
+        return total;
+    };
+    u64 total = 0;
+    int attempt = 0;
+    for (;; ++attempt) {
+        const u64 mine = piece(take);
+        if (lane == 0) s.warp_sum[warp] = mine;
+        __syncthreads();
+        if (attempt == 0) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+        if (tid < CL) {
+            u64 a = 0;
+            for (int w = 0; w < kVWarps; ++w) a += s.warp_sum[w];
+            cl.map_shared_rank(&s, tid)->cta_sum[attempt][rank] = a;
         }
-        VerifySmem* peer = cl.map_shared_rank(&s, tid);
-        peer->cta_rest[rank] = a;
-        peer->cta_p[rank] = b;
+        cl.sync();                                 // this attempt's sums are read from this CTA's own memory
+        total = 0;
+        for (int c = 0; c < CL; ++c) total += s.cta_sum[attempt][c];
+        if (total != 0 || take == 0) break;
+        take = 0;                                  // nothing left of p: sample from p itself
     }
-    cl.sync();                                     // only this CTA's own memory is read from here on
 
     // ---- where the cumulative sum passes sample_u of the total ----
-    u64 total = 0, total_p = 0;
-    for (int c = 0; c < CL; ++c) {
-        total += s.cta_rest[c];
-        total_p += s.cta_p[c];
-    }
-    const bool whole = total == 0;                 // nothing left of p: sample from p itself
-    if (whole) total = total_p;
     const int64_t slot = static_cast<int64_t>(i) * p.max_T + s.kept;
     if (total == 0) {
         if (rank == 0 && tid == 0) {
@@ -234,13 +291,11 @@ __global__ void __launch_bounds__(kVThreads) gdn_verify_kernel(const VerifyParam
     const double x = fmax(static_cast<double>(ld(p.sample_u + i)) * static_cast<double>(total), 0.0);   // NaN -> 0
     u64 level = x < static_cast<double>(total) ? static_cast<u64>(x) : total - 1;
     if (level >= total) level = total - 1;
-    const u64* sums = whole ? s.cta_p : s.cta_rest;
     int owner = 0;
-    while (owner < CL - 1 && level >= sums[owner]) level -= sums[owner++];
+    while (owner < CL - 1 && level >= s.cta_sum[attempt][owner]) level -= s.cta_sum[attempt][owner++];
     if (owner != rank) return;
-    sums = whole ? s.warp_p : s.warp_rest;
     int w = 0;
-    while (w < kVWarps - 1 && level >= sums[w]) level -= sums[w++];
+    while (w < kVWarps - 1 && level >= s.warp_sum[w]) level -= s.warp_sum[w++];
 
     // the entries of that warp's piece, spread over the CTA in order
     const int w0 = min(NV, (rank * kVWarps + w) * per), w1 = min(NV, w0 + per);
@@ -249,7 +304,6 @@ __global__ void __launch_bounds__(kVThreads) gdn_verify_kernel(const VerifyParam
     const int m0 = min(e_hi, e_lo + tid * each), m1 = min(e_hi, m0 + each);
     auto entry = [&](int e) {
         const u64 P = fixed(to_f(prow[e]));
-        if (whole) return P;
         return rest(take, P, take == 2 ? fixed(to_f(qrow[e])) : 0, e == d);
     };
     u64 mine = 0;
