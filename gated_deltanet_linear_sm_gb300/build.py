@@ -15,7 +15,7 @@ CSRC = os.path.join(PKG, "csrc")
 SRCS = [os.path.join(CSRC, f) for f in ("gdnspec.cu", "gdnprefill_chunked.cu", "gdnverify.cu", "gdnssm.cu",
                                         "gdnssm_prefill.cu")]
 HEADERS = [os.path.join(ROOT, "include", "gdnspec.h")] + [
-    os.path.join(CSRC, f) for f in ("gdn_internal.h", "gdn_common.h", "gdn_tcgen05.h", "gdnssm.h", "gdnssm_recur.cuh")]
+    os.path.join(CSRC, f) for f in ("gdn_internal.h", "gdn_common.h", "gdn_pairs.h", "gdn_tcgen05.h", "gdnssm.h", "gdnssm_recur.cuh")]
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD_DIR, "libgdnspec.so")
 

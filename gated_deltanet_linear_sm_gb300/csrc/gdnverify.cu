@@ -4,6 +4,7 @@
 #include <cooperative_groups.h>
 
 #include "gdn_common.h"
+#include "gdn_pairs.h"
 
 namespace cg = cooperative_groups;
 using namespace gdn_common;
@@ -48,8 +49,6 @@ struct VerifyParams {
     int32_t batch, num_tokens, vocab, max_T;
 };
 
-typedef unsigned long long u64;
-
 __device__ __forceinline__ float clamp01(float p) { return fminf(fmaxf(p, 0.0f), 1.0f); }   // NaN -> 0
 // a probability in units of 2^-52 (the scaling is exact, the conversion rounds to nearest)
 __device__ __forceinline__ u64 fixed(float p) {
@@ -64,15 +63,43 @@ __device__ __forceinline__ u64 rest(int take, u64 P, u64 Q, bool at_d) {
     return (take == 1 && at_d) ? 0 : P;
 }
 
-// the E = 16 / sizeof(T) entries of one 16-byte vector
+// the E = 16 / sizeof(T) entries of one 16-byte vector, clamped to [0, 1], as pairs
+// (clamped as packed words where they come packed)
 template <typename T>
-struct Vec {
-    static constexpr int E = 16 / sizeof(T);
-    __device__ static void load(const T* p, float (&x)[E]) {
-        const uint4 raw = ld(reinterpret_cast<const uint4*>(p));
-        const T* e = reinterpret_cast<const T*>(&raw);
+struct Vec;
+
+template <>
+struct Vec<float> {
+    static constexpr int E = 4;
+    __device__ static void pairs(uint4 v, u64 (&x)[2]) {
+        x[0] = pk2(clamp01(__uint_as_float(v.x)), clamp01(__uint_as_float(v.y)));
+        x[1] = pk2(clamp01(__uint_as_float(v.z)), clamp01(__uint_as_float(v.w)));
+    }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+    static constexpr int E = 8;
+    __device__ static void pairs(uint4 v, u64 (&x)[4]) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int k = 0; k < E; ++k) x[k] = to_f(e[k]);
+        for (int k = 0; k < 4; ++k) {
+            const __nv_bfloat162 c = __hmin2(__hmax2(*reinterpret_cast<const __nv_bfloat162*>(&w[k]), __floats2bfloat162_rn(0.f, 0.f)),
+                                             __floats2bfloat162_rn(1.f, 1.f));
+            x[k] = widen(*reinterpret_cast<const uint32_t*>(&c));
+        }
+    }
+};
+template <>
+struct Vec<__half> {
+    static constexpr int E = 8;
+    __device__ static void pairs(uint4 v, u64 (&x)[4]) {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float2 f = __half22float2(__hmin2(__hmax2(*reinterpret_cast<const __half2*>(&w[k]), __floats2half2_rn(0.f, 0.f)),
+                                                    __floats2half2_rn(1.f, 1.f)));
+            x[k] = pk2(f.x, f.y);
+        }
     }
 };
 
@@ -90,12 +117,14 @@ __device__ __forceinline__ u64 warp_sum(u64 x) {
 struct Sums {
     uint32_t h = 0, m = 0, l = 0;
     static constexpr float kH = 2.0f, kM = 1.5f / (1 << 21), kL = 1.5f / (1 << 29);
-    __device__ __forceinline__ void add(float p) {
-        const float t = p + kH, r = p - (t - kH);
-        const float u = r + kM, q = r - (u - kM);
-        h += __float_as_uint(t);
-        m += __float_as_uint(u);
-        l += __float_as_uint(q + kL);
+    __device__ __forceinline__ void add(u64 p) {                // two entries
+        const u64 t = add2(p, dup2(kH));
+        const u64 r = sub2(p, add2(t, dup2(-kH)));
+        const u64 u = add2(r, dup2(kM));
+        const u64 q = add2(sub2(r, add2(u, dup2(-kM))), dup2(kL));
+        h += static_cast<uint32_t>(t) + static_cast<uint32_t>(t >> 32);
+        m += static_cast<uint32_t>(u) + static_cast<uint32_t>(u >> 32);
+        l += static_cast<uint32_t>(q) + static_cast<uint32_t>(q >> 32);
     }
     // what `count` added entries sum to (32-bit sums of the parts fit: 256 * 2^22)
     __device__ __forceinline__ long long value(uint32_t count) const {
@@ -129,10 +158,18 @@ __global__ void __launch_bounds__(kVThreads) gdn_verify_kernel(const VerifyParam
     asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
     dep_wait();
 
+    const float sample_u = ld(p.sample_u + i);
     // ---- which drafts stay ----
     if (warp == 0) {
         const int bos = ld(p.cu + i);
-        const int eos = ld(p.cu + i + 1);
+        const int eos = ld(p.cu + i + 1), last = ld(p.cu + p.batch);
+        // (loaded whatever the length is, beside the offsets)
+        int d = -1;
+        float u = 0.f;
+        if (lane < p.max_T - 1) {
+            d = ld(p.tokens + i * p.token_stride + lane);
+            u = ld(p.accept_u + i * p.token_stride + lane);
+        }
         const int n = (eos > bos && bos >= 0) ? eos - bos : 0;
         int flag = 0;
         int64_t row = 0;
@@ -141,7 +178,7 @@ __global__ void __launch_bounds__(kVThreads) gdn_verify_kernel(const VerifyParam
         } else if (n > p.max_T) {
             flag = GDN_FLAG_QLEN;
         } else if (n > 0) {
-            bool bad = eos > ld(p.cu + p.batch);
+            bool bad = eos > last;
             if (!bad && lane < n) {
                 row = p.sti ? ld(p.sti + bos + lane) : bos + lane;
                 bad = row < 0 || row >= p.num_tokens;
@@ -149,17 +186,14 @@ __global__ void __launch_bounds__(kVThreads) gdn_verify_kernel(const VerifyParam
             if (__any_sync(kFull, bad)) flag = GDN_FLAG_TOKEN_ROW;
         }
         const bool valid = n > 0 && flag == 0;
-        int d = -1;
         bool keep = false, in_range = false;
         if (valid && lane < n - 1) {
-            d = ld(p.tokens + i * p.token_stride + lane);
             in_range = d >= 0 && d < p.vocab;
             if (in_range) {
                 const float pd = clamp01(to_f(target[row * p.target_stride + d]));
                 const float qd =
                     draft ? clamp01(to_f(draft[i * p.draft_seq + lane * p.draft_stride + d])) : 1.0f;
-                const double u = ld(p.accept_u + i * p.token_stride + lane);
-                keep = u * static_cast<double>(qd) < static_cast<double>(pd);   // the product of two floats is exact
+                keep = static_cast<double>(u) * static_cast<double>(qd) < static_cast<double>(pd);   // the product of two floats is exact
             }
         }
         const unsigned stays = __ballot_sync(kFull, keep);
@@ -176,7 +210,7 @@ __global__ void __launch_bounds__(kVThreads) gdn_verify_kernel(const VerifyParam
         }
         if (rank == 0) {
             if (lane < p.max_T && !(valid && lane == kept))
-                p.out[static_cast<int64_t>(i) * p.max_T + lane] = lane < kept ? d : -1;
+                p.out[static_cast<int64_t>(i) * p.max_T + lane] = valid && lane < kept ? d : -1;
             if (lane == 0) {
                 if (valid) p.accepted[i] = kept + 1;
                 if (flag) raise(p.status, flag);
@@ -200,62 +234,81 @@ __global__ void __launch_bounds__(kVThreads) gdn_verify_kernel(const VerifyParam
     const int NV = static_cast<int>((static_cast<int64_t>(mis) + V + E - 1) / E);
     const int per = (NV + CL * kVWarps - 1) / (CL * kVWarps);
     const int v0 = min(NV, (rank * kVWarps + warp) * per), v1 = min(NV, v0 + per);
+    // the warp's vectors that lie inside the row whole; the row's two ends come one by one
+    const int in0 = max(v0, mis > 0 ? 1 : 0), in1 = min(v1, static_cast<int>((static_cast<int64_t>(mis) + V) / E));
 
     // entries count as p (take 0), as p but for entry d (1), or as max(p - q, 0) (2):
     // fixed(p) > fixed(q) only where p > q, so the last is a difference of two sums
+    auto left_pair = [](u64 p, u64 q, Sums& P, Sums& Q) {
+        const bool a = lo2(p) > lo2(q), b = hi2(p) > hi2(q);
+        P.add(pk2(a ? lo2(p) : 0.f, b ? hi2(p) : 0.f));
+        Q.add(pk2(a ? lo2(q) : 0.f, b ? hi2(q) : 0.f));
+    };
     auto piece = [&](int how) {
+        // up to 256 entries a lane between two foldings into 64 bits; the loads of U vectors go out together
+        constexpr int kFold = 256 / E, U = 4;
+        const uint4 none = make_uint4(0, 0, 0, 0);
         long long sum = 0;
-        for (int base = v0 + lane; base < v1; base += 32 * (256 / E)) {
+        for (int base = in0 + lane; base < in1; base += 32 * kFold) {
             Sums P, Q;
             uint32_t n = 0;
-            const int stop = min(v1, base + 32 * (256 / E));
-            if (how == 2) {
-#pragma unroll 2
-                for (int v = base; v < stop; v += 32) {
-                    const int e0 = v * E - mis;
-                    float pe[E], qe[E];
-                    if (e0 >= 0 && e0 + E <= V) {
-                        Vec<T>::load(prow + e0, pe);
-                        if (qvec) {
-                            Vec<T>::load(qrow + e0, qe);
-                        } else {
+            const int stop = min(in1, base + 32 * kFold);
+            if (how == 2 && qvec) {
+                for (int v = base; v < stop; v += 32 * U) {
+                    uint4 pr[U], qr[U];
 #pragma unroll
-                            for (int k = 0; k < E; ++k) qe[k] = to_f(qrow[e0 + k]);
-                        }
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < E; ++k) {
-                            const bool in = e0 + k >= 0 && e0 + k < V;
-                            pe[k] = in ? to_f(prow[e0 + k]) : 0.f;
-                            qe[k] = in ? to_f(qrow[e0 + k]) : 0.f;
-                        }
+                    for (int u = 0; u < U; ++u) {
+                        const int e = (v + 32 * u) * E - mis;
+                        const bool in = v + 32 * u < stop;
+                        pr[u] = in ? ld(reinterpret_cast<const uint4*>(prow + e)) : none;
+                        qr[u] = in ? ld(reinterpret_cast<const uint4*>(qrow + e)) : none;
                     }
 #pragma unroll
-                    for (int k = 0; k < E; ++k) {
-                        const float a = clamp01(pe[k]), b = clamp01(qe[k]);
-                        P.add(a > b ? a : 0.f);
-                        Q.add(a > b ? b : 0.f);
+                    for (int u = 0; u < U; ++u) {
+                        u64 pe[E / 2], qe[E / 2];
+                        Vec<T>::pairs(pr[u], pe);
+                        Vec<T>::pairs(qr[u], qe);
+#pragma unroll
+                        for (int k = 0; k < E / 2; ++k) left_pair(pe[k], qe[k], P, Q);
                     }
+                    n += U * E;
+                }
+            } else if (how == 2) {
+                for (int v = base; v < stop; v += 32) {          // the rows lie differently: q entry by entry
+                    const int e = v * E - mis;
+                    u64 pe[E / 2];
+                    Vec<T>::pairs(ld(reinterpret_cast<const uint4*>(prow + e)), pe);
+#pragma unroll
+                    for (int k = 0; k < E / 2; ++k)
+                        left_pair(pe[k], pk2(clamp01(to_f(qrow[e + 2 * k])), clamp01(to_f(qrow[e + 2 * k + 1]))), P, Q);
                     n += E;
                 }
             } else {
-#pragma unroll 4
-                for (int v = base; v < stop; v += 32) {
-                    const int e0 = v * E - mis;
-                    float pe[E];
-                    if (e0 >= 0 && e0 + E <= V) {
-                        Vec<T>::load(prow + e0, pe);
-                    } else {
+                for (int v = base; v < stop; v += 32 * U) {
+                    uint4 pr[U];
 #pragma unroll
-                        for (int k = 0; k < E; ++k) pe[k] = e0 + k >= 0 && e0 + k < V ? to_f(prow[e0 + k]) : 0.f;
+                    for (int u = 0; u < U; ++u)
+                        pr[u] = v + 32 * u < stop ? ld(reinterpret_cast<const uint4*>(prow + (v + 32 * u) * E - mis)) : none;
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        u64 pe[E / 2];
+                        Vec<T>::pairs(pr[u], pe);
+#pragma unroll
+                        for (int k = 0; k < E / 2; ++k) P.add(pe[k]);
                     }
-#pragma unroll
-                    for (int k = 0; k < E; ++k) P.add(clamp01(pe[k]));
-                    n += E;
+                    n += U * E;
                 }
             }
             sum += P.value(n) - (how == 2 ? Q.value(n) : 0);
         }
+        // the ends of the row, if they are this warp's: lane k the entry k of a cut vector
+        auto cut = [&](int v) {
+            const int e = v * E - mis + lane;
+            if (lane < E && e >= 0 && e < V)
+                sum += static_cast<long long>(rest(how == 2 ? 2 : 0, fixed(to_f(prow[e])), how == 2 ? fixed(to_f(qrow[e])) : 0, false));
+        };
+        if (v0 < v1 && v0 < in0) cut(v0);
+        if (in1 < v1 && in1 >= in0) cut(v1 - 1);
         u64 total = warp_sum(static_cast<u64>(sum));
         if (how == 1 && d >= v0 * E - mis && d < v1 * E - mis) total -= fixed(to_f(prow[d]));
         return total;
@@ -288,7 +341,7 @@ __global__ void __launch_bounds__(kVThreads) gdn_verify_kernel(const VerifyParam
         }
         return;
     }
-    const double x = fmax(static_cast<double>(ld(p.sample_u + i)) * static_cast<double>(total), 0.0);   // NaN -> 0
+    const double x = fmax(static_cast<double>(sample_u) * static_cast<double>(total), 0.0);   // NaN -> 0
     u64 level = x < static_cast<double>(total) ? static_cast<u64>(x) : total - 1;
     if (level >= total) level = total - 1;
     int owner = 0;
@@ -328,12 +381,12 @@ __global__ void __launch_bounds__(kVThreads) gdn_verify_kernel(const VerifyParam
     }
 }
 
-// CTAs per sequence: as many as keep the launch within four CTAs an SM and
-// leave each at least 2048 entries.
+// CTAs per sequence: as many as keep the launch within four CTAs an SM (what is
+// resident at once) and leave each at least 1024 entries.
 int verify_cluster(int batch, int vocab) {
     const int64_t room = 4 * static_cast<int64_t>(sm_count() ? sm_count() : 148);
     int cl = 1;
-    while (cl < kMaxCluster && static_cast<int64_t>(batch) * cl * 2 <= room && vocab / (cl * 2) >= 2048) cl *= 2;
+    while (cl < kMaxCluster && static_cast<int64_t>(batch) * cl * 2 <= room && vocab / (cl * 2) >= 1024) cl *= 2;
     return cl;
 }
 
