@@ -15,15 +15,16 @@ namespace {
 //
 // A thread owns 8 (or 4) neighbouring channels of a run of rows and slides a
 // window of the last W - 1 inputs, in FP32 registers, along them: x is read
-// once (W - 1 rows a run twice) and y written once, in 16-byte accesses, with 4
-// rows of loads ahead of the arithmetic, which runs on pairs of channels.  Rows are cut into runs of the whole token batch,
+// once (W - 1 rows a run twice) and y written once, in 16-byte accesses.  Up to 12
+// rows a thread are on their way through asynchronous copies into places of its
+// own in shared memory; the arithmetic runs on pairs of channels.  Rows are cut into runs of the whole token batch,
 // not of a sequence, so ragged prompts fill the GPU evenly; a run that crosses
 // the start of a sequence takes its window from the conv slot instead.  The
 // first W - 1 rows of a sequence always belong to the run that holds its first
 // row: that run alone reads the sequence's slot, and writes the new one after
 // it, so a slot may be updated in place.  HBM bandwidth bounds it.
 
-constexpr int kCThreads = 128;
+constexpr int kCThreads = 128;                      // at most
 
 struct ConvParams {
     const __nv_bfloat16* x;
@@ -50,6 +51,16 @@ __device__ __forceinline__ void widen_all(const Raw<CV>& raw, u64 (&x)[CV / 2]) 
     for (int e = 0; e < CV / 2; ++e) x[e] = widen(w[e]);
 }
 
+// one row's channels into shared memory, asynchronously
+template <int CV>
+__device__ __forceinline__ void copy_async(Raw<CV>* dst, const __nv_bfloat16* src) {
+    const uint32_t at = static_cast<uint32_t>(__cvta_generic_to_shared(dst));
+    if constexpr (CV == 8)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at), "l"(src) : "memory");
+}
+
 // whether sequence j may run: its rows and conv slots are in range
 __device__ __forceinline__ int conv_flag(const ConvParams& p, int s, int e, int j) {
     if (s < 0 || e > p.num_tokens) return GDN_FLAG_TOKEN_ROW;
@@ -60,13 +71,15 @@ __device__ __forceinline__ int conv_flag(const ConvParams& p, int s, int e, int 
 template <int CV, int W>
 __global__ void __launch_bounds__(kCThreads, 4) gdn_conv_prefill_kernel(const ConvParams p) {
     constexpr int HN = W > 1 ? W - 1 : 1;
+    constexpr int U = 4, kAhead = 3, kRing = U * (kAhead + 1);
+    __shared__ Raw<CV> ring[kRing][kCThreads];
     dep_wait();
     dep_launch();
     const int cb = blockIdx.x % p.col_blocks;
     const int r0 = static_cast<int>(blockIdx.x / p.col_blocks) * p.run;
     const int r1 = min(p.num_tokens, r0 + p.run);
     if (blockIdx.x == 0) {                          // bad data, reported once
-        for (int j = threadIdx.x; j < p.batch; j += kCThreads) {
+        for (int j = threadIdx.x; j < p.batch; j += blockDim.x) {
             const int s = ld(p.cu + j), e = ld(p.cu + j + 1);
             const int flag = e > s ? conv_flag(p, s, e, j) : 0;
             if (flag) raise(p.status, flag);
@@ -74,13 +87,13 @@ __global__ void __launch_bounds__(kCThreads, 4) gdn_conv_prefill_kernel(const Co
     }
     // the first sequence that ends behind r0
     int j = 0;
-    for (int base = 0; base < p.batch; base += kCThreads) {
+    for (int base = 0; base < p.batch; base += blockDim.x) {
         const int k = base + threadIdx.x;
         const int done = __syncthreads_count(k < p.batch && ld(p.cu + k + 1) <= r0);
         j += done;
-        if (done < kCThreads) break;
+        if (done < static_cast<int>(blockDim.x)) break;
     }
-    const int c = (cb * kCThreads + threadIdx.x) * CV;
+    const int c = (cb * static_cast<int>(blockDim.x) + threadIdx.x) * CV;
     if (c >= p.dim) return;
 
     u64 wt2[CV / 2][W], bias2[CV / 2];              // pairs of channels
@@ -120,6 +133,16 @@ __global__ void __launch_bounds__(kCThreads, 4) gdn_conv_prefill_kernel(const Co
         if (first) b = max(b, min(e, s + W - 1));   // its first W - 1 rows, whole
         else a = max(a, min(e, s + W - 1));
         if (a >= b) continue;
+        // U rows a batch; kAhead batches on their way into this thread's own places of the ring
+        auto fetch = [&](int r) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (r + u < b)
+                    copy_async<CV>(&ring[(r - a + u) % kRing][threadIdx.x], p.x + (r + u) * p.x_stride + c);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) fetch(a + k * U);
         Raw<CV> win[HN] = {};
         if (W > 1 && first) {
             const int in = ld(p.in + j);
@@ -153,18 +176,12 @@ __global__ void __launch_bounds__(kCThreads, 4) gdn_conv_prefill_kernel(const Co
         u64 f[HN][CV / 2];
 #pragma unroll
         for (int k = 0; k < W - 1; ++k) widen_all<CV>(win[k], f[k]);
-        constexpr int U = 4;                        // rows of loads in flight, twice
-        Raw<CV> next[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (a + u < b) next[u] = row_of_x(a + u);
         for (int r = a; r < b; r += U) {
+            fetch(r + kAhead * U);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
             Raw<CV> raw[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) raw[u] = next[u];
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-                if (r + U + u < b) next[u] = row_of_x(r + U + u);
+            for (int u = 0; u < U; ++u) raw[u] = ring[(r - a + u) % kRing][threadIdx.x];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (r + u >= b) break;
@@ -196,17 +213,30 @@ __global__ void __launch_bounds__(kCThreads, 4) gdn_conv_prefill_kernel(const Co
 
 template <int CV>
 cudaError_t launch_conv(ConvParams p, int width, cudaStream_t stream) {
+    // CTAs of 64, 96 or 128 threads, whichever leaves the fewest idle behind the last channel
     const int64_t threads = (p.dim + CV - 1) / CV;
-    p.col_blocks = static_cast<int>((threads + kCThreads - 1) / kCThreads);
-    // rows of a run: 64, or fewer so that every SM gets eight CTAs
-    const int sms = sm_count() ? sm_count() : 148;
-    p.run = 64;
-    while (p.run > 4 && (static_cast<int64_t>(p.num_tokens) + p.run - 1) / p.run * p.col_blocks < 8 * sms) p.run /= 2;
+    int width_of = kCThreads;
+    for (int t : {96, 64})
+        if ((threads + t - 1) / t * t < (threads + width_of - 1) / width_of * width_of) width_of = t;
+    p.col_blocks = static_cast<int>((threads + width_of - 1) / width_of);
+    // Rows of a run: few enough that every SM has its 512 threads, and so that the last round of
+    // CTAs is no small one.  A run costs kStart rows' time beside its own (its taps, its window).
+    constexpr int kStart = 8;
+    const int64_t resident = static_cast<int64_t>(sm_count() ? sm_count() : 148) * (512 / width_of);
+    double best = 1e300;
+    for (int run = 4; run <= 64; ++run) {
+        const int64_t n = (static_cast<int64_t>(p.num_tokens) + run - 1) / run * p.col_blocks;
+        const double cost = static_cast<double>((n + resident - 1) / resident) * (run + kStart);
+        if (cost <= best) {
+            best = cost;
+            p.run = run;
+        }
+    }
     const int64_t ctas = (static_cast<int64_t>(p.num_tokens) + p.run - 1) / p.run * p.col_blocks;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
-    cfg.blockDim = dim3(kCThreads, 1, 1);
+    cfg.blockDim = dim3(static_cast<unsigned>(width_of), 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
