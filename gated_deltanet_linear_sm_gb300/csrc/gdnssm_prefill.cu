@@ -40,9 +40,10 @@
 // memory.
 //
 // With few (sequence, head) pairs the prompts are cut into segments: a first
-// launch computes what each segment adds to the state (dS alone: no G, Pm, Y1,
-// Y2), and the second starts each segment from the initial state and the
-// segments before it, which it combines itself.
+// launch computes what the tokens before the last segment add to the state (dS
+// alone: no G, Pm, Y1, Y2), by quarters of a segment, two CTAs an SM; the second
+// starts each segment from the initial state and the parts before it, which it
+// combines itself.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -67,30 +68,36 @@ constexpr int kPm = kWarps + 4;                  // the first that makes Pm (a m
 constexpr int kSThreads = 32 * (2 * kWarps + 4);
 constexpr int kStatesThreads = 32 * (kWarps + 3);
 constexpr int kGates = 3;                        // chunks whose decay factors are held
-constexpr int kXStages = 3;
+constexpr int kParts = 4;                        // of a segment, in the first launch
 
 struct ScanParams {
     CUtensorMap x, B, C, z, out;                 // boxes of 64 elements x 128 rows
     Params p;
-    float* part;                                 // segments: [segment][unit][N][64] what a segment adds
-    float* part_decay;                           // and its log2-decay, [segment][unit]
+    float* part;                                 // segments: [part][unit][N][64] what a part of one adds
+    float* part_decay;                           // and its log2-decay, [part][unit]
     int32_t seg_chunks;                          // chunks of a segment (0: whole sequences)
-    int32_t segs;                                // segments that the launch has room for
+    int32_t part_chunks;                         // and of a part, a kParts-th
+    int32_t part_room;                           // parts that the workspace holds
     uint32_t wait_limit;
 };
 
 // ---- shared memory (from a 1024-byte aligned base) ------------------------------
 // Tiles of 128-byte rows, 16-byte unit j of row r at r * 128 + ((j ^ (r & 7)) << 4).
-template <int N>
+// (The first launch over segments has x, B and Xw only, and room for two CTAs an SM;
+// a product with 128 rows of a 64-row B^T reads on into Xw: rows that nobody uses.)
+template <int N, bool kStates>
 struct Lay {
     static constexpr int kTile = kQ * 128;                      // 128 rows
+    static constexpr int kXStages = kStates ? 2 : 3;
     static constexpr int kX = 0;                                // kXStages tiles [s][p]
     static constexpr int kZ = kX + kXStages * kTile;            // 2 tiles [t][p]: z, then the outputs
-    static constexpr int kB = kZ + 2 * kTile;                   // N / 64 tiles [s][64 n]
+    static constexpr int kB = kZ + (kStates ? 0 : 2 * kTile);   // N / 64 tiles [s][64 n]
     static constexpr int kC = kB + N / 64 * kTile;              // N / 64 tiles [t][64 n]
-    static constexpr int kXw = kC + N / 64 * kTile;             // hi, lo [s][p]
+    static constexpr int kXw = kC + (kStates ? 0 : N / 64 * kTile);   // hi, lo [s][p]
     static constexpr int kS = kXw + 2 * kTile;                  // hi, lo [n][p], N rows each
-    static constexpr int kMisc = kS + 2 * N * 128;
+    static constexpr int kMisc = kS + (kStates ? 0 : 2 * N * 128);
+    static constexpr uint32_t kTmem = kStates ? 128 : 512;      // tensor-memory columns
+    static constexpr uint32_t kTdS = kStates ? 0 : 384;         // dS, the hi and the lo part's product side by side
 };
 
 // Decay factors of one chunk.  The log2-decays are added up as whole multiples
@@ -110,7 +117,7 @@ struct alignas(16) Gates {
 
 struct alignas(16) Misc {
     Gates gates[kGates];
-    unsigned long long x_full[kXStages], bc_full, z_full[2];    // copies have landed
+    unsigned long long x_full[3], bc_full, z_full[2];    // copies have landed
     unsigned long long gates_full[kGates];
     unsigned long long g_done, ds_done, y2_done, y1_done;       // products are complete
     unsigned long long ready, p_ready, chunk_done[2];           // the tile warps have written / read
@@ -121,15 +128,15 @@ struct alignas(16) Misc {
     uint32_t tmem;
     int abort;
 };
-template <int N>
-constexpr int scan_smem() { return Lay<N>::kMisc + static_cast<int>(sizeof(Misc)) + 1024; }
-static_assert(sizeof(Gates) % 16 == 0 && Lay<64>::kMisc % 16 == 0 && Lay<128>::kMisc % 16 == 0, "float4 accesses");
-static_assert(scan_smem<128>() <= 227 * 1024, "shared memory budget");
+template <int N, bool kStates>
+constexpr int scan_smem() { return Lay<N, kStates>::kMisc + static_cast<int>(sizeof(Misc)) + 1024; }
+static_assert(sizeof(Gates) % 16 == 0 && Lay<64, false>::kMisc % 16 == 0 && Lay<128, true>::kMisc % 16 == 0, "float4 accesses");
+static_assert(scan_smem<128, false>() <= 227 * 1024 && 2 * (scan_smem<128, true>() + 1024) <= 228 * 1024, "shared memory budget");
 
 // tensor-memory columns
 constexpr uint32_t kTG = 0;                      // G, then Pm in its place
 constexpr uint32_t kTY1 = 128;                   // two Y1 of 64
-constexpr uint32_t kTY2 = 256, kTdS = 384;       // Y2 and dS, the hi and the lo part's product side by side
+constexpr uint32_t kTY2 = 256;                   // Y2, the hi and the lo part's product side by side; then dS
 
 // ---- instructions -----------------------------------------------------------------
 
@@ -151,16 +158,6 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, 
         : "memory");
 }
 
-__device__ __forceinline__ void tm_ld32_nowait(uint32_t taddr, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-}
 __device__ __forceinline__ void tm_ld16_nowait(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -285,13 +282,15 @@ __device__ __forceinline__ void store_row32(T* p, const u64 (&x)[16]) {
 struct Work {
     int kind, seq, bos, len;                     // rows of the whole sequence
     int first, chunks;                           // chunks of this CTA
-    int seg, segs;                               // its segment's index in the sequence, and in the launch (its first)
+    int part, parts;                             // segments: the sequence's first part, and those before this CTA
     bool last;
 };
 
 // The whole-sequence form: sequence = blockIdx / units.  With segments, the
-// launch's segment index is looked up among the sequences' segment counts (one
-// warp, 32 sequences at a time; every warp does the same).
+// launch's index is looked up among the sequences' counts: of segments, or (the
+// states alone) of the parts before each sequence's last segment.  One warp, 32
+// sequences at a time; every warp does the same.
+template <bool kStates>
 __device__ Work find_work(const ScanParams& sp, int index, int lane) {
     const Params& p = sp.p;
     Work w = {};
@@ -311,7 +310,7 @@ __device__ Work find_work(const ScanParams& sp, int index, int lane) {
         w = {1, index, bos, eos - bos, 0, (eos - bos + kQ - 1) / kQ, 0, 0, true};
         return w;
     }
-    int base = 0;
+    int base = 0, part_base = 0;
     for (int i0 = 0; i0 < p.batch; i0 += 32) {
         const int i = i0 + lane;
         int bos = 0, eos = 0, n = 0;
@@ -320,35 +319,44 @@ __device__ Work find_work(const ScanParams& sp, int index, int lane) {
             if (f > 0 && blockIdx.x == 0 && threadIdx.x < 32) raise(p.status, f);
             if (f == -1) n = ((eos - bos + kQ - 1) / kQ + sp.seg_chunks - 1) / sp.seg_chunks;
         }
-        int upto = n;
+        const int parts = n > 0 ? (n - 1) * kParts : 0;
+        int upto = n, parts_upto = parts;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(kFull, upto, o);
-            if (lane >= o) upto += y;
+            const int x = __shfl_up_sync(kFull, upto, o), y = __shfl_up_sync(kFull, parts_upto, o);
+            if (lane >= o) upto += x, parts_upto += y;
         }
-        const unsigned hit = __ballot_sync(kFull, base + upto > index && base + upto - n <= index);
+        const int end = kStates ? part_base + parts_upto : base + upto, count = kStates ? parts : n;
+        const unsigned hit = __ballot_sync(kFull, end > index && end - count <= index);
         if (hit != 0) {
             const int src = __ffs(hit) - 1;
+            const int k = index - __shfl_sync(kFull, end - count, src);          // which of the sequence's
             w.kind = 1;
             w.seq = i0 + src;
             w.bos = __shfl_sync(kFull, bos, src);
             w.len = __shfl_sync(kFull, eos, src) - w.bos;
-            w.segs = __shfl_sync(kFull, base + upto - n, src);
-            w.seg = index - w.segs;
-            w.first = w.seg * sp.seg_chunks;
-            w.chunks = min(sp.seg_chunks, (w.len + kQ - 1) / kQ - w.first);
-            w.last = w.seg + 1 == __shfl_sync(kFull, n, src);
+            w.part = __shfl_sync(kFull, part_base + parts_upto - parts, src);
+            const int whole = (w.len + kQ - 1) / kQ, each = kStates ? sp.part_chunks : sp.seg_chunks;
+            w.first = k * each;
+            w.chunks = min(each, whole - w.first);
+            w.parts = kStates ? 0 : k * kParts;
+            w.last = k + 1 == __shfl_sync(kFull, n, src);
+            if (w.part + w.parts > sp.part_room) {               // offsets that overlap (more rows than there are)
+                if (threadIdx.x == 0) raise(p.status, GDN_FLAG_TOKEN_ROW);
+                w.kind = 0;
+            }
             return w;
         }
         base += __shfl_sync(kFull, upto, 31);
+        part_base += __shfl_sync(kFull, parts_upto, 31);
     }
     return w;
 }
 
 // kStates: the first launch over segments, which only computes what each adds to the state.
 template <typename StateT, int N, bool kStates>
-__global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_ssm_scan_kernel(const __grid_constant__ ScanParams sp) {
-    using L = Lay<N>;
+__global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates ? 2 : 1) gdn_ssm_scan_kernel(const __grid_constant__ ScanParams sp) {
+    using L = Lay<N, kStates>;
     const Params& p = sp.p;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* sm = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
@@ -361,15 +369,16 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
     const int col = h * p.P + pb * kPB;
     dep_wait();
     dep_launch();
-    const Work wk = find_work(sp, index, lane);
-    if (wk.kind == 0 || (kStates && wk.last)) return;            // (nothing follows the last segment)
+    const Work wk = find_work<kStates>(sp, index, lane);
+    if (wk.kind == 0) return;
 
     if (warp == kMma) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(saddr(&ms.tmem)));
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&ms.tmem)),
+                     "n"(L::kTmem));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
     if (tid == 0) {
-        for (int k = 0; k < kXStages; ++k) bar_init(&ms.x_full[k], 1);
+        for (int k = 0; k < L::kXStages; ++k) bar_init(&ms.x_full[k], 1);
         for (int k = 0; k < kGates; ++k) bar_init(&ms.gates_full[k], 1);
         bar_init(&ms.bc_full, 1);
         for (int k = 0; k < 2; ++k) {
@@ -446,7 +455,7 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
                 fence_after();
 #pragma unroll
                 for (int ks = 0; ks < kQ / 16; ++ks)
-                    mma_bf16(tm + kTdS, b_mn + ks * 128, xw_mn + ks * 128, id_ds, ks > 0);
+                    mma_bf16(tm + L::kTdS, b_mn + ks * 128, xw_mn + ks * 128, id_ds, ks > 0);
                 commit(saddr(&ms.ds_done));
                 if (!kStates) {
                     // the outputs of chunk c - 1 are made: Y2 has been read (so has Y1 of c - 2, before `ready`)
@@ -458,7 +467,7 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
                     commit(saddr(&ms.y2_done));
                     if (!need(&ms.p_ready, c)) break;
                     fence_after();
-                    const uint64_t x_mn = x_mn0 + c % kXStages * (L::kTile / 16);
+                    const uint64_t x_mn = x_mn0 + c % L::kXStages * (L::kTile / 16);
 #pragma unroll
                     for (int part = 0; part < 2; ++part)
 #pragma unroll
@@ -478,9 +487,9 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
         // ---- copies, each once what it overwrites has been read ----
         if (lane == 0) {
             auto load_x = [&](int c) {
-                unsigned long long* bar = &ms.x_full[c % kXStages];
+                unsigned long long* bar = &ms.x_full[c % L::kXStages];
                 bar_expect(bar, L::kTile);
-                tma_load(sbase + L::kX + c % kXStages * L::kTile, &sp.x, col, row0 + c * kQ, bar);
+                tma_load(sbase + L::kX + c % L::kXStages * L::kTile, &sp.x, col, row0 + c * kQ, bar);
             };
             auto load_bc = [&](int c) {
                 bar_expect(&ms.bc_full, (kStates ? 1 : 2) * (N / 64) * L::kTile);
@@ -500,13 +509,14 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
             if (!kStates && gated) load_z(0);
             int x_loads = wk.chunks > 1 ? 2 : 1, bc_loads = 1, z_loads = 1;
             for (int c = 0; c + 1 < wk.chunks; ++c) {
-                if (c + 2 < wk.chunks) {                         // into the stage of chunk c - 1
-                    if (c > 0 && !need(&ms.chunk_done[(c - 1) & 1], (c - 1) >> 1)) break;
+                if (kStates && !need(&ms.ds_done, c)) break;     // (so x of chunk c has been weighed)
+                if (c + 2 < wk.chunks) {                         // into the stage of chunk c - 1, or of c
+                    if (!kStates && c > 0 && !need(&ms.chunk_done[(c - 1) & 1], (c - 1) >> 1)) break;
                     load_x(c + 2);
                     ++x_loads;
                 }
                 if (!kStates && (!need(&ms.g_done, c) || !need(&ms.y2_done, c))) break;
-                if (!need(&ms.ds_done, c)) break;
+                if (!kStates && !need(&ms.ds_done, c)) break;
                 load_bc(c + 1);
                 ++bc_loads;
                 if (!kStates && gated) {
@@ -519,8 +529,8 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
             const int never = 0;
             bool landed = true;
 #pragma unroll 1
-            for (int k = 0; k < kXStages; ++k) {
-                const int n = (x_loads - k + kXStages - 1) / kXStages;       // copies into this stage
+            for (int k = 0; k < L::kXStages; ++k) {
+                const int n = (x_loads - k + L::kXStages - 1) / L::kXStages;       // copies into this stage
                 if (n > 0) landed &= wait(&ms.x_full[k], n - 1, 0, &never);
             }
             landed &= wait(&ms.bc_full, bc_loads - 1, 0, &never);
@@ -616,8 +626,8 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
                                32 * hh,
                            S);
             // segments: what lies before this one
-            for (int k = 0; k < wk.seg; ++k) {
-                const int64_t at = static_cast<int64_t>(wk.segs + k) * units + unit;
+            for (int k = 0; k < wk.parts; ++k) {
+                const int64_t at = static_cast<int64_t>(wk.part + k) * units + unit;
                 const u64 a2 = dup2(exp2f(ld(sp.part_decay + at)));
                 u64 x[16];
                 load_row32(sp.part + (at * N + row) * kPB + 32 * hh, x);
@@ -627,9 +637,9 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
         }
         // Xw of chunk c, and the rows past the sequence's end cleared
         auto weigh = [&](int c) {
-            if (!need_warp(&ms.gates_full[c % kGates], c / kGates) || !need_warp(&ms.x_full[c % kXStages], c / kXStages)) return;
+            if (!need_warp(&ms.gates_full[c % kGates], c / kGates) || !need_warp(&ms.x_full[c % L::kXStages], c / L::kXStages)) return;
             const int n = rows_of(c);
-            unsigned char* X = sm + L::kX + c % kXStages * L::kTile;
+            unsigned char* X = sm + L::kX + c % L::kXStages * L::kTile;
             const u64 w2 = dup2(ms.gates[c % kGates].w[row]);
             if (n < kQ) {
                 if (!need_warp(&ms.bc_full, c)) return;
@@ -687,8 +697,8 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     uint32_t x[16], y[16];
-                    tm_ld16_nowait(lanes + kTdS + 32 * hh + 16 * half, x);
-                    tm_ld16_nowait(lanes + kTdS + 64 + 32 * hh + 16 * half, y);
+                    tm_ld16_nowait(lanes + L::kTdS + 32 * hh + 16 * half, x);
+                    tm_ld16_nowait(lanes + L::kTdS + 64 + 32 * hh + 16 * half, y);
                     tm_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
@@ -860,7 +870,7 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, 1) gdn_s
     __syncthreads();
     fence_after();
     if (tid == 0 && *abort != 0) raise(p.status, GDN_FLAG_TIMEOUT);
-    if (warp == kMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tm));
+    if (warp == kMma) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tm), "n"(L::kTmem));
 }
 
 // ---- host side ----------------------------------------------------------------------
@@ -894,14 +904,14 @@ cudaError_t launch_kernel(const ScanParams& sp, int64_t ctas, cudaStream_t strea
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64 || !__atomic_load_n(&done[dev], __ATOMIC_ACQUIRE)) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, scan_smem<N>());
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, scan_smem<N, kStates>());
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) __atomic_store_n(&done[dev], true, __ATOMIC_RELEASE);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas), 1, 1);
     cfg.blockDim = dim3(kStates ? kStatesThreads : kSThreads, 1, 1);
-    cfg.dynamicSmemBytes = scan_smem<N>();
+    cfg.dynamicSmemBytes = scan_smem<N, kStates>();
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -923,7 +933,7 @@ int segment_chunks(int batch, int num_tokens, int units) {
     const double mean = static_cast<double>(chunks) / batch, longest = batch > 1 ? 2 * mean : mean;
     double best = std::max(longest + kStart, std::ceil(static_cast<double>(batch) * units / sms) * (mean + kStart));
     int take = 0;
-    for (int k = 1; k < longest && k <= 512; ++k) {
+    for (int k = kParts; k < longest && k <= 512; k += kParts) {
         const double ctas = (static_cast<double>(chunks) / k + (batch > 1 ? 0.5 * batch : 0.0)) * units;
         const double cost = (1 + kFirst) * std::ceil(std::ceil(ctas) / sms) * (k + kStart);
         if (cost < best) {
@@ -934,25 +944,30 @@ int segment_chunks(int batch, int num_tokens, int units) {
     return take;
 }
 
+// At most this many segments, and segments that are not a sequence's last.
 int64_t segment_room(int batch, int num_tokens, int chunks) {
     return static_cast<int64_t>(num_tokens) / (static_cast<int64_t>(chunks) * kQ) + batch;
+}
+int64_t part_room(int num_tokens, int chunks) {
+    return static_cast<int64_t>(num_tokens) / (static_cast<int64_t>(chunks) * kQ) * kParts;
 }
 
 template <typename StateT, int N>
 cudaError_t launch(ScanParams& sp, int units, void* workspace, cudaStream_t stream) {
     const Params& p = sp.p;
     sp.seg_chunks = segment_chunks(p.batch, p.num_tokens, units);
-    if (sp.seg_chunks == 0) {
-        sp.segs = p.batch;
-        return launch_kernel<StateT, N, false>(sp, static_cast<int64_t>(p.batch) * units, stream);
-    }
-    const int64_t room = segment_room(p.batch, p.num_tokens, sp.seg_chunks);
-    if (room * units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    sp.segs = static_cast<int32_t>(room);
+    if (sp.seg_chunks == 0) return launch_kernel<StateT, N, false>(sp, static_cast<int64_t>(p.batch) * units, stream);
+    sp.part_chunks = sp.seg_chunks / kParts;
+    const int64_t room = segment_room(p.batch, p.num_tokens, sp.seg_chunks), parts = part_room(p.num_tokens, sp.seg_chunks);
+    if (std::max(room, parts) * units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    sp.part_room = static_cast<int32_t>(parts);
     sp.part = static_cast<float*>(workspace);
-    sp.part_decay = sp.part + room * units * N * kPB;
-    const cudaError_t e = launch_kernel<StateT, N, true>(sp, room * units, stream);
-    return e != cudaSuccess ? e : launch_kernel<StateT, N, false>(sp, room * units, stream);
+    sp.part_decay = sp.part + parts * units * N * kPB;
+    if (parts > 0) {
+        const cudaError_t e = launch_kernel<StateT, N, true>(sp, parts * units, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_kernel<StateT, N, false>(sp, room * units, stream);
 }
 
 template <int N>
@@ -968,7 +983,7 @@ namespace gdn_ssm {
 
 int64_t prefill_workspace(int batch, int num_tokens, int units, int N) {
     const int chunks = segment_chunks(batch, num_tokens, units);
-    return chunks == 0 ? 0 : segment_room(batch, num_tokens, chunks) * units * (static_cast<int64_t>(N) * kPB + 1) * 4;
+    return chunks == 0 ? 0 : part_room(num_tokens, chunks) * units * (static_cast<int64_t>(N) * kPB + 1) * 4;
 }
 
 cudaError_t launch_prefill(const Params& p, int N, gdn_dtype state_dtype, void* workspace, cudaStream_t stream) {

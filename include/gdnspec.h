@@ -570,7 +570,8 @@ typedef struct {
  * Within a row the heads (groups) are contiguous; x, B and C may be views into
  * one packed row.  x, B, C, z, out and state_pool are 16-byte aligned and
  * x/B/C/z/out strides multiples of 8.  A head dim P > 64 runs as P / 64 column
- * blocks.  Caller contract and skips as for gdn_prefill.  An infinite or NaN
+ * blocks.  Caller contract and skips as for gdn_prefill; sequences do not
+ * overlap (cu_seqlens does not decrease).  An infinite or NaN
  * input spoils rows and the last state of its own sequence (rows shortly before
  * it among them: the products run over tiles of tokens), and no other's.
  */
