@@ -41,7 +41,7 @@
 //
 // With few (sequence, head) pairs the prompts are cut into segments: a first
 // launch computes what the tokens before the last segment add to the state (dS
-// alone: no G, Pm, Y1, Y2), by quarters of a segment, two CTAs an SM; the second
+// alone: no G, Pm, Y1, Y2), by parts of a segment, two CTAs an SM; the second
 // starts each segment from the initial state and the parts before it, which it
 // combines itself.
 #include <cuda.h>
@@ -68,7 +68,6 @@ constexpr int kPm = kWarps + 4;                  // the first that makes Pm (a m
 constexpr int kSThreads = 32 * (2 * kWarps + 4);
 constexpr int kStatesThreads = 32 * (kWarps + 3);
 constexpr int kGates = 3;                        // chunks whose decay factors are held
-constexpr int kParts = 4;                        // of a segment, in the first launch
 
 struct ScanParams {
     CUtensorMap x, B, C, z, out;                 // boxes of 64 elements x 128 rows
@@ -76,7 +75,7 @@ struct ScanParams {
     float* part;                                 // segments: [part][unit][N][64] what a part of one adds
     float* part_decay;                           // and its log2-decay, [part][unit]
     int32_t seg_chunks;                          // chunks of a segment (0: whole sequences)
-    int32_t part_chunks;                         // and of a part, a kParts-th
+    int32_t parts, part_chunks;                  // parts of a segment in the first launch, and their chunks
     int32_t part_room;                           // parts that the workspace holds
     uint32_t wait_limit;
 };
@@ -189,34 +188,22 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
         : "memory");
 }
 
-// Bounded wait for phase `use` of a barrier: blocking polls up to the default
-// bound, or non-blocking ones up to one set by gdn_set_wait_limit; gives up early
-// once another warp has.  (Kept small: there are some twenty of them, and with
-// the polls unrolled the kernel waited for its own instructions.)
-__device__ __forceinline__ bool poll(uint32_t addr, uint32_t parity, bool blocking) {
+// Bounded wait for phase `use` of a barrier: 2^17 polls that sleep up to 20 us each,
+// or, with a bound set by gdn_set_wait_limit, that many that do not sleep.  As few
+// instructions as it takes: there are some twenty waits in the five kinds of warps,
+// and what they add to the instruction stream shows (a bound by the clock and a look
+// at the other warps' state in each poll cost 15 % of the kernel's time).
+__device__ __forceinline__ bool wait(unsigned long long* bar, int use, uint32_t limit) {
     uint32_t done;
-    if (blocking)
-        asm volatile(
-            "{\n\t.reg .pred P;\n\tmbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2;\n\tselp.u32 %0, 1, 0, P;\n\t}"
-            : "=r"(done)
-            : "r"(addr), "r"(parity)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred P;\n\tmbarrier.test_wait.parity.shared::cta.b64 P, [%1], %2;\n\tselp.u32 %0, 1, 0, P;\n\t}"
-            : "=r"(done)
-            : "r"(addr), "r"(parity)
-            : "memory");
+    asm volatile(
+        "{\n\t.reg .pred P, Q;\n\t.reg .u32 n;\n\tmov.u32 n, %3;\n"
+        "POLL_%=:\n\tmbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2, %4;\n\t@P bra DONE_%=;\n\t"
+        "sub.u32 n, n, 1;\n\tsetp.ne.u32 Q, n, 0;\n\t@Q bra POLL_%=;\n"
+        "DONE_%=:\n\tselp.u32 %0, 1, 0, P;\n\t}"
+        : "=r"(done)
+        : "r"(saddr(bar)), "r"(use & 1), "r"(limit ? limit : 1u << 17), "r"(limit ? 0u : 20000u)
+        : "memory");
     return done != 0;
-}
-__device__ __forceinline__ bool wait(unsigned long long* bar, int use, uint32_t limit, const volatile int* abort) {
-    const uint32_t addr = saddr(bar), parity = use & 1, most = limit ? limit : kSpinLimit;
-#pragma unroll 1
-    for (uint32_t n = 0; n < most; ++n) {
-        if (poll(addr, parity, limit == 0)) return true;
-        if (*abort) return false;
-    }
-    return false;
 }
 
 // x as bf16 hi and lo words: lo = bf16(x - hi), the difference exact
@@ -319,7 +306,7 @@ __device__ Work find_work(const ScanParams& sp, int index, int lane) {
             if (f > 0 && blockIdx.x == 0 && threadIdx.x < 32) raise(p.status, f);
             if (f == -1) n = ((eos - bos + kQ - 1) / kQ + sp.seg_chunks - 1) / sp.seg_chunks;
         }
-        const int parts = n > 0 ? (n - 1) * kParts : 0;
+        const int parts = n > 0 ? (n - 1) * sp.parts : 0;
         int upto = n, parts_upto = parts;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -339,7 +326,7 @@ __device__ Work find_work(const ScanParams& sp, int index, int lane) {
             const int whole = (w.len + kQ - 1) / kQ, each = kStates ? sp.part_chunks : sp.seg_chunks;
             w.first = k * each;
             w.chunks = min(each, whole - w.first);
-            w.parts = kStates ? 0 : k * kParts;
+            w.parts = kStates ? 0 : k * sp.parts;
             w.last = k + 1 == __shfl_sync(kFull, n, src);
             if (w.part + w.parts > sp.part_room) {               // offsets that overlap (more rows than there are)
                 if (threadIdx.x == 0) raise(p.status, GDN_FLAG_TOKEN_ROW);
@@ -412,14 +399,14 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
     // waiter does after phase use.  need_warp: the whole warp takes one answer.
     bool ok = true;
     auto need = [&](unsigned long long* bar, int use) {
-        if (ok && !wait(bar, use, limit, abort)) {
+        if (ok && !wait(bar, use, limit)) {
             ok = false;
             *abort = 1;
         }
         return ok;
     };
     auto need_warp = [&](unsigned long long* bar, int use) {
-        if (ok && !__all_sync(kFull, wait(bar, use, limit, abort))) {
+        if (ok && !__all_sync(kFull, wait(bar, use, limit))) {
             ok = false;
             *abort = 1;
         }
@@ -479,8 +466,7 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
             // every product issued has to finish before tensor memory goes (with the default
             // bound; long complete, unless some warp gave up)
             commit(saddr(&ms.drain));
-            const int never = 0;
-            if (!wait(&ms.drain, 0, 0, &never)) raise(p.status, GDN_FLAG_DRAIN);
+            if (!wait(&ms.drain, 0, 0)) raise(p.status, GDN_FLAG_DRAIN);
         }
         __syncwarp();
     } else if (warp == kLoad) {
@@ -526,19 +512,18 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
                 }
             }
             // and every copy before shared memory goes
-            const int never = 0;
             bool landed = true;
 #pragma unroll 1
             for (int k = 0; k < L::kXStages; ++k) {
                 const int n = (x_loads - k + L::kXStages - 1) / L::kXStages;       // copies into this stage
-                if (n > 0) landed &= wait(&ms.x_full[k], n - 1, 0, &never);
+                if (n > 0) landed &= wait(&ms.x_full[k], n - 1, 0);
             }
-            landed &= wait(&ms.bc_full, bc_loads - 1, 0, &never);
+            landed &= wait(&ms.bc_full, bc_loads - 1, 0);
             if (!kStates && gated)
 #pragma unroll 1
                 for (int k = 0; k < 2; ++k) {
                     const int n = (z_loads - k + 1) / 2;
-                    if (n > 0) landed &= wait(&ms.z_full[k], n - 1, 0, &never);
+                    if (n > 0) landed &= wait(&ms.z_full[k], n - 1, 0);
                 }
             if (!landed) raise(p.status, GDN_FLAG_DRAIN);
         }
@@ -921,44 +906,56 @@ cudaError_t launch_kernel(const ScanParams& sp, int64_t ctas, cudaStream_t strea
     return cudaLaunchKernelEx(&cfg, kernel, sp);
 }
 
-// Chunks of a segment, 0 for whole sequences: whichever an estimate of the time,
-// in chunk times, says is shorter.  The host knows the rows and the sequences but
-// not their lengths; with several it takes the longest for twice the mean.  A
-// CTA costs kStart chunk times beside its chunks (its first copies, the state),
-// and the first launch over segments kFirst of the second.
-int segment_chunks(int batch, int num_tokens, int units) {
-    constexpr double kStart = 2.0, kFirst = 0.35;
+// How the prompts are cut: chunks of a segment (0: whole sequences) and parts of a
+// segment in the first launch, whichever an estimate of the time says is shorter.
+// The host knows the rows and the sequences but not their lengths; with several it
+// takes the longest for half as long again as the mean.  The estimate's constants, in us, are
+// measured: a chunk takes kChunk, or kAlone while every SM pair runs one CTA; a
+// chunk of the first launch kState with two CTAs an SM; a launch and a CTA's start
+// the rest.  (One prompt of 16384 tokens and 64 heads: 362 us whole, 299 cut at
+// 56 chunks; 4 of 1024 and 16 heads: 30.5 whole, 34.8 cut at 4.)
+struct Cut {
+    int chunks, parts;
+};
+Cut cut(int batch, int num_tokens, int units) {
+    constexpr double kChunk = 3.7, kAlone = 2.9, kState = 2.6, kLaunch = 6.0, kStart = 4.0, kStateStart = 5.0;
     const int sms = sm_count() ? sm_count() : 148;
-    const int64_t chunks = (static_cast<int64_t>(num_tokens) + kQ - 1) / kQ;
-    const double mean = static_cast<double>(chunks) / batch, longest = batch > 1 ? 2 * mean : mean;
-    double best = std::max(longest + kStart, std::ceil(static_cast<double>(batch) * units / sms) * (mean + kStart));
-    int take = 0;
-    for (int k = kParts; k < longest && k <= 512; k += kParts) {
-        const double ctas = (static_cast<double>(chunks) / k + (batch > 1 ? 0.5 * batch : 0.0)) * units;
-        const double cost = (1 + kFirst) * std::ceil(std::ceil(ctas) / sms) * (k + kStart);
-        if (cost < best) {
-            best = cost;
-            take = k;
+    const double chunks = static_cast<double>((static_cast<int64_t>(num_tokens) + kQ - 1) / kQ);
+    const double mean = chunks / batch, longest = batch > 1 ? 1.5 * mean : mean, whole = static_cast<double>(batch) * units;
+    double best = kLaunch + std::max(longest * (2 * whole <= sms ? kAlone : kChunk), std::ceil(whole / sms) * (mean * kChunk + kStart));
+    Cut take = {0, 1};
+    for (int parts = 1; parts <= 4; parts *= 2)
+        for (int k = parts; k < longest && k <= 512; k += parts) {
+            const double segments = batch > 1 ? chunks / k + 0.5 * batch : chunks / k;
+            const double before = batch > 1 ? std::max(chunks / k - 0.5 * batch, 0.0) : std::ceil(chunks / k) - 1;
+            const double ctas = segments * units;
+            const double cost = 2 * kLaunch + std::ceil(std::ceil(ctas) / sms) * (k * (2 * ctas <= sms ? kAlone : kChunk) + kStart) +
+                                std::ceil(std::ceil(before * parts * units) / (2 * sms)) * (k / parts * kState + kStateStart);
+            if (cost < best) {
+                best = cost;
+                take = {k, parts};
+            }
         }
-    }
     return take;
 }
 
-// At most this many segments, and segments that are not a sequence's last.
-int64_t segment_room(int batch, int num_tokens, int chunks) {
-    return static_cast<int64_t>(num_tokens) / (static_cast<int64_t>(chunks) * kQ) + batch;
+// At most this many segments, and parts of segments that are not a sequence's last.
+int64_t segment_room(int batch, int num_tokens, Cut c) {
+    return static_cast<int64_t>(num_tokens) / (static_cast<int64_t>(c.chunks) * kQ) + batch;
 }
-int64_t part_room(int num_tokens, int chunks) {
-    return static_cast<int64_t>(num_tokens) / (static_cast<int64_t>(chunks) * kQ) * kParts;
+int64_t part_room(int num_tokens, Cut c) {
+    return static_cast<int64_t>(num_tokens) / (static_cast<int64_t>(c.chunks) * kQ) * c.parts;
 }
 
 template <typename StateT, int N>
 cudaError_t launch(ScanParams& sp, int units, void* workspace, cudaStream_t stream) {
     const Params& p = sp.p;
-    sp.seg_chunks = segment_chunks(p.batch, p.num_tokens, units);
+    const Cut c = cut(p.batch, p.num_tokens, units);
+    sp.seg_chunks = c.chunks;
+    sp.parts = c.parts;
     if (sp.seg_chunks == 0) return launch_kernel<StateT, N, false>(sp, static_cast<int64_t>(p.batch) * units, stream);
-    sp.part_chunks = sp.seg_chunks / kParts;
-    const int64_t room = segment_room(p.batch, p.num_tokens, sp.seg_chunks), parts = part_room(p.num_tokens, sp.seg_chunks);
+    sp.part_chunks = c.chunks / c.parts;
+    const int64_t room = segment_room(p.batch, p.num_tokens, c), parts = part_room(p.num_tokens, c);
     if (std::max(room, parts) * units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     sp.part_room = static_cast<int32_t>(parts);
     sp.part = static_cast<float*>(workspace);
@@ -982,8 +979,8 @@ cudaError_t launch_n(ScanParams& sp, gdn_dtype t, int units, void* ws, cudaStrea
 namespace gdn_ssm {
 
 int64_t prefill_workspace(int batch, int num_tokens, int units, int N) {
-    const int chunks = segment_chunks(batch, num_tokens, units);
-    return chunks == 0 ? 0 : part_room(num_tokens, chunks) * units * (static_cast<int64_t>(N) * kPB + 1) * 4;
+    const Cut c = cut(batch, num_tokens, units);
+    return c.chunks == 0 ? 0 : part_room(num_tokens, c) * units * (static_cast<int64_t>(N) * kPB + 1) * 4;
 }
 
 cudaError_t launch_prefill(const Params& p, int N, gdn_dtype state_dtype, void* workspace, cudaStream_t stream) {

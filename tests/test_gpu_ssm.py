@@ -405,6 +405,38 @@ def test_scan_captured_beside_another_and_repeatable(cuda_device):
     assert torch.equal(_bits(a.out), _bits(want[0][0])) and torch.equal(_bits(b.pool), _bits(want[1][1]))
 
 
+@pytest.mark.parametrize("lens", [[700], [260, 90]])
+def test_scan_wait_that_runs_out_is_reported(cuda_device, lens):
+    """With a bound of one poll the tensor-core waits give up: a status bit and no state written, the GPU
+    stays usable, and the next call with the default bound is right."""
+    s = Scan(cuda_device, lens, 2, 1, 64, 128, "f32", seed=16)
+    before = s.pool.clone()
+    binding.set_wait_limit(1)
+    try:
+        s.run()
+    finally:
+        binding.set_wait_limit(0)
+    assert int(s.status) & binding.GDN_FLAG_TIMEOUT and not int(s.status) & binding.GDN_FLAG_DRAIN
+    assert torch.equal(_bits(s.pool), _bits(before))
+    s.status.zero_()
+    s.run()
+    s.check(before)
+    assert int(s.status) == 0
+
+
+def test_scan_of_overlapping_offsets_stays_inside_its_memory(cuda_device):
+    """Offsets that go back (against the caller contract) claim more rows than there are: nothing outside the
+    rows and slots is touched, and every output row is finite."""
+    s = Scan(cuda_device, [3000], 2, 1, 64, 64, "f32", seed=17)
+    pool = torch.zeros(12, 2, 64, 64, device=cuda_device)
+    n = 9
+    cu = _i32([0, 3000, 0, 10, 3000, 0, 20, 3000, 0, 3000], cuda_device)
+    gdn.gdn_ssm_prefill(s.x, s.B, s.C, s.dt, s.z, s.A_log, s.dt_bias, s.D, pool, _i32([-1] * n, cuda_device),
+                        _i32(list(range(n)), cuda_device), cu, s.out, status=s.status)
+    torch.cuda.synchronize()
+    assert torch.isfinite(s.out.float()).all() and (pool[9:] == 0).all()
+
+
 # ---- the step -------------------------------------------------------------------
 
 
