@@ -29,7 +29,6 @@ inline int sm_count() {
 }
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr float kSoftplusThreshold = 20.0f;                    // softplus(x) = x above this
 
 // Programmatic dependent launch.  A kernel launched with it may start while its
 // predecessor on the stream still runs: it waits (dep_wait) until that has
@@ -56,7 +55,23 @@ __device__ __forceinline__ void raise(int32_t* status, int flag) {
     if (status != nullptr) atomicOr(status, flag);
 }
 
-__device__ __forceinline__ float softplus(float x) { return x > kSoftplusThreshold ? x : log1pf(expf(x)); }
+// log(1 + e^x) = max(x, 0) + log(1 + u), u = e^-|x| <= 1, and log(1 + u) = 2 atanh(s)
+// = 2 s (1 + s^2 / 3 + s^4 / 5 + ...), s = u / (2 + u) <= 1/3: nine terms leave less
+// than 2^-30 of the value.
+__device__ __forceinline__ float softplus(float x) {
+    const float u = expf(-fabsf(x));
+    const float s = __fdividef(u, 2.0f + u), q = s * s;
+    float p = 1.0f / 17.0f;
+    p = fmaf(p, q, 1.0f / 15.0f);
+    p = fmaf(p, q, 1.0f / 13.0f);
+    p = fmaf(p, q, 1.0f / 11.0f);
+    p = fmaf(p, q, 1.0f / 9.0f);
+    p = fmaf(p, q, 1.0f / 7.0f);
+    p = fmaf(p, q, 1.0f / 5.0f);
+    p = fmaf(p, q, 1.0f / 3.0f);
+    p = fmaf(p, q, 1.0f);
+    return fmaxf(x, 0.0f) + 2.0f * s * p;
+}
 
 // silu(z) = z sigmoid(z); for very negative z the denominator overflows and
 // the fast division returns zero

@@ -104,8 +104,8 @@ struct Lay {
 // of 2^-10, and the difference of two neighbours, whose weight is near 1, would
 // be off by as much.
 struct alignas(16) Gates {
-    float l[kQ];       // running sum of the log2-decays,
-    float l_lo[kQ];    // and what rounding it to FP32 left
+    float l[kQ];       // running sum of the log2-decays: its multiple of 1/16,
+    float l_lo[kQ];    // and the rest
     float f[kQ];       // 2^(l at the end of the token's block of 32 - l_t) d_t
     float e[kQ];       // 2^(l_t)
     float w[kQ];       // 2^(l_last - l_t) d_t
@@ -122,8 +122,6 @@ struct alignas(16) Misc {
     unsigned long long ready, p_ready, chunk_done[2];           // the tile warps have written / read
     unsigned long long z_free[2];                               // the outputs have left their buffer
     unsigned long long drain;
-    long long log_decay[kQ];                                    // the gate warp's own
-    float step[kQ];
     uint32_t tmem;
     int abort;
 };
@@ -148,13 +146,35 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t mn) {
 }
 constexpr uint32_t kAMn = 1u << 15, kBMn = 1u << 16;            // instruction descriptor: MN-major A, B
 
-// A from tensor memory
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+// Products and their completion, by the lane that leads.  The whole warp runs up to
+// each instruction, so that the compiler keeps the descriptors in uniform registers
+// (with one lane alone in the loop every product took twice the instructions).
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t lead) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(acc)
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
         : "memory");
+}
+// A from tensor memory
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(acc), "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ void commit_to(unsigned long long* bar, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(saddr(bar)),
+        "r"(lead)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t elect() {
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes;
 }
 
 __device__ __forceinline__ void tm_ld16_nowait(uint32_t taddr, uint32_t (&r)[16]) {
@@ -205,6 +225,20 @@ __device__ __forceinline__ bool wait(unsigned long long* bar, int use, uint32_t 
         : "memory");
     return done != 0;
 }
+
+// Whole multiples of 2^-32 (below 2^18 in size): from a float above -2048; their
+// multiple of 1/16, exact in FP32, and the rest; and their value.  Through 32-bit
+// conversions: the 64-bit ones run on a slow pipe.
+__device__ __forceinline__ long long to_units(float x) {
+    const int a = __float2int_rn(x * 16.0f);
+    const int b = __float2int_rn((x - static_cast<float>(a) * 0.0625f) * 4294967296.0f);
+    return (static_cast<long long>(a) << 28) + b;
+}
+__device__ __forceinline__ float units_hi(long long v) { return static_cast<float>(static_cast<int>(v >> 28)) * 0.0625f; }
+__device__ __forceinline__ float units_lo(long long v) {
+    return static_cast<float>(static_cast<int>(v & 0x0fffffff)) * (1.0f / 4294967296.0f);
+}
+__device__ __forceinline__ float from_units(long long v) { return units_hi(v) + units_lo(v); }
 
 // x as bf16 hi and lo words: lo = bf16(x - hi), the difference exact
 __device__ __forceinline__ void split_pair(u64 x, uint32_t& hi, uint32_t& lo) {
@@ -415,7 +449,8 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
 
     if (warp == kMma) {
         // ---- products ----
-        if (lane == 0) {
+        {
+            const uint32_t lead = elect();
             constexpr uint32_t id_g = (1u << 4) | (1u << 7) | (1u << 10) | (128u >> 3 << 17) | (128u >> 4 << 24);
             constexpr uint32_t id_y2 = id_g | kBMn, id_ds = id_g | kAMn | kBMn;
             constexpr uint32_t id_y1 = (1u << 4) | (1u << 7) | (1u << 10) | (64u >> 3 << 17) | (128u >> 4 << 24) | kBMn;
@@ -426,47 +461,47 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
             const uint64_t s_mn = desc_mn(sbase + L::kS, N * 128), x_mn0 = desc_mn(sbase + L::kX, L::kTile);
             for (int c = 0; c < wk.chunks; ++c) {
                 const bool tail = rows_of(c) < kQ;               // its rows past the end are cleared before any product
-                if (!need(&ms.bc_full, c)) break;
-                if (tail && !need(&ms.ready, c)) break;
+                if (!need_warp(&ms.bc_full, c)) break;
+                if (tail && !need_warp(&ms.ready, c)) break;
                 fence_after();
                 if (!kStates) {
-                    if (c > 0 && !need(&ms.y1_done, c - 1)) break;               // Pm has been used
+                    if (c > 0 && !need_warp(&ms.y1_done, c - 1)) break;               // Pm has been used
 #pragma unroll
                     for (int ks = 0; ks < N / 16; ++ks) {
                         const uint64_t o = (ks >> 2) * (L::kTile / 16) + (ks & 3) * 2;
-                        mma_bf16(tm + kTG, c_km + o, b_km + o, id_g, ks > 0);
+                        mma_ss(tm + kTG, c_km + o, b_km + o, id_g, ks > 0, lead);
                     }
-                    commit(saddr(&ms.g_done));
+                    commit_to(&ms.g_done, lead);
                 }
-                if (!tail && !need(&ms.ready, c)) break;
+                if (!tail && !need_warp(&ms.ready, c)) break;
                 fence_after();
 #pragma unroll
                 for (int ks = 0; ks < kQ / 16; ++ks)
-                    mma_bf16(tm + L::kTdS, b_mn + ks * 128, xw_mn + ks * 128, id_ds, ks > 0);
-                commit(saddr(&ms.ds_done));
+                    mma_ss(tm + L::kTdS, b_mn + ks * 128, xw_mn + ks * 128, id_ds, ks > 0, lead);
+                commit_to(&ms.ds_done, lead);
                 if (!kStates) {
                     // the outputs of chunk c - 1 are made: Y2 has been read (so has Y1 of c - 2, before `ready`)
-                    if (c > 0 && !need(&ms.chunk_done[(c - 1) & 1], (c - 1) >> 1)) break;
+                    if (c > 0 && !need_warp(&ms.chunk_done[(c - 1) & 1], (c - 1) >> 1)) break;
                     fence_after();
 #pragma unroll
                     for (int ks = 0; ks < N / 16; ++ks)
-                        mma_bf16(tm + kTY2, c_km + (ks >> 2) * (L::kTile / 16) + (ks & 3) * 2, s_mn + ks * 128, id_y2, ks > 0);
-                    commit(saddr(&ms.y2_done));
-                    if (!need(&ms.p_ready, c)) break;
+                        mma_ss(tm + kTY2, c_km + (ks >> 2) * (L::kTile / 16) + (ks & 3) * 2, s_mn + ks * 128, id_y2, ks > 0, lead);
+                    commit_to(&ms.y2_done, lead);
+                    if (!need_warp(&ms.p_ready, c)) break;
                     fence_after();
                     const uint64_t x_mn = x_mn0 + c % L::kXStages * (L::kTile / 16);
 #pragma unroll
                     for (int part = 0; part < 2; ++part)
 #pragma unroll
                         for (int ks = 0; ks < kQ / 16; ++ks)
-                            mma_bf16_ts(tm + kTY1 + (c & 1) * 64, tm + kTG + ks * 16 + part * 8, x_mn + ks * 128, id_y1, part + ks > 0);
-                    commit(saddr(&ms.y1_done));
+                            mma_ts(tm + kTY1 + (c & 1) * 64, tm + kTG + ks * 16 + part * 8, x_mn + ks * 128, id_y1, part + ks > 0, lead);
+                    commit_to(&ms.y1_done, lead);
                 }
             }
             // every product issued has to finish before tensor memory goes (with the default
             // bound; long complete, unless some warp gave up)
-            commit(saddr(&ms.drain));
-            if (!wait(&ms.drain, 0, 0)) raise(p.status, GDN_FLAG_DRAIN);
+            commit_to(&ms.drain, lead);
+            if (!wait(&ms.drain, 0, 0) && lead) raise(p.status, GDN_FLAG_DRAIN);
         }
         __syncwarp();
     } else if (warp == kLoad) {
@@ -531,35 +566,25 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
     } else if (warp == kGate) {
         // ---- decay factors ----
         const float rate = -expf(ld(p.A_log + h)) * kLog2e, bias = __bfloat162float(p.dt_bias[h]);
-        __nv_bfloat16 raw[4];                                    // dt of tokens lane, lane + 32, ..
+        __nv_bfloat16 raw[4] = {};                               // dt of four neighbouring tokens
         auto fetch = [&](int c) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const int t = 32 * k + lane;
+                const int t = 4 * lane + k;
                 if (t < rows_of(c)) raw[k] = p.dt[(static_cast<int64_t>(row0) + c * kQ + t) * p.dt_stride + h];
             }
         };
         fetch(0);
         for (int c = 0; c < wk.chunks; ++c) {
             const int n = rows_of(c);
-            __syncwarp();
-#pragma unroll 1
-            for (int t = lane; t < kQ; t += 32) {
-                const float d = t < n ? softplus(__bfloat162float(raw[0]) + bias) : 0.f;
-                ms.step[t] = d;
-                ms.log_decay[t] = __float2ll_rn(fmaxf(rate * d, -1048576.0f) * 4294967296.0f);   // 2^-(2^20) is 0 as it is
-                raw[0] = raw[1];
-                raw[1] = raw[2];
-                raw[2] = raw[3];
+            float d[4];
+            long long l[4], up = 0;                              // sums up to and with a token
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                d[k] = 4 * lane + k < n ? softplus(__bfloat162float(raw[k]) + bias) : 0.f;
+                l[k] = up += to_units(fmaxf(rate * d[k], -2048.0f));   // 2^-2048 is 0 as it is
             }
             if (c + 1 < wk.chunks) fetch(c + 1);
-            __syncwarp();
-            // four tokens a lane; l: sums up to and with a token
-            const float4 dv = *reinterpret_cast<const float4*>(ms.step + 4 * lane);
-            const float d[4] = {dv.x, dv.y, dv.z, dv.w};
-            const longlong2 la0 = *reinterpret_cast<const longlong2*>(ms.log_decay + 4 * lane);
-            const longlong2 la1 = *reinterpret_cast<const longlong2*>(ms.log_decay + 4 * lane + 2);
-            long long l[4] = {la0.x, la0.x + la0.y, la0.x + la0.y + la1.x, la0.x + la0.y + la1.x + la1.y}, up = l[3];
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const long long a = __shfl_up_sync(kFull, up, o);
@@ -567,17 +592,15 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
             }
             const long long before = up - l[3];
             const long long all = __shfl_sync(kFull, up, 31), block_end = __shfl_sync(kFull, up, lane | 7);
-            auto real = [](long long v) { return __ll2float_rn(v) * (1.0f / 4294967296.0f); };
             float hi[4], lo[4], f[4], e[4], w[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 l[k] += before;
-                const float units_hi = __ll2float_rn(l[k]);
-                hi[k] = units_hi * (1.0f / 4294967296.0f);
-                lo[k] = real(l[k] - __float2ll_rn(units_hi));
-                f[k] = ex2(real(block_end - l[k])) * d[k];
-                e[k] = ex2(hi[k]);
-                w[k] = ex2(real(all - l[k])) * d[k];
+                hi[k] = units_hi(l[k]);
+                lo[k] = units_lo(l[k]);
+                f[k] = ex2(from_units(block_end - l[k])) * d[k];
+                e[k] = ex2(hi[k] + lo[k]);
+                w[k] = ex2(from_units(all - l[k])) * d[k];
             }
             if (c >= kGates && !need_warp(&ms.chunk_done[(c - kGates) & 1], (c - kGates) >> 1)) break;   // the buffer's last readers
             Gates& gt = ms.gates[c % kGates];
@@ -588,8 +611,8 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
             *reinterpret_cast<float4*>(gt.w + 4 * lane) = make_float4(w[0], w[1], w[2], w[3]);
             *reinterpret_cast<float4*>(gt.d + 4 * lane) = make_float4(d[0], d[1], d[2], d[3]);
             if (lane == 0) {
-                gt.total = ex2(real(all));
-                gt.total_log = real(all);
+                gt.total = ex2(from_units(all));
+                gt.total_log = from_units(all);
             }
             __syncwarp();
             if (lane == 0) bar_arrive(&ms.gates_full[c % kGates]);
@@ -639,7 +662,7 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
                     }
                 }
             }
-#pragma unroll
+#pragma unroll 1
             for (int j = 0; j < 4; ++j) {
                 const uint32_t at = unit16(row, 4 * hh + j);
                 const uint4 v = *reinterpret_cast<const uint4*>(X + at);
