@@ -41,9 +41,10 @@
 //
 // With few (sequence, head) pairs the prompts are cut into segments: a first
 // launch computes what the tokens before the last segment add to the state (dS
-// alone: no G, Pm, Y1, Y2), by parts of a segment, two CTAs an SM; the second
-// starts each segment from the initial state and the parts before it, which it
-// combines itself.
+// alone: no G, Pm, Y1, Y2), by parts of a segment, two CTAs an SM, and copies the
+// initial state; the second starts each segment from that copy and the parts
+// before it, which it combines itself (it does not read the slot: the sequence's
+// last segment may be writing it).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -68,15 +69,16 @@ constexpr int kPm = kWarps + 4;                  // the first that makes Pm (a m
 constexpr int kSThreads = 32 * (2 * kWarps + 4);
 constexpr int kStatesThreads = 32 * (kWarps + 3);
 constexpr int kGates = 3;                        // chunks whose decay factors are held
+constexpr float kLost = 1.0f;                    // no log2-decay: those are not positive
 
 struct ScanParams {
     CUtensorMap x, B, C, z, out;                 // boxes of 64 elements x 128 rows
     Params p;
     float* part;                                 // segments: [part][unit][N][64] what a part of one adds
-    float* part_decay;                           // and its log2-decay, [part][unit]
+    float* part_decay;                           // and its log2-decay, [part][unit] (kLost: it was given up)
     int32_t seg_chunks;                          // chunks of a segment (0: whole sequences)
     int32_t parts, part_chunks;                  // parts of a segment in the first launch, and their chunks
-    int32_t part_room;                           // parts that the workspace holds
+    int32_t part_room;                           // parts that the workspace holds, initial states among them
     uint32_t wait_limit;
 };
 
@@ -303,14 +305,15 @@ __device__ __forceinline__ void store_row32(T* p, const u64 (&x)[16]) {
 struct Work {
     int kind, seq, bos, len;                     // rows of the whole sequence
     int first, chunks;                           // chunks of this CTA
-    int part, parts;                             // segments: the sequence's first part, and those before this CTA
+    int part, parts;                             // segments: the part to write, or the first to start from and their number
     bool last;
 };
 
 // The whole-sequence form: sequence = blockIdx / units.  With segments, the
 // launch's index is looked up among the sequences' counts: of segments, or (the
-// states alone) of the parts before each sequence's last segment.  One warp, 32
-// sequences at a time; every warp does the same.
+// states alone) of the parts before each sequence's last segment.  In the
+// workspace a sequence of several segments has its initial state, then those
+// parts.  One warp, 32 sequences at a time; every warp does the same.
 template <bool kStates>
 __device__ Work find_work(const ScanParams& sp, int index, int lane) {
     const Params& p = sp.p;
@@ -331,7 +334,7 @@ __device__ Work find_work(const ScanParams& sp, int index, int lane) {
         w = {1, index, bos, eos - bos, 0, (eos - bos + kQ - 1) / kQ, 0, 0, true};
         return w;
     }
-    int base = 0, part_base = 0;
+    int base = 0, room_base = 0;
     for (int i0 = 0; i0 < p.batch; i0 += 32) {
         const int i = i0 + lane;
         int bos = 0, eos = 0, n = 0;
@@ -340,14 +343,15 @@ __device__ Work find_work(const ScanParams& sp, int index, int lane) {
             if (f > 0 && blockIdx.x == 0 && threadIdx.x < 32) raise(p.status, f);
             if (f == -1) n = ((eos - bos + kQ - 1) / kQ + sp.seg_chunks - 1) / sp.seg_chunks;
         }
-        const int parts = n > 0 ? (n - 1) * sp.parts : 0;
-        int upto = n, parts_upto = parts;
+        const int parts = n > 0 ? (n - 1) * sp.parts : 0, count = kStates ? parts : n;
+        const int room = parts > 0 ? parts + 1 : 0;
+        int upto = count, room_upto = room;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(kFull, upto, o), y = __shfl_up_sync(kFull, parts_upto, o);
-            if (lane >= o) upto += x, parts_upto += y;
+            const int x = __shfl_up_sync(kFull, upto, o), y = __shfl_up_sync(kFull, room_upto, o);
+            if (lane >= o) upto += x, room_upto += y;
         }
-        const int end = kStates ? part_base + parts_upto : base + upto, count = kStates ? parts : n;
+        const int end = base + upto;
         const unsigned hit = __ballot_sync(kFull, end > index && end - count <= index);
         if (hit != 0) {
             const int src = __ffs(hit) - 1;
@@ -356,20 +360,22 @@ __device__ Work find_work(const ScanParams& sp, int index, int lane) {
             w.seq = i0 + src;
             w.bos = __shfl_sync(kFull, bos, src);
             w.len = __shfl_sync(kFull, eos, src) - w.bos;
-            w.part = __shfl_sync(kFull, part_base + parts_upto - parts, src);
+            w.part = __shfl_sync(kFull, room_base + room_upto - room, src) + (kStates ? 1 + k : 0);
             const int whole = (w.len + kQ - 1) / kQ, each = kStates ? sp.part_chunks : sp.seg_chunks;
             w.first = k * each;
             w.chunks = min(each, whole - w.first);
-            w.parts = kStates ? 0 : k * sp.parts;
-            w.last = k + 1 == __shfl_sync(kFull, n, src);
-            if (w.part + w.parts > sp.part_room) {               // offsets that overlap (more rows than there are)
+            const int segments = __shfl_sync(kFull, n, src);
+            w.parts = kStates ? 1 : segments > 1 ? 1 + k * sp.parts : 0;
+            w.last = k + 1 == segments;
+            if (w.part < 0 || w.parts > sp.part_room || w.part > sp.part_room - w.parts) {
+                // offsets that overlap (more rows than there are)
                 if (threadIdx.x == 0) raise(p.status, GDN_FLAG_TOKEN_ROW);
                 w.kind = 0;
             }
             return w;
         }
         base += __shfl_sync(kFull, upto, 31);
-        part_base += __shfl_sync(kFull, parts_upto, 31);
+        room_base += __shfl_sync(kFull, room_upto, 31);
     }
     return w;
 }
@@ -627,16 +633,33 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
 #pragma unroll
         for (int j = 0; j < 16; ++j) S[j] = 0;
         float run_log = 0.f;
-        if (!kStates && state_row) {
+        auto part_at = [&](int part) { return static_cast<int64_t>(part) * units + unit; };
+        if (state_row && (kStates ? wk.first == 0 : wk.parts == 0)) {
             const long long rs = ld(p.read_slots + wk.seq);
             if (rs >= 0)
                 load_row32(static_cast<const StateT*>(p.pool) + ((rs * p.H + h) * N + row) * static_cast<int64_t>(p.P) + pb * kPB +
                                32 * hh,
                            S);
-            // segments: what lies before this one
+        }
+        if (kStates && wk.first == 0 && state_row) {             // the initial state, kept for the second launch
+            const int64_t at = part_at(wk.part - 1);
+            store_row32(sp.part + (at * N + row) * kPB + 32 * hh, S);
+            if (row == 0 && hh == 0) sp.part_decay[at] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) S[j] = 0;
+        }
+        if (!kStates) {
+            // segments: the initial state, and what lies before this one
             for (int k = 0; k < wk.parts; ++k) {
-                const int64_t at = static_cast<int64_t>(wk.part + k) * units + unit;
-                const u64 a2 = dup2(exp2f(ld(sp.part_decay + at)));
+                const int64_t at = part_at(wk.part + k);
+                const float decay = ld(sp.part_decay + at);
+                if (decay == kLost) {
+                    ok = false;
+                    *abort = 1;
+                    break;
+                }
+                if (!state_row) continue;
+                const u64 a2 = dup2(exp2f(decay));
                 u64 x[16];
                 load_row32(sp.part + (at * N + row) * kPB + 32 * hh, x);
 #pragma unroll
@@ -769,12 +792,12 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
         // what this CTA leaves, unless a warp gave up: its segment's part, or the sequence's last
         // state, rounded once
         asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
-        if (*abort == 0 && state_row) {
-            if (kStates) {
-                const int64_t at = static_cast<int64_t>(index) * units + unit;
-                store_row32(sp.part + (at * N + row) * kPB + 32 * hh, S);
-                if (row == 0 && hh == 0) sp.part_decay[at] = run_log;
-            } else if (wk.last) {
+        if (kStates) {
+            const int64_t at = part_at(wk.part);
+            if (state_row) store_row32(sp.part + (at * N + row) * kPB + 32 * hh, S);
+            if (tid == 0) sp.part_decay[at] = *abort == 0 ? run_log : kLost;
+        } else if (*abort == 0 && state_row) {
+            if (wk.last) {
                 const long long ws = ld(p.write_slots + wk.seq);
                 if (ws >= 0)
                     store_row32(static_cast<StateT*>(p.pool) + ((ws * p.H + h) * N + row) * static_cast<int64_t>(p.P) + pb * kPB +
@@ -962,12 +985,12 @@ Cut cut(int batch, int num_tokens, int units) {
     return take;
 }
 
-// At most this many segments, and parts of segments that are not a sequence's last.
-int64_t segment_room(int batch, int num_tokens, Cut c) {
-    return static_cast<int64_t>(num_tokens) / (static_cast<int64_t>(c.chunks) * kQ) + batch;
-}
-int64_t part_room(int num_tokens, Cut c) {
-    return static_cast<int64_t>(num_tokens) / (static_cast<int64_t>(c.chunks) * kQ) * c.parts;
+// At most this many segments that are not a sequence's last; and what the workspace
+// holds: their parts, and an initial state for each sequence that has some.
+int64_t segments_before(int num_tokens, Cut c) { return num_tokens / (static_cast<int64_t>(c.chunks) * kQ); }
+int64_t part_room(int batch, int num_tokens, Cut c) {
+    const int64_t n = segments_before(num_tokens, c);
+    return n * c.parts + std::min<int64_t>(n, batch);
 }
 
 template <typename StateT, int N>
@@ -978,16 +1001,16 @@ cudaError_t launch(ScanParams& sp, int units, void* workspace, cudaStream_t stre
     sp.parts = c.parts;
     if (sp.seg_chunks == 0) return launch_kernel<StateT, N, false>(sp, static_cast<int64_t>(p.batch) * units, stream);
     sp.part_chunks = c.chunks / c.parts;
-    const int64_t room = segment_room(p.batch, p.num_tokens, c), parts = part_room(p.num_tokens, c);
-    if (std::max(room, parts) * units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    sp.part_room = static_cast<int32_t>(parts);
+    const int64_t before = segments_before(p.num_tokens, c), room = part_room(p.batch, p.num_tokens, c);
+    if (std::max(before + p.batch, before * c.parts) * units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    sp.part_room = static_cast<int32_t>(room);
     sp.part = static_cast<float*>(workspace);
-    sp.part_decay = sp.part + parts * units * N * kPB;
-    if (parts > 0) {
-        const cudaError_t e = launch_kernel<StateT, N, true>(sp, parts * units, stream);
+    sp.part_decay = sp.part + room * units * N * kPB;
+    if (before > 0) {
+        const cudaError_t e = launch_kernel<StateT, N, true>(sp, before * c.parts * units, stream);
         if (e != cudaSuccess) return e;
     }
-    return launch_kernel<StateT, N, false>(sp, room * units, stream);
+    return launch_kernel<StateT, N, false>(sp, (before + p.batch) * units, stream);
 }
 
 template <int N>
@@ -1003,7 +1026,7 @@ namespace gdn_ssm {
 
 int64_t prefill_workspace(int batch, int num_tokens, int units, int N) {
     const Cut c = cut(batch, num_tokens, units);
-    return c.chunks == 0 ? 0 : part_room(num_tokens, c) * units * (static_cast<int64_t>(N) * kPB + 1) * 4;
+    return c.chunks == 0 ? 0 : part_room(batch, num_tokens, c) * units * (static_cast<int64_t>(N) * kPB + 1) * 4;
 }
 
 cudaError_t launch_prefill(const Params& p, int N, gdn_dtype state_dtype, void* workspace, cudaStream_t stream) {

@@ -23,7 +23,7 @@ import pytest
 import torch
 
 import gated_deltanet_linear_sm_gb300 as gdn
-from gated_deltanet_linear_sm_gb300 import binding
+from gated_deltanet_linear_sm_gb300 import binding, ops
 from tests import ops_ref
 
 pytestmark = pytest.mark.gpu
@@ -336,6 +336,27 @@ def test_scan_in_chunks_and_in_place(cuda_device):
     before = whole.pool.clone()
     whole.out, whole.pool = out, torch.cat([before[:1], pool[:1], before[2:]])
     whole.check(before)
+
+
+@pytest.mark.parametrize("state", ["f32", "f16"])
+def test_scan_of_cut_prompts_in_place(cuda_device, state):
+    """Prompts long enough to be cut into segments, their slots updated in place: the bits of the same prompts
+    whose states go to other slots (a segment never reads a slot that the sequence's last one may have written)."""
+    lens = [1900, 40, 1300, 700]
+    a = Scan(cuda_device, lens, 3, 1, 64, 128, state, seed=18, read=[0, 2, -1, 6])
+    b = Scan(cuda_device, lens, 3, 1, 64, 128, state, seed=18, read=[0, 2, -1, 6])
+    a.write, b.write = [1, 3, 5, 7], [0, 2, 5, 6]
+    d = ops._ssm_dims(4, a.N, 3, 1, 64, 128, a.pool, a.dt, a.z, a.out)
+    assert gdn.ssm_prefill_workspace(d, cuda_device) > 0                # they are cut
+    before = a.pool.clone()
+    a.run()
+    a.check(before)
+    for _ in range(5):
+        b.pool.copy_(before)
+        b.run()
+        assert torch.equal(_bits(a.out), _bits(b.out))
+        for i in range(4):
+            assert torch.equal(_bits(a.pool[a.write[i]]), _bits(b.pool[b.write[i]]))
 
 
 def test_scan_keeps_infinite_and_nan_rows_to_their_sequence(cuda_device):
