@@ -13,6 +13,7 @@
 namespace gdn_common {
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+constexpr int32_t kMaxRows = 1 << 30;            // of a call: a row number plus a tile's rows stays in 32 bits
 inline bool is_dtype(gdn_dtype t) { return t == GDN_F32 || t == GDN_BF16 || t == GDN_F16; }
 
 // SMs of the current device (asked once per device; 0 if that fails)
@@ -33,10 +34,10 @@ constexpr unsigned kFull = 0xffffffffu;
 // Programmatic dependent launch.  A kernel launched with it may start while its
 // predecessor on the stream still runs: it waits (dep_wait) until that has
 // completed before it touches memory, and after that wait it may let its own
-// successor start (dep_launch).  The kernels here that write the tables which
-// every step reads (gdn_verify_drafts, gdn_step_tables) do not call dep_launch,
-// so their successor starts when they have completed: it may then read tables
-// before any wait of its own.
+// successor start (dep_launch).  The kernels here that write what the steps read
+// through __ldg (gdn_verify_drafts and gdn_step_tables the tables, gdn_conv_prefill
+// conv slots) do not call dep_launch, so their successor starts when they have
+// completed: it may then read those before any wait of its own.
 __device__ __forceinline__ void dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 

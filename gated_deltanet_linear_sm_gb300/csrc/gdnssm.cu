@@ -23,6 +23,8 @@ namespace {
 // first W - 1 rows of a sequence always belong to the run that holds its first
 // row: that run alone reads the sequence's slot, and writes the new one after
 // it, so a slot may be updated in place.  HBM bandwidth bounds it.
+// (No early start of the next kernel: the step reads conv slots through __ldg,
+// which may run before its wait.)
 
 constexpr int kCThreads = 128;                      // at most
 
@@ -74,7 +76,6 @@ __global__ void __launch_bounds__(kCThreads, 4) gdn_conv_prefill_kernel(const Co
     constexpr int U = 4, kAhead = 3, kRing = U * (kAhead + 1);
     __shared__ Raw<CV> ring[kRing][kCThreads];
     dep_wait();
-    dep_launch();
     const int cb = blockIdx.x % p.col_blocks;
     const int r0 = static_cast<int>(blockIdx.x / p.col_blocks) * p.run;
     const int r1 = min(p.num_tokens, r0 + p.run);
@@ -433,7 +434,7 @@ cudaError_t launch_decode(const Params& p, int N, cudaStream_t stream) {
 // sizes that both entry points of the layer share
 gdn_status check_dims(const gdn_ssm_dims* d) {
     if (d == nullptr) return GDN_ERR_NULL_ARG;
-    if (d->batch < 0 || d->num_tokens < 0 || d->H < 1 || d->G < 1 || d->H % d->G != 0 || d->P < 1 || d->N < 1 ||
+    if (d->batch < 0 || d->num_tokens < 0 || d->num_tokens > kMaxRows || d->H < 1 || d->G < 1 || d->H % d->G != 0 || d->P < 1 || d->N < 1 ||
         d->num_slots < 1 || d->x_stride < 0 || d->b_stride < 0 || d->c_stride < 0 || d->dt_stride < 0 ||
         d->z_stride < 0 || d->out_stride < 0 || d->reserved[0] != 0 || d->reserved[1] != 0)
         return GDN_ERR_BAD_SHAPE;
@@ -483,7 +484,7 @@ gdn_status gdn_conv_prefill(const void* x, const void* conv_weight, const void* 
                             int32_t batch, int32_t num_tokens, int32_t conv_dim, int64_t y_stride,
                             const gdn_conv_dims* cdims, int32_t* status_word, gdn_stream_t stream) {
     if (cdims == nullptr) return GDN_ERR_NULL_ARG;
-    if (batch < 0 || num_tokens < 0 || conv_dim < 1 || conv_dim % 4 != 0 || y_stride < 0 || cdims->x_stride < 0 ||
+    if (batch < 0 || num_tokens < 0 || batch > kMaxRows || num_tokens > kMaxRows || conv_dim < 1 || conv_dim % 4 != 0 || y_stride < 0 || cdims->x_stride < 0 ||
         cdims->width < 1 || cdims->width > 4 || cdims->state_len < cdims->width || cdims->num_conv_slots < 1 ||
         cdims->reserved[0] != 0 || cdims->reserved[1] != 0)
         return GDN_ERR_BAD_SHAPE;

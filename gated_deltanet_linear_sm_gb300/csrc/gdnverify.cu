@@ -135,6 +135,11 @@ struct Sums {
     }
 };
 
+// Sums of up to 32 of these stay in 64 bits whatever a row holds, and only a row that
+// sums to 16 or more (which a distribution does not) meets one of them.
+constexpr long long kTooMuch = 1LL << 57;
+constexpr u64 kRowLimit = 1ULL << 56;
+
 struct VerifySmem {
     u64 warp_sum[kVWarps];                         // of each warp's piece
     u64 cta_sum[2][kMaxCluster];                   // and of each CTA's, written by its owner (two attempts)
@@ -299,7 +304,7 @@ __global__ void __launch_bounds__(kVThreads) gdn_verify_kernel(const VerifyParam
                     n += U * E;
                 }
             }
-            sum += P.value(n) - (how == 2 ? Q.value(n) : 0);
+            sum = min(sum + P.value(n) - (how == 2 ? Q.value(n) : 0), kTooMuch);
         }
         // the ends of the row, if they are this warp's: lane k the entry k of a cut vector
         auto cut = [&](int v) {
@@ -311,7 +316,7 @@ __global__ void __launch_bounds__(kVThreads) gdn_verify_kernel(const VerifyParam
         if (in1 < v1 && in1 >= in0) cut(v1 - 1);
         u64 total = warp_sum(static_cast<u64>(sum));
         if (how == 1 && d >= v0 * E - mis && d < v1 * E - mis) total -= fixed(to_f(prow[d]));
-        return total;
+        return min(total, static_cast<u64>(kTooMuch));
     };
     u64 total = 0;
     int attempt = 0;
@@ -323,7 +328,7 @@ __global__ void __launch_bounds__(kVThreads) gdn_verify_kernel(const VerifyParam
         if (tid < CL) {
             u64 a = 0;
             for (int w = 0; w < kVWarps; ++w) a += s.warp_sum[w];
-            cl.map_shared_rank(&s, tid)->cta_sum[attempt][rank] = a;
+            cl.map_shared_rank(&s, tid)->cta_sum[attempt][rank] = min(a, static_cast<u64>(kTooMuch));
         }
         cl.sync();                                 // this attempt's sums are read from this CTA's own memory
         total = 0;
@@ -334,7 +339,7 @@ __global__ void __launch_bounds__(kVThreads) gdn_verify_kernel(const VerifyParam
 
     // ---- where the cumulative sum passes sample_u of the total ----
     const int64_t slot = static_cast<int64_t>(i) * p.max_T + s.kept;
-    if (total == 0) {
+    if (total == 0 || total >= kRowLimit) {
         if (rank == 0 && tid == 0) {
             p.out[slot] = -1;
             raise(p.status, GDN_FLAG_NO_TOKEN);
@@ -603,7 +608,7 @@ gdn_status gdn_verify_drafts(const void* target_probs, const void* draft_probs, 
     if (dims == nullptr) return GDN_ERR_NULL_ARG;
     if (dims->batch < 0 || dims->num_tokens < 0 || dims->vocab < 1 || dims->vocab > 0x7fff0000 || dims->max_T < 1 ||
         dims->max_T > kMaxDraftT || dims->target_stride < 0 || dims->draft_stride < 0 || dims->draft_seq < 0 ||
-        dims->token_stride < 0 || dims->batch > 0x7fffffff / kMaxCluster)
+        dims->token_stride < 0 || dims->batch > 0x7fffffff / kMaxCluster || dims->num_tokens > kMaxRows)
         return GDN_ERR_BAD_SHAPE;
     if (!is_dtype(prob_dtype)) return GDN_ERR_UNSUPPORTED;
     if (dims->batch == 0) return GDN_OK;
@@ -647,6 +652,7 @@ gdn_status gdn_step_tables(const int32_t* q_lens, const int32_t* spec, const int
                            const gdn_tables_dims* dims, int32_t* status_word, gdn_stream_t stream) {
     if (dims == nullptr) return GDN_ERR_NULL_ARG;
     if (dims->batch < 0 || dims->num_tokens < 0 || dims->spec_stride < 1 || dims->num_requests < 0 ||
+        dims->batch > kMaxRows || dims->num_tokens > kMaxRows ||
         dims->spec_stride > 0x7fffffff / kTile || (request == nullptr && dims->batch > dims->num_requests))
         return GDN_ERR_BAD_SHAPE;
     if (!cu_seqlens) return GDN_ERR_NULL_ARG;

@@ -85,15 +85,15 @@ typedef enum { GDN_F32 = 0, GDN_BF16 = 1, GDN_F16 = 2 } gdn_dtype;
 #define GDN_FLAG_QLEN       4  /* q_len > max_T or q_len > spec_stride: sequence skipped */
 #define GDN_FLAG_TOKEN_ROW  8  /* a token row outside [0, num_tokens), or cu_seqlens[i] < 0 or
                                   cu_seqlens[i+1] > cu_seqlens[batch]: sequence skipped */
-#define GDN_FLAG_TIMEOUT    16 /* gdn_prefill_chunked only: a wait on the tensor cores ran past its
-                                  bound (gdn_set_wait_limit); that sequence's outputs and final
-                                  state are incomplete */
-#define GDN_FLAG_DRAIN      32 /* gdn_prefill_chunked only: after such a timeout, the wait (with the
+#define GDN_FLAG_TIMEOUT    16 /* gdn_prefill_chunked and gdn_ssm_prefill only: a wait on the tensor
+                                  cores ran past its bound (gdn_set_wait_limit); that sequence's
+                                  outputs and final state are incomplete */
+#define GDN_FLAG_DRAIN      32 /* the same two only: after such a timeout, the wait (with the
                                   default bound) for the products still in flight ran out too; the
                                   CTA released its tensor memory regardless, since holding it would
                                   block every later kernel on that SM */
 #define GDN_FLAG_NO_TOKEN   64 /* gdn_verify_drafts only: every probability of the row to sample from
-                                  counts as 0, so that no token was emitted */
+                                  counts as 0, or they sum to 16 or more: no token was emitted */
 
 /*
  * dims->split flag: each warp of the decode step owns 8 of a unit's 128 V
@@ -378,7 +378,13 @@ GDNSPEC_API gdn_status gdn_spec_decode_conv(
  * tables, status bits and conventions: asynchronous on `stream`, no allocation,
  * no host read of device data, capturable.  The device data of a call (tables,
  * lengths, slots) is checked on the device and reported through `status_word`;
- * outputs must not overlap inputs unless a call says so.
+ * outputs must not overlap inputs unless a call says so.  A call takes at most
+ * 2^30 rows (GDN_ERR_BAD_SHAPE beyond).
+ * Like the steps they start early behind a predecessor that lets them, and touch
+ * memory only when it has completed.  gdn_ssm_prefill and gdn_ssm_decode let
+ * their successor start early too, once their own predecessors have completed;
+ * the others, which write tables and conv slots, do not, so that a step right
+ * behind them reads what they wrote (without the GDN_PRE flag that covers it).
  */
 
 /* Sizes of gdn_verify_drafts. */
@@ -433,8 +439,9 @@ typedef struct {
  * num_accepted, as its states keep theirs; so does one with bad data, which the
  * step skips too (q_len > max_T: GDN_FLAG_QLEN; a row outside [0, num_tokens),
  * or cu_seqlens out of order with cu_seqlens[batch]: GDN_FLAG_TOKEN_ROW).  A
- * row to sample from that counts as 0 throughout emits -1 and sets
- * GDN_FLAG_NO_TOKEN.  Every pointer needs only its element's alignment.
+ * row to sample from that counts as 0 throughout, or whose entries sum to 16 or
+ * more (scores instead of probabilities), emits -1 and sets GDN_FLAG_NO_TOKEN.
+ * Every pointer needs only its element's alignment.
  */
 GDNSPEC_API gdn_status gdn_verify_drafts(
     const void* target_probs, const void* draft_probs, const int32_t* draft_tokens,
@@ -623,9 +630,10 @@ GDNSPEC_API gdn_status gdn_ssm_decode(
 GDNSPEC_API int32_t gdn_spec_decode_split(const gdn_dims* dims, gdn_dtype state_dtype);
 
 /*
- * Bound on each wait of gdn_prefill_chunked for its tensor-core products:
- * 0 (the default) waits with blocking polls of the completion barrier, 2^24
- * of them (well over a second); a non-zero bound counts non-blocking polls
+ * Bound on each wait of gdn_prefill_chunked for its tensor-core products, and
+ * of gdn_ssm_prefill for those, its copies and its own warps: 0 (the default)
+ * waits with blocking polls of the barrier, 2^24 of them (2^17 of up to 20 us;
+ * well over a second either way); a non-zero bound counts non-blocking polls
  * instead, so that a small one runs out for certain.  A wait that runs out
  * sets GDN_FLAG_TIMEOUT; the unit writes no final state and its CTAs end
  * after waiting, with the default bound, for the products still in flight

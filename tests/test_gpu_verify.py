@@ -161,6 +161,33 @@ def test_rows_that_leave_nothing(cuda_device):
     assert want[2, 0] == -1 and acc[2] == 1
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V,n", [(4096, 1), (50000, 1), (50000, 700)])
+def test_rows_of_scores_are_refused(cuda_device, dtype, V, n):
+    """Rows that sum to 16 or more, up to a 1 in every entry (more than 64 bits hold): no token and a flag,
+    whatever the number of CTAs; a row of just under 16 has one."""
+    target = torch.ones(n, V, dtype=DT[dtype], device=cuda_device)
+    target[0] = 0
+    target[0, ::V // 16] = 0.96875                                      # 16 or 17 entries: 15.5 or 16.47
+    target[0, 16 * (V // 16):] = 0                                      # 16
+    out = torch.full((n, 1), -77, dtype=torch.int32, device=cuda_device)
+    acc = torch.full((n,), -77, dtype=torch.int32, device=cuda_device)
+    status = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    gdn.gdn_verify_drafts(target, None, None, torch.full((n,), 0.97, device=cuda_device), _i32(np.arange(n + 1), cuda_device),
+                          out, acc, status=status)
+    assert out[0, 0] == 15 * (V // 16) and (out[1:] == -1).all() and (acc == 1).all()
+    assert int(status) == (binding.GDN_FLAG_NO_TOKEN if n > 1 else 0)
+    target[0, 1] = 0.5
+    gdn.gdn_verify_drafts(target, None, None, torch.full((n,), 0.97, device=cuda_device), _i32(np.arange(n + 1), cuda_device),
+                          out, acc, status=status)
+    assert (out == -1).all() and int(status) == binding.GDN_FLAG_NO_TOKEN
+    target[0] = 1
+    status.zero_()
+    gdn.gdn_verify_drafts(target, None, None, torch.full((n,), 0.97, device=cuda_device), _i32(np.arange(n + 1), cuda_device),
+                          out, acc, status=status)
+    assert (out == -1).all() and int(status) == binding.GDN_FLAG_NO_TOKEN
+
+
 @pytest.mark.parametrize("draft", [True, False])
 def test_drafts_that_are_no_token(cuda_device, draft):
     """A draft outside the vocabulary ends the drafts and is replaced from p alone."""

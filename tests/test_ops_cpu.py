@@ -172,6 +172,15 @@ def test_ssm_decode_refusals(lib, kw, code):
     assert _decode(lib, **kw) == code
 
 
+def test_more_rows_than_a_call_takes(lib):
+    n = 2 ** 30 + 1
+    assert _verify(lib, dims=dict(num_tokens=n)) == BAD_SHAPE
+    assert _tables(lib, dict(num_tokens=n)) == BAD_SHAPE
+    assert _tables(lib, dict(batch=n, num_requests=n)) == BAD_SHAPE
+    assert _conv(lib, n=n) == BAD_SHAPE and _conv(lib, batch=n) == BAD_SHAPE
+    assert _prefill(lib, dict(num_tokens=n)) == BAD_SHAPE and _decode(lib, dict(num_tokens=n)) == BAD_SHAPE
+
+
 # ---- the binding -----------------------------------------------------------------
 
 
