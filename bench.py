@@ -230,7 +230,7 @@ CSRC = "gated_deltanet_linear_sm_gb300/csrc/"
 # the sources of the kernel each kind of workload times
 KERNEL_SOURCES = {"decode": (CSRC + "gdnspec.cu", CSRC + "gdn_internal.h"),
                   "conv": (CSRC + "gdnspec.cu", CSRC + "gdn_internal.h"),
-                  "prefill": (CSRC + "gdnprefill_chunked.cu", CSRC + "gdn_internal.h")}
+                  "prefill": (CSRC + "gdnprefill_chunked.cu", CSRC + "gdn_tcgen05.h", CSRC + "gdn_internal.h")}
 
 
 def kernel_source_hash(kind="decode"):

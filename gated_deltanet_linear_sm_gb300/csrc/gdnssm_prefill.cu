@@ -74,7 +74,7 @@ constexpr float kLost = 1.0f;                    // no log2-decay: those are not
 struct ScanParams {
     CUtensorMap x, B, C, z, out;                 // boxes of 64 elements x 128 rows
     Params p;
-    float* part;                                 // segments: [part][unit][N][64] what a part of one adds
+    float* part;                                 // segments: [part][unit] of N x 64, what a part of one adds
     float* part_decay;                           // and its log2-decay, [part][unit] (kLost: it was given up)
     int32_t seg_chunks;                          // chunks of a segment (0: whole sequences)
     int32_t parts, part_chunks;                  // parts of a segment in the first launch, and their chunks
@@ -210,6 +210,10 @@ __device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, i
         : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // Bounded wait for phase `use` of a barrier: 2^17 polls that sleep up to 20 us each,
 // or, with a bound set by gdn_set_wait_limit, that many that do not sleep.  As few
 // instructions as it takes: there are some twenty waits in the five kinds of warps,
@@ -301,6 +305,25 @@ __device__ __forceinline__ void store_row32(T* p, const u64 (&x)[16]) {
                                                            from_pair(x[4 * j + 2], T()), from_pair(x[4 * j + 3], T())));
 }
 
+// A part of a segment in the workspace: the row of thread hh * N + row, 16 bytes of every
+// thread in turn, so that a warp's accesses are consecutive (row by row, 32 of them
+// apart, a part took 2.5 us to read).  p: where the thread's first 16 bytes are.
+template <int N>
+__device__ __forceinline__ void load_part(const float* p, u64 (&x)[16]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(p) + j * 2 * N);
+        x[2 * j] = pk2(v.x, v.y);
+        x[2 * j + 1] = pk2(v.z, v.w);
+    }
+}
+template <int N>
+__device__ __forceinline__ void store_part(float* p, const u64 (&x)[16]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        __stcg(reinterpret_cast<float4*>(p) + j * 2 * N, make_float4(lo2(x[2 * j]), hi2(x[2 * j]), lo2(x[2 * j + 1]), hi2(x[2 * j + 1])));
+}
+
 // What this CTA works on.  kind 0: nothing.
 struct Work {
     int kind, seq, bos, len;                     // rows of the whole sequence
@@ -309,7 +332,8 @@ struct Work {
     bool last;
 };
 
-// The whole-sequence form: sequence = blockIdx / units.  With segments, the
+// The whole-sequence form: of every 32 sequences the longest first, so that the CTAs
+// of the last round are short ones.  With segments, the
 // launch's index is looked up among the sequences' counts: of segments, or (the
 // states alone) of the parts before each sequence's last segment.  In the
 // workspace a sequence of several segments has its initial state, then those
@@ -327,11 +351,22 @@ __device__ Work find_work(const ScanParams& sp, int index, int lane) {
         return -1;
     };
     if (sp.seg_chunks == 0) {
-        int bos, eos;
-        const int f = bounds(index, bos, eos);
-        if (f > 0 && threadIdx.x == 0) raise(p.status, f);
-        if (f != -1) return w;
-        w = {1, index, bos, eos - bos, 0, (eos - bos + kQ - 1) / kQ, 0, 0, true};
+        const int i0 = index & ~31, i = i0 + lane;
+        int bos = 0, eos = 0, len = 0, rank = 0;
+        if (i < p.batch) {
+            const int f = bounds(i, bos, eos);
+            if (f > 0 && index == i0 && threadIdx.x < 32) raise(p.status, f);
+            if (f == -1) len = eos - bos;
+        }
+        for (int o = 0; o < min(32, p.batch - i0); ++o) {
+            const int other = __shfl_sync(kFull, len, o);
+            rank += other > len || (other == len && o < lane);
+        }
+        const unsigned hit = __ballot_sync(kFull, i < p.batch && rank == index - i0);
+        const int src = __ffs(hit) - 1;
+        bos = __shfl_sync(kFull, bos, src);
+        len = __shfl_sync(kFull, len, src);
+        if (len > 0) w = {1, i0 + src, bos, len, 0, (len + kQ - 1) / kQ, 0, 0, true};
         return w;
     }
     int base = 0, room_base = 0;
@@ -394,6 +429,15 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
     const int unit = static_cast<int>(blockIdx.x % units), index = static_cast<int>(blockIdx.x / units);
     const int h = unit / p.blocks, pb = unit - h * p.blocks, g = h / p.group;
     const int col = h * p.P + pb * kPB;
+    if (tid == 0) {
+        prefetch_map(&sp.x);
+        prefetch_map(&sp.B);
+        if (!kStates) {
+            prefetch_map(&sp.C);
+            prefetch_map(&sp.out);
+            if (p.z) prefetch_map(&sp.z);
+        }
+    }
     dep_wait();
     dep_launch();
     const Work wk = find_work<kStates>(sp, index, lane);
@@ -634,6 +678,7 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
         for (int j = 0; j < 16; ++j) S[j] = 0;
         float run_log = 0.f;
         auto part_at = [&](int part) { return static_cast<int64_t>(part) * units + unit; };
+        auto part_of = [&](int part) { return sp.part + part_at(part) * N * kPB + 4 * (hh * N + row); };
         if (state_row && (kStates ? wk.first == 0 : wk.parts == 0)) {
             const long long rs = ld(p.read_slots + wk.seq);
             if (rs >= 0)
@@ -642,28 +687,29 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
                            S);
         }
         if (kStates && wk.first == 0 && state_row) {             // the initial state, kept for the second launch
-            const int64_t at = part_at(wk.part - 1);
-            store_row32(sp.part + (at * N + row) * kPB + 32 * hh, S);
-            if (row == 0 && hh == 0) sp.part_decay[at] = 0.f;
+            store_part<N>(part_of(wk.part - 1), S);
+            if (row == 0 && hh == 0) sp.part_decay[part_at(wk.part - 1)] = 0.f;
 #pragma unroll
             for (int j = 0; j < 16; ++j) S[j] = 0;
         }
         if (!kStates) {
             // segments: the initial state, and what lies before this one
-            for (int k = 0; k < wk.parts; ++k) {
-                const int64_t at = part_at(wk.part + k);
-                const float decay = ld(sp.part_decay + at);
-                if (decay == kLost) {
+            for (int k0 = 0; k0 < wk.parts && ok; k0 += 32) {
+                const int n = min(32, wk.parts - k0);            // their decays come together
+                const float decay = lane < n ? ld(sp.part_decay + part_at(wk.part + k0 + lane)) : 0.f;
+                if (__any_sync(kFull, decay == kLost)) {
                     ok = false;
                     *abort = 1;
                     break;
                 }
-                if (!state_row) continue;
-                const u64 a2 = dup2(exp2f(decay));
-                u64 x[16];
-                load_row32(sp.part + (at * N + row) * kPB + 32 * hh, x);
+                const float scale = exp2f(decay);
+                for (int k = 0; k < n && state_row; ++k) {
+                    const u64 a2 = dup2(__shfl_sync(kFull, scale, k));
+                    u64 x[16];
+                    load_part<N>(part_of(wk.part + k0 + k), x);
 #pragma unroll
-                for (int j = 0; j < 16; ++j) S[j] = ffma2(a2, S[j], x[j]);
+                    for (int j = 0; j < 16; ++j) S[j] = ffma2(a2, S[j], x[j]);
+                }
             }
         }
         // Xw of chunk c, and the rows past the sequence's end cleared
@@ -793,9 +839,8 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
         // state, rounded once
         asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
         if (kStates) {
-            const int64_t at = part_at(wk.part);
-            if (state_row) store_row32(sp.part + (at * N + row) * kPB + 32 * hh, S);
-            if (tid == 0) sp.part_decay[at] = *abort == 0 ? run_log : kLost;
+            if (state_row) store_part<N>(part_of(wk.part), S);
+            if (tid == 0) sp.part_decay[part_at(wk.part)] = *abort == 0 ? run_log : kLost;
         } else if (*abort == 0 && state_row) {
             if (wk.last) {
                 const long long ws = ld(p.write_slots + wk.seq);
@@ -955,28 +1000,43 @@ cudaError_t launch_kernel(const ScanParams& sp, int64_t ctas, cudaStream_t strea
 // How the prompts are cut: chunks of a segment (0: whole sequences) and parts of a
 // segment in the first launch, whichever an estimate of the time says is shorter.
 // The host knows the rows and the sequences but not their lengths; with several it
-// takes the longest for half as long again as the mean.  The estimate's constants, in us, are
-// measured: a chunk takes kChunk, or kAlone while every SM pair runs one CTA; a
-// chunk of the first launch kState with two CTAs an SM; a launch and a CTA's start
-// the rest.  (One prompt of 16384 tokens and 64 heads: 362 us whole, 299 cut at
-// 56 chunks; 4 of 1024 and 16 heads: 30.5 whole, 34.8 cut at 4.)
+// takes the longest for half as long again as the mean.  The estimate's constants, in us,
+// are measured: a chunk takes kChunk, or kAlone while every SM pair runs one CTA; a
+// chunk of the first launch kState with two CTAs an SM; a CTA's start and end kStart
+// or kStateStart, and kPart for every part that it starts from; the first launch kLaunch.
 struct Cut {
     int chunks, parts;
 };
 Cut cut(int batch, int num_tokens, int units) {
-    constexpr double kChunk = 3.7, kAlone = 2.9, kState = 2.6, kLaunch = 6.0, kStart = 4.0, kStateStart = 5.0;
-    const int sms = sm_count() ? sm_count() : 148;
+    constexpr double kChunk = 2.8, kAlone = 2.45, kState = 1.75, kStart = 5.0, kStateStart = 4.0, kPart = 0.5, kLaunch = 3.0;
+    const double sms = sm_count() ? sm_count() : 148;
     const double chunks = static_cast<double>((static_cast<int64_t>(num_tokens) + kQ - 1) / kQ);
     const double mean = chunks / batch, longest = batch > 1 ? 1.5 * mean : mean, whole = static_cast<double>(batch) * units;
-    double best = kLaunch + std::max(longest * (2 * whole <= sms ? kAlone : kChunk), std::ceil(whole / sms) * (mean * kChunk + kStart));
+    const double c0 = 2 * whole <= sms ? kAlone : kChunk;
+    double best = batch > 1 ? std::max(longest * c0 + kStart, (chunks * c0 + batch * kStart) * units / sms + 0.5 * (mean * c0 + kStart))
+                            : std::ceil(whole / sms) * (chunks * c0 + kStart);
     Cut take = {0, 1};
     for (int parts = 1; parts <= 4; parts *= 2)
         for (int k = parts; k < longest && k <= 512; k += parts) {
-            const double segments = batch > 1 ? chunks / k + 0.5 * batch : chunks / k;
-            const double before = batch > 1 ? std::max(chunks / k - 0.5 * batch, 0.0) : std::ceil(chunks / k) - 1;
-            const double ctas = segments * units;
-            const double cost = 2 * kLaunch + std::ceil(std::ceil(ctas) / sms) * (k * (2 * ctas <= sms ? kAlone : kChunk) + kStart) +
-                                std::ceil(std::ceil(before * parts * units) / (2 * sms)) * (k / parts * kState + kStateStart);
+            double cost = kLaunch;
+            if (batch > 1) {
+                const double segments = chunks / k + 0.5 * batch, before = std::max(chunks / k - 0.5 * batch, 0.0);
+                const double c = 2 * segments * units <= sms ? kAlone : kChunk, start = kStart + kPart * 0.5 * parts * longest / k;
+                cost += std::max(k * c + start, (chunks * c + segments * start) * units / sms + 0.5 * (k * c + start)) +
+                        std::ceil(std::ceil(before * parts * units) / (2 * sms)) * (k / parts * kState + kStateStart);
+            } else {
+                // units * before segments of k chunks, then as many shorter ones as there are units
+                const double before = std::ceil(chunks / k) - 1, rest = chunks - before * k;
+                const double c = 2 * (before + 1) * units <= sms ? kAlone : kChunk, start = kStart + kPart * (1 + parts * before);
+                const double full = k * c + start, last = rest * c + start;
+                const double rounds = std::floor(before * units / sms), busy = before * units - rounds * sms, idle = sms - busy;
+                const double beside = busy > 0 ? idle * std::floor(full / last) : 0;     // that run beside the last long ones
+                cost += rounds * full + (busy == 0           ? std::ceil(units / sms) * last
+                                         : beside >= units ? full
+                                                           : std::min(std::ceil(units / idle) * last,
+                                                                      full + std::ceil((units - beside) / sms) * last)) +
+                        std::ceil(before * parts * units / (2 * sms)) * (k / parts * kState + kStateStart);
+            }
             if (cost < best) {
                 best = cost;
                 take = {k, parts};
