@@ -510,9 +510,8 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
             const uint64_t b_mn = desc_mn(sbase + L::kB, L::kTile), xw_mn = desc_mn(sbase + L::kXw, L::kTile);
             const uint64_t s_mn = desc_mn(sbase + L::kS, N * 128), x_mn0 = desc_mn(sbase + L::kX, L::kTile);
             for (int c = 0; c < wk.chunks; ++c) {
-                const bool tail = rows_of(c) < kQ;               // its rows past the end are cleared before any product
+                // (G of a last chunk reads what lies behind the sequence too: columns that Pm leaves out)
                 if (!need_warp(&ms.bc_full, c)) break;
-                if (tail && !need_warp(&ms.ready, c)) break;
                 fence_after();
                 if (!kStates) {
                     if (c > 0 && !need_warp(&ms.y1_done, c - 1)) break;               // Pm has been used
@@ -523,7 +522,7 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
                     }
                     commit_to(&ms.g_done, lead);
                 }
-                if (!tail && !need_warp(&ms.ready, c)) break;
+                if (!need_warp(&ms.ready, c)) break;
                 fence_after();
 #pragma unroll
                 for (int ks = 0; ks < kQ / 16; ++ks)
@@ -719,7 +718,7 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
             unsigned char* X = sm + L::kX + c % L::kXStages * L::kTile;
             const u64 w2 = dup2(ms.gates[c % kGates].w[row]);
             if (n < kQ) {
-                if (!need_warp(&ms.bc_full, c)) return;
+                if (!need_warp(kStates ? &ms.bc_full : &ms.g_done, c)) return;     // (G has read B)
                 if (row >= n) {
                     const uint4 zero = make_uint4(0, 0, 0, 0);
 #pragma unroll
