@@ -120,8 +120,8 @@ struct alignas(16) Misc {
     Gates gates[kGates];
     unsigned long long x_full[3], bc_full, z_full[2];    // copies have landed
     unsigned long long gates_full[kGates];
-    unsigned long long g_done, ds_done, y2_done, y1_done;       // products are complete
-    unsigned long long ready, p_ready, chunk_done[2];           // the tile warps have written / read
+    unsigned long long g_done, ds_done, y2_done, y1_done[2];    // products are complete
+    unsigned long long ready, xw_ready, p_ready, y_free, chunk_done[2];   // the tile warps have written / read
     unsigned long long z_free[2];                               // the outputs have left their buffer
     unsigned long long drain;
     uint32_t tmem;
@@ -455,13 +455,15 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
         for (int k = 0; k < 2; ++k) {
             bar_init(&ms.z_full[k], 1);
             bar_init(&ms.z_free[k], 1);
+            bar_init(&ms.y1_done[k], 1);
             bar_init(&ms.chunk_done[k], kWarps);
         }
         bar_init(&ms.g_done, 1);
         bar_init(&ms.ds_done, 1);
         bar_init(&ms.y2_done, 1);
-        bar_init(&ms.y1_done, 1);
         bar_init(&ms.ready, kWarps);
+        bar_init(&ms.xw_ready, kWarps);
+        bar_init(&ms.y_free, kWarps);
         bar_init(&ms.p_ready, kWarps);
         bar_init(&ms.drain, 1);
         ms.abort = 0;
@@ -497,6 +499,37 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
         return ok;
     };
 
+    // Xw of chunk c, and the rows past the sequence's end cleared
+    auto weigh = [&](int c, int row, int hh) {
+        if (!need_warp(&ms.gates_full[c % kGates], c / kGates) || !need_warp(&ms.x_full[c % L::kXStages], c / L::kXStages)) return;
+        const int n = rows_of(c);
+        unsigned char* X = sm + L::kX + c % L::kXStages * L::kTile;
+        const u64 w2 = dup2(ms.gates[c % kGates].w[row]);
+        if (n < kQ) {
+            if (!need_warp(kStates ? &ms.bc_full : &ms.g_done, c)) return;     // (G has read B)
+            if (row >= n) {
+                const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(X + unit16(row, 4 * hh + j)) = zero;
+#pragma unroll
+                for (int j = 0; j < N / 16; ++j) {           // this half of the row's N / 8 units
+                    const int u = hh * (N / 16) + j;
+                    *reinterpret_cast<uint4*>(sm + L::kB + (u >> 3) * L::kTile + unit16(row, u & 7)) = zero;
+                }
+            }
+        }
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t at = unit16(row, 4 * hh + j);
+            const uint4 v = *reinterpret_cast<const uint4*>(X + at);
+            const u64 x[4] = {fmul2(widen(v.x), w2), fmul2(widen(v.y), w2), fmul2(widen(v.z), w2), fmul2(widen(v.w), w2)};
+            uint4 hi, lo;
+            split_quads(x, hi, lo);
+            *reinterpret_cast<uint4*>(sm + L::kXw + at) = hi;
+            *reinterpret_cast<uint4*>(sm + L::kXw + L::kTile + at) = lo;
+        }
+    };
+
     if (warp == kMma) {
         // ---- products ----
         {
@@ -514,7 +547,7 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
                 if (!need_warp(&ms.bc_full, c)) break;
                 fence_after();
                 if (!kStates) {
-                    if (c > 0 && !need_warp(&ms.y1_done, c - 1)) break;               // Pm has been used
+                    if (c > 0 && !need_warp(&ms.y1_done[(c - 1) & 1], (c - 1) >> 1)) break;   // Pm has been used
 #pragma unroll
                     for (int ks = 0; ks < N / 16; ++ks) {
                         const uint64_t o = (ks >> 2) * (L::kTile / 16) + (ks & 3) * 2;
@@ -522,6 +555,8 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
                     }
                     commit_to(&ms.g_done, lead);
                 }
+                // Xw is there; and S is, so dS of c - 1 has been read
+                if (!kStates && !need_warp(&ms.xw_ready, c)) break;
                 if (!need_warp(&ms.ready, c)) break;
                 fence_after();
 #pragma unroll
@@ -529,8 +564,8 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
                     mma_ss(tm + L::kTdS, b_mn + ks * 128, xw_mn + ks * 128, id_ds, ks > 0, lead);
                 commit_to(&ms.ds_done, lead);
                 if (!kStates) {
-                    // the outputs of chunk c - 1 are made: Y2 has been read (so has Y1 of c - 2, before `ready`)
-                    if (c > 0 && !need_warp(&ms.chunk_done[(c - 1) & 1], (c - 1) >> 1)) break;
+                    // Y2 of chunk c - 1 has been read (so has Y1 of c - 2, before `ready`)
+                    if (c > 0 && !need_warp(&ms.y_free, c - 1)) break;
                     fence_after();
 #pragma unroll
                     for (int ks = 0; ks < N / 16; ++ks)
@@ -544,7 +579,7 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
 #pragma unroll
                         for (int ks = 0; ks < kQ / 16; ++ks)
                             mma_ts(tm + kTY1 + (c & 1) * 64, tm + kTG + ks * 16 + part * 8, x_mn + ks * 128, id_y1, part + ks > 0, lead);
-                    commit_to(&ms.y1_done, lead);
+                    commit_to(&ms.y1_done[c & 1], lead);
                 }
             }
             // every product issued has to finish before tensor memory goes (with the default
@@ -711,36 +746,6 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
                 }
             }
         }
-        // Xw of chunk c, and the rows past the sequence's end cleared
-        auto weigh = [&](int c) {
-            if (!need_warp(&ms.gates_full[c % kGates], c / kGates) || !need_warp(&ms.x_full[c % L::kXStages], c / L::kXStages)) return;
-            const int n = rows_of(c);
-            unsigned char* X = sm + L::kX + c % L::kXStages * L::kTile;
-            const u64 w2 = dup2(ms.gates[c % kGates].w[row]);
-            if (n < kQ) {
-                if (!need_warp(kStates ? &ms.bc_full : &ms.g_done, c)) return;     // (G has read B)
-                if (row >= n) {
-                    const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) *reinterpret_cast<uint4*>(X + unit16(row, 4 * hh + j)) = zero;
-#pragma unroll
-                    for (int j = 0; j < N / 16; ++j) {           // this half of the row's N / 8 units
-                        const int u = hh * (N / 16) + j;
-                        *reinterpret_cast<uint4*>(sm + L::kB + (u >> 3) * L::kTile + unit16(row, u & 7)) = zero;
-                    }
-                }
-            }
-#pragma unroll 1
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t at = unit16(row, 4 * hh + j);
-                const uint4 v = *reinterpret_cast<const uint4*>(X + at);
-                const u64 x[4] = {fmul2(widen(v.x), w2), fmul2(widen(v.y), w2), fmul2(widen(v.z), w2), fmul2(widen(v.w), w2)};
-                uint4 hi, lo;
-                split_quads(x, hi, lo);
-                *reinterpret_cast<uint4*>(sm + L::kXw + at) = hi;
-                *reinterpret_cast<uint4*>(sm + L::kXw + L::kTile + at) = lo;
-            }
-        };
         // the state's hi and lo images for the next chunk
         auto image = [&]() {
             if (state_row) {
@@ -758,11 +763,11 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
             __syncwarp();
             if (lane == 0) bar_arrive(&ms.ready);
         };
-        weigh(0);
-        if (!kStates) image();
+        if (kStates) weigh(0, row, hh);
+        else image();
         if (ok) publish();
+        if (!kStates) need_warp(&ms.gates_full[0], 0);
         for (int c = 0; c < wk.chunks && ok; ++c) {
-            const int n = rows_of(c);
             const Gates& gt = ms.gates[c % kGates];
             // the state after this chunk
             if (!need_warp(&ms.ds_done, c)) break;
@@ -782,50 +787,65 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
                 }
             }
             fence_before();
-            const u64 et2 = dup2(gt.e[row]);
-            if (c + 1 < wk.chunks) {
-                weigh(c + 1);
-                if (!kStates) {
-                    if (!need_warp(&ms.y2_done, c)) break;       // the images may be overwritten
-                    image();
+            if (kStates) {
+                if (c + 1 < wk.chunks) {
+                    weigh(c + 1, row, hh);
+                    if (!ok) break;
+                    publish();
                 }
-                if (!ok) break;
-                publish();
-            }
-            if (!kStates) {
-                // the outputs: (2^(l_t) Y2 + Y1) silu(z)
-                // (with a chunk to come y2_done has been waited for above, and may be a phase on)
-                if (c + 1 == wk.chunks && !need_warp(&ms.y2_done, c)) break;
-                if (!need_warp(&ms.y1_done, c)) break;
-                // z has landed; without it the buffer's last outputs have left
-                if (gated ? !need_warp(&ms.z_full[c & 1], c >> 1) : c >= 2 && !need_warp(&ms.z_free[c & 1], (c - 2) >> 1)) break;
+            } else {
+                if (!need_warp(&ms.y2_done, c)) break;           // the images may be overwritten
+                if (c + 1 < wk.chunks) {
+                    // (here, so that the gates are never two rounds ahead of a wait for chunk_done)
+                    if (!need_warp(&ms.gates_full[(c + 1) % kGates], (c + 1) / kGates)) break;
+                    image();
+                    publish();
+                }
+                // the outputs: (2^(l_t) Y2 + Y1) silu(z); Y2 first, so that the next may be made
                 fence_after();
-                unsigned char* Z = sm + L::kZ + (c & 1) * L::kTile;
-#pragma unroll 1
+                u64 o[16];
+                const u64 et2 = dup2(gt.e[row]);
+#pragma unroll
                 for (int half = 0; half < 2; ++half) {
-                    uint32_t y1[16], y2[16], y3[16];
-                    tm_ld16_nowait(lanes + kTY1 + (c & 1) * 64 + 32 * hh + 16 * half, y1);
+                    uint32_t y2[16], y3[16];
                     tm_ld16_nowait(lanes + kTY2 + 32 * hh + 16 * half, y2);
                     tm_ld16_nowait(lanes + kTY2 + 64 + 32 * hh + 16 * half, y3);
                     tm_wait_ld();
 #pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        o[8 * half + j] = fmul2(et2, add2(raw2(y2[2 * j], y2[2 * j + 1]), raw2(y3[2 * j], y3[2 * j + 1])));
+                }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) bar_arrive(&ms.y_free);
+                if (!need_warp(&ms.y1_done[c & 1], c >> 1)) break;
+                // z has landed; without it the buffer's last outputs have left
+                if (gated ? !need_warp(&ms.z_full[c & 1], c >> 1) : c >= 2 && !need_warp(&ms.z_free[c & 1], (c - 2) >> 1)) break;
+                fence_after();
+                unsigned char* Z = sm + L::kZ + (c & 1) * L::kTile;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t y1[16];
+                    tm_ld16_nowait(lanes + kTY1 + (c & 1) * 64 + 32 * hh + 16 * half, y1);
+                    tm_wait_ld();
+#pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         const uint32_t at = unit16(row, 4 * hh + 2 * half + j);
-                        u64 o[4];
+                        u64 v[4];
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int k = 8 * j + 2 * e;
-                            o[e] = ffma2(et2, add2(raw2(y2[k], y2[k + 1]), raw2(y3[k], y3[k + 1])), raw2(y1[k], y1[k + 1]));
+                            v[e] = add2(o[8 * half + 4 * j + e], raw2(y1[k], y1[k + 1]));
                         }
                         if (gated) {
                             const uint4 z = *reinterpret_cast<const uint4*>(Z + at);
-                            o[0] = gate_pair(o[0], z.x);
-                            o[1] = gate_pair(o[1], z.y);
-                            o[2] = gate_pair(o[2], z.z);
-                            o[3] = gate_pair(o[3], z.w);
+                            v[0] = gate_pair(v[0], z.x);
+                            v[1] = gate_pair(v[1], z.y);
+                            v[2] = gate_pair(v[2], z.z);
+                            v[3] = gate_pair(v[3], z.w);
                         }
-                        *reinterpret_cast<uint4*>(Z + at) = make_uint4(pack2(lo2(o[0]), hi2(o[0])), pack2(lo2(o[1]), hi2(o[1])),
-                                                                       pack2(lo2(o[2]), hi2(o[2])), pack2(lo2(o[3]), hi2(o[3])));
+                        *reinterpret_cast<uint4*>(Z + at) = make_uint4(pack2(lo2(v[0]), hi2(v[0])), pack2(lo2(v[1]), hi2(v[1])),
+                                                                       pack2(lo2(v[2]), hi2(v[2])), pack2(lo2(v[3]), hi2(v[3])));
                     }
                 }
                 fence_before();
@@ -883,7 +903,14 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
         const int quad = warp & 3, hh = (warp - kPm) >> 2;
         const int row = quad * 32 + lane;
         const float D = p.D ? ld(p.D + h) : 0.f;
-        for (int c = 0; c < wk.chunks; ++c) {
+        auto publish = [&]() {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) bar_arrive(&ms.xw_ready);
+        };
+        weigh(0, row, hh);
+        if (ok) publish();
+        for (int c = 0; c < wk.chunks && ok; ++c) {
             if (!need_warp(&ms.gates_full[c % kGates], c / kGates) || !need_warp(&ms.g_done, c)) break;
             fence_after();
             const Gates& gt = ms.gates[c % kGates];
@@ -939,6 +966,11 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
             fence_before();
             __syncwarp();
             if (lane == 0) bar_arrive(&ms.p_ready);
+            if (c + 1 < wk.chunks) {
+                if (!need_warp(&ms.ds_done, c)) break;           // Xw may be overwritten
+                weigh(c + 1, row, hh);
+                if (ok) publish();
+            }
         }
     }
     fence_before();
