@@ -1035,11 +1035,13 @@ cudaError_t launch_kernel(const ScanParams& sp, int64_t ctas, cudaStream_t strea
 // are measured: a chunk takes kChunk, or kAlone while every SM pair runs one CTA; a
 // chunk of the first launch kState with two CTAs an SM; a CTA's start and end kStart
 // or kStateStart, and kPart for every part that it starts from; the first launch kLaunch.
+// (Whole and cut: one prompt of 16384 tokens and 64 heads 317 and 208 us, of 4096 and 32
+// heads 83 and 43, of 1000 and 16 heads 25 and 18; below some 600 tokens whole is shorter.)
 struct Cut {
     int chunks, parts;
 };
 Cut cut(int batch, int num_tokens, int units) {
-    constexpr double kChunk = 2.8, kAlone = 2.45, kState = 1.75, kStart = 5.0, kStateStart = 4.0, kPart = 0.5, kLaunch = 3.0;
+    constexpr double kChunk = 2.6, kAlone = 2.25, kState = 1.75, kStart = 5.5, kStateStart = 4.0, kPart = 0.6, kLaunch = 3.0;
     const double sms = sm_count() ? sm_count() : 148;
     const double chunks = static_cast<double>((static_cast<int64_t>(num_tokens) + kQ - 1) / kQ);
     const double mean = chunks / batch, longest = batch > 1 ? 1.5 * mean : mean, whole = static_cast<double>(batch) * units;
