@@ -22,7 +22,10 @@ namespace {
 // the start of a sequence takes its window from the conv slot instead.  The
 // first W - 1 rows of a sequence always belong to the run that holds its first
 // row: that run alone reads the sequence's slot, and writes the new one after
-// it, so a slot may be updated in place.  HBM bandwidth bounds it.
+// it, so a slot may be updated in place.  HBM bandwidth bounds it: 16211 rows of
+// 4352 channels take 55 us, 5.2 TB/s of 6.8 measured (with the copies in registers 65, and
+// with one channel an instruction 81); half of the issue slots are in use, so the
+// rest is the start and the end of the runs.
 // (No early start of the next kernel: the step reads conv slots through __ldg,
 // which may run before its wait.)
 
@@ -262,7 +265,9 @@ cudaError_t launch_conv(ConvParams p, int width, cudaStream_t stream) {
 // the heads of a group repeat that of B and C (a few KB from L2 against 16 or
 // 32 KB of state a token), and the group's first CTA alone writes those
 // channels' conv slot.  HBM bandwidth on the state bounds large batches, the
-// chain of dependent reads small ones.
+// chain of dependent reads small ones: 64 sequences of up to 4 tokens and 64 heads with
+// N = 128 and FP32 states take 76 us, 6.0 TB/s of 6.8 measured (with the projection's rows
+// behind the state's 99); 2 of one token and 32 heads 6.2.
 
 template <typename StateT, int N>
 __global__ void __launch_bounds__(kRThreads, 4) gdn_ssm_decode_kernel(const Params p) {

@@ -26,15 +26,23 @@
 // with rows and depth exchanged need no transposed copy.  Pm goes back into the
 // tensor memory that G was in and is multiplied from there.
 //
-// Twenty warps.  0-7 keep the state: they weigh x, update S, write its images and
-// finish the outputs; 12-19 turn G into Pm, up to a chunk ahead of the others,
-// since G does not depend on the state; one warp each issues the products, issues
-// the copies, turns dt into decay factors some chunks ahead, and stores the
+// Twenty warps.  0-7 keep the state: they update S, write its images and finish
+// the outputs; 12-19 turn G into Pm and weigh the next chunk's x, ahead of the
+// others, since neither depends on the state; one warp each issues the products,
+// issues the copies, turns dt into decay factors some chunks ahead, and stores the
 // outputs.  (Two warps share the 32 rows of tensor memory that the hardware lets
-// them reach, and split the columns.)
+// them reach, and split the columns.)  In the first launch over segments 0-7 weigh.
 // They meet at mbarriers only.  dS of a chunk does not depend on the state either,
 // so the chain from chunk to chunk is the FP32 update of S and the product Y2.
 // Arithmetic runs on pairs of columns (fma.rn.f32x2).
+//
+// A chunk takes 4850 cycles with every SM at work (2.6 us; N = 128, gated): G, Pm
+// and Y1 one after another are 4400 of them, the state's warps are busy for 4000
+// (2050 for the outputs, 1024 of which the exponentials and reciprocals of the gate
+// fill their pipe), and the tensor pipe for 41 %.  16384 tokens of 64 heads take 208
+// us, 38 of them in the first launch (452 MB and 113 MB of DRAM traffic: 2.7 TB/s).
+// Loops that are not unrolled are so because five kinds of warps share the
+// instruction cache: with all of them unrolled that case took 466 us instead of 363.
 // Every wait is bounded: on a timeout the CTA sets GDN_FLAG_TIMEOUT, writes no
 // state, waits (bounded) for what it has in flight and releases its tensor
 // memory.
