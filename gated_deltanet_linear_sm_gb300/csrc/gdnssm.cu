@@ -516,7 +516,13 @@ gdn_status gdn_conv_prefill(const void* x, const void* conv_weight, const void* 
     p.batch = batch;
     p.num_tokens = num_tokens;
     p.dim = conv_dim;
-    const bool wide = conv_dim % 8 == 0 && p.x_stride % 8 == 0 && p.y_stride % 8 == 0 && aligned(x, 16) && aligned(y, 16) &&
+    // 8 channels a thread need twice the registers of 4, so half as many warps are resident: with few rows
+    // for each that shows (4096 rows of 2560 channels, 17 a thread: 15.7 us with 8, 13.0 with 4; 1000 of
+    // 2560 8.1 and 6.6), with many the wider accesses do (16211 of 4352, 113: 55 and 63; 2048 of 8448, 28:
+    // 18.1 and 19.3; alike around 20)
+    constexpr int kWideRows = 20;
+    const int64_t resident = static_cast<int64_t>(sm_count() ? sm_count() : 148) * 512;
+    const bool wide = static_cast<int64_t>(num_tokens) * (conv_dim / 8) >= kWideRows * resident && conv_dim % 8 == 0 && p.x_stride % 8 == 0 && p.y_stride % 8 == 0 && aligned(x, 16) && aligned(y, 16) &&
                       aligned(conv_pool, 16) && aligned(conv_bias, 16);
     const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t err = wide ? launch_conv<8>(p, cdims->width, st) : launch_conv<4>(p, cdims->width, st);

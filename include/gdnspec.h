@@ -527,7 +527,7 @@ GDNSPEC_API gdn_status gdn_step_tables(
  *
  * cdims->width 1..4.  conv_dim a multiple of 4; x, y, conv_weight, conv_bias
  * and conv_pool 8-byte aligned; x_stride and y_stride multiples of 4 (16-byte
- * aligned pointers and multiples of 8 run faster).  Sequences follow one
+ * aligned pointers and multiples of 8 run faster over many rows).  Sequences follow one
  * another: cu_seqlens does not decrease.  No conv_out[j] >= 0 equals another
  * sequence's conv_in or conv_out.  Bad device data skips the sequence: a conv
  * slot >= num_conv_slots sets GDN_FLAG_SLOT_RANGE, rows outside

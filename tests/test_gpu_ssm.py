@@ -132,6 +132,29 @@ def test_conv_run_lengths(cuda_device, lens):
     c.check(before)
 
 
+@pytest.mark.parametrize("W", [1, 2, 3, 4])
+def test_conv_of_many_rows_equals_its_slices(cuda_device, W):
+    """Enough rows and channels for 8 channels a thread: the bits of the same call on slices of the channels,
+    which are too few for that; and their definition on some channels."""
+    lens = [1, 2, 3, 700, 0, 5, 64, 1209, 4, 33]
+    D = 6464
+    c = Conv(cuda_device, lens, D, W, seed=40 + W, gap=3)
+    assert c.N * (D // 8) >= 20 * 512 * torch.cuda.get_device_properties(cuda_device).multi_processor_count
+    before = c.pool.clone()
+    c.run()
+    assert int(c.status) == 0
+    for lo in range(0, D, 1616):
+        cut = slice(lo, lo + 1616)
+        part = Conv(cuda_device, lens, 1616, W, seed=1, gap=3)
+        part.x, part.w, part.bias = c.x[:, cut], c.w[cut].contiguous(), c.bias[cut].contiguous()
+        part.pool = before[:, :, cut].contiguous()
+        old = part.pool.clone()
+        part.run()
+        if lo == 0:
+            part.check(old)
+        assert torch.equal(_bits(part.y), _bits(c.y[:, cut])) and torch.equal(_bits(part.pool), _bits(c.pool[:, :, cut]))
+
+
 def test_conv_in_place_and_in_chunks(cuda_device):
     """A prompt in three chunks, its slot updated in place, gives the bits of the whole prompt."""
     D, W = 520, 4
