@@ -27,9 +27,9 @@ namespace {
 // runs on a slow pipe: it held this kernel to a tenth of the memory's rate) but
 // as three sums of 22, 22 and 8 bits that floating-point additions of a constant
 // leave in the low bits of a float (Sums below).  The chain of dependent loads
-// bounds small batches (1 sequence of 5 rows of 32000: 5.6 us; 32 of 8 rows of 151936,
-// two FP32 rows read a sequence: 13.4, 2.0 TB/s), the issue slots of the sums large
-// ones (256 sequences of 128256 bf16 entries: 25.8 us, 2.5 TB/s; 92 with an integer an entry).
+// bounds small batches (1 sequence of 5 rows of 32000: 5.1 us; 32 of 8 rows of 151936,
+// two FP32 rows read a sequence: 11.2, 2.4 TB/s), the issue slots of the sums large
+// ones (256 sequences of 128256 bf16 entries: 24.7 us, 2.7 TB/s; 92 with an integer an entry).
 
 constexpr int kVThreads = 512;
 constexpr int kVWarps = kVThreads / 32;
@@ -151,7 +151,7 @@ struct VerifySmem {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kVThreads) gdn_verify_kernel(const VerifyParams p) {
+__global__ void __launch_bounds__(kVThreads, 2) gdn_verify_kernel(const VerifyParams p) {
     constexpr int E = Vec<T>::E;
     __shared__ VerifySmem s;
     cg::cluster_group cl = cg::this_cluster();
@@ -245,15 +245,15 @@ __global__ void __launch_bounds__(kVThreads) gdn_verify_kernel(const VerifyParam
     const int in0 = max(v0, mis > 0 ? 1 : 0), in1 = min(v1, static_cast<int>((static_cast<int64_t>(mis) + V) / E));
 
     // entries count as p (take 0), as p but for entry d (1), or as max(p - q, 0) (2):
-    // fixed(p) > fixed(q) only where p > q, so the last is a difference of two sums
+    // fixed does not decrease, so the last is fixed(max(p, q)) - fixed(q), a difference of two sums
     auto left_pair = [](u64 p, u64 q, Sums& P, Sums& Q) {
-        const bool a = lo2(p) > lo2(q), b = hi2(p) > hi2(q);
-        P.add(pk2(a ? lo2(p) : 0.f, b ? hi2(p) : 0.f));
-        Q.add(pk2(a ? lo2(q) : 0.f, b ? hi2(q) : 0.f));
+        P.add(pk2(fmaxf(lo2(p), lo2(q)), fmaxf(hi2(p), hi2(q))));
+        Q.add(q);
     };
     auto piece = [&](int how) {
-        // up to 256 entries a lane between two foldings into 64 bits; the loads of U vectors go out together
-        constexpr int kFold = 256 / E, U = 4;
+        // up to 256 entries a lane between two foldings into 64 bits; the loads of U vectors (UQ of each of two
+        // rows) go out together (1, 2, 3 of each: 12.9, 11.2, 13.2 us for 32 sequences of 151936 FP32 entries)
+        constexpr int kFold = 256 / E, U = 4, UQ = 2;
         const uint4 none = make_uint4(0, 0, 0, 0);
         long long sum = 0;
         for (int base = in0 + lane; base < in1; base += 32 * kFold) {
@@ -261,24 +261,24 @@ __global__ void __launch_bounds__(kVThreads) gdn_verify_kernel(const VerifyParam
             uint32_t n = 0;
             const int stop = min(in1, base + 32 * kFold);
             if (how == 2 && qvec) {
-                for (int v = base; v < stop; v += 32 * U) {
-                    uint4 pr[U], qr[U];
+                for (int v = base; v < stop; v += 32 * UQ) {
+                    uint4 pr[UQ], qr[UQ];
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
+                    for (int u = 0; u < UQ; ++u) {
                         const int e = (v + 32 * u) * E - mis;
                         const bool in = v + 32 * u < stop;
                         pr[u] = in ? ld(reinterpret_cast<const uint4*>(prow + e)) : none;
                         qr[u] = in ? ld(reinterpret_cast<const uint4*>(qrow + e)) : none;
                     }
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
+                    for (int u = 0; u < UQ; ++u) {
                         u64 pe[E / 2], qe[E / 2];
                         Vec<T>::pairs(pr[u], pe);
                         Vec<T>::pairs(qr[u], qe);
 #pragma unroll
                         for (int k = 0; k < E / 2; ++k) left_pair(pe[k], qe[k], P, Q);
                     }
-                    n += U * E;
+                    n += UQ * E;
                 }
             } else if (how == 2) {
                 for (int v = base; v < stop; v += 32) {          // the rows lie differently: q entry by entry
@@ -404,9 +404,8 @@ __global__ void __launch_bounds__(kVThreads) gdn_verify_kernel(const VerifyParam
 
 // CTAs per sequence: as many as are resident at once (two an SM: a second round
 // pays the chain of dependent loads again; 256 sequences of 128256 bf16 entries
-// take 25.8 us with one CTA each and 29.6 with two; 32 of 151936 FP32 entries 13.4 with
-// eight each) and leave each at least 1024
-// entries.
+// take 24.7 us with one CTA each; when that was 26, two each took 30) and leave each
+// at least 1024 entries.
 int verify_cluster(int batch, int vocab) {
     const int64_t room = 2 * static_cast<int64_t>(sm_count() ? sm_count() : 148);
     int cl = 1;
