@@ -267,7 +267,7 @@ cudaError_t launch_conv(ConvParams p, int width, cudaStream_t stream) {
 // channels' conv slot.  HBM bandwidth on the state bounds large batches, the
 // chain of dependent reads small ones: 64 sequences of up to 4 tokens and 64 heads with
 // N = 128 and FP32 states take 76 us, 6.0 TB/s of 6.8 measured (with the projection's rows
-// behind the state's 99); 2 of one token and 32 heads 6.2.
+// behind the state's 99); 2 of one token and 32 heads 4.9.
 
 template <typename StateT, int N>
 __global__ void __launch_bounds__(kRThreads, 4) gdn_ssm_decode_kernel(const Params p) {

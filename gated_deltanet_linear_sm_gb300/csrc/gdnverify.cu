@@ -439,8 +439,8 @@ cudaError_t launch_verify(const VerifyParams& p, cudaStream_t stream) {
 // the two totals, so that no CTA waits for another, then writes its tile's
 // per-request tables and the row numbers of its tile's rows, one thread a row
 // (a prompt's thousands of rows are spread over the CTA like any others).
-// Launch latency and two dependent reads bound it (128 requests 6.1 us, 4096 with
-// prompts among them 7.8).
+// Launch latency and two dependent reads bound it (128 requests 4.6 us, 4096 with
+// prompts among them 7.7).
 
 constexpr int kTThreads = 256;
 constexpr int kTile = 64;

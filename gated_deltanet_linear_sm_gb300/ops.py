@@ -83,10 +83,13 @@ class PreparedOp:
     def __call__(self, stream=None):
         """Launch on `stream`: a torch.cuda.Stream, a raw cudaStream_t handle
         (int), or None for the current stream."""
+        # (the handle and the device without the objects around them: the host's time bounds the
+        # smallest calls, 5.2 us each with torch.cuda.current_stream, 3.8 like this)
         if stream is None:
-            stream = torch.cuda.current_stream(self._index)
-        handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
-        if torch.cuda.current_device() == self._index:
+            handle = torch._C._cuda_getCurrentRawStream(self._index)
+        else:
+            handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+        if torch._C._cuda_getDevice() == self._index:
             rc = self._fn(*self._args, handle)
         else:
             with torch.cuda.device(self._index):
