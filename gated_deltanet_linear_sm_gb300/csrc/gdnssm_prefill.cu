@@ -1039,7 +1039,9 @@ cudaError_t launch_kernel(const ScanParams& sp, int64_t ctas, cudaStream_t strea
 // How the prompts are cut: chunks of a segment (0: whole sequences) and parts of a
 // segment in the first launch, whichever an estimate of the time says is shorter.
 // The host knows the rows and the sequences but not their lengths; with several it
-// takes the longest for half as long again as the mean.  The estimate's constants, in us,
+// takes the longest for twice as long as the mean (four prompts of 4096 tokens in all, 16
+// heads, us whole and cut at 6 chunks: 45 and 31 with lengths far apart, 26 and 31 alike).
+// The estimate's constants, in us,
 // are measured: a chunk takes kChunk, or kAlone while every SM pair runs one CTA; a
 // chunk of the first launch kState with two CTAs an SM; a CTA's start and end kStart
 // or kStateStart, and kPart for every part that it starts from; the first launch kLaunch.
@@ -1052,9 +1054,13 @@ Cut cut(int batch, int num_tokens, int units) {
     constexpr double kChunk = 2.6, kAlone = 2.25, kState = 1.75, kStart = 5.5, kStateStart = 4.0, kPart = 0.6, kLaunch = 3.0;
     const double sms = sm_count() ? sm_count() : 148;
     const double chunks = static_cast<double>((static_cast<int64_t>(num_tokens) + kQ - 1) / kQ);
-    const double mean = chunks / batch, longest = batch > 1 ? 1.5 * mean : mean, whole = static_cast<double>(batch) * units;
+    const double mean = chunks / batch, longest = batch > 1 ? 2 * mean : mean, whole = static_cast<double>(batch) * units;
     const double c0 = 2 * whole <= sms ? kAlone : kChunk;
-    double best = batch > 1 ? std::max(longest * c0 + kStart, (chunks * c0 + batch * kStart) * units / sms + 0.5 * (mean * c0 + kStart))
+    // CTAs that are resident at once take as long as the longest; more, their sum and half of one
+    auto several = [&](double ctas, double sum, double each, double most) {
+        return ctas <= sms ? most : std::max(most, sum / sms + 0.5 * each);
+    };
+    double best = batch > 1 ? several(whole, (chunks * c0 + batch * kStart) * units, mean * c0 + kStart, longest * c0 + kStart)
                             : std::ceil(whole / sms) * (chunks * c0 + kStart);
     Cut take = {0, 1};
     for (int parts = 1; parts <= 4; parts *= 2)
@@ -1063,8 +1069,8 @@ Cut cut(int batch, int num_tokens, int units) {
             if (batch > 1) {
                 const double segments = chunks / k + 0.5 * batch, before = std::max(chunks / k - 0.5 * batch, 0.0);
                 const double c = 2 * segments * units <= sms ? kAlone : kChunk, start = kStart + kPart * 0.5 * parts * longest / k;
-                cost += std::max(k * c + start, (chunks * c + segments * start) * units / sms + 0.5 * (k * c + start)) +
-                        std::ceil(std::ceil(before * parts * units) / (2 * sms)) * (k / parts * kState + kStateStart);
+                cost += several(segments * units, (chunks * c + segments * start) * units, k * c + start, k * c + start) +
+                        std::max(std::ceil(before * parts * units / (2 * sms)), 1.0) * (k / parts * kState + kStateStart);
             } else {
                 // units * before segments of k chunks, then as many shorter ones as there are units
                 const double before = std::ceil(chunks / k) - 1, rest = chunks - before * k;
