@@ -1109,12 +1109,13 @@ cudaError_t launch(ScanParams& sp, int units, void* workspace, cudaStream_t stre
     if (sp.seg_chunks == 0) return launch_kernel<StateT, N, false>(sp, static_cast<int64_t>(p.batch) * units, stream);
     sp.part_chunks = c.chunks / c.parts;
     const int64_t before = segments_before(p.num_tokens, c), room = part_room(p.batch, p.num_tokens, c);
-    if (std::max(before + p.batch, before * c.parts) * units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (std::max(before + p.batch, room) * units > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     sp.part_room = static_cast<int32_t>(room);
     sp.part = static_cast<float*>(workspace);
     sp.part_decay = sp.part + room * units * N * kPB;
     if (before > 0) {
-        const cudaError_t e = launch_kernel<StateT, N, true>(sp, before * c.parts * units, stream);
+        // (some more than there are parts, so that every part in the workspace is written whatever the offsets)
+        const cudaError_t e = launch_kernel<StateT, N, true>(sp, room * units, stream);
         if (e != cudaSuccess) return e;
     }
     return launch_kernel<StateT, N, false>(sp, (before + p.batch) * units, stream);
