@@ -382,6 +382,31 @@ def test_scan_of_cut_prompts_in_place(cuda_device, state):
             assert torch.equal(_bits(a.pool[a.write[i]]), _bits(b.pool[b.write[i]]))
 
 
+def _random_scan(dev, seed):
+    """Sizes from short prompts to ones that are cut, with and without every option."""
+    rng = np.random.default_rng(1000 + seed)
+    n = int(rng.choice([1, 1, 2, 3, 7, 40]))
+    total = int(np.exp(rng.uniform(np.log(20), np.log(2600))))
+    lens = rng.multinomial(total, rng.dirichlet(np.ones(n) * float(rng.choice([0.3, 1.0, 20.0])))).tolist()
+    G = int(rng.choice([1, 1, 2, 3]))
+    H = G * int(rng.choice([1, 2, 4]))
+    read = [2 * i if rng.random() < 0.7 else -1 for i in range(n)]
+    s = Scan(dev, lens, H, G, 64 * int(rng.choice([1, 1, 2])), int(rng.choice([64, 128])), str(rng.choice(["f32", "bf16", "f16"])),
+             gap=int(rng.integers(0, 9)), read=read, packed=bool(rng.random() < 0.5), gate=bool(rng.random() < 0.6),
+             skip=bool(rng.random() < 0.6), strong=bool(rng.random() < 0.3), seed=seed)
+    s.write = [(r if r >= 0 and rng.random() < 0.5 else 2 * i + 1) if rng.random() < 0.9 else -1 for i, r in enumerate(read)]
+    return s
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_scan_of_random_sizes(cuda_device, seed):
+    s = _random_scan(cuda_device, seed)
+    before = s.pool.clone()
+    s.run()
+    s.check(before)
+    assert int(s.status) == 0
+
+
 def test_scan_keeps_infinite_and_nan_rows_to_their_sequence(cuda_device):
     """Rows of NaN and infinity in the neighbouring sequences, and behind the last one, reach nobody else."""
     lens = [130, 70, 129]
