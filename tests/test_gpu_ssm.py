@@ -155,6 +155,21 @@ def test_conv_of_many_rows_equals_its_slices(cuda_device, W):
         assert torch.equal(_bits(part.y), _bits(c.y[:, cut])) and torch.equal(_bits(part.pool), _bits(c.pool[:, :, cut]))
 
 
+@pytest.mark.parametrize("seed", range(8))
+def test_conv_of_random_sizes(cuda_device, seed):
+    rng = np.random.default_rng(seed)
+    n = int(rng.choice([1, 2, 5, 60]))
+    lens = rng.integers(0, int(rng.choice([3, 9, 200])), n).tolist()
+    lens[0] += 1
+    c = Conv(cuda_device, lens, 4 * int(rng.integers(1, 300)), int(rng.integers(1, 5)), seed=seed, bias=bool(rng.random() < 0.6),
+             gap=int(rng.integers(0, 5)), pad_x=4 * int(rng.integers(0, 4)), pad_y=4 * int(rng.integers(0, 4)),
+             shift=int(rng.choice([0, 0, 4, 8])))
+    before = c.pool.clone()
+    c.run()
+    c.check(before)
+    assert int(c.status) == 0
+
+
 def test_conv_in_place_and_in_chunks(cuda_device):
     """A prompt in three chunks, its slot updated in place, gives the bits of the whole prompt."""
     D, W = 520, 4
@@ -611,6 +626,23 @@ def test_step_widths(cuda_device, W, bias):
 @pytest.mark.parametrize("kw", [dict(gate=False), dict(skip=False), dict(strong=True)])
 def test_step_options(cuda_device, kw):
     Step(cuda_device, [2, 4], 4, 2, 1, 64, 128, "f32", seed=31, **kw).go()
+
+
+@pytest.mark.parametrize("seed", range(8))
+def test_step_of_random_sizes(cuda_device, seed):
+    rng = np.random.default_rng(seed)
+    n, T = int(rng.choice([1, 3, 9, 40])), int(rng.integers(1, 9))
+    q = rng.integers(0, T + 1, n).tolist()
+    q[0] = max(q[0], 1)
+    G = int(rng.choice([1, 2, 3]))
+    s = Step(cuda_device, q, T, G * int(rng.choice([1, 2, 4])), G, 64 * int(rng.choice([1, 1, 2, 3])), int(rng.choice([64, 128])),
+             str(rng.choice(["f32", "bf16", "f16"])), W=int(rng.integers(1, 5)), gather=bool(rng.random() < 0.5),
+             bias=bool(rng.random() < 0.5), seed=seed, gate=bool(rng.random() < 0.6), skip=bool(rng.random() < 0.6),
+             strong=bool(rng.random() < 0.3))
+    pool, conv = s.pool.clone(), s.conv_pool.clone()
+    s.run()
+    s.check(pool, conv)
+    assert int(s.status) == 0
 
 
 def test_step_padded_slots(cuda_device):

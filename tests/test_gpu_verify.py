@@ -95,6 +95,20 @@ def test_rows_at_any_element(cuda_device, dtype, offset):
     b.check()
 
 
+@pytest.mark.parametrize("seed", range(8))
+def test_random_sizes(cuda_device, seed):
+    rng = np.random.default_rng(seed)
+    n, T = int(rng.choice([1, 2, 9, 80])), int(rng.integers(1, 9))
+    q = rng.integers(0, T + 1, n).tolist()
+    q[0] = max(q[0], 1)
+    V = int(np.exp(rng.uniform(0, np.log(9000 if n > 9 else 60000))))
+    b = Batch(cuda_device, q, T, V, str(rng.choice(["f32", "bf16", "f16"])), draft=bool(rng.random() < 0.6), seed=seed,
+              gather=bool(rng.random() < 0.5), sharp=float(rng.choice([0.5, 3, 8])), near=float(rng.choice([0.1, 0.7, 2])),
+              offset=int(rng.choice([0, 0, 1, 3, 5])))
+    b.run()
+    b.check()
+
+
 def test_gathered_rows_and_strides(cuda_device):
     """Rows through spec_token_indx; the target's rows and the draft tables inside wider tensors; the
     drafter's rows stacked step by step."""
