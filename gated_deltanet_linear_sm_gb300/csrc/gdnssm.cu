@@ -15,7 +15,7 @@ namespace {
 //
 // A thread owns 8 (or 4) neighbouring channels of a run of rows and slides a
 // window of the last W - 1 inputs, in FP32 registers, along them: x is read
-// once (W - 1 rows a run twice) and y written once, in 16-byte accesses.  Up to 12
+// once (W - 1 rows a run twice) and y written once, in 16-byte accesses.  Up to 8
 // rows a thread are on their way through asynchronous copies into places of its
 // own in shared memory; the arithmetic runs on pairs of channels.  Rows are cut into runs of the whole token batch,
 // not of a sequence, so ragged prompts fill the GPU evenly; a run that crosses
@@ -23,7 +23,7 @@ namespace {
 // first W - 1 rows of a sequence always belong to the run that holds its first
 // row: that run alone reads the sequence's slot, and writes the new one after
 // it, so a slot may be updated in place.  HBM bandwidth bounds it: 16211 rows of
-// 4352 channels take 55 us, 5.2 TB/s of 6.8 measured (with the copies in registers 65, and
+// 4352 channels take 53 us, 5.3 TB/s of 6.8 measured (with the copies in registers 65, and
 // with one channel an instruction 81); half of the issue slots are in use, so the
 // rest is the start and the end of the runs.
 // (No early start of the next kernel: the step reads conv slots through __ldg,
@@ -76,7 +76,7 @@ __device__ __forceinline__ int conv_flag(const ConvParams& p, int s, int e, int 
 template <int CV, int W>
 __global__ void __launch_bounds__(kCThreads, 4) gdn_conv_prefill_kernel(const ConvParams p) {
     constexpr int HN = W > 1 ? W - 1 : 1;
-    constexpr int U = 4, kAhead = 3, kRing = U * (kAhead + 1);
+    constexpr int U = 4, kAhead = 2, kRing = U * (kAhead + 1);
     __shared__ Raw<CV> ring[kRing][kCThreads];
     dep_wait();
     const int cb = blockIdx.x % p.col_blocks;
@@ -183,12 +183,11 @@ __global__ void __launch_bounds__(kCThreads, 4) gdn_conv_prefill_kernel(const Co
         for (int r = a; r < b; r += U) {
             fetch(r + kAhead * U);
             asm volatile("cp.async.wait_group %0;" ::"n"(kAhead) : "memory");
-            Raw<CV> raw[U];
+            Raw<CV> raw[U];                         // (rows behind b are worked on too, for the sake of one block of code)
 #pragma unroll
             for (int u = 0; u < U; ++u) raw[u] = ring[(r - a + u) % kRing][threadIdx.x];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (r + u >= b) break;
                 u64 v[CV / 2];
                 widen_all<CV>(raw[u], v);
                 Raw<CV> o;
@@ -209,7 +208,7 @@ __global__ void __launch_bounds__(kCThreads, 4) gdn_conv_prefill_kernel(const Co
 #pragma unroll
                     for (int e2 = 0; e2 < CV / 2; ++e2) f[W - 2][e2] = v[e2];
                 }
-                *reinterpret_cast<Raw<CV>*>(p.y + (r + u) * p.y_stride + c) = o;
+                if (r + u < b) *reinterpret_cast<Raw<CV>*>(p.y + (r + u) * p.y_stride + c) = o;
             }
         }
     }
