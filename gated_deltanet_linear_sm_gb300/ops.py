@@ -64,9 +64,8 @@ binding.EXPORTS.update({
 
 class PreparedOp:
     """A marshalled call; invoking it launches on the given stream (default:
-    the current stream of its device).  It keeps its tensors alive, the
-    workspace of gdn_ssm_prefill among them: two streams must not run one
-    prepared prefill at the same time."""
+    the current stream of its device).  It keeps its tensors alive; keep it
+    while a graph that captured it may be replayed."""
 
     __slots__ = ("_fn", "_args", "_device", "_index", "_keep")
 
@@ -89,13 +88,37 @@ class PreparedOp:
             handle = torch._C._cuda_getCurrentRawStream(self._index)
         else:
             handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+        self._launch(self._args, handle)
+
+    def _launch(self, args, handle):
         if torch._C._cuda_getDevice() == self._index:
-            rc = self._fn(*self._args, handle)
+            rc = self._fn(*args, handle)
         else:
             with torch.cuda.device(self._index):
-                rc = self._fn(*self._args, handle)
+                rc = self._fn(*args, handle)
         if rc != 0:
             raise GdnError(rc, binding.status_str(rc))
+
+
+class PreparedScan(PreparedOp):
+    """A prepared gdn_ssm_prefill whose caller gave no workspace: each launch
+    takes one from the memory of the stream that it runs on, where nothing else
+    can be given it before the launch has run.  So one such call may run on
+    several streams at once and be dropped while it runs, and a graph that
+    captures it holds a workspace of its own."""
+
+    __slots__ = ("_at", "_bytes")
+
+    def __init__(self, entry, args, device, keep, at, nbytes):
+        super().__init__(entry, args, device, keep)
+        self._at, self._bytes = at, nbytes
+
+    def _launch(self, args, handle):
+        workspace = torch.cuda.caching_allocator_alloc(self._bytes, self._index, handle)
+        try:
+            super()._launch(args[:self._at] + (workspace,) + args[self._at + 1:], handle)
+        finally:
+            torch.cuda.caching_allocator_delete(workspace)
 
 
 # ---- checks ------------------------------------------------------------------
@@ -359,7 +382,9 @@ def _ssm_dims(B, N, H, G, P, S, state_pool, dt, z, out) -> gdn_ssm_dims:
 
 def prepare_ssm_prefill(x, B, C, dt, z, A_log, dt_bias, D, state_pool, read_slots, write_slots, cu_seqlens, out, *,
                         workspace=None, status=None) -> PreparedOp:
-    """A prepared gdn_ssm_prefill call (see there)."""
+    """A prepared gdn_ssm_prefill call (see there).  Without ``workspace`` each
+    of its launches takes one (PreparedScan); with it, calls on two streams or
+    from two graphs must not run at the same time."""
     _shape(x, "x", (None, None, None))
     N, H, P = x.shape
     _shape(B, "B", (N, None, None))
@@ -379,18 +404,17 @@ def prepare_ssm_prefill(x, B, C, dt, z, A_log, dt_bias, D, state_pool, read_slot
     d = _ssm_dims(n, N, H, G, P, S, state_pool, dt, z, out)
     d.x_stride, d.b_stride, d.c_stride = _rows(x, "x"), _rows(B, "B"), _rows(C, "C")
     need = ssm_prefill_workspace(d, dev)
-    if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need > 0 else None
-    else:
+    if workspace is not None:
         _typed(dev, torch.uint8, contiguous=True, workspace=workspace)
         if workspace.numel() < need:
             raise ValueError(f"expected workspace of at least {need} bytes; got {workspace.numel()}")
-    return PreparedOp("gdn_ssm_prefill",
-                      [_ptr(x), _ptr(B), _ptr(C), _ptr(dt), _ptr(z), _ptr(A_log), _ptr(dt_bias), _ptr(D),
-                       _ptr(state_pool), _ptr(read_slots), _ptr(write_slots), _ptr(cu_seqlens), _ptr(out),
-                       _ptr(workspace), max(need, 0), d, _STATE_DTYPES[state_pool.dtype], _ptr(status)], dev,
-                      (x, B, C, dt, z, A_log, dt_bias, D, state_pool, read_slots, write_slots, cu_seqlens, out,
-                       workspace, status))
+    args = [_ptr(x), _ptr(B), _ptr(C), _ptr(dt), _ptr(z), _ptr(A_log), _ptr(dt_bias), _ptr(D), _ptr(state_pool),
+            _ptr(read_slots), _ptr(write_slots), _ptr(cu_seqlens), _ptr(out), _ptr(workspace), need, d,
+            _STATE_DTYPES[state_pool.dtype], _ptr(status)]
+    keep = (x, B, C, dt, z, A_log, dt_bias, D, state_pool, read_slots, write_slots, cu_seqlens, out, workspace, status)
+    if need == 0 or workspace is not None:
+        return PreparedOp("gdn_ssm_prefill", args, dev, keep)
+    return PreparedScan("gdn_ssm_prefill", args, dev, keep, at=13, nbytes=need)
 
 
 def ssm_prefill_workspace(dims, device=None) -> int:
@@ -410,18 +434,10 @@ def gdn_ssm_prefill(x, B, C, dt, z, A_log, dt_bias, D, state_pool, read_slots, w
     dt_bias [H] bf16, A_log and D [H] fp32 (z and D may be None), state_pool
     [slots, H, S, P] fp32 / bf16 / fp16 (slots write_slots written), read_slots,
     write_slots [B] and cu_seqlens [B+1] int32.  ``workspace``: uint8, at least
-    what gdn_ssm_prefill_workspace asks for (default: allocated on the call's
-    stream).  Returns ``out``."""
-    def call():
-        prepare_ssm_prefill(x, B, C, dt, z, A_log, dt_bias, D, state_pool, read_slots, write_slots, cu_seqlens, out,
-                            workspace=workspace, status=status)(stream)
-    if stream is None or workspace is not None:
-        call()
-    else:
-        # the workspace belongs to the stream that uses it
-        s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(stream, device=x.device)
-        with torch.cuda.stream(s):
-            call()
+    what gdn_ssm_prefill_workspace asks for, used by this call alone until it
+    has run (default: each launch takes one on its stream).  Returns ``out``."""
+    prepare_ssm_prefill(x, B, C, dt, z, A_log, dt_bias, D, state_pool, read_slots, write_slots, cu_seqlens, out,
+                        workspace=workspace, status=status)(stream)
     return out
 
 
