@@ -345,7 +345,9 @@ struct Work {
 // launch's index is looked up among the sequences' counts: of segments, or (the
 // states alone) of the parts before each sequence's last segment.  In the
 // workspace a sequence of several segments has its initial state, then those
-// parts.  One warp, 32 sequences at a time; every warp does the same.
+// parts.  One warp, 32 sequences at a time; every warp does the same.  Bad data is
+// reported once: by the first CTA of every 32 sequences, or, with segments, by the
+// second launch's first CTA, which therefore looks at all sequences.
 template <bool kStates>
 __device__ Work find_work(const ScanParams& sp, int index, int lane) {
     const Params& p = sp.p;
@@ -383,7 +385,7 @@ __device__ Work find_work(const ScanParams& sp, int index, int lane) {
         int bos = 0, eos = 0, n = 0;
         if (i < p.batch) {
             const int f = bounds(i, bos, eos);
-            if (f > 0 && blockIdx.x == 0 && threadIdx.x < 32) raise(p.status, f);
+            if (!kStates && f > 0 && blockIdx.x == 0 && threadIdx.x < 32) raise(p.status, f);
             if (f == -1) n = ((eos - bos + kQ - 1) / kQ + sp.seg_chunks - 1) / sp.seg_chunks;
         }
         const int parts = n > 0 ? (n - 1) * sp.parts : 0, count = kStates ? parts : n;
@@ -415,7 +417,7 @@ __device__ Work find_work(const ScanParams& sp, int index, int lane) {
                 if (threadIdx.x == 0) raise(p.status, GDN_FLAG_TOKEN_ROW);
                 w.kind = 0;
             }
-            return w;
+            if (kStates || blockIdx.x != 0) return w;
         }
         base += __shfl_sync(kFull, upto, 31);
         room_base += __shfl_sync(kFull, room_upto, 31);
