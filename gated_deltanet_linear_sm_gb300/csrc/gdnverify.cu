@@ -1,6 +1,6 @@
 // libgdnspec: what runs between two steps of speculative decoding -- the
-// verification of the drafted tokens (gdn_verify_drafts) and the tables of the
-// next step (gdn_step_tables).  Declared in include/gdnspec.h.
+// verification of the drafted tokens (gdn_verify_drafts, and
+// gdn_verify_drafts_by_request for its counts by request) and the tables of the next step (gdn_step_tables).  Declared in include/gdnspec.h.
 #include <cooperative_groups.h>
 
 #include "gdn_common.h"
@@ -44,11 +44,12 @@ struct VerifyParams {
     const float* sample_u;
     const int32_t* cu;
     const int32_t* sti;
+    const int32_t* request;                     // null: counts in batch order
     int32_t* out;
     int32_t* accepted;
     int32_t* status;
     int64_t target_stride, draft_stride, draft_seq, token_stride;
-    int32_t batch, num_tokens, vocab, max_T;
+    int32_t batch, num_tokens, vocab, max_T, num_requests;
 };
 
 __device__ __forceinline__ float clamp01(float p) { return fminf(fmaxf(p, 0.0f), 1.0f); }   // NaN -> 0
@@ -219,7 +220,12 @@ __global__ void __launch_bounds__(kVThreads, 2) gdn_verify_kernel(const VerifyPa
             if (lane < p.max_T && !(valid && lane == kept))
                 p.out[static_cast<int64_t>(i) * p.max_T + lane] = valid && lane < kept ? d : -1;
             if (lane == 0) {
-                if (valid) p.accepted[i] = kept + 1;
+                if (valid) {                       // (read only here: beside the offsets it costs 256 x 128256 2.8 us, by the
+                                                   //  order that the compiler then gives the sums)
+                    const int at = p.request ? ld(p.request + i) : i;
+                    if (p.request && at >= p.num_requests) flag = GDN_FLAG_SLOT_RANGE;
+                    else if (at >= 0) p.accepted[at] = kept + 1;
+                }
                 if (flag) raise(p.status, flag);
             }
         }
@@ -599,27 +605,24 @@ __global__ void __launch_bounds__(kTThreads) gdn_step_tables_kernel(const Tables
     }
 }
 
-}  // namespace
-
-extern "C" {
-
-gdn_status gdn_verify_drafts(const void* target_probs, const void* draft_probs, const int32_t* draft_tokens,
-                             const float* accept_u, const float* sample_u, const int32_t* cu_seqlens,
-                             const int32_t* spec_token_indx, int32_t* out_tokens, int32_t* num_accepted,
-                             const gdn_verify_dims* dims, gdn_dtype prob_dtype, int32_t* status_word,
-                             gdn_stream_t stream) {
+// what both entry points of the verification check and launch (request null: num_accepted in batch order)
+gdn_status verify(const void* target_probs, const void* draft_probs, const int32_t* draft_tokens, const float* accept_u,
+                  const float* sample_u, const int32_t* cu_seqlens, const int32_t* spec_token_indx, const int32_t* request,
+                  int32_t* out_tokens, int32_t* num_accepted, const gdn_verify_dims* dims, int32_t num_requests,
+                  gdn_dtype prob_dtype, int32_t* status_word, gdn_stream_t stream) {
     if (dims == nullptr) return GDN_ERR_NULL_ARG;
     if (dims->batch < 0 || dims->num_tokens < 0 || dims->vocab < 1 || dims->vocab > 0x7fff0000 || dims->max_T < 1 ||
         dims->max_T > kMaxDraftT || dims->target_stride < 0 || dims->draft_stride < 0 || dims->draft_seq < 0 ||
         dims->token_stride < 0 || dims->batch > 0x7fffffff / kMaxCluster || dims->num_tokens > kMaxRows)
         return GDN_ERR_BAD_SHAPE;
+    if (num_requests < 0) return GDN_ERR_BAD_SHAPE;
     if (!is_dtype(prob_dtype)) return GDN_ERR_UNSUPPORTED;
     if (dims->batch == 0) return GDN_OK;
     if ((dims->num_tokens > 0 && !target_probs) || !sample_u || !cu_seqlens || !out_tokens || !num_accepted) return GDN_ERR_NULL_ARG;
     if (dims->max_T > 1 && (!draft_tokens || !accept_u)) return GDN_ERR_NULL_ARG;
     const uintptr_t elem = prob_dtype == GDN_F32 ? 4 : 2;
     if (!aligned(target_probs, elem) || !aligned(draft_probs, elem) || !aligned(draft_tokens, 4) ||
-        !aligned(accept_u, 4) || !aligned(sample_u, 4) || !aligned(cu_seqlens, 4) || !aligned(spec_token_indx, 4) ||
+        !aligned(accept_u, 4) || !aligned(sample_u, 4) || !aligned(cu_seqlens, 4) || !aligned(spec_token_indx, 4) || !aligned(request, 4) ||
         !aligned(out_tokens, 4) || !aligned(num_accepted, 4) || !aligned(status_word, 4))
         return GDN_ERR_MISALIGNED;
     VerifyParams p;
@@ -630,6 +633,8 @@ gdn_status gdn_verify_drafts(const void* target_probs, const void* draft_probs, 
     p.sample_u = sample_u;
     p.cu = cu_seqlens;
     p.sti = spec_token_indx;
+    p.request = request;
+    p.num_requests = num_requests;
     p.out = out_tokens;
     p.accepted = num_accepted;
     p.status = status_word;
@@ -646,6 +651,29 @@ gdn_status gdn_verify_drafts(const void* target_probs, const void* draft_probs, 
                             : prob_dtype == GDN_BF16 ? launch_verify<__nv_bfloat16>(p, s)
                                                      : launch_verify<__half>(p, s);
     return err == cudaSuccess ? GDN_OK : GDN_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+gdn_status gdn_verify_drafts(const void* target_probs, const void* draft_probs, const int32_t* draft_tokens,
+                             const float* accept_u, const float* sample_u, const int32_t* cu_seqlens,
+                             const int32_t* spec_token_indx, int32_t* out_tokens, int32_t* num_accepted,
+                             const gdn_verify_dims* dims, gdn_dtype prob_dtype, int32_t* status_word,
+                             gdn_stream_t stream) {
+    return verify(target_probs, draft_probs, draft_tokens, accept_u, sample_u, cu_seqlens, spec_token_indx, nullptr, out_tokens,
+                  num_accepted, dims, 0, prob_dtype, status_word, stream);
+}
+
+gdn_status gdn_verify_drafts_by_request(const void* target_probs, const void* draft_probs, const int32_t* draft_tokens,
+                                        const float* accept_u, const float* sample_u, const int32_t* cu_seqlens,
+                                        const int32_t* spec_token_indx, const int32_t* request, int32_t* out_tokens,
+                                        int32_t* num_accepted, const gdn_verify_dims* dims, int32_t num_requests,
+                                        gdn_dtype prob_dtype, int32_t* status_word, gdn_stream_t stream) {
+    if (dims != nullptr && dims->batch > 0 && !request) return GDN_ERR_NULL_ARG;
+    return verify(target_probs, draft_probs, draft_tokens, accept_u, sample_u, cu_seqlens, spec_token_indx, request, out_tokens,
+                  num_accepted, dims, num_requests, prob_dtype, status_word, stream);
 }
 
 gdn_status gdn_step_tables(const int32_t* q_lens, const int32_t* spec, const int32_t* request,

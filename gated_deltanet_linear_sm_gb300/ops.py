@@ -52,6 +52,8 @@ class gdn_ssm_dims(ctypes.Structure):
 _VP = ctypes.c_void_p
 binding.EXPORTS.update({
     "gdn_verify_drafts": (ctypes.c_int, [_VP] * 9 + [ctypes.POINTER(gdn_verify_dims), ctypes.c_int, _VP, _VP]),
+    "gdn_verify_drafts_by_request": (ctypes.c_int, [_VP] * 10 + [ctypes.POINTER(gdn_verify_dims), ctypes.c_int32, ctypes.c_int,
+                                                                 _VP, _VP]),
     "gdn_step_tables": (ctypes.c_int, [_VP] * 14 + [ctypes.POINTER(gdn_tables_dims), _VP, _VP]),
     "gdn_conv_prefill": (ctypes.c_int, [_VP] * 8 + [ctypes.c_int32] * 3 +
                          [ctypes.c_int64, ctypes.POINTER(gdn_conv_dims), _VP, _VP]),
@@ -185,7 +187,7 @@ def _pool(pool, dev):
 
 
 def prepare_verify_drafts(target_probs, draft_tokens, accept_u, sample_u, cu_seqlens, out_tokens, num_accepted, *,
-                          draft_probs=None, spec_token_indx=None, status=None) -> PreparedOp:
+                          draft_probs=None, spec_token_indx=None, request=None, status=None) -> PreparedOp:
     """A prepared gdn_verify_drafts call (see there)."""
     if target_probs.dim() != 2 or out_tokens.dim() != 2 or target_probs.shape[1] < 1 or out_tokens.shape[1] < 1:
         raise ValueError(f"expected target_probs [N, V] and out_tokens [B, T]; got {tuple(target_probs.shape)}, "
@@ -202,7 +204,9 @@ def prepare_verify_drafts(target_probs, draft_tokens, accept_u, sample_u, cu_seq
     else:
         draft_tokens = accept_u = draft_probs = None
     _shape(sample_u, "sample_u", (B,))
-    _shape(num_accepted, "num_accepted", (B,))
+    if request is not None:
+        _shape(request, "request", (B,))
+    _shape(num_accepted, "num_accepted", (B if request is None else None,))
     _shape(cu_seqlens, "cu_seqlens", (B + 1,))
     dev = target_probs.device
     _cuda(dev, "gdn_verify_drafts")
@@ -212,8 +216,8 @@ def prepare_verify_drafts(target_probs, draft_tokens, accept_u, sample_u, cu_seq
     _typed(dev, _F32, accept_u=accept_u)
     _typed(dev, _F32, contiguous=True, sample_u=sample_u)
     _typed(dev, _I32, draft_tokens=draft_tokens)
-    _dense(dev, cu_seqlens=cu_seqlens, spec_token_indx=spec_token_indx, out_tokens=out_tokens,
-           num_accepted=num_accepted, status=status)
+    _dense(dev, cu_seqlens=cu_seqlens, spec_token_indx=spec_token_indx, request=request,
+           out_tokens=out_tokens, num_accepted=num_accepted, status=status)
     d = gdn_verify_dims()
     d.batch, d.num_tokens, d.vocab, d.max_T = B, N, V, T
     d.target_stride = _rows(target_probs, "target_probs")
@@ -229,24 +233,30 @@ def prepare_verify_drafts(target_probs, draft_tokens, accept_u, sample_u, cu_seq
             d.draft_stride = draft_probs.stride(1) if draft_probs.shape[1] > 1 else 0
             if (B > 1 and d.draft_seq < V) or (draft_probs.shape[1] > 1 and d.draft_stride < V):
                 raise ValueError("draft_probs: rows overlap")
-    return PreparedOp("gdn_verify_drafts",
-                      [_ptr(target_probs), _ptr(draft_probs), _ptr(draft_tokens), _ptr(accept_u), _ptr(sample_u),
-                       _ptr(cu_seqlens), _ptr(spec_token_indx), _ptr(out_tokens), _ptr(num_accepted), d,
-                       _STATE_DTYPES[target_probs.dtype], _ptr(status)], dev,
-                      (target_probs, draft_probs, draft_tokens, accept_u, sample_u, cu_seqlens, spec_token_indx,
-                       out_tokens, num_accepted, status))
+    ins = [_ptr(target_probs), _ptr(draft_probs), _ptr(draft_tokens), _ptr(accept_u), _ptr(sample_u), _ptr(cu_seqlens),
+           _ptr(spec_token_indx)]
+    outs, dtype = [_ptr(out_tokens), _ptr(num_accepted), d], _STATE_DTYPES[target_probs.dtype]
+    keep = (target_probs, draft_probs, draft_tokens, accept_u, sample_u, cu_seqlens, spec_token_indx, request, out_tokens,
+            num_accepted, status)
+    if request is None:
+        return PreparedOp("gdn_verify_drafts", ins + outs + [dtype, _ptr(status)], dev, keep)
+    return PreparedOp("gdn_verify_drafts_by_request",
+                      ins + [_ptr(request)] + outs + [num_accepted.shape[0], dtype, _ptr(status)], dev, keep)
 
 
 def gdn_verify_drafts(target_probs, draft_tokens, accept_u, sample_u, cu_seqlens, out_tokens, num_accepted, *,
-                      draft_probs=None, spec_token_indx=None, status=None, stream=None):
+                      draft_probs=None, spec_token_indx=None, request=None, status=None, stream=None):
     """Which drafted tokens the target keeps, and the next token (see
     include/gdnspec.h): target_probs [N, V] fp32 / bf16 / fp16; draft_tokens
     int32 and accept_u fp32 [B, T-1]; sample_u [B] fp32; cu_seqlens [B+1];
     draft_probs [B, T-1, V] of target_probs' dtype, or None for drafts without
     distributions.  Writes out_tokens [B, T] and num_accepted [B] (int32);
-    returns both.  With T = 1 the draft arguments are not used."""
+    returns both.  With ``request`` [B] (as given to gdn_step_tables)
+    num_accepted is that call's ``accepted`` [R] and sequence i's count goes to
+    its entry request[i].  With T = 1 the draft arguments are not used."""
     prepare_verify_drafts(target_probs, draft_tokens, accept_u, sample_u, cu_seqlens, out_tokens, num_accepted,
-                          draft_probs=draft_probs, spec_token_indx=spec_token_indx, status=status)(stream)
+                          draft_probs=draft_probs, spec_token_indx=spec_token_indx, request=request,
+                          status=status)(stream)
     return out_tokens, num_accepted
 
 
@@ -294,7 +304,7 @@ def gdn_step_tables(q_lens, slot_table, cu_seqlens, token_indx, state_indices, n
                     status=None, stream=None):
     """The tables of one step from its requests' lengths (see
     include/gdnspec.h); every tensor int32: q_lens [B], slot_table [R, S],
-    accepted [R], optional spec [B], request [B], conv_table [R, 2] and
+    accepted [R] (by request: see gdn_verify_drafts), optional spec [B], request [B], conv_table [R, 2] and
     conv_turn [R] (updated).  Writes cu_seqlens [B+1], token_indx [N],
     state_indices [B, S], num_accepted [B], and where given row_starts [B+1],
     conv_in and conv_out [B]."""

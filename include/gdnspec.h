@@ -53,8 +53,9 @@ extern "C" {
    4: dims->split accepts GDN_SPLIT_HALFK | 1 and | 2, the automatic choice for small
       FP32 batches
    5: gdn_verify_drafts, gdn_step_tables, gdn_conv_prefill, gdn_ssm_prefill, gdn_ssm_decode
-      and GDN_FLAG_NO_TOKEN */
-#define GDNSPEC_VERSION 5
+      and GDN_FLAG_NO_TOKEN
+   6: gdn_verify_drafts_by_request */
+#define GDNSPEC_VERSION 6
 
 #if defined(__GNUC__)
 #define GDNSPEC_API __attribute__((visibility("default")))
@@ -418,7 +419,8 @@ typedef struct {
  *   out_tokens[i]    d_0 .. d_{a-1}, the next token, then -1 up to max_T
  *   num_accepted[i]  a + 1: the step's tokens that stay, as gdn_spec_decode
  *                    and gdn_ssm_decode count them (the state after the last
- *                    kept token is in slot state_indices[i, a])
+ *                    kept token is in slot state_indices[i, a]); in batch order:
+ *                    with request tables, see gdn_verify_drafts_by_request
  *
  * Arithmetic: a probability counts as a whole multiple of 2^-52 (rounded to
  * nearest; below 0 and NaN count as 0, above 1 as 1), so that the sums are
@@ -449,6 +451,28 @@ GDNSPEC_API gdn_status gdn_verify_drafts(
     const int32_t* cu_seqlens, const int32_t* spec_token_indx,
     int32_t* out_tokens, int32_t* num_accepted,
     const gdn_verify_dims* dims, gdn_dtype prob_dtype,
+    int32_t* status_word, gdn_stream_t stream);
+
+/*
+ * gdn_verify_drafts_by_request -- the same where the sequences of the batch are
+ * requests in some other order: sequence i's count goes to
+ * num_accepted[request[i]], the table by request that gdn_step_tables reads as
+ * `accepted` (the entries of requests that are not in the batch stay).  out_tokens
+ * and everything else stay in batch order.
+ *
+ *   request        int32 [batch], as given to gdn_step_tables; negative: no request,
+ *                  its count is not kept; those that have rows are distinct
+ *   num_accepted   int32 [num_requests]
+ *
+ * The request of a sequence that is skipped is not looked at.  A request >=
+ * num_requests sets GDN_FLAG_SLOT_RANGE; its tokens are written, its count is not.
+ */
+GDNSPEC_API gdn_status gdn_verify_drafts_by_request(
+    const void* target_probs, const void* draft_probs, const int32_t* draft_tokens,
+    const float* accept_u, const float* sample_u,
+    const int32_t* cu_seqlens, const int32_t* spec_token_indx, const int32_t* request,
+    int32_t* out_tokens, int32_t* num_accepted,
+    const gdn_verify_dims* dims, int32_t num_requests, gdn_dtype prob_dtype,
     int32_t* status_word, gdn_stream_t stream);
 
 /* Sizes of gdn_step_tables. */
@@ -484,7 +508,8 @@ typedef struct {
  *   request      int32 [batch] row of the request in the tables below, or NULL
  *                (row i); negative: none (a padded entry); distinct
  *   slot_table   int32 [num_requests, spec_stride] the state slots of a request
- *   accepted     int32 [num_requests] (gdn_verify_drafts' num_accepted)
+ *   accepted     int32 [num_requests], by request: gdn_verify_drafts' num_accepted
+ *                where sequence i is request i, else gdn_verify_drafts_by_request's
  *   conv_table   int32 [num_requests, 2], conv_turn int32 [num_requests]
  *                (updated), conv_in, conv_out int32 [batch]: all four or none
  *   row_starts   may be NULL
