@@ -135,6 +135,13 @@ def _shape(t, name, want):
         raise ValueError(f"expected {name} [{sizes}]; got {tuple(t.shape)}")
 
 
+def _int32(**sizes):
+    """Sizes that a call takes as 32-bit numbers (ctypes would cut larger ones off)."""
+    for name, v in sizes.items():
+        if not -2 ** 31 <= v < 2 ** 31:
+            raise ValueError(f"{name} = {v}: a call takes at most 2^31 - 1")
+
+
 def _dense(dev, **tensors):
     """Contiguous int32 tensors (or None) on the device."""
     for name, t in tensors.items():
@@ -208,6 +215,7 @@ def prepare_verify_drafts(target_probs, draft_tokens, accept_u, sample_u, cu_seq
         _shape(request, "request", (B,))
     _shape(num_accepted, "num_accepted", (B if request is None else None,))
     _shape(cu_seqlens, "cu_seqlens", (B + 1,))
+    _int32(sequences=B, rows=N, vocab=V, T=T, requests=num_accepted.shape[0])
     dev = target_probs.device
     _cuda(dev, "gdn_verify_drafts")
     if target_probs.dtype not in _STATE_DTYPES:
@@ -283,6 +291,7 @@ def prepare_step_tables(q_lens, slot_table, cu_seqlens, token_indx, state_indice
                        (conv_out, "conv_out", (B,))):
         if t is not None:
             _shape(t, n, want)
+    _int32(requests=B, rows=token_indx.shape[0], slots_of_a_request=S, request_rows=R)
     dev = q_lens.device
     _cuda(dev, "gdn_step_tables")
     _dense(dev, q_lens=q_lens, slot_table=slot_table, cu_seqlens=cu_seqlens, token_indx=token_indx,
@@ -323,6 +332,7 @@ def _conv_dims(conv_weight, conv_bias, conv_pool, conv_in, conv_out, B, D) -> gd
         _shape(conv_bias, "conv_bias", (D,))
     _shape(conv_in, "conv_in", (B,))
     _shape(conv_out, "conv_out", (B,))
+    _int32(width=conv_weight.shape[1], state_len=conv_pool.shape[1])
     cd = gdn_conv_dims()
     cd.width = conv_weight.shape[1]
     cd.num_conv_slots, cd.state_len = conv_pool.shape[0], conv_pool.shape[1]
@@ -338,6 +348,7 @@ def prepare_conv_prefill(x, conv_weight, conv_bias, conv_pool, conv_in, conv_out
     if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError(f"expected cu_seqlens [B+1]; got {tuple(cu_seqlens.shape)}")
     B = cu_seqlens.shape[0] - 1
+    _int32(sequences=B, rows=N, channels=D)
     cd = _conv_dims(conv_weight, conv_bias, conv_pool, conv_in, conv_out, B, D)
     dev = x.device
     _cuda(dev, "gdn_conv_prefill")
@@ -406,6 +417,7 @@ def prepare_ssm_prefill(x, B, C, dt, z, A_log, dt_bias, D, state_pool, read_slot
     n = read_slots.shape[0]
     _shape(write_slots, "write_slots", (n,))
     _shape(cu_seqlens, "cu_seqlens", (n + 1,))
+    _int32(sequences=n, rows=N, H=H, G=G, P=P, S=S)
     dev = x.device
     _cuda(dev, "gdn_ssm_prefill")
     _typed(dev, _BF16, x=x, B=B, C=C)
@@ -467,6 +479,9 @@ def prepare_ssm_decode(xbc, conv_weight, conv_bias, conv_pool, conv_in, conv_out
     n, stride = state_indices.shape
     _shape(num_accepted, "num_accepted", (n,))
     _shape(cu_seqlens, "cu_seqlens", (n + 1,))
+    if max_T is None:
+        max_T = min(stride, 8)
+    _int32(sequences=n, rows=N, channels=CD, H=H, G=G, P=P, S=S, slots_of_a_sequence=stride, max_T=max_T)
     cd = _conv_dims(conv_weight, conv_bias, conv_pool, conv_in, conv_out, n, CD)
     dev = xbc.device
     _cuda(dev, "gdn_ssm_decode")
@@ -477,7 +492,7 @@ def prepare_ssm_decode(xbc, conv_weight, conv_bias, conv_pool, conv_in, conv_out
            cu_seqlens=cu_seqlens, spec_token_indx=spec_token_indx, status=status)
     d = _ssm_dims(n, N, H, G, P, S, state_pool, dt, z, out)
     d.spec_stride = stride
-    d.max_T = min(stride, 8) if max_T is None else max_T
+    d.max_T = max_T
     cd.x_stride = _rows(xbc, "xbc")
     return PreparedOp("gdn_ssm_decode",
                       [_ptr(xbc), _ptr(conv_weight), _ptr(conv_bias), _ptr(conv_pool), _ptr(conv_in), _ptr(conv_out), cd,
