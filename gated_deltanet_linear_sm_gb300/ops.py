@@ -203,8 +203,8 @@ def prepare_verify_drafts(target_probs, draft_tokens, accept_u, sample_u, cu_seq
     B, T = out_tokens.shape
     if T > 1:
         for t, n in ((draft_tokens, "draft_tokens"), (accept_u, "accept_u")):
-            if t.dim() != 2 or t.shape[0] != B or t.shape[1] < T - 1:
-                raise ValueError(f"expected {n} [B={B}, at least T-1={T - 1}]; got {tuple(t.shape)}")
+            if t is None or t.dim() != 2 or t.shape[0] != B or t.shape[1] < T - 1:
+                raise ValueError(f"expected {n} [B={B}, at least T-1={T - 1}]; got {None if t is None else tuple(t.shape)}")
         if draft_probs is not None and (draft_probs.dim() != 3 or draft_probs.shape[0] != B or
                                         draft_probs.shape[1] < T - 1 or draft_probs.shape[2] != V):
             raise ValueError(f"expected draft_probs [B={B}, at least T-1={T - 1}, V={V}]; got {tuple(draft_probs.shape)}")

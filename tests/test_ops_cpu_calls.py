@@ -39,6 +39,12 @@ def test_verify_by_request_sizes_are_refused_before_the_library(no_library):  # 
         gdn.gdn_verify_drafts(**args)
 
 
+@pytest.mark.parametrize("name", ["draft_tokens", "accept_u"])
+def test_verify_without_its_drafts_is_refused(no_library, name):  # noqa: F811
+    with pytest.raises(ValueError, match=f"expected {name}"):
+        gdn.gdn_verify_drafts(**_verify_args(**{name: None}))
+
+
 # ---- sizes that do not fit the 32 bits of the C structs (tensors without memory) ----
 
 BIG = 2 ** 32 + 5
