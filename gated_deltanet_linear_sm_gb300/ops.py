@@ -231,10 +231,10 @@ def prepare_verify_drafts(target_probs, draft_tokens, accept_u, sample_u, cu_seq
     d.target_stride = _rows(target_probs, "target_probs")
     if T > 1:
         d.token_stride = _rows(draft_tokens, "draft_tokens")
-        if _rows(accept_u, "accept_u") != d.token_stride:
+        if _rows(accept_u, "accept_u") != d.token_stride and B > 1:    # (one sequence: no stride is used)
             raise ValueError("draft_tokens and accept_u must have the same row stride")
         if draft_probs is not None:
-            if draft_probs.stride(2) != 1:
+            if V > 1 and draft_probs.stride(2) != 1:
                 raise ValueError("draft_probs: the elements of a row must be contiguous")
             # a drafter that runs step by step may stack its rows [T-1, B, V] and pass the transposed view
             d.draft_seq = draft_probs.stride(0) if B > 1 else 0
