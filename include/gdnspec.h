@@ -550,7 +550,7 @@ GDNSPEC_API gdn_status gdn_step_tables(
  *   y            bf16 [num_tokens, conv_dim], row stride y_stride (0: conv_dim);
  *                rows of no sequence are left as they were
  *
- * cdims->width 1..4.  conv_dim a multiple of 4; x, y, conv_weight, conv_bias
+ * cdims->width 1..4.  conv_dim a multiple of 4, at most 2^30; x, y, conv_weight, conv_bias
  * and conv_pool 8-byte aligned; x_stride and y_stride multiples of 4 (16-byte
  * aligned pointers and multiples of 8 run faster over many rows).  Sequences follow one
  * another: cu_seqlens does not decrease.  No conv_out[j] >= 0 equals another

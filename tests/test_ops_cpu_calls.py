@@ -9,7 +9,7 @@ import torch
 
 import gated_deltanet_linear_sm_gb300 as gdn
 from gated_deltanet_linear_sm_gb300 import ops
-from tests.test_ops_cpu import (A, BAD_SHAPE, MISALIGNED, NULL, UNSUPPORTED, _i, _set, _verify_args, lib,  # noqa: F401
+from tests.test_ops_cpu import (A, BAD_SHAPE, MISALIGNED, NULL, UNSUPPORTED, _conv, _i, _set, _verify_args, lib,  # noqa: F401
                                 no_library)
 
 
@@ -43,6 +43,12 @@ def test_verify_by_request_sizes_are_refused_before_the_library(no_library):  # 
 def test_verify_without_its_drafts_is_refused(no_library, name):  # noqa: F811
     with pytest.raises(ValueError, match=f"expected {name}"):
         gdn.gdn_verify_drafts(**_verify_args(**{name: None}))
+
+
+@pytest.mark.parametrize("dim", [2 ** 30 + 4, 2 ** 31 - 1020, 2 ** 31 - 4])
+def test_conv_of_more_channels_than_it_counts(lib, dim):  # noqa: F811
+    """The last CTA's channel numbers would pass 31 bits."""
+    assert _conv(lib, dim=dim) == BAD_SHAPE
 
 
 # ---- sizes that do not fit the 32 bits of the C structs (tensors without memory) ----
