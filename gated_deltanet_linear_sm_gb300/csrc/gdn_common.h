@@ -14,6 +14,9 @@ namespace gdn_common {
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 constexpr int32_t kMaxRows = 1 << 30;            // of a call: a row number plus a tile's rows stays in 32 bits
+// Sequences of a call whose every CTA reads the offsets of those before its own (the tables, the prompt
+// convolution): the reads grow with batch times CTAs, to minutes for the offsets that would still fit.
+constexpr int32_t kMaxScanned = 1 << 20;
 inline bool is_dtype(gdn_dtype t) { return t == GDN_F32 || t == GDN_BF16 || t == GDN_F16; }
 
 // SMs of the current device (asked once per device; 0 if that fails)

@@ -489,7 +489,7 @@ gdn_status gdn_conv_prefill(const void* x, const void* conv_weight, const void* 
                             const gdn_conv_dims* cdims, int32_t* status_word, gdn_stream_t stream) {
     if (cdims == nullptr) return GDN_ERR_NULL_ARG;
     // (channels: those that a CTA's threads would have behind the last one stay in 32 bits)
-    if (batch < 0 || num_tokens < 0 || batch > kMaxRows || num_tokens > kMaxRows || conv_dim < 1 || conv_dim > kMaxRows ||
+    if (batch < 0 || num_tokens < 0 || batch > kMaxScanned || num_tokens > kMaxRows || conv_dim < 1 || conv_dim > kMaxRows ||
         conv_dim % 4 != 0 || y_stride < 0 || cdims->x_stride < 0 || cdims->width < 1 || cdims->width > 4 ||
         cdims->state_len < cdims->width || cdims->num_conv_slots < 1 || cdims->reserved[0] != 0 || cdims->reserved[1] != 0)
         return GDN_ERR_BAD_SHAPE;

@@ -683,7 +683,7 @@ gdn_status gdn_step_tables(const int32_t* q_lens, const int32_t* spec, const int
                            const gdn_tables_dims* dims, int32_t* status_word, gdn_stream_t stream) {
     if (dims == nullptr) return GDN_ERR_NULL_ARG;
     if (dims->batch < 0 || dims->num_tokens < 0 || dims->spec_stride < 1 || dims->num_requests < 0 ||
-        dims->batch > kMaxRows || dims->num_tokens > kMaxRows ||
+        dims->batch > kMaxScanned || dims->num_tokens > kMaxRows ||
         dims->spec_stride > 0x7fffffff / kTile || (request == nullptr && dims->batch > dims->num_requests))
         return GDN_ERR_BAD_SHAPE;
     if (!cu_seqlens) return GDN_ERR_NULL_ARG;

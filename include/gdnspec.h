@@ -380,7 +380,8 @@ GDNSPEC_API gdn_status gdn_spec_decode_conv(
  * no host read of device data, capturable.  The device data of a call (tables,
  * lengths, slots) is checked on the device and reported through `status_word`;
  * outputs must not overlap inputs unless a call says so.  A call takes at most
- * 2^30 rows (GDN_ERR_BAD_SHAPE beyond).
+ * 2^30 rows, and gdn_step_tables and gdn_conv_prefill at most 2^20 sequences
+ * (GDN_ERR_BAD_SHAPE beyond).
  * Like the steps they start early behind a predecessor that lets them, and touch
  * memory only when it has completed.  gdn_ssm_prefill and gdn_ssm_decode let
  * their successor start early too, once their own predecessors have completed;

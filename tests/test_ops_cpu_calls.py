@@ -9,8 +9,8 @@ import torch
 
 import gated_deltanet_linear_sm_gb300 as gdn
 from gated_deltanet_linear_sm_gb300 import ops
-from tests.test_ops_cpu import (A, BAD_SHAPE, MISALIGNED, NULL, UNSUPPORTED, _conv, _i, _set, _verify_args, lib,  # noqa: F401
-                                no_library)
+from tests.test_ops_cpu import (A, BAD_SHAPE, MISALIGNED, NULL, UNSUPPORTED, _conv, _i, _set, _tables,  # noqa: F401
+                                _verify_args, lib, no_library)
 
 
 def _by_request(lib, dims={}, request=A, counts=A, num_requests=4, dtype=0):
@@ -49,6 +49,12 @@ def test_verify_without_its_drafts_is_refused(no_library, name):  # noqa: F811
 def test_conv_of_more_channels_than_it_counts(lib, dim):  # noqa: F811
     """The last CTA's channel numbers would pass 31 bits."""
     assert _conv(lib, dim=dim) == BAD_SHAPE
+
+
+def test_more_sequences_than_each_cta_can_look_at(lib):  # noqa: F811
+    n = 2 ** 20 + 1
+    assert _tables(lib, dict(batch=n, num_requests=n)) == BAD_SHAPE
+    assert _conv(lib, batch=n) == BAD_SHAPE
 
 
 # ---- sizes that do not fit the 32 bits of the C structs (tensors without memory) ----
