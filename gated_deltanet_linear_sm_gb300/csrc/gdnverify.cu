@@ -138,8 +138,8 @@ struct Sums {
     }
 };
 
-// Sums of up to 32 of these stay in 64 bits whatever a row holds, and only a row that
-// sums to 16 or more (which a distribution does not) meets one of them.
+// Sums of up to 32 of these stay in 64 bits whatever a row holds, and only where what is
+// left to sample from sums to 16 or more (of a distribution it does not) one of them is met.
 constexpr long long kTooMuch = 1LL << 57;
 constexpr u64 kRowLimit = 1ULL << 56;
 

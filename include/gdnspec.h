@@ -93,8 +93,8 @@ typedef enum { GDN_F32 = 0, GDN_BF16 = 1, GDN_F16 = 2 } gdn_dtype;
                                   default bound) for the products still in flight ran out too; the
                                   CTA released its tensor memory regardless, since holding it would
                                   block every later kernel on that SM */
-#define GDN_FLAG_NO_TOKEN   64 /* gdn_verify_drafts only: every probability of the row to sample from
-                                  counts as 0, or they sum to 16 or more: no token was emitted */
+#define GDN_FLAG_NO_TOKEN   64 /* gdn_verify_drafts only: what is left to sample from (r there) counts
+                                  as 0 throughout, or sums to 16 or more: no token was emitted */
 
 /*
  * dims->split flag: each warp of the decode step owns 8 of a unit's 128 V
@@ -442,8 +442,9 @@ typedef struct {
  * num_accepted, as its states keep theirs; so does one with bad data, which the
  * step skips too (q_len > max_T: GDN_FLAG_QLEN; a row outside [0, num_tokens),
  * or cu_seqlens out of order with cu_seqlens[batch]: GDN_FLAG_TOKEN_ROW).  A
- * row to sample from that counts as 0 throughout, or whose entries sum to 16 or
- * more (scores instead of probabilities), emits -1 and sets GDN_FLAG_NO_TOKEN.
+ * sequence whose r counts as 0 throughout, or sums to 16 or more (scores instead of
+ * probabilities), emits -1 in the next token's place and sets GDN_FLAG_NO_TOKEN; a
+ * row of p or q that sums to more is fine where r does not.
  * Every pointer needs only its element's alignment.
  */
 GDNSPEC_API gdn_status gdn_verify_drafts(

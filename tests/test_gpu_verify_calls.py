@@ -28,3 +28,74 @@ def test_one_request_with_tables_of_different_widths(cuda_device):
     two.tokens = torch.cat([two.tokens, two.tokens], 1)
     with pytest.raises(ValueError, match="same row stride"):
         two.run()
+
+
+def _units(p):
+    """Probabilities as whole multiples of 2^-52; a row's sums stay far below 2^64."""
+    x = np.asarray(p, np.float64)
+    return np.rint(np.where(np.isnan(x), 0.0, np.clip(x, 0.0, 1.0)) * 2.0 ** 52).astype(np.uint64)
+
+
+def _draw(left, u):
+    """The lowest entry whose cumulative sum is above u times the sum; -1 for sums of 0 and of 16 or more."""
+    total = int(left.sum())
+    if total == 0 or total >= 16 * 2 ** 52:
+        return -1
+    return int(np.searchsorted(np.cumsum(left), np.uint64(int(float(u) * total)), side="right"))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("draft", [True, False])
+@pytest.mark.parametrize("V,n", [(4096, 1), (4099, 1), (40000, 200)])
+def test_the_limit_of_16_is_on_what_is_left(cuda_device, dtype, draft, V, n):
+    """Rows of scores after a refused draft, on both sides of the limit: a row may sum to more where the
+    remainder does not."""
+    d, step = V // 2, V // 64
+    ones = np.array([k * step for k in range(60) if k * step != d])
+
+    def row(entries, at_d):
+        p = np.zeros(V)
+        p[ones[:int(entries)]] = 1.0
+        if entries % 1:
+            p[ones[int(entries)]] = entries % 1
+        p[d] = at_d
+        return p
+    if draft:
+        # (p, q) with q(d) = 1 and p(d) = 0.5, refused by u = 0.75: r sums to the difference of the ones
+        pairs = [(row(20, 0.5), row(10, 1)), (row(26, 0.5), row(10, 1)), (row(25.75, 0.5), row(10, 1)), (row(40, 0.5), row(24, 1)),
+                 (row(20, 0.5), row(30, 1)),                            # nothing left: p itself, 20.5
+                 (row(15, 0.5), row(30, 1)),                            # p itself, 15.5
+                 (row(15.5, 0.5), row(30, 1))]                          # p itself, 16
+    else:
+        # r is p without the draft
+        pairs = [(row(15.75, 0.5), None), (row(16, 0.5), None), (row(15, 0.5), None), (row(17, 0.5), None)]
+    target = np.stack([p for p, _ in pairs])
+    want, u = [], []
+    for k, (p, q) in enumerate(pairs):
+        left = _units(p)
+        if draft:
+            left = np.where(left > _units(q), left - np.minimum(left, _units(q)), np.uint64(0))
+            if left.sum() == 0:
+                left = _units(p)
+        else:
+            left[d] = 0
+        u.append(np.float32(0.0625 + 0.125 * (k % 7)))
+        want.append(_draw(left, u[-1]))
+    assert -1 in want and max(want) >= 0
+    B = len(pairs) * n
+    pick = np.tile(np.arange(len(pairs)), n)
+    # every sequence: row k and a row behind its draft that is not reached; the rows are shared
+    rows = torch.from_numpy(np.concatenate([target, np.full((1, V), 1.0 / V)])).to(DT[dtype]).to(cuda_device)
+    indx = np.stack([pick, np.full(B, len(pairs))], 1).reshape(-1)
+    q = torch.from_numpy(np.stack([q for _, q in pairs])).to(DT[dtype]).to(cuda_device)[_i32(pick, cuda_device).long()][:, None] \
+        if draft else None
+    out, acc = (torch.full(s, -77, dtype=torch.int32, device=cuda_device) for s in ((B, 2), (B,)))
+    status = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    gdn.gdn_verify_drafts(rows, torch.full((B, 1), d, dtype=torch.int32, device=cuda_device),
+                          torch.full((B, 1), 0.75, device=cuda_device), torch.tensor(np.array(u)[pick], device=cuda_device),
+                          _i32(np.arange(B + 1) * 2, cuda_device), out, acc, draft_probs=q,
+                          spec_token_indx=_i32(indx, cuda_device), status=status)
+    torch.cuda.synchronize()
+    assert (acc == 1).all() and (out[:, 1] == -1).all()
+    assert out[:, 0].tolist() == [want[k] for k in pick]
+    assert int(status) == binding.GDN_FLAG_NO_TOKEN
