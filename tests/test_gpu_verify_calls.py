@@ -99,3 +99,39 @@ def test_the_limit_of_16_is_on_what_is_left(cuda_device, dtype, draft, V, n):
     assert (acc == 1).all() and (out[:, 1] == -1).all()
     assert out[:, 0].tolist() == [want[k] for k in pick]
     assert int(status) == binding.GDN_FLAG_NO_TOKEN
+
+
+@pytest.mark.parametrize("dtype,draft", [("f32", True), ("f32", False), ("bf16", True), ("bf16", False), ("f16", False)])
+def test_rows_that_are_folded_more_than_once(cuda_device, dtype, draft):
+    """A vocabulary above 131072 with one CTA a sequence: a lane adds up more than 256 entries of its piece.
+    The rows are shared, the sampling numbers reach every part of them."""
+    V, B, T = 151936, 400, 2
+    g = torch.Generator(device=cuda_device).manual_seed(30)
+    assert 2 * B > 2 * torch.cuda.get_device_properties(cuda_device).multi_processor_count
+    P = torch.softmax(torch.randn(3, V, generator=g, device=cuda_device), -1).to(DT[dtype])
+    Q = torch.softmax(torch.randn(2, V, generator=g, device=cuda_device), -1).to(DT[dtype]) if draft else None
+    d = P[:2].float().argmin(-1).int()                                  # drafts that the target hardly ever takes
+    if draft:
+        Q[torch.arange(2), d.long()] = 1.0
+    pick = np.arange(B) % 2
+    u = (np.arange(B) + 0.5) / B
+    lefts = []
+    for k in range(2):
+        left = _units(_host(P)[k])
+        if draft:
+            q = _units(_host(Q)[k])
+            left = np.where(left > q, left - np.minimum(left, q), np.uint64(0))
+        else:
+            left[int(d[k])] = 0
+        lefts.append(left)
+    want = [_draw(lefts[k], np.float32(x)) for k, x in zip(pick, u)]
+    rows = _i32(np.stack([pick, np.full(B, 2)], 1).reshape(-1), cuda_device)
+    out, acc = (torch.full(s, -77, dtype=torch.int32, device=cuda_device) for s in ((B, T), (B,)))
+    status = torch.zeros(1, dtype=torch.int32, device=cuda_device)
+    sel = _i32(pick, cuda_device).long()
+    gdn.gdn_verify_drafts(P, d[sel][:, None].contiguous(), torch.full((B, 1), 0.9999, device=cuda_device),
+                          torch.tensor(u, dtype=torch.float32, device=cuda_device), _i32(np.arange(B + 1) * 2, cuda_device), out, acc,
+                          draft_probs=None if Q is None else Q[sel][:, None].contiguous(), spec_token_indx=rows, status=status)
+    torch.cuda.synchronize()
+    assert int(status) == 0 and (acc == 1).all()
+    assert out[:, 0].tolist() == want
