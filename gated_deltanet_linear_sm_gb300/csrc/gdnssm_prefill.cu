@@ -121,7 +121,7 @@ struct alignas(16) Gates {
     float w[kQ];       // 2^(l_last - l_t) d_t
     float d[kQ];       // step sizes
     float total;       // 2^(l_last)
-    float total_log;
+    long long units;   // l_last in units of 2^-32, at least -2^43 (2^-2048 is 0 as it is)
 };
 
 struct alignas(16) Misc {
@@ -240,7 +240,7 @@ __device__ __forceinline__ bool wait(unsigned long long* bar, int use, uint32_t 
     return done != 0;
 }
 
-// Whole multiples of 2^-32 (below 2^18 in size): from a float above -2048; their
+// Whole multiples of 2^-32 (up to 2^20 in size): from a float above -2048; their
 // multiple of 1/16, exact in FP32, and the rest; and their value.  Through 32-bit
 // conversions: the 64-bit ones run on a slow pipe.
 __device__ __forceinline__ long long to_units(float x) {
@@ -706,7 +706,7 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
             *reinterpret_cast<float4*>(gt.d + 4 * lane) = make_float4(d[0], d[1], d[2], d[3]);
             if (lane == 0) {
                 gt.total = ex2(from_units(all));
-                gt.total_log = from_units(all);
+                gt.units = max(all, -(1LL << 43));
             }
             __syncwarp();
             if (lane == 0) bar_arrive(&ms.gates_full[c % kGates]);
@@ -720,7 +720,7 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
         u64 S[16];                                               // state row `row`, columns 32 hh ..
 #pragma unroll
         for (int j = 0; j < 16; ++j) S[j] = 0;
-        float run_log = 0.f;
+        long long run = 0;                                       // the log2-decay of the part (at most 512 chunks: 2^52)
         auto part_at = [&](int part) { return static_cast<int64_t>(part) * units + unit; };
         auto part_of = [&](int part) { return sp.part + part_at(part) * N * kPB + 4 * (hh * N + row); };
         if (state_row && (kStates ? wk.first == 0 : wk.parts == 0)) {
@@ -782,7 +782,7 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
             // the state after this chunk
             if (!need_warp(&ms.ds_done, c)) break;
             fence_after();
-            run_log += gt.total_log;
+            if (kStates) run += gt.units;
             if (state_row) {
                 const u64 a2 = dup2(gt.total);
 #pragma unroll
@@ -869,7 +869,7 @@ __global__ void __launch_bounds__(kStates ? kStatesThreads : kSThreads, kStates 
         asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory");
         if (kStates) {
             if (state_row) store_part<N>(part_of(wk.part), S);
-            if (tid == 0) sp.part_decay[part_at(wk.part)] = *abort == 0 ? run_log : kLost;
+            if (tid == 0) sp.part_decay[part_at(wk.part)] = *abort == 0 ? from_units(run) : kLost;
         } else if (*abort == 0 && state_row) {
             if (wk.last) {
                 const long long ws = ld(p.write_slots + wk.seq);
