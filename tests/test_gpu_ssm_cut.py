@@ -1,4 +1,7 @@
-"""gdn_ssm_prefill of prompts that are cut into segments."""
+"""gdn_ssm_prefill of prompts that are cut into segments.
+
+Which prompts are cut and how is an estimate's choice (152 SMs); the tests that
+want one form check by the workspace that they got it."""
 from __future__ import annotations
 
 import pytest
@@ -6,7 +9,7 @@ import torch
 
 import gated_deltanet_linear_sm_gb300 as gdn
 from gated_deltanet_linear_sm_gb300 import binding, ops
-from tests.test_gpu_ssm import Scan
+from tests.test_gpu_ssm import MARK, Scan, _bits
 
 pytestmark = pytest.mark.gpu
 
@@ -14,6 +17,68 @@ pytestmark = pytest.mark.gpu
 def _workspace(s):
     """Bytes that the call takes for its segments (0: the prompts are not cut)."""
     return gdn.ssm_prefill_workspace(ops._ssm_dims(len(s.lens), s.N, s.H, s.G, s.P, s.S, s.pool, s.dt, s.z, s.out), s.dev)
+
+
+def _check(s, before):
+    """Scan.check on the GPU, for prompts of tens of thousands of tokens: the recurrence token by token in 64
+    bits, with the sums of absolute values that the bounds are relative to."""
+    f = torch.float64
+    dt = s.dt.to(f) + s.dt_bias.to(f)
+    d = torch.nn.functional.softplus(dt, threshold=40.0)
+    a = torch.exp(-torch.exp(s.A_log.to(f)) * d)
+    x, B, C = s.x.to(f), s.B.to(f), s.C.to(f)
+    D = s.D.to(f) if s.D is not None else torch.zeros(s.H, dtype=f, device=s.dev)
+    z = s.z.to(f) if s.z is not None else None
+    kept, done = list(range(s.pool.shape[0])), torch.zeros(s.N, dtype=torch.bool, device=s.dev)
+    for i, n in enumerate(s.lens):
+        if n <= 0:
+            continue
+        S = before[s.read[i]].to(f) if s.read[i] >= 0 else torch.zeros(s.H, s.S, s.P, dtype=f, device=s.dev)
+        M = S.abs()
+        y, my = (torch.empty(n, s.H, s.P, dtype=f, device=s.dev) for _ in range(2))
+        lo = int(s.cu[i])
+        for t in range(n):
+            r = lo + t
+            b, c = (v[r].repeat_interleave(s.H // s.G, 0)[:, :, None] for v in (B, C))
+            add = b * (d[r][:, None] * x[r])[:, None, :]
+            S = S * a[r][:, None, None] + add
+            M = M * a[r][:, None, None] + add.abs()
+            y[t], my[t] = (c * S).sum(1), (c.abs() * M).sum(1)
+        rows = slice(lo, lo + n)
+        y, my = y + D[:, None] * x[rows], my + (D[:, None] * x[rows]).abs()
+        if z is not None:
+            gate = z[rows] * torch.sigmoid(z[rows])
+            y, my = y * gate, my * gate.abs()
+        err = (s.out[rows].to(f) - y).abs()
+        assert (err <= 2.0 ** -8 * y.abs() + 2.0 ** -15 * my + 2.0 ** -17 * y.abs()).all(), f"sequence {i} outputs"
+        done[rows] = True
+        if s.write[i] >= 0:
+            half = {"f32": 0.0, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}[s.state]
+            tol = half * S.abs() + 2.0 ** -16 * M + (2.0 ** -25 if s.state == "f16" else 0.0)
+            assert ((s.pool[s.write[i]].to(f) - S).abs() <= tol).all(), f"sequence {i} state"
+            kept.remove(s.write[i])
+    assert (s.out[~done] == s.out.new_tensor(MARK)).all()
+    assert torch.equal(_bits(s.pool[kept]), _bits(before[kept]))
+    assert int(s.status) == 0
+
+
+@pytest.mark.parametrize("lens,H,G,S,state,chunks,parts,kw", [
+    ([2000], 64, 8, 64, "f32", 8, 4, {}),                               # four parts of two chunks
+    ([4096], 32, 4, 128, "bf16", 8, 2, {}),                             # two parts of four chunks
+    ([8192], 16, 1, 64, "f16", 7, 1, dict(gate=False)),                 # parts of seven chunks
+    ([30000], 1, 1, 128, "f32", 6, 1, dict(skip=False)),                # a segment that starts from 40 parts
+    ([700, 2100, 96, 1200], 16, 2, 128, "f32", 6, 2, {}),               # long, short and uncut prompts together
+    ([1, 7000, 250, 0, 300, 129, 128, 127, 385, 60, 500, 120], 8, 8, 64, "f32", 6, 2, dict(strong=True)),
+    ([6000, 1000, 3000], 24, 3, 128, "bf16", 20, 4, dict(packed=False)),
+])
+def test_every_form_of_the_cut_against_the_definition(cuda_device, lens, H, G, S, state, chunks, parts, kw):
+    s = Scan(cuda_device, lens, H, G, 64, S, state, seed=sum(lens), **kw)
+    before_last = s.N // (chunks * 128)                                 # segments that are not a sequence's last, at most
+    room = before_last * parts + min(before_last, len(lens))
+    assert _workspace(s) == room * H * (S * 64 + 1) * 4
+    before = s.pool.clone()
+    s.run()
+    _check(s, before)
 
 
 @pytest.mark.parametrize("what", ["read", "write", "rows"])
