@@ -412,7 +412,9 @@ __device__ Work find_work(const ScanParams& sp, int index, int lane) {
             const int segments = __shfl_sync(kFull, n, src);
             w.parts = kStates ? 1 : segments > 1 ? 1 + k * sp.parts : 0;
             w.last = k + 1 == segments;
-            if (w.part < 0 || w.parts > sp.part_room || w.part > sp.part_room - w.parts) {
+            // (an initial state comes with the part behind it, whose CTA writes it)
+            const int span = !kStates && w.parts == 1 ? 2 : w.parts;
+            if (w.part < 0 || span > sp.part_room || w.part > sp.part_room - span) {
                 // offsets that overlap (more rows than there are)
                 if (threadIdx.x == 0) raise(p.status, GDN_FLAG_TOKEN_ROW);
                 w.kind = 0;

@@ -126,3 +126,34 @@ def test_decays_of_long_parts_are_added_exactly(cuda_device):
     bound = l * 2.0 ** -21 + 144 * (2.0 ** -22 + 2 * 2.0 ** -24) + 5 * (2 * 2.0 ** -23 + 2.0 ** -20)
     err = ((pool[1].double() - want).abs() / want).amax((1, 2))
     assert (err <= bound).all(), (err.max(), bound.max())
+
+
+@pytest.mark.parametrize("cu", [[0, 3000, 2700, 3000, 0, 3000],         # the third one's parts begin at the room's last place
+                                [0, 3000, 0, 3000, 0, 3000], [0, 2990, 10, 3000, 20, 2000]])
+def test_overlapping_offsets_touch_nothing_outside(cuda_device, cu):
+    """Offsets that go back (against the caller contract) claim more rows than there are: a flag, and whatever is
+    computed stays inside the workspace, the rows, the heads and the slots, and comes from what was written."""
+    s = Scan(cuda_device, [3000], 2, 1, 64, 64, "f32", seed=61)
+    n = 5
+    cu = torch.tensor(cu, dtype=torch.int32, device=s.dev)
+    slots = torch.arange(2, 2 + n, dtype=torch.int32, device=s.dev)
+    wide = torch.full((s.N + 8, 4, 64), MARK, dtype=torch.bfloat16, device=s.dev)
+    pool = torch.full((n + 4, 2, 64, 64), 0.25, dtype=s.pool.dtype, device=s.dev)
+    need = gdn.ssm_prefill_workspace(ops._ssm_dims(n, s.N, 2, 1, 64, 64, pool, s.dt, s.z, s.out), s.dev)
+    assert need == 28 * 2 * (64 * 64 + 1) * 4                           # 23 parts and 5 initial states
+    room = torch.full((need + 8192,), 0xff, dtype=torch.uint8, device=s.dev)     # (NaN)
+    inside = torch.zeros(wide.shape, dtype=torch.bool, device=s.dev)
+    inside[4:4 + s.N, 1:3] = True
+    mark = wide.new_tensor(MARK)
+    for _ in range(4):
+        room.fill_(0xff)
+        s.status.zero_()
+        gdn.gdn_ssm_prefill(s.x, s.B, s.C, s.dt, s.z, s.A_log, s.dt_bias, s.D, pool, torch.full_like(slots, -1), slots, cu,
+                            wide[4:4 + s.N, 1:3], workspace=room[4096:4096 + need], status=s.status)
+        torch.cuda.synchronize()
+        assert int(s.status) == binding.GDN_FLAG_TOKEN_ROW
+        assert (room[:4096] == 0xff).all() and (room[4096 + need:] == 0xff).all()
+        assert torch.isfinite(room[4096:4096 + need].view(torch.float32)[:2 * 64 * 64]).all()     # the first initial states
+        assert (wide[~inside] == mark).all() and torch.isfinite(wide.float()).all()
+        assert (wide[inside] != mark).any()
+        assert (pool[[0, 1, n + 2, n + 3]] == 0.25).all() and torch.isfinite(pool).all()
