@@ -543,7 +543,9 @@ GDNSPEC_API gdn_status gdn_step_tables(
  * (history included) in rows 0 .. W-1, bit for bit; its other rows are left as
  * they were.  A step after it passes num_accepted = 1; a further chunk of the
  * prompt passes conv_in[i] = that slot.  conv_in[i] == conv_out[i] updates a
- * slot in place.
+ * slot in place.  A sequence without rows (cu_seqlens[i+1] <= cu_seqlens[i]) is
+ * skipped: slot conv_out[i] keeps what it holds, also where conv_in[i] is another
+ * slot, so its history stays in slot conv_in[i].
  *
  *   x            bf16 [num_tokens, conv_dim], row stride cdims->x_stride
  *   conv_weight  bf16 [conv_dim, W];  conv_bias bf16 [conv_dim], or NULL
@@ -604,7 +606,8 @@ typedef struct {
  * Within a row the heads (groups) are contiguous; x, B and C may be views into
  * one packed row.  x, B, C, z, out and state_pool are 16-byte aligned and
  * x/B/C/z/out strides multiples of 8.  A head dim P > 64 runs as P / 64 column
- * blocks.  Caller contract and skips as for gdn_prefill; sequences do not
+ * blocks.  Caller contract and skips as for gdn_prefill (a sequence without rows
+ * writes no slot: its state stays in slot read_slots[i]); sequences do not
  * overlap (cu_seqlens does not decrease).  An infinite or NaN
  * input spoils rows and the last state of its own sequence (rows shortly before
  * it among them: the products run over tiles of tokens), and no other's.
