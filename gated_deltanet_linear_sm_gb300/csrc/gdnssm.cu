@@ -23,9 +23,11 @@ namespace {
 // first W - 1 rows of a sequence always belong to the run that holds its first
 // row: that run alone reads the sequence's slot, and writes the new one after
 // it, so a slot may be updated in place.  HBM bandwidth bounds it: 16211 rows of
-// 4352 channels take 53 us, 5.3 TB/s of 6.8 measured (with the copies in registers 65, and
+// 4352 channels take 52.5 us, 5.4 TB/s of 6.8 measured (with the copies in registers 65, and
 // with one channel an instruction 81); half of the issue slots are in use, so the
-// rest is the start and the end of the runs.
+// rest is the start and the end of the runs.  (The window behind the sequence's last rows
+// is picked by a number known at run time: 48 bytes of local memory a thread with W = 4
+// and 8 channels, used once a sequence.)
 // (No early start of the next kernel: the step reads conv slots through __ldg,
 // which may run before its wait.)
 
@@ -265,8 +267,9 @@ cudaError_t launch_conv(ConvParams p, int width, cudaStream_t stream) {
 // 32 KB of state a token), and the group's first CTA alone writes those
 // channels' conv slot.  HBM bandwidth on the state bounds large batches, the
 // chain of dependent reads small ones: 64 sequences of up to 4 tokens and 64 heads with
-// N = 128 and FP32 states take 76 us, 6.0 TB/s of 6.8 measured (with the projection's rows
-// behind the state's 99); 2 of one token and 32 heads 4.9.
+// N = 128 and FP32 states take 76.5 us, 6.0 TB/s of 6.8 measured (with the projection's rows
+// behind the state's 99); 2 of one token and 32 heads 5.2.  States of 16 bits or of N = 64 put
+// half the bytes or fewer behind the same chain: 3.8 TB/s at 256 x 4 tokens, N = 64, bf16.
 
 template <typename StateT, int N>
 __global__ void __launch_bounds__(kRThreads, 4) gdn_ssm_decode_kernel(const Params p) {
@@ -517,9 +520,9 @@ gdn_status gdn_conv_prefill(const void* x, const void* conv_weight, const void* 
     p.num_tokens = num_tokens;
     p.dim = conv_dim;
     // 8 channels a thread need twice the registers of 4, so half as many warps are resident: with few rows
-    // for each that shows (4096 rows of 2560 channels, 17 a thread: 15.7 us with 8, 13.0 with 4; 1000 of
-    // 2560 8.1 and 6.6), with many the wider accesses do (16211 of 4352, 113: 55 and 63; 2048 of 8448, 28:
-    // 18.1 and 19.3; alike around 20)
+    // for each that shows (4096 rows of 2560 channels, 17 a thread: 13.4 us with 8, 12.5 with 4; 1000 of
+    // 2560, 4: 6.1 and 5.3; 2048 of 4352, 14: 11.9 and 11.0), with many the wider accesses do (16211 of 4352,
+    // 113: 52.1 and 56.6; 2048 of 8448, 28: 16.9 and 19.1; 8000 of 2560, 33: 20.1 and 21.8)
     constexpr int kWideRows = 20;
     const int64_t resident = static_cast<int64_t>(sm_count() ? sm_count() : 148) * 512;
     const bool wide = static_cast<int64_t>(num_tokens) * (conv_dim / 8) >= kWideRows * resident && conv_dim % 8 == 0 && p.x_stride % 8 == 0 && p.y_stride % 8 == 0 && aligned(x, 16) && aligned(y, 16) &&

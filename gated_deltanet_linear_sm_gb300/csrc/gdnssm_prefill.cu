@@ -39,7 +39,7 @@
 // A chunk takes 4850 cycles with every SM at work (2.6 us; N = 128, gated): G, Pm
 // and Y1 one after another are 4400 of them, the state's warps are busy for 4000
 // (2050 for the outputs, 1024 of which the exponentials and reciprocals of the gate
-// fill their pipe), and the tensor pipe for 41 %.  16384 tokens of 64 heads take 208
+// fill their pipe), and the tensor pipe for 41 %.  16384 tokens of 64 heads take 210
 // us, 38 of them in the first launch (452 MB and 113 MB of DRAM traffic: 2.7 TB/s).
 // Loops that are not unrolled are so because five kinds of warps share the
 // instruction cache: with all of them unrolled that case took 466 us instead of 363.
@@ -1044,13 +1044,13 @@ cudaError_t launch_kernel(const ScanParams& sp, int64_t ctas, cudaStream_t strea
 // segment in the first launch, whichever an estimate of the time says is shorter.
 // The host knows the rows and the sequences but not their lengths; with several it
 // takes the longest for twice as long as the mean (four prompts of 4096 tokens in all, 16
-// heads, us whole and cut at 6 chunks: 45 and 31 with lengths far apart, 26 and 31 alike).
-// The estimate's constants, in us,
-// are measured: a chunk takes kChunk, or kAlone while every SM pair runs one CTA; a
+// heads, us whole and cut at 6 chunks: 44 and 33 with lengths far apart, 28 and 33 alike),
+// and cuts all or none.  The estimate's constants, in us, are measured: a chunk takes kChunk, or kAlone while every SM pair runs one CTA; a
 // chunk of the first launch kState with two CTAs an SM; a CTA's start and end kStart
 // or kStateStart, and kPart for every part that it starts from; the first launch kLaunch.
-// (Whole and cut: one prompt of 16384 tokens and 64 heads 317 and 208 us, of 4096 and 32
-// heads 83 and 43, of 1000 and 16 heads 25 and 18; below some 600 tokens whole is shorter.)
+// (Whole and cut: one prompt of 16384 tokens and 64 heads 312 and 210 us, of 4096 and 32
+// heads 83 and 45, of 2000 and 64 heads 47 and 43, of 1000 and 16 heads 25 and 17, of 600
+// and 16 heads 18.6 and 19.7; below that whole is shorter.)
 struct Cut {
     int chunks, parts;
 };

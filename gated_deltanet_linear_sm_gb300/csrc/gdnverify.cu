@@ -1,6 +1,7 @@
 // libgdnspec: what runs between two steps of speculative decoding -- the
-// verification of the drafted tokens (gdn_verify_drafts, and
-// gdn_verify_drafts_by_request for its counts by request) and the tables of the next step (gdn_step_tables).  Declared in include/gdnspec.h.
+// verification of the drafted tokens (gdn_verify_drafts, and with its counts by
+// request gdn_verify_drafts_by_request) and the tables of the next step
+// (gdn_step_tables).  Declared in include/gdnspec.h.
 #include <cooperative_groups.h>
 
 #include "gdn_common.h"
@@ -27,8 +28,9 @@ namespace {
 // runs on a slow pipe: it held this kernel to a tenth of the memory's rate) but
 // as three sums of 22, 22 and 8 bits that floating-point additions of a constant
 // leave in the low bits of a float (Sums below).  The chain of dependent loads
-// bounds small batches (1 sequence of 5 rows of 32000: 5.1 us; 32 of 8 rows of 151936,
-// two FP32 rows read a sequence: 11.2, 2.4 TB/s), the issue slots of the sums large
+// bounds small batches (1 sequence of 5 rows of 32000: 5.2 us; 32 of up to 8 rows of 151936
+// FP32 entries, a row of each and the drafter's where a draft was refused, 1.4 on average:
+// 11.0, 2.4 TB/s), the issue slots of the sums large
 // ones (256 sequences of 128256 bf16 entries: 24.7 us, 2.7 TB/s; 92 with an integer an entry).
 
 constexpr int kVThreads = 512;

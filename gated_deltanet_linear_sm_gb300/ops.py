@@ -107,7 +107,8 @@ class PreparedScan(PreparedOp):
     takes one from the memory of the stream that it runs on, where nothing else
     can be given it before the launch has run.  So one such call may run on
     several streams at once and be dropped while it runs, and a graph that
-    captures it holds a workspace of its own."""
+    captures it (through torch.cuda.graph, whose memory that is; a capture
+    begun by other means needs a given workspace) holds one of its own."""
 
     __slots__ = ("_at", "_bytes")
 
