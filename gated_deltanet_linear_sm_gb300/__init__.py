@@ -11,3 +11,5 @@ from .ops import (PreparedOp, gdn_conv_prefill, gdn_ssm_decode, gdn_ssm_dims, gd
                   gdn_step_tables, gdn_tables_dims, gdn_verify_dims, gdn_verify_drafts, prepare_conv_prefill,
                   prepare_ssm_decode, prepare_ssm_prefill, prepare_step_tables, prepare_verify_drafts,
                   ssm_prefill_workspace)
+from .kv import (attn_decode_workspace, gdn_attn_decode, gdn_kv_dims, gdn_kv_read, gdn_kv_write,  # noqa: F401
+                 prepare_attn_decode, prepare_kv_read, prepare_kv_write)

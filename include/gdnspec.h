@@ -54,8 +54,10 @@ extern "C" {
       FP32 batches
    5: gdn_verify_drafts, gdn_step_tables, gdn_conv_prefill, gdn_ssm_prefill, gdn_ssm_decode
       and GDN_FLAG_NO_TOKEN
-   6: gdn_verify_drafts_by_request */
-#define GDNSPEC_VERSION 6
+   6: gdn_verify_drafts_by_request
+   7: gdn_kv_write, gdn_kv_read, gdn_attn_decode, GDN_E4M3 and GDN_I8 (their caches' types; no
+      other call takes these two) */
+#define GDNSPEC_VERSION 7
 
 #if defined(__GNUC__)
 #define GDNSPEC_API __attribute__((visibility("default")))
@@ -73,8 +75,9 @@ typedef enum {
     GDN_ERR_CUDA = 5         /* the launch failed (the CUDA error is left for the caller to query) */
 } gdn_status;
 
-/* Element type of the recurrent-state pool. */
-typedef enum { GDN_F32 = 0, GDN_BF16 = 1, GDN_F16 = 2 } gdn_dtype;
+/* Element type of the recurrent-state pool (the first three), or of a key-value cache (the
+ * last four; with GDN_E4M3 and GDN_I8 every head's row has a scale). */
+typedef enum { GDN_F32 = 0, GDN_BF16 = 1, GDN_F16 = 2, GDN_E4M3 = 3, GDN_I8 = 4 } gdn_dtype;
 
 /*
  * Bits the kernel ORs into *status_word (when given) for bad DEVICE data.
@@ -649,6 +652,135 @@ GDNSPEC_API gdn_status gdn_ssm_decode(
     const int32_t* cu_seqlens, const int32_t* spec_token_indx, void* out,
     const gdn_ssm_dims* dims, gdn_dtype state_dtype,
     int32_t* status_word, gdn_stream_t stream);
+
+/* ---- the attention layers beside the recurrent ones: a paged key-value cache, and the
+ *      attention of a step's tokens over it ------------------------------------------------
+ *
+ * A hybrid model's full attention layers run in the same loop, on the same batches and
+ * tables (cu_seqlens and spec_token_indx from gdn_step_tables): gdn_kv_write puts the
+ * step's keys and values behind the sequence's cached ones, gdn_attn_decode attends to
+ * all of them, and what gdn_verify_drafts keeps moves the length on (kv_lens[i] +=
+ * num_accepted[i]; rows behind it are written again by the next step).  The conventions
+ * of the calls around the step hold; all three calls let their successor start early
+ * once their own predecessors have completed.
+ *
+ * The cache.  k_cache and v_cache hold num_pages pages of page_size positions of H_kv rows
+ * of D elements; position x of sequence i is row x % page_size of page
+ * page_table[i, x / page_size].  page_table is int32 [batch, table_cols], rows
+ * table_stride apart.  A negative page is none: its positions are not written, not read
+ * and not attended to.  A page >= num_pages counts as none and sets GDN_FLAG_SLOT_RANGE.
+ * Both caches have the same strides (in elements, any order of pages, positions and
+ * heads; a row's D elements are contiguous), so they may be views of one tensor.
+ *
+ * 8-bit caches (GDN_E4M3, GDN_I8) hold codes; k_scale and v_scale, fp32 [num_pages,
+ * page_size, H_kv] with strides of their own, a scale for each row: the row's elements
+ * stand for code * scale.  gdn_kv_write makes them from the row's largest absolute value a:
+ *     GDN_E4M3  scale = 2^e, the least e >= -100 with a <= 448 * 2^e; codes are rounded to
+ *               the nearest e4m3 value (a power of two: x / scale is exact, and so is what
+ *               a bf16 row reads back)
+ *     GDN_I8    scale = a / 127 rounded up to 8 significant bits, at least 2^-100; codes
+ *               are x / scale rounded to the nearest whole number
+ * (ties to even).  A row that holds an infinity or NaN gets the scale NaN and codes 0: it
+ * reads back as NaN and spoils the attention of those that see it.
+ */
+
+/* Sizes of the key-value cache and of the calls on it. */
+typedef struct {
+    int32_t batch;          /* sequences */
+    int32_t num_tokens;     /* rows of the token tensors */
+    int32_t H_q, H_kv;      /* heads of q (gdn_attn_decode alone), and of the cache; H_q % H_kv == 0 */
+    int32_t D;              /* head dim: 64, 128, 192 or 256 */
+    int32_t page_size;      /* positions of a page, >= 1 */
+    int32_t table_cols;     /* columns of page_table */
+    int32_t max_T;          /* gdn_attn_decode: host-known bound on every q_len, 1..8 */
+    int32_t window;         /* gdn_attn_decode: a token sees this many positions, itself included; 0: all */
+    int32_t reserved;       /* must be 0 */
+    int64_t num_pages;      /* pages of the caches */
+    /* strides in ELEMENTS, 0 = dense ([pages, positions, heads, D]; rows H*D apart; table_cols) */
+    int64_t page_stride, token_stride, head_stride;
+    int64_t scale_page_stride, scale_token_stride, scale_head_stride;
+    int64_t table_stride;
+    int64_t q_stride, k_stride, v_stride, z_stride, out_stride;   /* k, v: rows of gdn_kv_write and gdn_kv_read */
+} gdn_kv_dims;
+
+/*
+ * gdn_kv_write -- rows of keys and values into the cache, quantised where it has 8 bits.
+ * Sequence i's rows are cu_seqlens[i] .. cu_seqlens[i+1]-1 (of the token batch, or of
+ * spec_token_indx); row t of it goes to position kv_lens[i] + t.  One step's drafted
+ * tokens or whole prompts alike.
+ *
+ *   k, v         bf16 [num_tokens, H_kv, D], rows k_stride, v_stride apart
+ *   k_cache, v_cache  cache_type; k_scale, v_scale fp32 (8-bit types; else not used)
+ *   page_table   int32;  kv_lens int32 [batch];  cu_seqlens int32 [batch + 1]
+ *   spec_token_indx  int32 [cu_seqlens[batch]], or NULL
+ *
+ * A 16-bit cache gets each element rounded to its type.  cu_seqlens does not decrease; no
+ * two rows of a call go to the same place.  Bad device data skips the sequence: kv_lens[i]
+ * < 0 or kv_lens[i] + q_len > table_cols * page_size sets GDN_FLAG_SLOT_RANGE, rows outside
+ * [0, num_tokens) set GDN_FLAG_TOKEN_ROW (an entry of spec_token_indx outside skips its row
+ * alone).  k, v and the caches 16-byte aligned, k_stride and v_stride multiples of 8, the
+ * caches' strides multiples of 16 bytes; scales 4-byte aligned.
+ */
+GDNSPEC_API gdn_status gdn_kv_write(
+    const void* k, const void* v, void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+    const int32_t* page_table, const int32_t* kv_lens, const int32_t* cu_seqlens,
+    const int32_t* spec_token_indx, const gdn_kv_dims* dims, gdn_dtype cache_type,
+    int32_t* status_word, gdn_stream_t stream);
+
+/*
+ * gdn_kv_read -- cached rows back as dense ones: positions kv_begin[i] + t (t alone where
+ * kv_begin is NULL) of sequence i to rows cu_seqlens[i] + t of k and v.  For a prompt's
+ * attention over a cached prefix, or to move a sequence.
+ *
+ *   k, v         row_type (GDN_F32, GDN_BF16 or GDN_F16) [num_tokens, H_kv, D], rows k_stride,
+ *                v_stride apart; each element code * scale rounded once
+ *   kv_begin     int32 [batch], or NULL;  everything else as for gdn_kv_write
+ *
+ * Rows of no sequence, of a skipped sequence and of positions without a page are left as
+ * they were.  k and v do not overlap the cache.  Strides of k and v: multiples of 8.
+ */
+GDNSPEC_API gdn_status gdn_kv_read(
+    const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+    const int32_t* page_table, const int32_t* kv_begin, const int32_t* cu_seqlens,
+    void* k, void* v, const gdn_kv_dims* dims, gdn_dtype cache_type, gdn_dtype row_type,
+    int32_t* status_word, gdn_stream_t stream);
+
+/*
+ * gdn_attn_decode -- the attention of one to eight tokens of each sequence over its cached
+ * keys and values, those of the step itself (written before, by gdn_kv_write) among them.
+ * With x = kv_lens[i] + t the position of token t, row r = its row, head h using head
+ * h / (H_q / H_kv) of the cache:
+ *     s_j  = scale * q[r,h] . k_j    for max(0, x - window + 1) <= j <= x (window 0: from 0)
+ *     o    = sum_j e^(s_j) v_j / sum_j e^(s_j)          (0 where no position is left)
+ *     out[r,h] = round_bf16( o * sigmoid(z[r,h]) )       (o itself without z)
+ *
+ *   q, z, out    bf16 [num_tokens, H_q, D]; z may be NULL; rows of no sequence and of skipped
+ *                ones are left as they were
+ *   spec_token_indx  int32 [cu_seqlens[batch]], or NULL
+ *   workspace    gdn_attn_decode_workspace(dims, cache_type) bytes of device memory, 16-byte
+ *                aligned, used by this call alone until it has run; what it holds before and
+ *                after does not matter
+ *
+ * Scores, the softmax's maximum and sum, and the output are held in FP32; the weights are
+ * rounded to 16 significant bits for a bf16 cache (two bf16 parts) and to 11 for the others
+ * (fp16).  The positions of a batch are cut evenly among the CTAs and the parts joined in
+ * order, so equal calls give equal results; how a sequence is cut depends on the others'
+ * lengths, by rounding in FP32.  Bad device data: q_len > max_T sets GDN_FLAG_QLEN, the rest
+ * as for gdn_kv_write, except that any row of a sequence outside [0, num_tokens) skips the
+ * sequence.  An infinity or NaN in k or v spoils the tokens that see it, in q its own row.
+ * q, z, out 16-byte aligned with strides that are multiples of 8; the caches as above.
+ * batch at most 2^20 sequences.
+ */
+GDNSPEC_API gdn_status gdn_attn_decode(
+    const void* q, const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+    const int32_t* page_table, const int32_t* kv_lens, const int32_t* cu_seqlens,
+    const int32_t* spec_token_indx, const void* z, void* out, void* workspace, int64_t workspace_bytes,
+    const gdn_kv_dims* dims, float scale, gdn_dtype cache_type,
+    int32_t* status_word, gdn_stream_t stream);
+
+/* Workspace that gdn_attn_decode needs for these sizes, in bytes (-1: invalid dims or type).
+ * Host only; depends on the current device's number of SMs. */
+GDNSPEC_API int64_t gdn_attn_decode_workspace(const gdn_kv_dims* dims, gdn_dtype cache_type);
 
 /*
  * The split code that gdn_spec_decode would use for these sizes and state
