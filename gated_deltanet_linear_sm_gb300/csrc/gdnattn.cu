@@ -12,169 +12,21 @@
 // among the CTAs, whatever the lengths; a CTA computes from the lengths alone where its part
 // begins.  A part that is a whole unit is finished where it is; the others go to the workspace
 // and a second launch joins them in order.
-#include <cuda_fp8.h>
+#include "gdnattn.cuh"
 
-#include "gdnkv.h"
-
-using namespace gdn_common;
-using namespace gdn_kv;
+using namespace gdn_attn;
 
 namespace {
 
-constexpr int kBlock = 64;              // keys that the line is cut by
-constexpr int kKeys = 16;               // keys that a warp works on at a time
-
-// ---- the line of all units' key blocks ---------------------------------------------------
-
-struct Span {
-    int lo, hi;                         // positions that some row sees, lo rounded down to kKeys
-    int n;                              // tokens
-    int blocks;                         // of kBlock keys
-    int tiles;                          // of query rows
+constexpr int kTileRows = 16, kCutKeys = 64;
+template <int kT>
+struct Cut {                            // (gdnattn.cuh)
+    static constexpr int kThreads = kT;
+    static constexpr int kBlock = kCutKeys;
+    static constexpr int kRows = kTileRows;
 };
-
-// Sequence i's part of the line (blocks 0: nothing to do), and a flag for bad data.
-__device__ __forceinline__ int span_of(const AttnParams& p, int i, Span& s) {
-    s.blocks = 0;
-    const int a = ld(p.cu + i), e = ld(p.cu + i + 1), end = ld(p.cu + p.batch);
-    const int64_t past = ld(p.kv_lens + i);
-    if (e <= a) return 0;
-    if (a < 0 || e > end || e > p.num_tokens) return GDN_FLAG_TOKEN_ROW;
-    const int n = e - a;
-    if (n > p.max_T) return GDN_FLAG_QLEN;
-    if (past < 0 || past + n > static_cast<int64_t>(p.pg.cols) * p.pg.page) return GDN_FLAG_SLOT_RANGE;
-    if (p.sti) {
-        bool fine = true;
-        for (int t = 0; t < n; ++t) {
-            const int r = ld(p.sti + a + t);
-            fine = fine && r >= 0 && r < p.num_tokens;
-        }
-        if (!fine) return GDN_FLAG_TOKEN_ROW;
-    }
-    s.n = n;
-    s.hi = static_cast<int>(past) + n;
-    s.lo = p.window > 0 && past + 1 > p.window ? static_cast<int>(past + 1 - p.window) & ~(kKeys - 1) : 0;
-    s.blocks = (s.hi - s.lo + kBlock - 1) / kBlock;
-    s.tiles = (n * p.ratio + kTileRows - 1) / kTileRows;
-    return 0;
-}
-
-// The line as a CTA walks it: the blocks in front of each of `kT` sequences at a time.
-template <int kT>
-struct Line {
-    int64_t total;                      // blocks of the whole line
-    int64_t base;                       // blocks in front of the chunk
-    int chunk;                          // first sequence of the chunk
-    int64_t before[kT + 1];             // in front of each of its sequences, from base on
-    int64_t warp_sum[kT / 32];
-};
-
-template <int kT>
-__device__ __forceinline__ int64_t block_sum(Line<kT>& L, int64_t v) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) L.warp_sum[threadIdx.x / 32] = v;
-    __syncthreads();
-    int64_t sum = 0;
-#pragma unroll
-    for (int w = 0; w < kT / 32; ++w) sum += L.warp_sum[w];
-    return sum;
-}
-
-// The blocks in front of each sequence of the chunk that begins at `first`.
-template <int kT>
-__device__ __forceinline__ void scan_chunk(const AttnParams& p, Line<kT>& L, int first, int64_t base, bool tell) {
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int i = first + tid;
-    int64_t v = 0;
-    if (i < p.batch) {
-        Span s;
-        const int flag = span_of(p, i, s);
-        if (flag && tell) raise(p.status, flag);
-        if (s.blocks > 0) v = static_cast<int64_t>(s.blocks) * s.tiles * p.heads;
-    }
-    int64_t sum = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t u = __shfl_up_sync(kFull, sum, o);
-        if (lane >= o) sum += u;
-    }
-    __syncthreads();
-    if (lane == 31) L.warp_sum[tid / 32] = sum;
-    __syncthreads();
-    int64_t in = 0;
-#pragma unroll
-    for (int w = 0; w < kT / 32; ++w)
-        if (w < tid / 32) in += L.warp_sum[w];
-    if (tid == 0) {
-        L.before[0] = 0;
-        L.chunk = first;
-        L.base = base;
-    }
-    L.before[tid + 1] = in + sum;
-    __syncthreads();
-}
-
-// The whole line's length; the first chunk is scanned on the way.
-template <int kT>
-__device__ __forceinline__ void begin_line(const AttnParams& p, Line<kT>& L) {
-    scan_chunk<kT>(p, L, 0, 0, blockIdx.x == 0);
-    int64_t rest = 0;
-    for (int i = kT + threadIdx.x; i < p.batch; i += kT) {
-        Span s;
-        const int flag = span_of(p, i, s);
-        if (flag && blockIdx.x == 0) raise(p.status, flag);
-        if (s.blocks > 0) rest += static_cast<int64_t>(s.blocks) * s.tiles * p.heads;
-    }
-    const int64_t more = p.batch > kT ? block_sum<kT>(L, rest) : 0;
-    if (threadIdx.x == 0) L.total = L.before[kT] + more;
-    __syncthreads();
-}
-
-// The sequence whose blocks contain block w of the line (0 <= w < total), chunks moving on.
-template <int kT>
-__device__ __forceinline__ int sequence_at(const AttnParams& p, Line<kT>& L, int64_t w) {
-    while (w >= L.base + L.before[kT] && L.chunk + kT < p.batch) {
-        const int64_t base = L.base + L.before[kT];
-        const int first = L.chunk + kT;
-        __syncthreads();
-        scan_chunk<kT>(p, L, first, base, false);
-    }
-    int lo = 0, hi = kT - 1;            // the last one that begins at or before w: it has blocks
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (L.base + L.before[mid] <= w) lo = mid; else hi = mid - 1;
-    }
-    return lo;
-}
-
-// CTAs that share the line: no more than leave each kLeast blocks
-constexpr int kLeast = 2;
-__device__ __forceinline__ int ctas_of(int64_t total, int grid) {
-    const int64_t most = (total + kLeast - 1) / kLeast;
-    return static_cast<int>(most < grid ? (most > 0 ? most : 1) : grid);
-}
 
 // ---- instructions ---------------------------------------------------------------------------
-
-__device__ __forceinline__ uint32_t saddr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
-    const int bytes = live ? 16 : 0;    // (0: zeros, and nothing is read)
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool live) {
-    const int bytes = live ? 4 : 0;
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t a) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a) : "memory");
@@ -192,15 +44,6 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
         asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ uint32_t pack_h(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t pack_b(float a, float b) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
 // ---- what the cache's types differ in -------------------------------------------------------
 
 enum Kind { kBf16, kF16, kE4m3, kI8 };
@@ -275,20 +118,6 @@ __device__ __forceinline__ int join_col(int r, int col) {
     return kQuantised ? col ^ ((r & 1) << 4) : col ^ ((r & 3) << 3);
 }
 
-__device__ __forceinline__ int64_t token_row(const AttnParams& p, int i) { return p.sti ? ld(p.sti + i) : i; }
-
-// O of one row and column quad, weighed: to the output
-__device__ __forceinline__ void put_out(const AttnParams& p, int64_t row, int head, int D, int col, const float (&o)[4]) {
-    float x[4] = {o[0], o[1], o[2], o[3]};
-    if (p.z) {
-        const uint2 raw = ld(reinterpret_cast<const uint2*>(p.z + row * p.z_stride + static_cast<int64_t>(head) * D + col));
-        const float z[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u), __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u)};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = __fdividef(x[e], 1.0f + __expf(-z[e]));
-    }
-    *reinterpret_cast<uint2*>(p.out + row * p.out_stride + static_cast<int64_t>(head) * D + col) = make_uint2(pack_b(x[0], x[1]), pack_b(x[2], x[3]));
-}
-
 // An infinity or NaN among values that some rows see and some do not: its products would reach the
 // others as 0 * NaN.  It is added to the rows that see it (whatever its weight: the sum is no number
 // then) and taken out of the tile.
@@ -350,11 +179,12 @@ template <int kKind, int D>
 __global__ void __launch_bounds__(Shape<kKind, D>::kThreads, Shape<kKind, D>::kCtas) gdn_attn_decode_kernel(const AttnParams p) {
     using S = Shape<kKind, D>;
     constexpr int kT = S::kThreads;
+    using G = Cut<kT>;
     constexpr bool kQuantised = S::kBytes == 1;
     constexpr bool kB = kKind == kBf16;
     constexpr int kSteps = D / 16;                  // of the products over D
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ Line<kT> line;
+    __shared__ Line<G> line;
     __shared__ float row_m[S::kWarps][kTileRows], row_l[S::kWarps][kTileRows];
     __shared__ float q_scale[kTileRows];
     __shared__ float join_m[kTileRows], join_l[kTileRows];
@@ -363,44 +193,26 @@ __global__ void __launch_bounds__(Shape<kKind, D>::kThreads, Shape<kKind, D>::kC
     unsigned char* const ring0 = smem + S::kQ;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
     dep_wait();
-    begin_line<kT>(p, line);
+    begin_line<G>(p, line);
     dep_launch();
     const int64_t total = line.total;
-    const int ctas = ctas_of(total, gridDim.x);
+    const int ctas = ctas_of(total, gridDim.x, 2);
     const int cta = blockIdx.x;
     int32_t* const meta = p.meta + static_cast<int64_t>(cta) * kMetaInts;
     if (tid == 0) meta[0] = meta[8] = -1;           // (no part yet)
     if (cta >= ctas) return;
-    const int64_t w0 = total * cta / ctas, w1 = total * (cta + 1) / ctas;
+    const int64_t w0 = quotient(total * cta, ctas), w1 = quotient(total * (cta + 1), ctas);
     const uint32_t my_ring = saddr(ring0) + warp * S::kRing * S::kItem;
 
     for (int64_t w = w0; w < w1;) {
         // ---- the unit at block w of the line ----
-        const int k = sequence_at<kT>(p, line, w);
-        const int seq = line.chunk + k;
-        const int64_t in_seq = w - line.base - line.before[k];
-        Span sp;
-        span_of(p, seq, sp);
-        const int unit = static_cast<int>(in_seq / sp.blocks);          // (head, tile of rows)
-        const int b0 = static_cast<int>(in_seq - static_cast<int64_t>(unit) * sp.blocks);
-        const int b1 = static_cast<int>(w1 - w < sp.blocks - b0 ? b0 + (w1 - w) : sp.blocks);
-        const int head = unit / sp.tiles, tile = unit - head * sp.tiles;
-        const int past = sp.hi - sp.n, row0 = ld(p.cu + seq);
-        const int rows = min(kTileRows, sp.n * p.ratio - tile * kTileRows);
-        const bool whole = b0 == 0 && b1 == sp.blocks;
+        const int k = sequence_at<G>(p, line, w);
+        const Piece d = piece_at<G>(p, line, k, w, w1);
+        const int seq = d.seq, head = d.head, tile = d.tile, past = d.past, row0 = d.row0, rows = d.rows, key0 = d.key0, key1 = d.key1;
+        const int b0 = d.b0, b1 = d.b1;
+        const bool whole = b0 == 0 && b1 == d.blocks;
         const int part = whole ? -1 : b0 > 0 ? 2 * cta : 2 * cta + 1;
-        if (!whole && tid == 0) {
-            const int64_t u0 = w - b0, u1 = u0 + sp.blocks;             // the unit's blocks; block b is CTA ((b + 1) ctas - 1) / total's
-            int32_t* rec = meta + 8 * (b0 > 0 ? 0 : 1);
-            rec[0] = seq;
-            rec[1] = head;
-            rec[2] = tile;
-            rec[3] = static_cast<int>(((u0 + 1) * ctas - 1) / total);
-            rec[4] = static_cast<int>((u1 * ctas - 1) / total);
-            rec[5] = rows;
-            rec[6] = row0;
-        }
-        const int key0 = sp.lo + b0 * kBlock, key1 = min(sp.hi, sp.lo + b1 * kBlock);
+        if (!whole && tid == 0) put_record(meta, d, w, total, ctas);
         const int items = 2 * max(0, ((key1 - key0 + kKeys - 1) / kKeys - warp + S::kWarps - 1) / S::kWarps);
 
         // ---- the ring ----
@@ -525,14 +337,14 @@ __global__ void __launch_bounds__(Shape<kKind, D>::kThreads, Shape<kKind, D>::kC
         int last[2], first[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const int t = min((tile * kTileRows + g + 8 * h) / p.ratio, sp.n - 1);
+            const int t = min((tile * kTileRows + g + 8 * h) / p.ratio, d.n - 1);
             qs[h] = q_scale[g + 8 * h];
             last[h] = past + t;
             first[h] = p.window > 0 ? max(0, last[h] - p.window + 1) : 0;
             m[h] = -INFINITY;
             l[h] = 0.f;
         }
-        const int all_lo = p.window > 0 ? max(0, sp.hi - p.window) : 0, all_hi = past + 1;      // seen by every row
+        const int all_lo = p.window > 0 ? max(0, past + d.n - p.window) : 0, all_hi = past + 1;      // seen by every row
         float o[D / 8][4];
 #pragma unroll
         for (int n = 0; n < D / 8; ++n)
@@ -796,89 +608,6 @@ __global__ void __launch_bounds__(Shape<kKind, D>::kThreads, Shape<kKind, D>::kC
     }
 }
 
-// ---- the second launch: parts of a unit joined ------------------------------------------------------
-//
-// Each of the CTAs that share a unit joins some of its rows: CTA c of c0 .. c1 those whose number is
-// c - c0 modulo their count.  A row's parts are summed by the warps that are left over for it.
-
-constexpr int kJThreads = 256, kJWarps = 8;
-
-template <int D>
-__global__ void __launch_bounds__(kJThreads) gdn_attn_join_kernel(const AttnParams p, const int grid) {
-    __shared__ float sum[kJWarps][D];
-    __shared__ float sum_l[kJWarps];
-    dep_wait();
-    dep_launch();
-    const int cta = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int32_t* const meta = p.meta + static_cast<int64_t>(cta) * kMetaInts;
-    const float* const all_ml = p.ws + static_cast<int64_t>(2 * grid) * kTileRows * D;
-    for (int which = 0; which < 2; ++which) {
-        const int32_t* const rec = meta + 8 * which;
-        const int seq = ld(rec);
-        if (seq < 0) continue;
-        const int head = ld(rec + 1), tile = ld(rec + 2), c0 = ld(rec + 3), c1 = ld(rec + 4), rows = ld(rec + 5), row0 = ld(rec + 6);
-        const int parts = c1 - c0 + 1, mine = cta - c0;
-        const int count = rows > mine ? (rows - mine + parts - 1) / parts : 0;      // rows of this CTA
-        int per = 1;                                                                // warps of a row
-        while (2 * per * count <= kJWarps && per < kJWarps) per *= 2;
-        const int at_once = kJWarps / per;
-        for (int base = 0; base < count; base += at_once) {
-            const int j = base + warp / per, sub = warp % per;
-            const int r = mine + j * parts;
-            constexpr int kV = D / 32;                                              // columns of a lane
-            float top = -INFINITY, x[kV], l = 0.f;
-#pragma unroll
-            for (int e = 0; e < kV; ++e) x[e] = 0.f;
-            if (j < count) {
-                // the first part was left by c0 as its last, the others as their first
-                for (int k = lane; k < parts; k += 32)
-                    top = fmaxf(top, ld(all_ml + static_cast<int64_t>(2 * (c0 + k) + (k == 0 ? 1 : 0)) * 2 * kTileRows + r));
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-#pragma unroll 4
-                for (int k = sub; k < parts; k += per) {
-                    const int64_t part = 2 * (c0 + k) + (k == 0 ? 1 : 0);
-                    const float pm = ld(all_ml + part * 2 * kTileRows + r), pl = ld(all_ml + part * 2 * kTileRows + kTileRows + r);
-                    const float* src = p.ws + (part * kTileRows + r) * D;
-                    const float a = pm == -INFINITY ? 0.f : ex2(pm - top);
-                    l += a * pl;
-#pragma unroll
-                    for (int e = 0; e < kV; e += 2) {
-                        const float2 y = ld(reinterpret_cast<const float2*>(src + 32 * e + 2 * lane));
-                        x[e] += a == 0.f ? 0.f : a * y.x;
-                        x[e + 1] += a == 0.f ? 0.f : a * y.y;
-                    }
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < kV; e += 2) *reinterpret_cast<float2*>(&sum[warp][32 * e + 2 * lane]) = make_float2(x[e], x[e + 1]);
-            if (lane == 0) sum_l[warp] = l;
-            __syncthreads();
-            // (all rows of this pass, their columns by all threads)
-            for (int id = tid; id < at_once * (D / 4); id += kJThreads) {
-                const int q = id / (D / 4), col = 4 * (id - q * (D / 4));
-                const int jj = base + q;
-                if (jj >= count) continue;
-                const int rj = mine + jj * parts;
-                float y[4] = {0.f, 0.f, 0.f, 0.f}, den = 0.f;
-                for (int s2 = 0; s2 < per; ++s2) {
-                    const float4 v = *reinterpret_cast<const float4*>(&sum[q * per + s2][col]);
-                    y[0] += v.x;
-                    y[1] += v.y;
-                    y[2] += v.z;
-                    y[3] += v.w;
-                    den += sum_l[q * per + s2];
-                }
-                const float inv = den == 0.f ? 0.f : 1.0f / den;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] *= inv;
-                const int rr = tile * kTileRows + rj, t = rr / p.ratio;
-                put_out(p, token_row(p, row0 + t), head * p.ratio + rr - t * p.ratio, D, col, y);
-            }
-            __syncthreads();
-        }
-    }
-}
 
 template <int kKind, int D>
 cudaError_t launch(const AttnParams& p, bool joins, int grid, cudaStream_t stream) {
@@ -906,7 +635,7 @@ cudaError_t launch(const AttnParams& p, bool joins, int grid, cudaStream_t strea
     if (err != cudaSuccess || !joins) return err;
     cfg.blockDim = dim3(kJThreads, 1, 1);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, gdn_attn_join_kernel<D>, p, grid);
+    return cudaLaunchKernelEx(&cfg, gdn_attn_join_kernel<D, kTileRows>, p, grid);
 }
 
 template <int kKind>
@@ -937,17 +666,31 @@ int grid_of(int D, gdn_dtype type) {
 
 namespace gdn_kv {
 
-int64_t attn_workspace(const AttnParams&, int D, gdn_dtype type) {
+// Which kernel: the tcgen05 one pays from the second tile of 16 query rows on, which this one would read the cache for
+// once more (16 sequences of up to 16384 positions, head dim 256, bf16: 32 rows 82 us here and 76 there; 2 of 65535,
+// 64 rows: 136 and 66; 32 of 8192, head dim 128, e4m3, 64 rows: 313 and 167); up to 16 rows this one is faster (32 sequences
+// of up to 4096 positions, 4 rows: 67 and 85; 256 of up to 500, one row: 71 and 125).  It wants pages of whole groups of 8
+// positions, and has no int8 products.
+static bool on_tc(const AttnParams& p, gdn_dtype type) {
+    return type != GDN_I8 && p.ratio * p.max_T > kTileRows && p.pg.page % 8 == 0 && p.pg.num_pages < (1ll << 31);
+}
+
+int64_t attn_workspace(const AttnParams& p, int D, gdn_dtype type) {
+    if (on_tc(p, type)) return attn_tc_workspace(D);
     const int64_t grid = grid_of(D, type);
     return grid * kMetaInts * 4 + 2 * grid * kTileRows * (D + 2) * 4;
 }
 
 cudaError_t launch_attn(AttnParams p, int D, gdn_dtype type, void* workspace, cudaStream_t stream) {
+    if (on_tc(p, type))
+        return type == GDN_BF16  ? launch_attn_tc_bf16(p, D, workspace, stream)
+               : type == GDN_F16 ? launch_attn_tc_f16(p, D, workspace, stream)
+                                 : launch_attn_tc_e4m3(p, D, workspace, stream);
     const int grid = grid_of(D, type);
     p.meta = static_cast<int32_t*>(workspace);
     p.ws = reinterpret_cast<float*>(p.meta + static_cast<int64_t>(grid) * kMetaInts);
     // a unit of one block has nothing to join
-    const bool joins = static_cast<int64_t>(p.pg.cols) * p.pg.page + kKeys > kBlock;
+    const bool joins = static_cast<int64_t>(p.pg.cols) * p.pg.page + kKeys > kCutKeys;
     return type == GDN_BF16   ? by_dim<kBf16>(p, D, joins, grid, stream)
            : type == GDN_F16  ? by_dim<kF16>(p, D, joins, grid, stream)
            : type == GDN_E4M3 ? by_dim<kE4m3>(p, D, joins, grid, stream)

@@ -1,0 +1,387 @@
+// Internal to libgdnspec: what the two attention kernels (gdnattn.cu, gdnattn_tc.cu) share: how a
+// batch's keys are laid on one line and cut among the CTAs, loads, outputs, and the launch that
+// joins the parts of units that several CTAs worked on.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "gdnkv.h"
+
+namespace gdn_attn {
+
+using namespace gdn_common;
+using namespace gdn_kv;
+
+constexpr int kKeys = 16;               // a sequence's first position is rounded down to a multiple of this
+
+// What a kernel cuts by: G::kThreads that scan, G::kBlock keys of the line, G::kRows query rows of a unit.
+
+// ---- the line of all units' key blocks ---------------------------------------------------
+
+struct Span {
+    int lo, hi;                         // positions that some row sees, lo rounded down to kKeys
+    int n;                              // tokens
+    int row0;                           // the first one's place in the order of cu_seqlens
+    int blocks;                         // of G::kBlock keys
+    int tiles;                          // of query rows
+};
+
+template <typename G>
+__device__ __forceinline__ void make_span(const AttnParams& p, int past, int n, int row0, Span& s) {
+    s.n = n;
+    s.row0 = row0;
+    s.hi = past + n;
+    s.lo = p.window > 0 && past >= p.window ? (past + 1 - p.window) & ~(kKeys - 1) : 0;
+    s.blocks = (s.hi - s.lo + G::kBlock - 1) / G::kBlock;
+    s.tiles = (n * p.ratio + G::kRows - 1) / G::kRows;
+}
+
+// Sequence i's part of the line (blocks 0: nothing to do), and a flag for bad data.
+template <typename G>
+__device__ __forceinline__ int span_of(const AttnParams& p, int i, Span& s) {
+    s.blocks = 0;
+    const int a = ld(p.cu + i), e = ld(p.cu + i + 1), end = ld(p.cu + p.batch);
+    const int64_t past = ld(p.kv_lens + i);
+    if (e <= a) return 0;
+    if (a < 0 || e > end || e > p.num_tokens) return GDN_FLAG_TOKEN_ROW;
+    const int n = e - a;
+    if (n > p.max_T) return GDN_FLAG_QLEN;
+    if (past < 0 || past + n > static_cast<int64_t>(p.pg.cols) * p.pg.page) return GDN_FLAG_SLOT_RANGE;
+    if (p.sti) {
+        bool fine = true;
+        for (int t = 0; t < n; ++t) {
+            const int r = ld(p.sti + a + t);
+            fine = fine && r >= 0 && r < p.num_tokens;
+        }
+        if (!fine) return GDN_FLAG_TOKEN_ROW;
+    }
+    make_span<G>(p, static_cast<int>(past), n, a, s);
+    return 0;
+}
+
+// The line as a CTA walks it: the blocks in front of each of `kT` sequences at a time.
+template <typename G>
+struct Line {
+    static constexpr int kT = G::kThreads;
+    int64_t total;                      // blocks of the whole line
+    int64_t base;                       // blocks in front of the chunk
+    int chunk;                          // first sequence of the chunk
+    int64_t before[kT + 1];             // in front of each of its sequences, from base on
+    int64_t warp_sum[kT / 32];
+    int past[kT], n[kT], row0[kT];      // of each (where it has blocks)
+
+    __device__ __forceinline__ void keep(int k, const Span& s) {
+        past[k] = s.hi - s.n;
+        n[k] = s.n;
+        row0[k] = s.row0;
+    }
+};
+
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {     // (32 bits where they do: the division is part of a call's latency)
+    return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+
+template <typename G>
+__device__ __forceinline__ int64_t block_sum(Line<G>& L, int64_t v) {
+    constexpr int kT = G::kThreads;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) L.warp_sum[threadIdx.x / 32] = v;
+    __syncthreads();
+    int64_t sum = 0;
+#pragma unroll
+    for (int w = 0; w < kT / 32; ++w) sum += L.warp_sum[w];
+    return sum;
+}
+
+// The blocks in front of each sequence of the chunk that begins at `first`.
+template <typename G>
+__device__ __forceinline__ void scan_chunk(const AttnParams& p, Line<G>& L, int first, int64_t base, bool tell) {
+    constexpr int kT = G::kThreads;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int i = first + tid;
+    int64_t v = 0;
+    if (i < p.batch) {
+        Span s;
+        const int flag = span_of<G>(p, i, s);
+        if (flag && tell) raise(p.status, flag);
+        if (s.blocks > 0) {
+            v = static_cast<int64_t>(s.blocks) * s.tiles * p.heads;
+            L.keep(tid, s);
+        }
+    }
+    int64_t sum = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(kFull, sum, o);
+        if (lane >= o) sum += u;
+    }
+    __syncthreads();
+    if (lane == 31) L.warp_sum[tid / 32] = sum;
+    __syncthreads();
+    int64_t in = 0;
+#pragma unroll
+    for (int w = 0; w < kT / 32; ++w)
+        if (w < tid / 32) in += L.warp_sum[w];
+    if (tid == 0) {
+        L.before[0] = 0;
+        L.chunk = first;
+        L.base = base;
+    }
+    L.before[tid + 1] = in + sum;
+    __syncthreads();
+}
+
+// The whole line's length; the first chunk is scanned on the way.
+template <typename G>
+__device__ __forceinline__ void begin_line(const AttnParams& p, Line<G>& L) {
+    constexpr int kT = G::kThreads;
+    scan_chunk<G>(p, L, 0, 0, blockIdx.x == 0);
+    int64_t rest = 0;
+    for (int i = kT + threadIdx.x; i < p.batch; i += kT) {
+        Span s;
+        const int flag = span_of<G>(p, i, s);
+        if (flag && blockIdx.x == 0) raise(p.status, flag);
+        if (s.blocks > 0) rest += static_cast<int64_t>(s.blocks) * s.tiles * p.heads;
+    }
+    const int64_t more = p.batch > kT ? block_sum<G>(L, rest) : 0;
+    if (threadIdx.x == 0) L.total = L.before[kT] + more;
+    __syncthreads();
+}
+
+// The sequence whose blocks contain block w of the line (0 <= w < total), chunks moving on.
+template <typename G>
+__device__ __forceinline__ int sequence_at(const AttnParams& p, Line<G>& L, int64_t w) {
+    constexpr int kT = G::kThreads;
+    while (w >= L.base + L.before[kT] && L.chunk + kT < p.batch) {
+        const int64_t base = L.base + L.before[kT];
+        const int first = L.chunk + kT;
+        __syncthreads();
+        scan_chunk<G>(p, L, first, base, false);
+    }
+    int lo = 0, hi = kT - 1;            // the last one that begins at or before w: it has blocks
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (L.base + L.before[mid] <= w) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+// The same by one warp.
+template <typename G>
+__device__ __forceinline__ int sequence_at_warp(const AttnParams& p, Line<G>& L, int64_t w) {
+    constexpr int kT = G::kThreads;
+    const int lane = threadIdx.x & 31;
+    while (w >= L.base + L.before[kT] && L.chunk + kT < p.batch) {
+        const int64_t base = L.base + L.before[kT];
+        const int first = L.chunk + kT;
+        __syncwarp();
+        int64_t run = 0;
+        for (int k = 0; k < kT / 32; ++k) {
+            const int i = first + 32 * k + lane;
+            int64_t sum = 0;
+            Span s;
+            if (i < p.batch) {
+                span_of<G>(p, i, s);
+                if (s.blocks > 0) {
+                    sum = static_cast<int64_t>(s.blocks) * s.tiles * p.heads;
+                    L.keep(32 * k + lane, s);
+                }
+            }
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t u = __shfl_up_sync(kFull, sum, o);
+                if (lane >= o) sum += u;
+            }
+            L.before[32 * k + lane + 1] = run + sum;
+            run += __shfl_sync(kFull, sum, 31);
+        }
+        if (lane == 0) {
+            L.before[0] = 0;
+            L.chunk = first;
+            L.base = base;
+        }
+        __syncwarp();
+    }
+    int lo = 0, hi = kT - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (L.base + L.before[mid] <= w) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+}
+
+// CTAs that share the line: no more than leave each `least` blocks
+__device__ __forceinline__ int ctas_of(int64_t total, int grid, int least) {
+    const int64_t most = (total + least - 1) / least;
+    return static_cast<int>(most < grid ? (most > 0 ? most : 1) : grid);
+}
+
+// What a CTA works on next: the unit at block w of the line, up to block w1.
+struct Piece {
+    int seq, head, tile, rows, past, n, row0;
+    int b0, b1, blocks;                 // of the unit's blocks
+    int key0, key1;
+};
+template <typename G>
+__device__ __forceinline__ Piece piece_at(const AttnParams& p, const Line<G>& L, int k, int64_t w, int64_t w1) {
+    Piece d;
+    Span s;
+    make_span<G>(p, L.past[k], L.n[k], L.row0[k], s);
+    const int64_t in_seq = w - L.base - L.before[k];
+    const int unit = static_cast<int>(quotient(in_seq, s.blocks));          // (head, tile of rows)
+    d.seq = L.chunk + k;
+    d.b0 = static_cast<int>(in_seq - static_cast<int64_t>(unit) * s.blocks);
+    d.b1 = static_cast<int>(w1 - w < s.blocks - d.b0 ? d.b0 + (w1 - w) : s.blocks);
+    d.blocks = s.blocks;
+    d.head = unit / s.tiles;
+    d.tile = unit - d.head * s.tiles;
+    d.rows = min(G::kRows, s.n * p.ratio - d.tile * G::kRows);
+    d.past = s.hi - s.n;
+    d.n = s.n;
+    d.row0 = s.row0;
+    d.key0 = s.lo + d.b0 * G::kBlock;
+    d.key1 = min(s.hi, s.lo + d.b1 * G::kBlock);
+    return d;
+}
+// the record of a part that is not a whole unit (block b of the line is CTA ((b + 1) ctas - 1) / total's)
+__device__ __forceinline__ void put_record(int32_t* meta, const Piece& d, int64_t w, int64_t total, int ctas) {
+    const int64_t u0 = w - d.b0, u1 = u0 + d.blocks;
+    int32_t* rec = meta + 8 * (d.b0 > 0 ? 0 : 1);
+    rec[0] = d.seq;
+    rec[1] = d.head;
+    rec[2] = d.tile;
+    rec[3] = static_cast<int>(quotient((u0 + 1) * ctas - 1, total));
+    rec[4] = static_cast<int>(quotient(u1 * ctas - 1, total));
+    rec[5] = d.rows;
+    rec[6] = d.row0;
+}
+
+// ---- instructions ---------------------------------------------------------------------------
+
+__device__ __forceinline__ uint32_t saddr(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+    const int bytes = live ? 16 : 0;    // (0: zeros, and nothing is read)
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool live) {
+    const int bytes = live ? 4 : 0;
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ uint32_t pack_h(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_b(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ int64_t token_row(const AttnParams& p, int i) { return p.sti ? ld(p.sti + i) : i; }
+
+// O of one row and column quad, weighed: to the output
+__device__ __forceinline__ void put_out(const AttnParams& p, int64_t row, int head, int D, int col, const float (&o)[4]) {
+    float x[4] = {o[0], o[1], o[2], o[3]};
+    if (p.z) {
+        const uint2 raw = ld(reinterpret_cast<const uint2*>(p.z + row * p.z_stride + static_cast<int64_t>(head) * D + col));
+        const float z[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u), __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u)};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = __fdividef(x[e], 1.0f + __expf(-z[e]));
+    }
+    *reinterpret_cast<uint2*>(p.out + row * p.out_stride + static_cast<int64_t>(head) * D + col) = make_uint2(pack_b(x[0], x[1]), pack_b(x[2], x[3]));
+}
+
+// ---- the second launch: parts of a unit joined ------------------------------------------------------
+//
+// Each of the CTAs that share a unit joins some of its rows: CTA c of c0 .. c1 those whose number is
+// c - c0 modulo their count.  A row's parts are summed by the warps that are left over for it.
+
+constexpr int kJThreads = 256, kJWarps = 8;
+
+template <int D, int kTileRows>
+__global__ void __launch_bounds__(kJThreads) gdn_attn_join_kernel(const AttnParams p, const int grid) {
+    __shared__ float sum[kJWarps][D];
+    __shared__ float sum_l[kJWarps];
+    dep_wait();
+    dep_launch();
+    const int cta = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int32_t* const meta = p.meta + static_cast<int64_t>(cta) * kMetaInts;
+    const float* const all_ml = p.ws + static_cast<int64_t>(2 * grid) * kTileRows * D;
+    for (int which = 0; which < 2; ++which) {
+        const int32_t* const rec = meta + 8 * which;
+        const int seq = ld(rec);
+        if (seq < 0) continue;
+        const int head = ld(rec + 1), tile = ld(rec + 2), c0 = ld(rec + 3), c1 = ld(rec + 4), rows = ld(rec + 5), row0 = ld(rec + 6);
+        const int parts = c1 - c0 + 1, mine = cta - c0;
+        const int count = rows > mine ? (rows - mine + parts - 1) / parts : 0;      // rows of this CTA
+        int per = 1;                                                                // warps of a row
+        while (2 * per * count <= kJWarps && per < kJWarps) per *= 2;
+        const int at_once = kJWarps / per;
+        for (int base = 0; base < count; base += at_once) {
+            const int j = base + warp / per, sub = warp % per;
+            const int r = mine + j * parts;
+            constexpr int kV = D / 32;                                              // columns of a lane
+            float top = -INFINITY, x[kV], l = 0.f;
+#pragma unroll
+            for (int e = 0; e < kV; ++e) x[e] = 0.f;
+            if (j < count) {
+                // the first part was left by c0 as its last, the others as their first
+                for (int k = lane; k < parts; k += 32)
+                    top = fmaxf(top, ld(all_ml + static_cast<int64_t>(2 * (c0 + k) + (k == 0 ? 1 : 0)) * 2 * kTileRows + r));
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+#pragma unroll 4
+                for (int k = sub; k < parts; k += per) {
+                    const int64_t part = 2 * (c0 + k) + (k == 0 ? 1 : 0);
+                    const float pm = ld(all_ml + part * 2 * kTileRows + r), pl = ld(all_ml + part * 2 * kTileRows + kTileRows + r);
+                    const float* src = p.ws + (part * kTileRows + r) * D;
+                    const float a = pm == -INFINITY ? 0.f : ex2(pm - top);
+                    l += a * pl;
+#pragma unroll
+                    for (int e = 0; e < kV; e += 2) {
+                        const float2 y = ld(reinterpret_cast<const float2*>(src + 32 * e + 2 * lane));
+                        x[e] += a == 0.f ? 0.f : a * y.x;
+                        x[e + 1] += a == 0.f ? 0.f : a * y.y;
+                    }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < kV; e += 2) *reinterpret_cast<float2*>(&sum[warp][32 * e + 2 * lane]) = make_float2(x[e], x[e + 1]);
+            if (lane == 0) sum_l[warp] = l;
+            __syncthreads();
+            // (all rows of this pass, their columns by all threads)
+            for (int id = tid; id < at_once * (D / 4); id += kJThreads) {
+                const int q = id / (D / 4), col = 4 * (id - q * (D / 4));
+                const int jj = base + q;
+                if (jj >= count) continue;
+                const int rj = mine + jj * parts;
+                float y[4] = {0.f, 0.f, 0.f, 0.f}, den = 0.f;
+                for (int s2 = 0; s2 < per; ++s2) {
+                    const float4 v = *reinterpret_cast<const float4*>(&sum[q * per + s2][col]);
+                    y[0] += v.x;
+                    y[1] += v.y;
+                    y[2] += v.z;
+                    y[3] += v.w;
+                    den += sum_l[q * per + s2];
+                }
+                const float inv = den == 0.f ? 0.f : 1.0f / den;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] *= inv;
+                const int rr = tile * kTileRows + rj, t = rr / p.ratio;
+                put_out(p, token_row(p, row0 + t), head * p.ratio + rr - t * p.ratio, D, col, y);
+            }
+            __syncthreads();
+        }
+    }
+}
+}  // namespace gdn_attn

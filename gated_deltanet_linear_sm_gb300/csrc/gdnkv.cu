@@ -464,6 +464,8 @@ AttnParams attn_sizes(const gdn_kv_dims* d) {
     p.ratio = d->H_q / d->H_kv;
     p.max_T = d->max_T;
     p.window = d->window;
+    p.pg.page = d->page_size;
+    p.pg.num_pages = d->num_pages;
     return p;
 }
 

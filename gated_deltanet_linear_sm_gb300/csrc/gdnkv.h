@@ -72,10 +72,14 @@ struct AttnParams {
 
 constexpr int kMaxCtas = 1024;      // of an attention launch
 constexpr int kMetaInts = 16;       // of a CTA: two records of 8
-constexpr int kTileRows = 16;       // query rows (heads of a group, times tokens) that a CTA works on at a time
 
 // Workspace in bytes on the current device (gdnattn.cu).
 int64_t attn_workspace(const AttnParams& p, int D, gdn_dtype type);
 cudaError_t launch_attn(AttnParams p, int D, gdn_dtype type, void* workspace, cudaStream_t stream);
+// The same on the tcgen05 tensor cores, by the cache's type (gdnattn_tc.cuh).
+int64_t attn_tc_workspace(int D);
+cudaError_t launch_attn_tc_bf16(const AttnParams& p, int D, void* workspace, cudaStream_t stream);
+cudaError_t launch_attn_tc_f16(const AttnParams& p, int D, void* workspace, cudaStream_t stream);
+cudaError_t launch_attn_tc_e4m3(const AttnParams& p, int D, void* workspace, cudaStream_t stream);
 
 }  // namespace gdn_kv

@@ -89,10 +89,10 @@ typedef enum { GDN_F32 = 0, GDN_BF16 = 1, GDN_F16 = 2, GDN_E4M3 = 3, GDN_I8 = 4 
 #define GDN_FLAG_QLEN       4  /* q_len > max_T or q_len > spec_stride: sequence skipped */
 #define GDN_FLAG_TOKEN_ROW  8  /* a token row outside [0, num_tokens), or cu_seqlens[i] < 0 or
                                   cu_seqlens[i+1] > cu_seqlens[batch]: sequence skipped */
-#define GDN_FLAG_TIMEOUT    16 /* gdn_prefill_chunked and gdn_ssm_prefill only: a wait on the tensor
-                                  cores ran past its bound (gdn_set_wait_limit); that sequence's
-                                  outputs and final state are incomplete */
-#define GDN_FLAG_DRAIN      32 /* the same two only: after such a timeout, the wait (with the
+#define GDN_FLAG_TIMEOUT    16 /* gdn_prefill_chunked, gdn_ssm_prefill and gdn_attn_decode only: a wait on
+                                  the tensor cores ran past its bound (gdn_set_wait_limit); that sequence's
+                                  outputs and final state are incomplete (gdn_attn_decode: the call's) */
+#define GDN_FLAG_DRAIN      32 /* the same three only: after such a timeout, the wait (with the
                                   default bound) for the products still in flight ran out too; the
                                   CTA released its tensor memory regardless, since holding it would
                                   block every later kernel on that SM */
@@ -793,7 +793,8 @@ GDNSPEC_API int32_t gdn_spec_decode_split(const gdn_dims* dims, gdn_dtype state_
 
 /*
  * Bound on each wait of gdn_prefill_chunked for its tensor-core products, and
- * of gdn_ssm_prefill for those, its copies and its own warps: 0 (the default)
+ * of gdn_ssm_prefill and gdn_attn_decode (above 16 query rows) for those, their copies and their own
+ * warps: 0 (the default)
  * waits with blocking polls of the barrier, 2^24 of them (2^17 of up to 20 us;
  * well over a second either way); a non-zero bound counts non-blocking polls
  * instead, so that a small one runs out for certain.  A wait that runs out

@@ -32,6 +32,9 @@ from tests import kv_ref as ref
 
 pytestmark = pytest.mark.gpu
 KINDS = list(ref.TYPES)
+# one tile of 16 query rows or fewer, and more: there are two kernels (int8 caches, and pages that are no whole groups of 8
+# positions, run on the first with more rows too)
+BOTH = pytest.mark.parametrize("wide", [1, 7])
 SENTINEL = 0x7FBF               # a NaN bf16 pattern that no kernel writes
 
 
@@ -153,8 +156,9 @@ LENS = [0, 1, 14, 15, 16, 17, 47, 62, 63, 64, 65, 126, 127, 128, 129, 200, 511, 
 
 @pytest.mark.parametrize("D", [64, 128, 192, 256])
 @pytest.mark.parametrize("kind", KINDS)
-def test_single_tokens_of_every_length(cuda_device, kind, D):
-    c = Case(cuda_device, LENS, [1] * len(LENS), 8, 2, D, kind, seed=D)
+@BOTH
+def test_single_tokens_of_every_length(cuda_device, kind, D, wide):
+    c = Case(cuda_device, LENS, [1] * len(LENS), 8 * wide, 2, D, kind, seed=D)
     c.run()
     assert int(c.status) == 0
     c.check()
@@ -172,27 +176,30 @@ def test_drafted_tokens_and_head_layouts(cuda_device, kind, H, G, T):
     c.check()
 
 
-@pytest.mark.parametrize("page", [1, 7, 16, 48, 544])
+@pytest.mark.parametrize("page", [1, 7, 8, 16, 40, 48, 64, 128, 256, 544])
 @pytest.mark.parametrize("layout", ["nhd", "hnd", "pair"])
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
-def test_page_sizes_and_layouts(cuda_device, kind, layout, page):
-    c = Case(cuda_device, [0, 40, 129, 700, 1200], [2, 1, 3, 2, 3], 6, 2, 64, kind, page=page, layout=layout, seed=page)
+@BOTH
+def test_page_sizes_and_layouts(cuda_device, kind, layout, page, wide):
+    c = Case(cuda_device, [0, 40, 129, 700, 1200], [2, 1, 3, 2, 3], 6 * wide, 2, 64, kind, page=page, layout=layout, seed=page)
     c.run()
     c.check()
 
 
 @pytest.mark.parametrize("window", [1, 2, 15, 16, 17, 64, 100, 5000])
 @pytest.mark.parametrize("kind", KINDS)
-def test_windows(cuda_device, kind, window):
-    c = Case(cuda_device, [0, 5, 16, 99, 100, 640, 1500], [1, 4, 3, 4, 2, 4, 4], 8, 2, 128, kind, seed=window)
+@BOTH
+def test_windows(cuda_device, kind, window, wide):
+    c = Case(cuda_device, [0, 5, 16, 99, 100, 640, 1500], [1, 4, 3, 4, 2, 4, 4], 8 * wide, 2, 128, kind, page=64 if wide > 1 else 16, seed=window)
     c.run(window=window)
     c.check(window=window)
 
 
 @pytest.mark.parametrize("kind", KINDS)
-def test_pages_that_are_none(cuda_device, kind):
+@BOTH
+def test_pages_that_are_none(cuda_device, kind, wide):
     """Pages that a window has left behind, a hole, and a sequence with no page at all: its rows are zero."""
-    c = Case(cuda_device, [100, 400, 70, 33], [1, 3, 2, 1], 4, 2, 128, kind, seed=5)
+    c = Case(cuda_device, [100, 400, 70, 33], [1, 3, 2, 1], 4 * wide, 2, 128, kind, seed=5)
     c.table[0, 0] = -1
     c.table[1, 3:9] = -7
     c.table[2, :] = -1
@@ -219,10 +226,11 @@ def test_a_negative_scale_is_that_of_negated_queries(cuda_device):
 
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("order", ["rising", "falling", "loud"])
-def test_references_that_move(cuda_device, kind, order):
+@BOTH
+def test_references_that_move(cuda_device, kind, order, wide):
     """Scores that rise or fall by hundreds along a sequence, and large random ones."""
     dev = cuda_device
-    c = Case(dev, [900, 2000], [1, 3], 8, 1, 64, kind, seed=9, q_size=1.0 if order != "loud" else 30.0)
+    c = Case(dev, [900, 2000], [1, 3], 8 * wide, 1, 64, kind, seed=9, q_size=1.0 if order != "loud" else 30.0)
     if order != "loud":
         u = torch.randn(64, generator=torch.Generator().manual_seed(1)).sign().to(dev)
         c.q = (u * 1.0 + 0.05 * c.q.float()).bfloat16()
@@ -247,9 +255,10 @@ def test_references_that_move(cuda_device, kind, order):
 
 
 @pytest.mark.parametrize("kind", ["e4m3", "int8"])
-def test_scales_of_very_different_sizes(cuda_device, kind):
+@BOTH
+def test_scales_of_very_different_sizes(cuda_device, kind, wide):
     """Values' scales from 2^-40 to 2^40 in turn, zero among them; keys' scales that leave the scores small."""
-    c = Case(cuda_device, [500, 80], [2, 1], 4, 1, 128, kind, seed=3)
+    c = Case(cuda_device, [500, 80], [2, 1], 4 * wide, 1, 128, kind, seed=3)
     g = torch.Generator(device=cuda_device).manual_seed(4)
     live = ~torch.isnan(c.vs)
     c.vs[live] = 2.0 ** torch.randint(-40, 41, (int(live.sum()),), generator=g, device=cuda_device).float()
@@ -260,11 +269,13 @@ def test_scales_of_very_different_sizes(cuda_device, kind):
 
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
-def test_a_token_that_is_no_number_spoils_those_that_see_it(cuda_device, kind, bad):
+@BOTH
+def test_a_token_that_is_no_number_spoils_those_that_see_it(cuda_device, kind, bad, wide):
     """The third of four drafted tokens has a value (16 bit) or a scale (8 bit) that is no number, and so has a row just outside
     another sequence's window: who does not see them is not touched."""
     for which in ("v", "k"):
-        c = Case(cuda_device, [61, 200, 30], [4, 2, 1], 8, 2, 64, kind, seed=11)
+        H = 8 * wide
+        c = Case(cuda_device, [61, 200, 30], [4, 2, 1], H, 2, 64, kind, seed=11)
         cache, scale = (c.v, c.vs) if which == "v" else (c.k, c.ks)
         for i, x in ((0, 63), (1, 100)):
             pg, row = int(c.table[i, x // c.page]), x % c.page
@@ -276,10 +287,10 @@ def test_a_token_that_is_no_number_spoils_those_that_see_it(cuda_device, kind, b
         c.run(window=window)
         out = c.out.double().cpu()
         first = [int(c.cu[i]) for i in range(3)]
-        spoiled = torch.zeros(7, 8, 64, dtype=torch.bool)
+        spoiled = torch.zeros(7, H, 64, dtype=torch.bool)
         cols = slice(None) if which == "k" or scale is not None else slice(5, 6)
         for r in (first[0] + 2, first[0] + 3, first[1]):
-            spoiled[r, 4:, cols] = True
+            spoiled[r, H // 2:, cols] = True
         if which == "v":
             assert torch.equal(~torch.isfinite(out), spoiled)
         else:                                        # an infinite score: NaN, or no weight where it is the negative one
@@ -308,73 +319,86 @@ def _check_unspoiled(c, window, spoiled):
             assert bool((((out[r] - want).abs() <= bound) | spoiled[r]).all()), (i, t)
 
 
-def test_queries_that_are_no_numbers_spoil_their_own_head(cuda_device):
+@BOTH
+def test_queries_that_are_no_numbers_spoil_their_own_head(cuda_device, wide):
     for kind in KINDS:
-        c = Case(cuda_device, [300, 20], [2, 1], 8, 2, 128, kind, seed=21)
+        c = Case(cuda_device, [300, 20], [2, 1], 8 * wide, 2, 128, kind, seed=21)
         c.run()
         want = c.out.clone()
         c.q[1, 3, 7] = math.nan
         c.q[2, 0, 0] = math.inf
         c.run()
-        hit = torch.zeros(3, 8, dtype=torch.bool, device=cuda_device)
+        hit = torch.zeros(3, 8 * wide, dtype=torch.bool, device=cuda_device)
         hit[1, 3] = hit[2, 0] = True
         assert bool(torch.isnan(c.out[hit].float()).all())
         assert torch.equal(c.out[~hit].view(torch.int16), want[~hit].view(torch.int16))
 
 
-@pytest.mark.parametrize("kind,D,H,G", [("bf16", 128, 8, 1), ("e4m3", 128, 8, 1), ("int8", 256, 4, 2), ("f16", 64, 40, 1)])
+@pytest.mark.parametrize("kind,D,H,G", [("bf16", 128, 8, 1), ("e4m3", 128, 8, 1), ("int8", 256, 4, 2), ("f16", 64, 40, 1),
+                                          ("bf16", 128, 40, 1), ("bf16", 256, 40, 1), ("e4m3", 192, 40, 1), ("e4m3", 256, 20, 1)])
 def test_one_long_sequence_in_many_parts(cuda_device, kind, D, H, G):
     c = Case(cuda_device, [100003], [2], H, G, D, kind, page=64, seed=1, q_size=2.0)
     c.run()
     c.check()
     again = c.out.clone()
-    c.run()
-    assert torch.equal(again.view(torch.int16), c.out.view(torch.int16))
+    call = gdn.prepare_attn_decode(*c.args(), **c.kw())
+    for _ in range(20):
+        c.out.view(torch.int16).fill_(SENTINEL)
+        call()
+        assert torch.equal(again.view(torch.int16), c.out.view(torch.int16))
+    assert int(c.status) == 0
 
 
-@pytest.mark.parametrize("batch", [127, 129, 257, 700])
-def test_many_sequences(cuda_device, batch):
+@pytest.mark.parametrize("batch", [127, 129, 257, 480, 481, 700, 1000])
+@BOTH
+def test_many_sequences(cuda_device, batch, wide):
     """More sequences than a CTA scans at a time, many of them without tokens."""
     rng = random.Random(batch)
     past = [rng.choice([0, 1, 30, 64, 100, 333]) for _ in range(batch)]
     n = [rng.choice([0, 0, 1, 2]) for _ in range(batch)]
     n[-1] = 2
-    c = Case(cuda_device, past, n, 4, 2, 64, "bf16", seed=batch)
+    c = Case(cuda_device, past, n, 4 * wide, 2, 64, "bf16", seed=batch)
     c.run()
     assert int(c.status) == 0
     c.check()
 
 
-def test_a_batch_without_tokens(cuda_device):
-    c = Case(cuda_device, [5, 9], [0, 0], 4, 2, 64, "bf16")
-    c.q, c.out = torch.randn(3, 4, 64, device=cuda_device).bfloat16(), _sentinel((3, 4, 64), cuda_device)
+@BOTH
+def test_a_batch_without_tokens(cuda_device, wide):
+    H = 6 * wide
+    c = Case(cuda_device, [5, 9], [0, 0], H, 2, 64, "bf16")
+    c.q, c.out = torch.randn(3, H, 64, device=cuda_device).bfloat16(), _sentinel((3, H, 64), cuda_device)
     c.run()
     assert int(c.status) == 0 and bool((c.out.view(torch.int16) == SENTINEL).all())
 
 
-def test_strided_rows(cuda_device):
-    dev = cuda_device
-    c = Case(dev, [40, 300], [2, 3], 8, 2, 128, "bf16", gate=True, seed=6)
-    packed = torch.zeros(5, 8 * 128 * 2 + 64, device=dev, dtype=torch.bfloat16)
-    packed[:, :1024] = c.q.view(5, -1)
-    packed[:, 1024:2048] = c.z.view(5, -1)
-    c.q, c.z = packed[:, :1024].view(5, 8, 128), packed[:, 1024:2048].view(5, 8, 128)
-    wide = _sentinel((5, 8 * 128 + 8), dev)
-    c.out = wide[:, :1024].view(5, 8, 128)
+@BOTH
+def test_strided_rows(cuda_device, wide):
+    dev, H = cuda_device, 8 * wide
+    W = H * 128
+    c = Case(dev, [40, 300], [2, 3], H, 2, 128, "bf16", gate=True, seed=6)
+    packed = torch.zeros(5, W * 2 + 64, device=dev, dtype=torch.bfloat16)
+    packed[:, :W] = c.q.view(5, -1)
+    packed[:, W:2 * W] = c.z.view(5, -1)
+    c.q, c.z = packed[:, :W].view(5, H, 128), packed[:, W:2 * W].view(5, H, 128)
+    wider = _sentinel((5, W + 8), dev)
+    c.out = wider[:, :W].view(5, H, 128)
     table = torch.full((2, 40), -1, dtype=torch.int32, device=dev)
     table[:, :c.table.shape[1]] = c.table.to(dev)
     gdn.gdn_attn_decode(c.q, c.k, c.v, table[:, :c.table.shape[1]], _i32(c.past, dev), c.cu.to(dev), c.out, **c.kw())
     torch.cuda.synchronize()
     c.check()
-    assert bool((wide[:, 1024:].contiguous().view(torch.int16) == SENTINEL).all())
+    assert bool((wider[:, W:].contiguous().view(torch.int16) == SENTINEL).all())
 
 
 FLAGS = [("page", 1), ("long", 1), ("negative", 1), ("q_len", 4), ("row", 8), ("offsets", 8)]
 
 
 @pytest.mark.parametrize("what,flag", FLAGS)
-def test_bad_data_skips_the_sequence(cuda_device, what, flag):
-    c = Case(cuda_device, [40, 90, 200], [2, 2, 1], 4, 2, 128, "bf16", gather=what == "row", seed=8)
+@BOTH
+def test_bad_data_skips_the_sequence(cuda_device, what, flag, wide):
+    # (20 rows for a single token: the bound on the tokens is part of which kernel runs)
+    c = Case(cuda_device, [40, 90, 200], [2, 2, 1], 4 if wide == 1 else 40, 2, 128, "bf16", gather=what == "row", seed=8)
     skipped = (1,)
     table, past, cu, sti = c.table.clone(), list(c.past), c.cu.clone(), c.sti
     if what == "page":
@@ -402,36 +426,40 @@ def test_bad_data_skips_the_sequence(cuda_device, what, flag):
     c.check(skipped=skipped)
 
 
-def test_rows_and_places_beyond_two_to_the_31_elements(cuda_device):
+@BOTH
+def test_rows_and_places_beyond_two_to_the_31_elements(cuda_device, wide):
     """Pages so far apart that the last lies beyond 2^31 elements, 8 and 16 bits."""
     dev = cuda_device
-    for kind in ("bf16", "int8"):
-        c = Case(dev, [70, 33], [1, 2], 4, 1, 64, kind, seed=2)
+    for kind in ("bf16", "int8" if wide == 1 else "e4m3"):
+        c = Case(dev, [70, 33], [1, 2], 4 * wide, 1, 64, kind, seed=2)
         pages = c.k.shape[0]
-        apart = (2 ** 31 // (pages - 2) // 64 + 1) * 64
-        big = [torch.zeros(apart * (pages - 1) + c.page * 64, dtype=c.k.dtype, device=dev) for _ in range(2)]
+        apart = (2 ** 31 // max(int(c.table.max()), 1) // 64 + 1) * 64
+        big = [torch.zeros(apart * (pages - 1) + c.page * 64, dtype=torch.int8 if c.ks is not None else c.k.dtype, device=dev).view(c.k.dtype)
+               for _ in range(2)]
         views = [b.as_strided((pages, c.page, 1, 64), (apart, 64, 64, 1)) for b in big]
         for v, old in zip(views, (c.k, c.v)):
-            v.copy_(old)
+            (v.view(torch.int8) if c.ks is not None else v).copy_(old.view(torch.int8) if c.ks is not None else old)
         assert int(c.table.max()) * apart > 2 ** 31
         c.k, c.v = views
         c.run()
-        small = [v.clone() for v in views]
-        c.k, c.v = small
+        c.k, c.v = ((v.view(torch.int8) if c.ks is not None else v).contiguous().view(v.dtype) for v in views)
         c.check()
         k = torch.randn(3, 1, 64, device=dev).bfloat16()
         gdn.gdn_kv_write(k, -k, *views, c.table.to(dev), _i32(c.past, dev), c.cu.to(dev), k_scale=c.ks, v_scale=c.vs)
         got = [torch.empty(3, 1, 64, device=dev) for _ in range(2)]
         gdn.gdn_kv_read(*views, c.table.to(dev), _i32(c.past, dev), c.cu.to(dev), *got, k_scale=c.ks, v_scale=c.vs)
-        assert float((got[0] - k.float()).abs().max()) <= float(k.float().abs().max()) / 126 / 2 and torch.equal(got[1], -got[0])
+        off = (got[0] - k.float()).abs()             # half a step of 8-bit codes (e4m3: of its 4 bits)
+        assert bool((off <= k.float().abs().amax(-1, keepdim=True) * (2.0 ** -4 if kind == "e4m3" else 1 / 252)).all())
+        assert torch.equal(got[1], -got[0])
         del big, views
 
 
-def test_captured_on_two_streams_with_lengths_that_grow(cuda_device):
+@BOTH
+def test_captured_on_two_streams_with_lengths_that_grow(cuda_device, wide):
     dev = cuda_device
     cases, graphs, lens = [], [], []
     for s in range(2):
-        c = Case(dev, [900, 40, 3000], [4, 4, 4], 16, 2, 128, ("bf16", "e4m3")[s], seed=s)
+        c = Case(dev, [900, 40, 3000], [4, 4, 4], 8 * wide, 2, 128, ("bf16", "e4m3")[s], seed=s)
         lens.append(_i32(c.past, dev))
         a = list(c.args())
         a[4] = lens[-1]
@@ -457,8 +485,9 @@ def test_captured_on_two_streams_with_lengths_that_grow(cuda_device):
             c.check()
 
 
-def test_a_given_workspace_holds_anything(cuda_device):
-    c = Case(cuda_device, [3000, 20], [2, 1], 8, 2, 128, "f16", seed=3)
+@BOTH
+def test_a_given_workspace_holds_anything(cuda_device, wide):
+    c = Case(cuda_device, [3000, 20], [2, 1], 8 * wide, 2, 128, "f16", seed=3)
     need = gdn.prepare_attn_decode(*c.args(), **c.kw())._bytes
     ws = torch.full((need,), 0xFF, dtype=torch.uint8, device=cuda_device)
     with pytest.raises(ValueError, match="workspace"):
@@ -471,7 +500,7 @@ def test_a_given_workspace_holds_anything(cuda_device):
     c.check()
 
 
-@pytest.mark.parametrize("seed", range(24))
+@pytest.mark.parametrize("seed", range(48))
 def test_random_batches(cuda_device, seed):
     rng = random.Random(1000 + seed)
     T = rng.randint(1, 8)
@@ -481,12 +510,30 @@ def test_random_batches(cuda_device, seed):
     past = [int(math.exp(rng.uniform(0, math.log(4000)))) - 1 for _ in range(batch)]
     n = [rng.randint(0 if batch > 1 else 1, T) for _ in range(batch)]
     window = rng.choice([0, 0, 1, 33, 500])
-    c = Case(cuda_device, past, n, G * rng.choice([1, 2, 5, 8, 12]), G, rng.choice([64, 128, 192, 256]), kind, page=rng.choice([1, 16, 24, 64, 100]),
+    c = Case(cuda_device, past, n, G * rng.choice([1, 2, 5, 8, 12, 20]), G, rng.choice([64, 128, 192, 256]), kind, page=rng.choice([1, 16, 24, 64, 100, 128]),
              layout=rng.choice(["nhd", "hnd", "pair"]), gate=rng.random() < 0.5, gather=rng.random() < 0.5, max_T=T, q_size=rng.choice([0.3, 1, 4]),
              seed=seed, loud=rng.choice([0.01, 1.0, 5.0]))
     c.run(window=window)
     assert int(c.status) == 0
     c.check(window=window)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "e4m3"])
+def test_waits_that_run_out_end_the_call(cuda_device, kind):
+    """With a bound of one poll every wait of the tensor-core kernel runs out: the call ends, says so, and the next one is right."""
+    from gated_deltanet_linear_sm_gb300 import binding
+    c = Case(cuda_device, [3000, 500, 77], [4, 1, 2], 32, 2, 128, kind, page=64, seed=4)
+    binding.set_wait_limit(1)
+    try:
+        c.run()
+    finally:
+        binding.set_wait_limit(0)
+    assert int(c.status) == binding.GDN_FLAG_TIMEOUT
+    c.status.zero_()
+    c.out.view(torch.int16).fill_(SENTINEL)
+    c.run()
+    assert int(c.status) == 0
+    c.check()
 
 
 # ---- the cache -----------------------------------------------------------------------------
