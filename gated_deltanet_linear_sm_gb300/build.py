@@ -13,10 +13,11 @@ CSRC = os.path.join(PKG, "csrc")
 # layer's C entry points, its tensor-core chunked prefill, the verification and
 # tables between steps, and the state-space layer's step and scan
 SRCS = [os.path.join(CSRC, f) for f in ("gdnspec.cu", "gdnprefill_chunked.cu", "gdnverify.cu", "gdnssm.cu",
-                                        "gdnssm_prefill.cu", "gdnkv.cu", "gdnattn.cu", "gdnattn_tc_bf16.cu",
-                                        "gdnattn_tc_f16.cu", "gdnattn_tc_e4m3.cu")]
+                                        "gdnssm_prefill.cu", "gdnkv.cu", "gdnattn.cu", "gdnattn_bf16.cu",
+                                        "gdnattn_f16.cu", "gdnattn_e4m3.cu", "gdnattn_i8.cu")]
 HEADERS = [os.path.join(ROOT, "include", "gdnspec.h")] + [
-    os.path.join(CSRC, f) for f in ("gdn_internal.h", "gdn_common.h", "gdn_pairs.h", "gdn_tcgen05.h", "gdnssm.h", "gdnssm_recur.cuh", "gdnkv.h", "gdnattn.cuh", "gdnattn_tc.cuh")]
+    os.path.join(CSRC, f) for f in ("gdn_internal.h", "gdn_common.h", "gdn_pairs.h", "gdn_tcgen05.h", "gdnssm.h", "gdnssm_recur.cuh", "gdnkv.h", "gdnattn.cuh", "gdnattn_warp.cuh",
+                                "gdnattn_tc.cuh")]
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD_DIR, "libgdnspec.so")
 

@@ -14,7 +14,9 @@ using namespace gdn_kv;
 
 constexpr int kKeys = 16;               // a sequence's first position is rounded down to a multiple of this
 
-// What a kernel cuts by: G::kThreads that scan, G::kBlock keys of the line, G::kRows query rows of a unit.
+// What a kernel cuts by: G::kThreads that scan, G::kPer sequences each at a time, G::kBlock keys of the line,
+// G::kRows query rows of a unit, and G::kCost, what a unit costs beyond its keys, in blocks: so many places in
+// front of a unit's blocks on the line have nothing to do.
 
 // ---- the line of all units' key blocks ---------------------------------------------------
 
@@ -24,6 +26,7 @@ struct Span {
     int row0;                           // the first one's place in the order of cu_seqlens
     int blocks;                         // of G::kBlock keys
     int tiles;                          // of query rows
+    int len;                            // of a unit on the line
 };
 
 template <typename G>
@@ -34,6 +37,7 @@ __device__ __forceinline__ void make_span(const AttnParams& p, int past, int n, 
     s.lo = p.window > 0 && past >= p.window ? (past + 1 - p.window) & ~(kKeys - 1) : 0;
     s.blocks = (s.hi - s.lo + G::kBlock - 1) / G::kBlock;
     s.tiles = (n * p.ratio + G::kRows - 1) / G::kRows;
+    s.len = s.blocks + G::kCost;
 }
 
 // Sequence i's part of the line (blocks 0: nothing to do), and a flag for bad data.
@@ -59,15 +63,15 @@ __device__ __forceinline__ int span_of(const AttnParams& p, int i, Span& s) {
     return 0;
 }
 
-// The line as a CTA walks it: the blocks in front of each of `kT` sequences at a time.
+// The line as a CTA walks it: the blocks in front of each of kT sequences at a time.
 template <typename G>
 struct Line {
-    static constexpr int kT = G::kThreads;
+    static constexpr int kT = G::kThreads * G::kPer;
     int64_t total;                      // blocks of the whole line
     int64_t base;                       // blocks in front of the chunk
     int chunk;                          // first sequence of the chunk
     int64_t before[kT + 1];             // in front of each of its sequences, from base on
-    int64_t warp_sum[kT / 32];
+    int64_t warp_sum[G::kThreads / 32];
     int past[kT], n[kT], row0[kT];      // of each (where it has blocks)
 
     __device__ __forceinline__ void keep(int k, const Span& s) {
@@ -83,7 +87,6 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {     // (32 b
 
 template <typename G>
 __device__ __forceinline__ int64_t block_sum(Line<G>& L, int64_t v) {
-    constexpr int kT = G::kThreads;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
     __syncthreads();
@@ -91,27 +94,31 @@ __device__ __forceinline__ int64_t block_sum(Line<G>& L, int64_t v) {
     __syncthreads();
     int64_t sum = 0;
 #pragma unroll
-    for (int w = 0; w < kT / 32; ++w) sum += L.warp_sum[w];
+    for (int w = 0; w < G::kThreads / 32; ++w) sum += L.warp_sum[w];
     return sum;
 }
 
-// The blocks in front of each sequence of the chunk that begins at `first`.
+// The blocks in front of each sequence of the chunk that begins at `first`: kPer neighbours a thread.
 template <typename G>
 __device__ __forceinline__ void scan_chunk(const AttnParams& p, Line<G>& L, int first, int64_t base, bool tell) {
-    constexpr int kT = G::kThreads;
     const int tid = threadIdx.x, lane = tid & 31;
-    const int i = first + tid;
-    int64_t v = 0;
-    if (i < p.batch) {
-        Span s;
-        const int flag = span_of<G>(p, i, s);
-        if (flag && tell) raise(p.status, flag);
-        if (s.blocks > 0) {
-            v = static_cast<int64_t>(s.blocks) * s.tiles * p.heads;
-            L.keep(tid, s);
+    int64_t v[G::kPer], sum = 0;
+#pragma unroll
+    for (int k = 0; k < G::kPer; ++k) {
+        const int i = first + tid * G::kPer + k;
+        v[k] = 0;
+        if (i < p.batch) {
+            Span s;
+            const int flag = span_of<G>(p, i, s);
+            if (flag && tell) raise(p.status, flag);
+            if (s.blocks > 0) {
+                v[k] = static_cast<int64_t>(s.len) * s.tiles * p.heads;
+                L.keep(tid * G::kPer + k, s);
+            }
         }
+        sum += v[k];
     }
-    int64_t sum = v;
+    const int64_t mine = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t u = __shfl_up_sync(kFull, sum, o);
@@ -120,32 +127,38 @@ __device__ __forceinline__ void scan_chunk(const AttnParams& p, Line<G>& L, int 
     __syncthreads();
     if (lane == 31) L.warp_sum[tid / 32] = sum;
     __syncthreads();
-    int64_t in = 0;
+    int64_t in = sum - mine;
 #pragma unroll
-    for (int w = 0; w < kT / 32; ++w)
+    for (int w = 0; w < G::kThreads / 32; ++w)
         if (w < tid / 32) in += L.warp_sum[w];
     if (tid == 0) {
         L.before[0] = 0;
         L.chunk = first;
         L.base = base;
     }
-    L.before[tid + 1] = in + sum;
+#pragma unroll
+    for (int k = 0; k < G::kPer; ++k) {
+        in += v[k];
+        L.before[tid * G::kPer + k + 1] = in;
+    }
     __syncthreads();
 }
 
 // The whole line's length; the first chunk is scanned on the way.
 template <typename G>
 __device__ __forceinline__ void begin_line(const AttnParams& p, Line<G>& L) {
-    constexpr int kT = G::kThreads;
+    constexpr int kT = Line<G>::kT;
     scan_chunk<G>(p, L, 0, 0, blockIdx.x == 0);
-    int64_t rest = 0;
-    for (int i = kT + threadIdx.x; i < p.batch; i += kT) {
-        Span s;
-        const int flag = span_of<G>(p, i, s);
-        if (flag && blockIdx.x == 0) raise(p.status, flag);
-        if (s.blocks > 0) rest += static_cast<int64_t>(s.blocks) * s.tiles * p.heads;
+    int64_t more = 0;
+    if (p.batch > kT) {
+        for (int i = kT + threadIdx.x; i < p.batch; i += G::kThreads) {
+            Span s;
+            const int flag = span_of<G>(p, i, s);
+            if (flag && blockIdx.x == 0) raise(p.status, flag);
+            if (s.blocks > 0) more += static_cast<int64_t>(s.len) * s.tiles * p.heads;
+        }
+        more = block_sum<G>(L, more);
     }
-    const int64_t more = p.batch > kT ? block_sum<G>(L, rest) : 0;
     if (threadIdx.x == 0) L.total = L.before[kT] + more;
     __syncthreads();
 }
@@ -153,14 +166,14 @@ __device__ __forceinline__ void begin_line(const AttnParams& p, Line<G>& L) {
 // The sequence whose blocks contain block w of the line (0 <= w < total), chunks moving on.
 template <typename G>
 __device__ __forceinline__ int sequence_at(const AttnParams& p, Line<G>& L, int64_t w) {
-    constexpr int kT = G::kThreads;
+    constexpr int kT = Line<G>::kT;
     while (w >= L.base + L.before[kT] && L.chunk + kT < p.batch) {
         const int64_t base = L.base + L.before[kT];
         const int first = L.chunk + kT;
         __syncthreads();
         scan_chunk<G>(p, L, first, base, false);
     }
-    int lo = 0, hi = kT - 1;            // the last one that begins at or before w: it has blocks
+    int lo = 0, hi = min(kT, p.batch - L.chunk) - 1;    // the last one that begins at or before w: it has blocks
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (L.base + L.before[mid] <= w) lo = mid; else hi = mid - 1;
@@ -171,7 +184,7 @@ __device__ __forceinline__ int sequence_at(const AttnParams& p, Line<G>& L, int6
 // The same by one warp.
 template <typename G>
 __device__ __forceinline__ int sequence_at_warp(const AttnParams& p, Line<G>& L, int64_t w) {
-    constexpr int kT = G::kThreads;
+    constexpr int kT = Line<G>::kT;
     const int lane = threadIdx.x & 31;
     while (w >= L.base + L.before[kT] && L.chunk + kT < p.batch) {
         const int64_t base = L.base + L.before[kT];
@@ -185,7 +198,7 @@ __device__ __forceinline__ int sequence_at_warp(const AttnParams& p, Line<G>& L,
             if (i < p.batch) {
                 span_of<G>(p, i, s);
                 if (s.blocks > 0) {
-                    sum = static_cast<int64_t>(s.blocks) * s.tiles * p.heads;
+                    sum = static_cast<int64_t>(s.len) * s.tiles * p.heads;
                     L.keep(32 * k + lane, s);
                 }
             }
@@ -204,7 +217,7 @@ __device__ __forceinline__ int sequence_at_warp(const AttnParams& p, Line<G>& L,
         }
         __syncwarp();
     }
-    int lo = 0, hi = kT - 1;
+    int lo = 0, hi = min(kT, p.batch - L.chunk) - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
         if (L.base + L.before[mid] <= w) lo = mid; else hi = mid - 1;
@@ -221,7 +234,9 @@ __device__ __forceinline__ int ctas_of(int64_t total, int grid, int least) {
 // What a CTA works on next: the unit at block w of the line, up to block w1.
 struct Piece {
     int seq, head, tile, rows, past, n, row0;
-    int b0, b1, blocks;                 // of the unit's blocks
+    int places;                         // of the line
+    int b0, b1, blocks;                 // of the unit's blocks (none where b0 = b1)
+    int64_t u0;                         // the line's place of the unit's first block
     int key0, key1;
 };
 template <typename G>
@@ -230,11 +245,14 @@ __device__ __forceinline__ Piece piece_at(const AttnParams& p, const Line<G>& L,
     Span s;
     make_span<G>(p, L.past[k], L.n[k], L.row0[k], s);
     const int64_t in_seq = w - L.base - L.before[k];
-    const int unit = static_cast<int>(quotient(in_seq, s.blocks));          // (head, tile of rows)
+    const int unit = static_cast<int>(quotient(in_seq, s.len));             // (head, tile of rows)
+    const int at = static_cast<int>(in_seq - static_cast<int64_t>(unit) * s.len);
     d.seq = L.chunk + k;
-    d.b0 = static_cast<int>(in_seq - static_cast<int64_t>(unit) * s.blocks);
-    d.b1 = static_cast<int>(w1 - w < s.blocks - d.b0 ? d.b0 + (w1 - w) : s.blocks);
+    d.places = static_cast<int>(w1 - w < s.len - at ? w1 - w : s.len - at);
+    d.b0 = max(at - G::kCost, 0);
+    d.b1 = max(at + d.places - G::kCost, 0);
     d.blocks = s.blocks;
+    d.u0 = w - at + G::kCost;
     d.head = unit / s.tiles;
     d.tile = unit - d.head * s.tiles;
     d.rows = min(G::kRows, s.n * p.ratio - d.tile * G::kRows);
@@ -246,16 +264,10 @@ __device__ __forceinline__ Piece piece_at(const AttnParams& p, const Line<G>& L,
     return d;
 }
 // the record of a part that is not a whole unit (block b of the line is CTA ((b + 1) ctas - 1) / total's)
-__device__ __forceinline__ void put_record(int32_t* meta, const Piece& d, int64_t w, int64_t total, int ctas) {
-    const int64_t u0 = w - d.b0, u1 = u0 + d.blocks;
-    int32_t* rec = meta + 8 * (d.b0 > 0 ? 0 : 1);
-    rec[0] = d.seq;
-    rec[1] = d.head;
-    rec[2] = d.tile;
-    rec[3] = static_cast<int>(quotient((u0 + 1) * ctas - 1, total));
-    rec[4] = static_cast<int>(quotient(u1 * ctas - 1, total));
-    rec[5] = d.rows;
-    rec[6] = d.row0;
+__device__ __forceinline__ void put_record(int32_t* meta, const Piece& d, int64_t total, int ctas) {
+    int4* rec = reinterpret_cast<int4*>(meta) + 2 * (d.b0 > 0 ? 0 : 1);
+    rec[0] = make_int4(d.seq, d.head, d.tile, static_cast<int>(quotient((d.u0 + 1) * ctas - 1, total)));
+    rec[1] = make_int4(static_cast<int>(quotient((d.u0 + d.blocks) * ctas - 1, total)), d.rows, d.row0, 0);
 }
 
 // ---- instructions ---------------------------------------------------------------------------
@@ -289,16 +301,16 @@ __device__ __forceinline__ uint32_t pack_b(float a, float b) {
 
 __device__ __forceinline__ int64_t token_row(const AttnParams& p, int i) { return p.sti ? ld(p.sti + i) : i; }
 
-// O of one row and column quad, weighed: to the output
-__device__ __forceinline__ void put_out(const AttnParams& p, int64_t row, int head, int D, int col, const float (&o)[4]) {
+// four columns of a row, weighed: to the output, through the gate z
+__device__ __forceinline__ void put_out(const AttnParams& p, int64_t at, int64_t z_at, const float (&o)[4]) {
     float x[4] = {o[0], o[1], o[2], o[3]};
     if (p.z) {
-        const uint2 raw = ld(reinterpret_cast<const uint2*>(p.z + row * p.z_stride + static_cast<int64_t>(head) * D + col));
+        const uint2 raw = ld(reinterpret_cast<const uint2*>(p.z + z_at));
         const float z[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u), __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u)};
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] = __fdividef(x[e], 1.0f + __expf(-z[e]));
     }
-    *reinterpret_cast<uint2*>(p.out + row * p.out_stride + static_cast<int64_t>(head) * D + col) = make_uint2(pack_b(x[0], x[1]), pack_b(x[2], x[3]));
+    *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_b(x[0], x[1]), pack_b(x[2], x[3]));
 }
 
 // ---- the second launch: parts of a unit joined ------------------------------------------------------
@@ -315,18 +327,20 @@ __global__ void __launch_bounds__(kJThreads) gdn_attn_join_kernel(const AttnPara
     dep_wait();
     dep_launch();
     const int cta = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int32_t* const meta = p.meta + static_cast<int64_t>(cta) * kMetaInts;
+    const int4* const meta = reinterpret_cast<const int4*>(p.meta + static_cast<int64_t>(cta) * kMetaInts);
+    const int4 rec[2][2] = {{ld(meta), ld(meta + 1)}, {ld(meta + 2), ld(meta + 3)}};
     const float* const all_ml = p.ws + static_cast<int64_t>(2 * grid) * kTileRows * D;
+#pragma unroll 1
     for (int which = 0; which < 2; ++which) {
-        const int32_t* const rec = meta + 8 * which;
-        const int seq = ld(rec);
-        if (seq < 0) continue;
-        const int head = ld(rec + 1), tile = ld(rec + 2), c0 = ld(rec + 3), c1 = ld(rec + 4), rows = ld(rec + 5), row0 = ld(rec + 6);
+        const int4 r0 = which ? rec[1][0] : rec[0][0], r1 = which ? rec[1][1] : rec[0][1];
+        if (r0.x < 0) continue;
+        const int head = r0.y, tile = r0.z, c0 = r0.w, c1 = r1.x, rows = r1.y, row0 = r1.z;
         const int parts = c1 - c0 + 1, mine = cta - c0;
         const int count = rows > mine ? (rows - mine + parts - 1) / parts : 0;      // rows of this CTA
         int per = 1;                                                                // warps of a row
         while (2 * per * count <= kJWarps && per < kJWarps) per *= 2;
         const int at_once = kJWarps / per;
+#pragma unroll 1
         for (int base = 0; base < count; base += at_once) {
             const int j = base + warp / per, sub = warp % per;
             const int r = mine + j * parts;
@@ -334,26 +348,41 @@ __global__ void __launch_bounds__(kJThreads) gdn_attn_join_kernel(const AttnPara
             float top = -INFINITY, x[kV], l = 0.f;
 #pragma unroll
             for (int e = 0; e < kV; ++e) x[e] = 0.f;
+            // the first part was left by c0 as its last, the others as their first
+            auto part_of = [&](int k) { return static_cast<int64_t>(2 * (c0 + k) + (k == 0 ? 1 : 0)); };
             if (j < count) {
-                // the first part was left by c0 as its last, the others as their first
-                for (int k = lane; k < parts; k += 32)
-                    top = fmaxf(top, ld(all_ml + static_cast<int64_t>(2 * (c0 + k) + (k == 0 ? 1 : 0)) * 2 * kTileRows + r));
+                // every lane has the references and sums of some parts, and the first 32 of this warp in place
+                float pm = -INFINITY, pl = 0.f;
+                const int own = sub + lane * per;
+                if (own < parts) {
+                    pm = ld(all_ml + part_of(own) * 2 * kTileRows + r);
+                    pl = ld(all_ml + part_of(own) * 2 * kTileRows + kTileRows + r);
+                }
+                for (int k = lane; k < parts; k += 32) top = fmaxf(top, ld(all_ml + part_of(k) * 2 * kTileRows + r));
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-#pragma unroll 4
-                for (int k = sub; k < parts; k += per) {
-                    const int64_t part = 2 * (c0 + k) + (k == 0 ? 1 : 0);
-                    const float pm = ld(all_ml + part * 2 * kTileRows + r), pl = ld(all_ml + part * 2 * kTileRows + kTileRows + r);
-                    const float* src = p.ws + (part * kTileRows + r) * D;
+                for (int k0 = 0; sub + k0 * per < parts; k0 += 32) {
+                    if (k0 > 0) {
+                        const int k = sub + (k0 + lane) * per;
+                        pm = k < parts ? ld(all_ml + part_of(k) * 2 * kTileRows + r) : -INFINITY;
+                        pl = k < parts ? ld(all_ml + part_of(k) * 2 * kTileRows + kTileRows + r) : 0.f;
+                    }
                     const float a = pm == -INFINITY ? 0.f : ex2(pm - top);
                     l += a * pl;
+#pragma unroll 4
+                    for (int q = 0; q < 32 && sub + (k0 + q) * per < parts; ++q) {
+                        const float* src = p.ws + (part_of(sub + (k0 + q) * per) * kTileRows + r) * D;
+                        const float aq = __shfl_sync(kFull, a, q);
 #pragma unroll
-                    for (int e = 0; e < kV; e += 2) {
-                        const float2 y = ld(reinterpret_cast<const float2*>(src + 32 * e + 2 * lane));
-                        x[e] += a == 0.f ? 0.f : a * y.x;
-                        x[e + 1] += a == 0.f ? 0.f : a * y.y;
+                        for (int e = 0; e < kV; e += 2) {
+                            const float2 y = ld(reinterpret_cast<const float2*>(src + 32 * e + 2 * lane));
+                            x[e] += aq == 0.f ? 0.f : aq * y.x;
+                            x[e + 1] += aq == 0.f ? 0.f : aq * y.y;
+                        }
                     }
                 }
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kFull, l, o);
             }
 #pragma unroll
             for (int e = 0; e < kV; e += 2) *reinterpret_cast<float2*>(&sum[warp][32 * e + 2 * lane]) = make_float2(x[e], x[e + 1]);
@@ -365,6 +394,8 @@ __global__ void __launch_bounds__(kJThreads) gdn_attn_join_kernel(const AttnPara
                 const int jj = base + q;
                 if (jj >= count) continue;
                 const int rj = mine + jj * parts;
+                const int rr = tile * kTileRows + rj, t = rr / p.ratio;
+                const int64_t row = token_row(p, row0 + t), h = static_cast<int64_t>(head * p.ratio + rr - t * p.ratio) * D + col;
                 float y[4] = {0.f, 0.f, 0.f, 0.f}, den = 0.f;
                 for (int s2 = 0; s2 < per; ++s2) {
                     const float4 v = *reinterpret_cast<const float4*>(&sum[q * per + s2][col]);
@@ -377,11 +408,11 @@ __global__ void __launch_bounds__(kJThreads) gdn_attn_join_kernel(const AttnPara
                 const float inv = den == 0.f ? 0.f : 1.0f / den;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[e] *= inv;
-                const int rr = tile * kTileRows + rj, t = rr / p.ratio;
-                put_out(p, token_row(p, row0 + t), head * p.ratio + rr - t * p.ratio, D, col, y);
+                put_out(p, row * p.out_stride + h, row * p.z_stride + h, y);
             }
             __syncthreads();
         }
     }
 }
+
 }  // namespace gdn_attn

@@ -1,5 +1,5 @@
 // Internal to libgdnspec: the attention of a step's tokens over the paged key-value cache on the
-// tcgen05 tensor cores, for bf16, fp16 and e4m3 caches (gdnattn_tc_*.cu instantiate it; gdnattn.cu
+// tcgen05 tensor cores, for bf16, fp16 and e4m3 caches (gdnattn_bf16.cu and its like instantiate it; gdnattn.cu
 // has the mathematics, the line that the work is cut from, the kernel for what does not run here, and
 // the choice between the two).
 //
@@ -33,13 +33,13 @@
 #include "gdn_tcgen05.h"
 #include "gdnattn.cuh"
 
+namespace gdn_attn_tc {
+
 using namespace gdn_attn;
 using gdn_tc::desc_sw128;
 using gdn_tc::fence_after;
 using gdn_tc::fence_async_smem;
 using gdn_tc::fence_before;
-
-namespace {
 
 enum Kind { kBf16, kF16, kE4m3 };
 
@@ -51,6 +51,7 @@ constexpr int kKeyRing = 8;             // tiles whose keys' scales and presence
 
 struct Cut {                            // (gdnattn.cuh)
     static constexpr int kThreads = kThreadsT;
+    static constexpr int kPer = 1, kCost = 1;
     static constexpr int kBlock = kTile;
     static constexpr int kRows = kRowsT;
 };
@@ -329,7 +330,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) gdn_attn_tc_kernel(const AttnPar
     fence_after();
     const uint32_t tm = ms.tmem;
     const int64_t total = ms.line.total;
-    const int ctas = ctas_of(total, gridDim.x, 1);
+    const int ctas = ctas_of(total, gridDim.x, 1 + Cut::kCost);
     const int cta = blockIdx.x;
     volatile int* const abort = &ms.abort;
     int it = 0, edges = 0;                          // items of the ring that this role is past; edge tiles that were loaded
@@ -351,9 +352,11 @@ __global__ void __launch_bounds__(kThreadsT, 1) gdn_attn_tc_kernel(const AttnPar
             }
             Desc d = {};
             Piece pc = {};
-            if (w < w1) {
+            while (w < w1) {                        // (places that have nothing to do are passed by)
                 const int k = sequence_at_warp<Cut>(p, ms.line, w);
                 pc = piece_at<Cut>(p, ms.line, k, w, w1);
+                w += pc.places;
+                if (pc.b0 == pc.b1) continue;
                 d.seq = pc.seq;
                 d.head = pc.head;
                 d.tile = pc.tile;
@@ -365,14 +368,14 @@ __global__ void __launch_bounds__(kThreadsT, 1) gdn_attn_tc_kernel(const AttnPar
                 d.key1 = pc.key1;
                 d.tiles = pc.b1 - pc.b0;
                 d.part = pc.b0 == 0 && pc.b1 == pc.blocks ? -1 : pc.b0 > 0 ? 2 * cta : 2 * cta + 1;
+                break;
             }
             if (lane == 0) {
                 ms.desc[u % kUnits] = d;
                 bar_arrive(&ms.u_full[u % kUnits]);
-                if (d.tiles > 0 && d.part >= 0) put_record(meta, pc, w, total, ctas);
+                if (d.tiles > 0 && d.part >= 0) put_record(meta, pc, total, ctas);
             }
             __syncwarp();
-            w += d.tiles;
             if (d.tiles == 0) break;
         }
     } else if (warp == kLoadWarp) {
@@ -1061,7 +1064,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) gdn_attn_tc_kernel(const AttnPar
 }
 
 // A cache as [pages][heads][positions of a page][D], read in boxes of 128 bytes by `box` positions.
-bool encode_map(CUtensorMap& map, const void* base, const AttnParams& p, int D, int kind, int box) {
+inline bool encode_map(CUtensorMap& map, const void* base, const AttnParams& p, int D, int kind, int box) {
     using Encode = PFN_cuTensorMapEncodeTiled_v12000;
     static const Encode encode = [] {
         void* fn = nullptr;
@@ -1146,4 +1149,9 @@ cudaError_t launch_kind(AttnParams p, int D, void* workspace, cudaStream_t s) {
                       : launch<kKind, 256>(p, joins, grid, s);
 }
 
-}  // namespace
+inline int64_t workspace_of(int D) {
+    const int64_t grid = grid_of();
+    return grid * kMetaInts * 4 + 2 * grid * kRowsT * (D + 2) * 4;
+}
+
+}  // namespace gdn_attn_tc

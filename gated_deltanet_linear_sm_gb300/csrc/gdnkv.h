@@ -73,13 +73,23 @@ struct AttnParams {
 constexpr int kMaxCtas = 1024;      // of an attention launch
 constexpr int kMetaInts = 16;       // of a CTA: two records of 8
 
-// Workspace in bytes on the current device (gdnattn.cu).
+// Workspace in bytes on the current device, and the launch (gdnattn.cu).
 int64_t attn_workspace(const AttnParams& p, int D, gdn_dtype type);
-cudaError_t launch_attn(AttnParams p, int D, gdn_dtype type, void* workspace, cudaStream_t stream);
-// The same on the tcgen05 tensor cores, by the cache's type (gdnattn_tc.cuh).
+cudaError_t launch_attn(const AttnParams& p, int D, gdn_dtype type, void* workspace, cudaStream_t stream);
+
+// The two kernels, by the cache's type (gdnattn_bf16.cu and its like): for few query rows, and on the
+// tcgen05 tensor cores.
 int64_t attn_tc_workspace(int D);
+int64_t attn_workspace_bf16(int rows, int D);
+cudaError_t launch_attn_bf16(const AttnParams& p, int rows, int D, void* workspace, cudaStream_t stream);
 cudaError_t launch_attn_tc_bf16(const AttnParams& p, int D, void* workspace, cudaStream_t stream);
+int64_t attn_workspace_f16(int rows, int D);
+cudaError_t launch_attn_f16(const AttnParams& p, int rows, int D, void* workspace, cudaStream_t stream);
 cudaError_t launch_attn_tc_f16(const AttnParams& p, int D, void* workspace, cudaStream_t stream);
+int64_t attn_workspace_e4m3(int rows, int D);
+cudaError_t launch_attn_e4m3(const AttnParams& p, int rows, int D, void* workspace, cudaStream_t stream);
 cudaError_t launch_attn_tc_e4m3(const AttnParams& p, int D, void* workspace, cudaStream_t stream);
+int64_t attn_workspace_i8(int rows, int D);
+cudaError_t launch_attn_i8(const AttnParams& p, int rows, int D, void* workspace, cudaStream_t stream);
 
 }  // namespace gdn_kv
