@@ -112,7 +112,7 @@ __device__ __forceinline__ void scan_chunk(const AttnParams& p, Line<G>& L, int 
             const int flag = span_of<G>(p, i, s);
             if (flag && tell) raise(p.status, flag);
             if (s.blocks > 0) {
-                v[k] = static_cast<int64_t>(s.len) * s.tiles * p.heads;
+                v[k] = static_cast<int64_t>(s.len) * s.tiles * p.groups;
                 L.keep(tid * G::kPer + k, s);
             }
         }
@@ -155,7 +155,7 @@ __device__ __forceinline__ void begin_line(const AttnParams& p, Line<G>& L) {
             Span s;
             const int flag = span_of<G>(p, i, s);
             if (flag && blockIdx.x == 0) raise(p.status, flag);
-            if (s.blocks > 0) more += static_cast<int64_t>(s.len) * s.tiles * p.heads;
+            if (s.blocks > 0) more += static_cast<int64_t>(s.len) * s.tiles * p.groups;
         }
         more = block_sum<G>(L, more);
     }
@@ -198,7 +198,7 @@ __device__ __forceinline__ int sequence_at_warp(const AttnParams& p, Line<G>& L,
             if (i < p.batch) {
                 span_of<G>(p, i, s);
                 if (s.blocks > 0) {
-                    sum = static_cast<int64_t>(s.len) * s.tiles * p.heads;
+                    sum = static_cast<int64_t>(s.len) * s.tiles * p.groups;
                     L.keep(32 * k + lane, s);
                 }
             }
@@ -225,7 +225,7 @@ __device__ __forceinline__ int sequence_at_warp(const AttnParams& p, Line<G>& L,
     return lo;
 }
 
-// CTAs that share the line: no more than leave each `least` blocks
+// CTAs (of one member of the groups of heads) that share the line: no more than leave each `least` blocks
 __device__ __forceinline__ int ctas_of(int64_t total, int grid, int least) {
     const int64_t most = (total + least - 1) / least;
     return static_cast<int>(most < grid ? (most > 0 ? most : 1) : grid);
@@ -240,12 +240,12 @@ struct Piece {
     int key0, key1;
 };
 template <typename G>
-__device__ __forceinline__ Piece piece_at(const AttnParams& p, const Line<G>& L, int k, int64_t w, int64_t w1) {
+__device__ __forceinline__ Piece piece_at(const AttnParams& p, const Line<G>& L, int k, int64_t w, int64_t w1, int member) {
     Piece d;
     Span s;
     make_span<G>(p, L.past[k], L.n[k], L.row0[k], s);
     const int64_t in_seq = w - L.base - L.before[k];
-    const int unit = static_cast<int>(quotient(in_seq, s.len));             // (head, tile of rows)
+    const int unit = static_cast<int>(quotient(in_seq, s.len));             // (group of heads, tile of rows)
     const int at = static_cast<int>(in_seq - static_cast<int64_t>(unit) * s.len);
     d.seq = L.chunk + k;
     d.places = static_cast<int>(w1 - w < s.len - at ? w1 - w : s.len - at);
@@ -253,8 +253,9 @@ __device__ __forceinline__ Piece piece_at(const AttnParams& p, const Line<G>& L,
     d.b1 = max(at + d.places - G::kCost, 0);
     d.blocks = s.blocks;
     d.u0 = w - at + G::kCost;
-    d.head = unit / s.tiles;
-    d.tile = unit - d.head * s.tiles;
+    const int group = unit / s.tiles;
+    d.head = group * p.side + member;
+    d.tile = unit - group * s.tiles;
     d.rows = min(G::kRows, s.n * p.ratio - d.tile * G::kRows);
     d.past = s.hi - s.n;
     d.n = s.n;
@@ -315,8 +316,8 @@ __device__ __forceinline__ void put_out(const AttnParams& p, int64_t at, int64_t
 
 // ---- the second launch: parts of a unit joined ------------------------------------------------------
 //
-// Each of the CTAs that share a unit joins some of its rows: CTA c of c0 .. c1 those whose number is
-// c - c0 modulo their count.  A row's parts are summed by the warps that are left over for it.
+// Each of the CTAs that share a unit joins some of its rows: the one at place c of c0 .. c1 of the line those whose
+// number is c - c0 modulo their count.  A row's parts are summed by the warps that are left over for it.
 
 constexpr int kJThreads = 256, kJWarps = 8;
 
@@ -335,7 +336,7 @@ __global__ void __launch_bounds__(kJThreads) gdn_attn_join_kernel(const AttnPara
         const int4 r0 = which ? rec[1][0] : rec[0][0], r1 = which ? rec[1][1] : rec[0][1];
         if (r0.x < 0) continue;
         const int head = r0.y, tile = r0.z, c0 = r0.w, c1 = r1.x, rows = r1.y, row0 = r1.z;
-        const int parts = c1 - c0 + 1, mine = cta - c0;
+        const int parts = c1 - c0 + 1, mine = cta / p.side - c0, member = cta % p.side;
         const int count = rows > mine ? (rows - mine + parts - 1) / parts : 0;      // rows of this CTA
         int per = 1;                                                                // warps of a row
         while (2 * per * count <= kJWarps && per < kJWarps) per *= 2;
@@ -349,7 +350,7 @@ __global__ void __launch_bounds__(kJThreads) gdn_attn_join_kernel(const AttnPara
 #pragma unroll
             for (int e = 0; e < kV; ++e) x[e] = 0.f;
             // the first part was left by c0 as its last, the others as their first
-            auto part_of = [&](int k) { return static_cast<int64_t>(2 * (c0 + k) + (k == 0 ? 1 : 0)); };
+            auto part_of = [&](int k) { return static_cast<int64_t>(2 * ((c0 + k) * p.side + member) + (k == 0 ? 1 : 0)); };
             if (j < count) {
                 // every lane has the references and sums of some parts, and the first 32 of this warp in place
                 float pm = -INFINITY, pl = 0.f;

@@ -330,8 +330,8 @@ __global__ void __launch_bounds__(kThreadsT, 1) gdn_attn_tc_kernel(const AttnPar
     fence_after();
     const uint32_t tm = ms.tmem;
     const int64_t total = ms.line.total;
-    const int ctas = ctas_of(total, gridDim.x, 1 + Cut::kCost);
-    const int cta = blockIdx.x;
+    const int ctas = ctas_of(total, gridDim.x / p.side, 1 + Cut::kCost);
+    const int cta = blockIdx.x, place = cta / p.side, member = cta - place * p.side;
     volatile int* const abort = &ms.abort;
     int it = 0, edges = 0;                          // items of the ring that this role is past; edge tiles that were loaded
     const uint32_t ring = saddr(sm + L::kORing), pbuf = saddr(sm + L::kOP), qbuf = saddr(sm + L::kOQ);
@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) gdn_attn_tc_kernel(const AttnPar
         int32_t* const meta = p.meta + static_cast<int64_t>(cta) * kMetaInts;
         if (lane == 0) meta[0] = meta[8] = -1;
         __syncwarp();
-        const int64_t w0 = cta < ctas ? quotient(total * cta, ctas) : 0, w1 = cta < ctas ? quotient(total * (cta + 1), ctas) : 0;
+        const int64_t w0 = place < ctas ? quotient(total * place, ctas) : 0, w1 = place < ctas ? quotient(total * (place + 1), ctas) : 0;
         int64_t w = w0;
         for (int u = 0;; ++u) {
             if (!__all_sync(kFull, wait(&ms.u_free[u % kUnits], u / kUnits + 1, limit))) {
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) gdn_attn_tc_kernel(const AttnPar
             Piece pc = {};
             while (w < w1) {                        // (places that have nothing to do are passed by)
                 const int k = sequence_at_warp<Cut>(p, ms.line, w);
-                pc = piece_at<Cut>(p, ms.line, k, w, w1);
+                pc = piece_at<Cut>(p, ms.line, k, w, w1, member);
                 w += pc.places;
                 if (pc.b0 == pc.b1) continue;
                 d.seq = pc.seq;
@@ -1141,6 +1141,7 @@ cudaError_t launch_kind(AttnParams p, int D, void* workspace, cudaStream_t s) {
     const int grid = grid_of();
     p.meta = static_cast<int32_t*>(workspace);
     p.ws = reinterpret_cast<float*>(p.meta + static_cast<int64_t>(grid) * kMetaInts);
+    p.stand_side_by_side();
     // a unit of one block has nothing to join
     const bool joins = static_cast<int64_t>(p.pg.cols) * p.pg.page + kKeys > kTile;
     return D == 64    ? launch<kKind, 64>(p, joins, grid, s)

@@ -93,11 +93,12 @@ struct Shape {
     static constexpr int kBytes = kKind <= kF16 ? 2 : 1;
     static constexpr int kRow = D * kBytes;                     // bytes of a key
     static constexpr int kItem = kKeys * kRow + (kBytes == 1 ? 4 * kKeys : 0);      // K or V of 16 keys, with their scales
-    // CTAs of an SM: what the accumulators, D / 16 x 4 registers for 8 rows, and the ring leave room for
-    static constexpr int kRegs = kOct * D;
-    static constexpr int kCtas = kRegs <= 128 ? 4 : kRegs <= 256 && kRow <= 256 ? 3 : 2;
+    // CTAs of an SM: short rows (64 x 16 bits, 128 x 8) leave room for three with long rings, whose units' starts and
+    // ends overlap (256 sequences of up to 500, head dim 64: 59 us with two or four, 49 with three); with more bytes a
+    // row two long rings do better than four short ones (32 of up to 4096, head dim 128, bf16: 64 us, 69 with three, 78 with four)
+    static constexpr int kCtas = kRow <= 128 && kOct == 1 ? 3 : 2;
     static constexpr int kQ = 8 * kOct * D * 2;
-    static constexpr int kStatic = 5 * 1024;                    // (the line and what the warps exchange)
+    static constexpr int kStatic = 8 * 1024;                    // (the line and what the warps exchange)
     static constexpr int kRing0 = (227 * 1024 / kCtas - 1024 - kStatic - kQ) / (kWarps * kItem);
     static constexpr int kRing = kRing0 > 8 ? 8 : kRing0;       // items of a warp, on their way or in use
     static constexpr int kRingBytes = kWarps * kRing * kItem;
@@ -177,18 +178,18 @@ __global__ void __launch_bounds__(kThreads, Shape<kKind, D, kOct>::kCtas) gdn_at
     begin_line<G>(p, line);
     dep_launch();
     const int64_t total = line.total;
-    const int ctas = ctas_of(total, gridDim.x, 1 + G::kCost);
-    const int cta = blockIdx.x;
+    const int ctas = ctas_of(total, gridDim.x / p.side, 1 + G::kCost);
+    const int cta = blockIdx.x, place = cta / p.side, member = cta - place * p.side;
     int32_t* const meta = p.meta + static_cast<int64_t>(cta) * kMetaInts;
     if (tid == 0) meta[0] = meta[8] = -1;           // (no part yet)
-    if (cta >= ctas) return;
-    const int64_t w0 = quotient(total * cta, ctas), w1 = quotient(total * (cta + 1), ctas);
+    if (place >= ctas) return;
+    const int64_t w0 = quotient(total * place, ctas), w1 = quotient(total * (place + 1), ctas);
     const uint32_t my_ring = saddr(ring0) + warp * S::kRing * S::kItem;
     const bool aligned_pages = p.pg.page % kKeys == 0;          // 16 keys lie in one page
 
     for (int64_t w = w0; w < w1;) {
         const int k = sequence_at<G>(p, line, w);
-        const Piece d = piece_at<G>(p, line, k, w, w1);
+        const Piece d = piece_at<G>(p, line, k, w, w1, member);
         w += d.places;
         if (d.b0 == d.b1) continue;
         const bool whole = d.b0 == 0 && d.b1 == d.blocks;
@@ -263,9 +264,10 @@ __global__ void __launch_bounds__(kThreads, Shape<kKind, D, kOct>::kCtas) gdn_at
 
         // ---- q: [rows][D] in shared memory, fp16 with a power of two per row, or bf16 as it is; the rows' places ----
         {
-            constexpr int kPer = kThreads / kRowsU;                 // threads of a row
+            constexpr int kPer = kThreads / (kRowsU > 16 ? 32 : kRowsU);        // threads of a row
             constexpr int kN = (D / 8 + kPer - 1) / kPer;           // 16-byte pieces of each
             const int r = tid / kPer, j = tid % kPer;
+            const bool in = r < kRowsU;
             const int rr = d.tile * kRowsU + r, t = min(rr / p.ratio, d.n - 1);
             const bool has = r < d.rows;
             const int64_t row = token_row(p, d.row0 + t);
@@ -298,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kKind, D, kOct>::kCtas) gdn_at
                     up = __uint_as_float(static_cast<uint32_t>(e) << 23);
                 }
             }
-            if (j == 0) {
+            if (j == 0 && in) {
                 q_scale[r] = p.scale * up;
                 row_last[r] = d.past + t;
                 row_first[r] = p.window > 0 ? max(0, d.past + t - p.window + 1) : 0;
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kKind, D, kOct>::kCtas) gdn_at
 #pragma unroll
             for (int u = 0; u < kN; ++u) {
                 const int c = j + u * kPer;
-                if (c < D / 8) {
+                if (c < D / 8 && in) {
                     uint4 y = raw[u];
                     if constexpr (!kB) {
                         uint32_t* w2 = reinterpret_cast<uint32_t*>(&y);
@@ -679,17 +681,19 @@ cudaError_t launch(const AttnParams& p, bool joins, int grid, cudaStream_t strea
 // the launch for one type of cache (a translation unit each), and its CTAs: what is resident at once
 template <int kKind, int kOct>
 cudaError_t by_dim(const AttnParams& p, int D, bool joins, int grid, cudaStream_t s) {
-    return D == 64    ? launch<kKind, 64, kOct>(p, joins, grid, s)
-           : D == 128 ? launch<kKind, 128, kOct>(p, joins, grid, s)
-           : D == 192 ? launch<kKind, 192, kOct>(p, joins, grid, s)
-                      : launch<kKind, 256, kOct>(p, joins, grid, s);
+    if constexpr (kOct <= 2) {
+        if (D == 192) return launch<kKind, 192, kOct>(p, joins, grid, s);
+        if (D == 256) return launch<kKind, 256, kOct>(p, joins, grid, s);
+    }
+    return D == 64 ? launch<kKind, 64, kOct>(p, joins, grid, s) : launch<kKind, 128, kOct>(p, joins, grid, s);
 }
 template <int kKind, int kOct>
 int ctas_of_sm(int D) {
-    return D == 64    ? Shape<kKind, 64, kOct>::kCtas
-           : D == 128 ? Shape<kKind, 128, kOct>::kCtas
-           : D == 192 ? Shape<kKind, 192, kOct>::kCtas
-                      : Shape<kKind, 256, kOct>::kCtas;
+    if constexpr (kOct <= 2) {
+        if (D == 192) return Shape<kKind, 192, kOct>::kCtas;
+        if (D == 256) return Shape<kKind, 256, kOct>::kCtas;
+    }
+    return D == 64 ? Shape<kKind, 64, kOct>::kCtas : Shape<kKind, 128, kOct>::kCtas;
 }
 template <int kKind, int kOct>
 int grid_of(int D) {
@@ -706,17 +710,33 @@ cudaError_t launch_oct(AttnParams p, int D, void* workspace, cudaStream_t s) {
     const int grid = grid_of<kKind, kOct>(D);
     p.meta = static_cast<int32_t*>(workspace);
     p.ws = reinterpret_cast<float*>(p.meta + static_cast<int64_t>(grid) * kMetaInts);
+    p.stand_side_by_side();
     // a unit of one block has nothing to join
     const bool joins = static_cast<int64_t>(p.pg.cols) * p.pg.page + kKeys > kCutKeys;
     return by_dim<kKind, kOct>(p, D, joins, grid, s);
 }
+// (int8 caches have no other kernel: their units have up to 32 rows where the accumulators fit)
+template <int kKind>
+constexpr int octets(int rows, int D) {
+    return rows <= 8 ? 1 : rows <= 16 || kKind != kI8 || D > 128 ? 2 : rows <= 24 ? 3 : 4;
+}
 template <int kKind>
 int64_t workspace_kind(int rows, int D) {
-    return rows <= 8 ? workspace_of<kKind, 1>(D) : workspace_of<kKind, 2>(D);
+    const int n = octets<kKind>(rows, D);
+    if constexpr (kKind == kI8) {
+        if (n == 3) return workspace_of<kKind, 3>(D);
+        if (n == 4) return workspace_of<kKind, 4>(D);
+    }
+    return n == 1 ? workspace_of<kKind, 1>(D) : workspace_of<kKind, 2>(D);
 }
 template <int kKind>
 cudaError_t launch_kind(const AttnParams& p, int rows, int D, void* workspace, cudaStream_t s) {
-    return rows <= 8 ? launch_oct<kKind, 1>(p, D, workspace, s) : launch_oct<kKind, 2>(p, D, workspace, s);
+    const int n = octets<kKind>(rows, D);
+    if constexpr (kKind == kI8) {
+        if (n == 3) return launch_oct<kKind, 3>(p, D, workspace, s);
+        if (n == 4) return launch_oct<kKind, 4>(p, D, workspace, s);
+    }
+    return n == 1 ? launch_oct<kKind, 1>(p, D, workspace, s) : launch_oct<kKind, 2>(p, D, workspace, s);
 }
 
 }  // namespace gdn_attn_warp

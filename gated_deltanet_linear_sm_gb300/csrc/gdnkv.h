@@ -68,6 +68,16 @@ struct AttnParams {
     int64_t q_stride, z_stride, out_stride;
     float scale;                    // of the scores, times log2(e)
     int32_t batch, num_tokens, heads, ratio, max_T, window;
+    // heads whose CTAs stand side by side, on the same keys at the same time (their rows are neighbours in a
+    // cache that keeps heads within positions), and groups of so many heads
+    int32_t side, groups;
+
+    void stand_side_by_side() {
+        side = 1;
+        for (int s = 2; s <= 8; ++s)
+            if (heads % s == 0) side = s;
+        groups = heads / side;
+    }
 };
 
 constexpr int kMaxCtas = 1024;      // of an attention launch
