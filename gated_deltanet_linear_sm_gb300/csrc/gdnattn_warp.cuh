@@ -200,12 +200,13 @@ __global__ void __launch_bounds__(kThreads, Shape<kKind, D, kOct>::kCtas) gdn_at
         const char* const kc = static_cast<const char*>(p.k) + d.head * p.pg.head_stride * S::kBytes;
         const char* const vc = static_cast<const char*>(p.v) + d.head * p.pg.head_stride * S::kBytes;
         const int32_t* const table = p.pg.table + static_cast<int64_t>(d.seq) * p.pg.table_stride;
-        const int my_key = aligned_pages ? 0 : lane & 15;
-        int next_page = -1;                         // of the next block (each lane's key of it)
-        auto look_up = [&](int block) {
-            const int x = d.key0 + (warp + block * kWarps) * kKeys + my_key;
-            next_page = x < d.key1 ? ld(table + p.pg.page_of(x)) : -1;
-        };
+        // Pages: where 16 keys lie in one, lane l knows that of this warp's block l of the present 32 (and of the next
+        // 32), so that a lookup's latency shows once a unit; else each lane that of its key of the next block.
+        const int my_key = lane & 15;
+        auto page_at = [&](int x) { return x < d.key1 ? ld(table + p.pg.page_of(x)) : -1; };
+        auto block_at = [&](int block) { return d.key0 + (warp + block * kWarps) * kKeys; };
+        int pages = aligned_pages ? page_at(block_at(lane)) : page_at(block_at(0) + my_key);
+        int pages_next = aligned_pages && items > 64 ? page_at(block_at(32 + lane)) : -1;
         int64_t at = 0;                             // bytes: this lane's key, or the first of the 16
         int64_t sat = 0;
         uint32_t live = 0;
@@ -216,13 +217,17 @@ __global__ void __launch_bounds__(kThreads, Shape<kKind, D, kOct>::kCtas) gdn_at
                 const uint32_t dst = my_ring + slot * S::kItem;
                 const bool is_k = (issued & 1) == 0;
                 if (is_k) {
-                    const int block = issued >> 1;
-                    const int x0 = d.key0 + (warp + block * kWarps) * kKeys, x = x0 + my_key;
-                    const bool has = next_page >= 0 && next_page < p.pg.num_pages;
-                    if (next_page >= p.pg.num_pages) raise(p.status, GDN_FLAG_SLOT_RANGE);
+                    const int block = issued >> 1, x0 = block_at(block), x = aligned_pages ? x0 : x0 + my_key;
+                    if (aligned_pages && block > 0 && (block & 31) == 0) {
+                        pages = pages_next;
+                        pages_next = page_at(block_at(block + 32 + lane));
+                    }
+                    const int page = aligned_pages ? __shfl_sync(kFull, pages, block & 31) : pages;
+                    const bool has = page >= 0 && page < p.pg.num_pages;
+                    if (page >= p.pg.num_pages) raise(p.status, GDN_FLAG_SLOT_RANGE);
                     const int64_t in = x - p.pg.page_of(x) * p.pg.page;
-                    at = has ? (next_page * p.pg.page_stride + in * p.pg.token_stride) * S::kBytes : 0;
-                    if constexpr (kQuantised) sat = has ? next_page * p.pg.s_page + in * p.pg.s_token + d.head * p.pg.s_head : 0;
+                    at = has ? (page * p.pg.page_stride + in * p.pg.token_stride) * S::kBytes : 0;
+                    if constexpr (kQuantised) sat = has ? page * p.pg.s_page + in * p.pg.s_token + d.head * p.pg.s_head : 0;
                     if (aligned_pages) {
                         const int n = has ? min(kKeys, d.key1 - x0) : 0;
                         live = (1u << n) - 1;
@@ -230,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kKind, D, kOct>::kCtas) gdn_at
                         live = __ballot_sync(kFull, has) & 0xffffu;
                     }
                     if (lane == 0) live_keys[warp][slot] = live;
-                    look_up(block + 1);
+                    if (!aligned_pages) pages = page_at(block_at(block + 1) + my_key);
                 }
                 const char* const src = (is_k ? kc : vc);
                 constexpr int kChunks = S::kRow / 16;               // of a key
@@ -260,7 +265,6 @@ __global__ void __launch_bounds__(kThreads, Shape<kKind, D, kOct>::kCtas) gdn_at
             copies_commit();
             ++issued;
         };
-        look_up(0);
 
         // ---- q: [rows][D] in shared memory, fp16 with a power of two per row, or bf16 as it is; the rows' places ----
         {
