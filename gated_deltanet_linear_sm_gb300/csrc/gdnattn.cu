@@ -22,11 +22,10 @@ using namespace gdn_kv;
 
 namespace {
 
-// Which kernel: the tcgen05 one pays from the second tile of 16 query rows on, which this one would read the cache for
-// once more (16 sequences of up to 16384 positions, head dim 256, bf16: 32 rows 82 us here and 76 there; 2 of 65535,
-// 64 rows: 136 and 66; 32 of 8192, head dim 128, e4m3, 64 rows: 313 and 167); up to 16 rows this one is faster (32 sequences
-// of up to 4096 positions, 4 rows: 67 and 85; 256 of up to 500, one row: 71 and 125).  It wants pages of whole groups of 8
-// positions, and has no int8 products.
+// Which kernel: the tcgen05 one pays from the second tile of 16 query rows on, for which the other one would read the
+// cache once more (with tiles of 16 rows of a first form, 16 sequences of up to 16384, head dim 256, bf16, 32 rows: 82 us there and
+// 72 here; 2 of 65535, 64 rows: 136 and 65; 32 of 8192, head dim 128, e4m3, 64 rows: 313 and 148).  It wants pages of whole
+// groups of 8 positions, and has no int8 products.
 bool on_tc(const AttnParams& p, gdn_dtype type) {
     return type != GDN_I8 && p.ratio * p.max_T > 16 && p.pg.page % 8 == 0 && p.pg.num_pages < (1ll << 31);
 }

@@ -12,12 +12,18 @@
 // as long as the rows' references stand (one vote a tile); sums over keys are made once
 // per unit.
 //
-// Warps: 0-7 softmax and output (a quarter of the keys each, half of the rows), 8-11 copies,
-// 12 products, 13 the line.  All run over the same sequence of tiles, units behind one another,
-// through rings: the copies are up to a ring ahead whatever unit that is, the scores of the
-// next tile are made while the weights of this one are.  Copies are 16-byte cp.async, not
-// TMA: a page may have any size and begin anywhere in a tile, positions behind a sequence's end
-// are not read at all (their place is zero: what a page holds there may be NaN).
+// Warps: softmax and output (a quarter of the keys each, and a half or quarter of the rows), helpers
+// (what goes with a tile's keys, q, and values that are not to be taken as they lie), loads, products, the
+// line.  All run over the same sequence of tiles, units behind one another, through rings: the loads are
+// up to a ring ahead whatever unit that is, the scores of the next tile are made while the weights of this
+// one are.  TMA brings boxes of positions that lie in one page, from a tensor of pages, heads, positions
+// and elements.  What a page holds behind a unit's keys may be NaN: the helpers clear those values before
+// the products take them (a score is masked; 0 times NaN is not).
+//
+// What bounds it: with few bytes and many rows the softmax (32 sequences of 8192, head dim 128, 64 rows, e4m3:
+// 148 us, 1.9 TB/s; the time stays when the products, the exponentials, the stores or the loads are left out
+// one at a time: it is the chain of a tile's steps in 4 warps a quarter), with more bytes a row
+// the ring's four places and the call's start and end (2 of 65535, head dim 256, 64 rows, bf16: 65 us, 4.1 TB/s).
 //
 // bf16: weights as two bf16 parts (16 significant bits), two products.  fp16: one.  e4m3: the
 // codes are operands as they are; q is the sum of two e4m3 parts (its 8 bits), a weight times the
@@ -44,13 +50,24 @@ using gdn_tc::fence_before;
 enum Kind { kBf16, kF16, kE4m3 };
 
 constexpr int kTile = 128, kRowsT = 64;
-constexpr int kSoft = 8, kHelp = 4, kLoadWarp = 12, kMmaWarp = 13, kLineWarp = 14;
-constexpr int kThreadsT = 15 * 32;
 constexpr int kUnits = 4;               // units known at a time
 constexpr int kKeyRing = 8;             // tiles whose keys' scales and presence are known at a time
+constexpr int kHelp = 4;
 
+// Roles by warp: softmax and output, helpers, loads, products, the line.  16 softmax warps of at most two chunks of 8
+// rows do better than 8 of four where a weight takes most work (32 sequences of 8192, head dim 128, 64 rows, e4m3: 148 us and
+// 158), 8 with twice the registers where it takes less (16 of up to 16384, head dim 256, 32 rows, bf16: 76 and 72).
+template <int kKind>
+struct Warps {
+    static constexpr int kSoft = kKind == kE4m3 ? 16 : 8;
+    static constexpr int kLoad = kSoft + kHelp, kMma = kLoad + 1, kLine = kMma + 1;
+    static constexpr int kThreads = (kLine + 1) * 32;
+    static constexpr int kMine = kRowsT / 8 / (kSoft / 4);      // chunks of 8 rows of a softmax warp, at most
+};
+
+template <int kKind>
 struct Cut {                            // (gdnattn.cuh)
-    static constexpr int kThreads = kThreadsT;
+    static constexpr int kThreads = Warps<kKind>::kThreads;
     static constexpr int kPer = 1, kCost = 1;
     static constexpr int kBlock = kTile;
     static constexpr int kRows = kRowsT;
@@ -72,7 +89,7 @@ struct Lay {
     static constexpr int kP = kPAtoms * kTile * 128;
     static constexpr int kQTerm = (kQuantised ? (D + 127) / 128 : D / 64) * kRowsT * 128;
     static constexpr int kQ = kQTerm * (kQuantised ? 2 : 1);
-    static constexpr int kBudget = 204 * 1024;
+    static constexpr int kBudget = 198 * 1024;
     static constexpr int kQs = kQ <= 16 * 1024 ? 2 : 1;                     // buffers of q
     static constexpr int kRing0 = (kBudget - kP - kQs * kQ) / kItem;
     static constexpr int kRing = kRing0 > 9 ? 9 : kRing0;
@@ -88,7 +105,7 @@ struct Lay {
 
 struct TcParams {
     uint32_t limit;                     // of waits (gdn_set_wait_limit)
-    int parts;                          // softmax warps of a quarter of the keys that have rows, 1 or 2
+    int parts;                          // softmax warps of a quarter of the keys that have rows
     int chunks;                         // chunks of 8 rows of each
     int box, box_log2;                  // positions that one TMA copy brings: they divide a page
 };
@@ -100,8 +117,9 @@ struct Desc {                           // a unit's part of one CTA
     int poison;                         // a value that is no number was taken out of its tiles
 };
 
+template <int kKind>
 struct Misc {
-    Line<Cut> line;
+    Line<Cut<kKind>> line;
     unsigned long long full[9], empty[9], s_full[2], s_free[2], p_full, p_free, q_full[2], q_free[2], o_full[2], o_free[2];
     unsigned long long keys_full[kKeyRing], keys_free[kKeyRing], edge_full[8], fixed[8], u_full[kUnits], u_free[kUnits], qs_full[kUnits], drain;
     Desc desc[kUnits];
@@ -113,13 +131,13 @@ struct Misc {
     float col[4][kRowsT], inv[kRowsT];
     int first[kRowsT], last[kRowsT];
     int64_t out_at[kRowsT], z_at[kRowsT];
-    int warp_e[kSoft];
+    int warp_e[16];
     uint32_t tmem;
     int abort;
 };
 
 template <int kKind, int D>
-constexpr int smem_of() { return Lay<kKind, D>::kOMisc + static_cast<int>(sizeof(Misc)) + 1024; }
+constexpr int smem_of() { return Lay<kKind, D>::kOMisc + static_cast<int>(sizeof(Misc<kKind>)) + 1024; }
 
 // ---- instructions -------------------------------------------------------------------------
 
@@ -260,29 +278,34 @@ __device__ __noinline__ void add_no_numbers(const AttnParams& p, const Desc& d, 
     }
 }
 
-// Each of 32 columns joined over the 32 lanes: lane c gets column c.  Halves of the columns change places
-// between halves of the lanes, so it takes 31 exchanges instead of 160.
-template <typename Op>
-__device__ __forceinline__ float over_lanes(float (&v)[32], int lane, Op op) {
+// Each of N columns joined over the 32 lanes: lane c gets column c mod N.  Halves of the columns change places
+// between halves of the lanes, so it takes about N exchanges instead of 5 N.
+template <int N, typename Op>
+__device__ __forceinline__ float over_lanes(float (&v)[N], int lane, Op op) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
+    for (int o = N / 2; o > 0; o >>= 1)
 #pragma unroll
         for (int k = 0; k < o; ++k) {
             const float mine = lane & o ? v[k + o] : v[k], other = lane & o ? v[k] : v[k + o];
             v[k] = op(mine, __shfl_xor_sync(kFull, other, o));
         }
+#pragma unroll
+    for (int o = 16; o >= N; o >>= 1) v[0] = op(v[0], __shfl_xor_sync(kFull, v[0], o));
     return v[0];
 }
 
 template <int kKind, int D>
-__global__ void __launch_bounds__(kThreadsT, 1) gdn_attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const TcParams tc) {
+__global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(const AttnParams p, const __grid_constant__ CUtensorMap k_map, const __grid_constant__ CUtensorMap v_map, const TcParams tc) {
     const uint32_t limit = tc.limit;
     const int parts = tc.parts;
     using L = Lay<kKind, D>;
+    using G = Cut<kKind>;
+    constexpr int kSoft = Warps<kKind>::kSoft, kLoadWarp = Warps<kKind>::kLoad, kMmaWarp = Warps<kKind>::kMma, kLineWarp = Warps<kKind>::kLine;
+    constexpr int kMine = Warps<kKind>::kMine;
     constexpr bool kQ8 = L::kQuantised, kB = kKind == kBf16;
     extern __shared__ unsigned char raw_smem[];
     unsigned char* const sm = raw_smem + ((1024 - (saddr(raw_smem) & 1023)) & 1023);
-    Misc& ms = *reinterpret_cast<Misc*>(sm + L::kOMisc);
+    Misc<kKind>& ms = *reinterpret_cast<Misc<kKind>*>(sm + L::kOMisc);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
@@ -323,14 +346,14 @@ __global__ void __launch_bounds__(kThreadsT, 1) gdn_attn_tc_kernel(const AttnPar
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&ms.tmem)), "n"(512));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    begin_line<Cut>(p, ms.line);
+    begin_line<G>(p, ms.line);
     dep_launch();
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tm = ms.tmem;
     const int64_t total = ms.line.total;
-    const int ctas = ctas_of(total, gridDim.x / p.side, 1 + Cut::kCost);
+    const int ctas = ctas_of(total, gridDim.x / p.side, 1 + G::kCost);
     const int cta = blockIdx.x, place = cta / p.side, member = cta - place * p.side;
     volatile int* const abort = &ms.abort;
     int it = 0, edges = 0;                          // items of the ring that this role is past; edge tiles that were loaded
@@ -353,8 +376,8 @@ __global__ void __launch_bounds__(kThreadsT, 1) gdn_attn_tc_kernel(const AttnPar
             Desc d = {};
             Piece pc = {};
             while (w < w1) {                        // (places that have nothing to do are passed by)
-                const int k = sequence_at_warp<Cut>(p, ms.line, w);
-                pc = piece_at<Cut>(p, ms.line, k, w, w1, member);
+                const int k = sequence_at_warp<G>(p, ms.line, w);
+                pc = piece_at<G>(p, ms.line, k, w, w1, member);
                 w += pc.places;
                 if (pc.b0 == pc.b1) continue;
                 d.seq = pc.seq;
@@ -780,9 +803,9 @@ __global__ void __launch_bounds__(kThreadsT, 1) gdn_attn_tc_kernel(const AttnPar
             const int chunks = tc.chunks;
             const int all_lo = p.window > 0 ? max(0, d.past + d.n - p.window) : 0, all_hi = d.past + 1;
             const float* const qs = ms.q_scale[u % kUnits];
-            u64 l[4][4];
+            u64 l[kMine][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < kMine; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) l[i][e] = 0;
             int cur = 0;                            // which of the two ref arrays
@@ -805,7 +828,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) gdn_attn_tc_kernel(const AttnPar
                 const bool live = (lives >> lane) & 1u;
                 // scores (in units of log2 e) less the references of `ref`; those that a row does not see are -infinity
                 auto unseen = [&](int c) { return !live || x < ms.first[c] || x > ms.last[c]; };
-                uint32_t s[4][8];
+                uint32_t s[kMine][8];
                 auto score = [&](uint32_t (&y)[8], int c0, const float* ref) {      // one chunk, in place
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
@@ -836,16 +859,16 @@ __global__ void __launch_bounds__(kThreadsT, 1) gdn_attn_tc_kernel(const AttnPar
                 for (;; ++mode) {
                     const float* const ref = mode == 1 ? ms.zero : ms.ref[cur];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < kMine; ++i)
                         if (i < chunks) tm_ld8(S + 8 * (parts * i + part), s[i]);
                     tm_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
+                    for (int i = 0; i < kMine; ++i)
                         if (i < chunks) score(s[i], 8 * (parts * i + part), ref);
                     if (mode == 0) {
                         float most[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
+                        for (int i = 0; i < kMine; ++i)
                             if (i < chunks) {
 #pragma unroll
                                 for (int e = 0; e < 8; ++e) most[e & 3] = fmaxf(most[e & 3], __uint_as_float(s[i][e]));
@@ -859,9 +882,9 @@ __global__ void __launch_bounds__(kThreadsT, 1) gdn_attn_tc_kernel(const AttnPar
                         }
                     } else if (mode == 1) {
                         // each row's largest score over the tile's keys, and the largest scale of its values
-                        float v[32];
+                        float v[8 * kMine];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(s[e >> 3][e & 7]);
+                        for (int e = 0; e < 8 * kMine; ++e) v[e] = __uint_as_float(s[e >> 3][e & 7]);
                         const float mx = over_lanes(v, lane, [](float x, float y) { return fmaxf(x, y); });
                         if ((lane >> 3) < chunks) ms.col[quad][8 * (parts * (lane >> 3) + part) + (lane & 7)] = mx;
                         if constexpr (kQ8) {
@@ -890,7 +913,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) gdn_attn_tc_kernel(const AttnPar
                     } else {
                         if (j == 0) break;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
+                        for (int i = 0; i < kMine; ++i)
                             if (i < chunks) {
                                 const float4* const a = reinterpret_cast<const float4*>(ms.alpha + 8 * (parts * i + part));
                                 l[i][0] = fmul2(l[i][0], pk2(a[0].x, a[0].y));
@@ -929,9 +952,9 @@ __global__ void __launch_bounds__(kThreadsT, 1) gdn_attn_tc_kernel(const AttnPar
                 // weights
                 u64 vu = dup2(1.f);
                 if constexpr (kQ8) vu = dup2(vs * __uint_as_float(static_cast<uint32_t>(254 - unit_e) << 23));
-                uint32_t w[4][4], w2[4][4];
+                uint32_t w[kMine][4], w2[kMine][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < kMine; ++i)
                     if (i < chunks) {
                         u64 pe[4];
 #pragma unroll
@@ -960,7 +983,7 @@ __global__ void __launch_bounds__(kThreadsT, 1) gdn_attn_tc_kernel(const AttnPar
                     }
                 if (t > 0) need(&ms.p_free, t - 1);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < kMine; ++i)
                     if (i < chunks) {
                         const int c = parts * i + part;     // chunk of 8 rows
                         if constexpr (!kQ8) {
@@ -986,9 +1009,9 @@ __global__ void __launch_bounds__(kThreadsT, 1) gdn_attn_tc_kernel(const AttnPar
             if (stop) break;
             // ---- the unit's output ----
             {
-                float v[32];
+                float v[8 * kMine];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = e & 1 ? hi2(l[e >> 3][(e >> 1) & 3]) : lo2(l[e >> 3][(e >> 1) & 3]);
+                for (int e = 0; e < 8 * kMine; ++e) v[e] = e & 1 ? hi2(l[e >> 3][(e >> 1) & 3]) : lo2(l[e >> 3][(e >> 1) & 3]);
                 const float sum = over_lanes(v, lane, [](float x, float y) { return x + y; });
                 if ((lane >> 3) < chunks) ms.col[quad][8 * (parts * (lane >> 3) + part) + (lane & 7)] = sum;
             }
@@ -1103,7 +1126,7 @@ cudaError_t launch(const AttnParams& p, bool joins, int grid, cudaStream_t strea
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid), 1, 1);
-    cfg.blockDim = dim3(kThreadsT, 1, 1);
+    cfg.blockDim = dim3(Warps<kKind>::kThreads, 1, 1);
     cfg.dynamicSmemBytes = smem_of<kKind, D>();
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -1115,7 +1138,8 @@ cudaError_t launch(const AttnParams& p, bool joins, int grid, cudaStream_t strea
     TcParams tc;
     tc.limit = __atomic_load_n(&gdn_internal::g_wait_limit, __ATOMIC_RELAXED);
     const int rows = p.ratio * p.max_T < kRowsT ? p.ratio * p.max_T : kRowsT;
-    tc.parts = rows > 8 ? 2 : 1;
+    constexpr int kMost = Warps<kKind>::kSoft / 4;
+    tc.parts = (rows + 7) / 8 < kMost ? (rows + 7) / 8 : kMost;
     tc.chunks = ((rows + 7) / 8 + tc.parts - 1) / tc.parts;
     // positions of a box: a power of two that divides a page, and 16 at most where a window may begin a unit at any multiple of 16
     tc.box_log2 = 3;
