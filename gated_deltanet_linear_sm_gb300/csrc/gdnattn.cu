@@ -13,8 +13,8 @@
 // begins.  A part that is a whole unit is finished where it is; the others go to the workspace
 // and a second launch joins them in order.
 //
-// Two kernels run the units: one whose warps have keys of their own (gdnattn_warp.cuh), for up to
-// 16 query rows, and one on the tcgen05 tensor cores (gdnattn_tc.cuh) for more.
+// Two kernels run the units: one whose warps have keys of their own (gdnattn_warp.cuh), for few
+// query rows, and one on the tcgen05 tensor cores (gdnattn_tc.cuh) for more.
 #include "gdnkv.h"
 
 using namespace gdn_common;
@@ -22,12 +22,14 @@ using namespace gdn_kv;
 
 namespace {
 
-// Which kernel: the tcgen05 one pays from the second tile of 16 query rows on, for which the other one would read the
-// cache once more (with tiles of 16 rows of a first form, 16 sequences of up to 16384, head dim 256, bf16, 32 rows: 82 us there and
-// 72 here; 2 of 65535, 64 rows: 136 and 65; 32 of 8192, head dim 128, e4m3, 64 rows: 313 and 148).  It wants pages of whole
-// groups of 8 positions, and has no int8 products.
-bool on_tc(const AttnParams& p, gdn_dtype type) {
-    return type != GDN_I8 && p.ratio * p.max_T > 16 && p.pg.page % 8 == 0 && p.pg.num_pages < (1ll << 31);
+// Which kernel: the tcgen05 one pays where the other one would read the cache a second time: from more than 32 query
+// rows on, and for a head dim over 128, where that one's units end at 16 rows, from more than 16.  32 sequences of up to 4096,
+// tcgen05 and other: bf16, head dim 128, 24 rows 60 and 50 us, 32 rows 62 and 59, 48 rows 71 and 94, 64 rows 79 and 97;
+// e4m3, 24 rows 55 and 45, 48 rows 74 and 85; bf16, head dim 256, 16 rows 88 and 70, 24 rows 93 and 109.  (Head dim 64 is a
+// tie at 48 rows; at 64 rows the other one has 63 us, 60 in e4m3, where this one has 75 and 76, but it falls behind
+// as the sequences grow: fp16, 3 of 65535 84 and 81.)  It wants pages of whole groups of 8 positions, and has no int8 products.
+bool on_tc(const AttnParams& p, int D, gdn_dtype type) {
+    return type != GDN_I8 && p.ratio * p.max_T > (D > 128 ? 16 : 32) && p.pg.page % 8 == 0 && p.pg.num_pages < (1ll << 31);
 }
 
 }  // namespace
@@ -36,7 +38,7 @@ namespace gdn_kv {
 
 int64_t attn_workspace(const AttnParams& p, int D, gdn_dtype type) {
     const int rows = p.ratio * p.max_T;
-    if (on_tc(p, type)) return attn_tc_workspace(D);
+    if (on_tc(p, D, type)) return attn_tc_workspace(D);
     return type == GDN_BF16   ? attn_workspace_bf16(rows, D)
            : type == GDN_F16  ? attn_workspace_f16(rows, D)
            : type == GDN_E4M3 ? attn_workspace_e4m3(rows, D)
@@ -45,7 +47,7 @@ int64_t attn_workspace(const AttnParams& p, int D, gdn_dtype type) {
 
 cudaError_t launch_attn(const AttnParams& p, int D, gdn_dtype type, void* workspace, cudaStream_t stream) {
     const int rows = p.ratio * p.max_T;
-    if (on_tc(p, type))
+    if (on_tc(p, D, type))
         return type == GDN_BF16  ? launch_attn_tc_bf16(p, D, workspace, stream)
                : type == GDN_F16 ? launch_attn_tc_f16(p, D, workspace, stream)
                                  : launch_attn_tc_e4m3(p, D, workspace, stream);

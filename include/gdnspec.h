@@ -793,7 +793,7 @@ GDNSPEC_API int32_t gdn_spec_decode_split(const gdn_dims* dims, gdn_dtype state_
 
 /*
  * Bound on each wait of gdn_prefill_chunked for its tensor-core products, and
- * of gdn_ssm_prefill and gdn_attn_decode (above 16 query rows) for those, their copies and their own
+ * of gdn_ssm_prefill and gdn_attn_decode (many query rows) for those, their copies and their own
  * warps: 0 (the default)
  * waits with blocking polls of the barrier, 2^24 of them (2^17 of up to 20 us;
  * well over a second either way); a non-zero bound counts non-blocking polls
