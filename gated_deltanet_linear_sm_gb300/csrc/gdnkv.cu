@@ -4,8 +4,10 @@
 // (gdnattn.cu).  Declared in include/gdnspec.h.
 #include <cuda_fp8.h>
 
+#include <algorithm>
 #include <cmath>
 #include <initializer_list>
+#include <type_traits>
 
 #include "gdnkv.h"
 
@@ -16,14 +18,19 @@ namespace {
 
 // ---- rows to and from the cache ------------------------------------------------------
 //
-// Both are copies, one with a maximum over each row's D elements: bandwidth bounds them
-// for many rows, the chain offsets -> page -> row for few.  A CTA takes a tile of
-// neighbouring rows; first a thread per row finds its sequence, page and place, then
-// groups of D / 8 lanes move one head's row of k or v each, 8 elements a lane (16-byte
-// accesses on the 16-bit side), kAhead of them on their way at a time.
+// Both are copies, one with a maximum over each row's D elements: the bytes bound them for
+// many rows, the chain offsets -> page -> row for few (32 rows of 8 heads 2.4 us).  A CTA takes a
+// tile of neighbouring rows; first a thread per row finds its sequence, page and place, then
+// groups of D / 32 lanes move one head's row of k or v each, kParts pieces of 8 elements a lane,
+// all loads of a row on their way at once.  The instructions for an item's place come close to the
+// bytes' time, so a lane has four pieces of it: 16211 rows of 8 heads of 128 into an e4m3 cache and back
+// 35 us (5.7 TB/s), with two pieces 40, with one 49; 120007 rows read from it 117 us (6.3 TB/s), 118, 142.
+// Loads for the next item ahead of the stores of this one gained nothing (35, 116).
 
-constexpr int kRThreads = 256;
+constexpr int kRThreads = 256, kRCtas = 4;      // (CTAs of an SM)
+constexpr int kParts = 4;
 constexpr int kMaxTile = 64;            // rows of a CTA
+constexpr int kRounds = 8;              // items of a group, at most
 constexpr int kSamples = 256;
 
 struct RowPlace {
@@ -193,93 +200,107 @@ struct I8 {
 template <typename C>
 constexpr bool kQuantised = C::kBytes == 1;
 
+template <int D>
+struct Group {                          // of lanes that move a head's row
+    static constexpr int kLanes = D == 192 ? 8 : D / 8 / kParts;       // (192: 6 of them work)
+    static constexpr int kNum = kRThreads / kLanes;
+};
+
 template <typename C, typename Row, int D, bool kWrite>
-__global__ void __launch_bounds__(kRThreads) gdn_kv_rows_kernel(const RowsParams p, const int tile) {
-    constexpr int kLanes = D == 192 ? 32 : D / 8;      // of a head's row (192: 24 of them work)
-    constexpr int kGroups = kRThreads / kLanes;
-    constexpr int kAhead = 4;
+__global__ void __launch_bounds__(kRThreads, kRCtas) gdn_kv_rows_kernel(const RowsParams p, const int tile) {
+    constexpr int kLanes = Group<D>::kLanes, kGroups = Group<D>::kNum;
+    constexpr int kApart = D / kParts;                  // a lane's pieces
     __shared__ int32_t sample[kSamples + 1];
     __shared__ RowPlace place[kMaxTile];
-    dep_wait();
     const int tid = threadIdx.x;
+    const int r0 = static_cast<int>(blockIdx.x) * tile;
+    const int rows = min(tile, p.num_tokens - r0);
+    const int lane = tid % kLanes, col = 8 * lane;
+    const bool works = col < kApart;
+    // The tile's items: head h of k (kv even) or v (odd) of its row kv / 2; a group takes every kGroups-th.
+    const int dkv = kGroups / p.heads, dh = kGroups - dkv * p.heads;
+    int kv = tid / kLanes / p.heads, h = tid / kLanes - kv * p.heads;
+    const int rounds = (2 * rows * p.heads + kGroups - 1) / kGroups;
+    dep_wait();
+
+    using Raw = std::conditional_t<kWrite, uint4, typename C::Raw>;
+    Raw raw[kParts];
+    float scale = 0.f;
+    auto load_row = [&](int64_t row) {
+        const __nv_bfloat16* src = (kv & 1 ? p.v : p.k) + row * (kv & 1 ? p.v_stride : p.k_stride) + h * D + col;
+#pragma unroll
+        for (int c = 0; c < kParts; ++c) raw[c] = ld(reinterpret_cast<const Raw*>(src + c * kApart));
+    };
+    // a written row that is where its number says need not wait for its place
+    const bool direct = kWrite && p.sti == nullptr;
+    if constexpr (kWrite)
+        if (direct && works && kv < 2 * rows) load_row(r0 + (kv >> 1));
+
     const int stride = (p.batch + 1 + kSamples - 1) / kSamples;
     const int samples = (p.batch + 1 + stride - 1) / stride;
     for (int k = tid; k < samples; k += kRThreads) sample[k] = ld(p.cu + static_cast<int64_t>(k) * stride);
     if (blockIdx.x == 0 && tid == 0 && ld(p.cu + p.batch) > p.num_tokens) raise(p.status, GDN_FLAG_TOKEN_ROW);
     __syncthreads();
-    const int r0 = static_cast<int>(blockIdx.x) * tile;
-    const int rows = min(tile, p.num_tokens - r0);
     if (tid < rows) place[tid] = place_of(p, sample, stride, samples, r0 + tid);
     __syncthreads();
     dep_launch();
-    const int lane = tid % kLanes, col = 8 * lane;
-    const bool works = col < D;
-    const int items = rows * 2 * p.heads;               // a head's row of k or of v
-    for (int base = 0; base < items; base += kAhead * kGroups) {      // (all threads alike: the maximum goes through shuffles)
-        typename C::Raw held[kAhead];
-        uint4 raw[kAhead];
-        float scale[kAhead];
-        int64_t at[kAhead], sat[kAhead], dense[kAhead];
-        bool live[kAhead], is_v[kAhead];
+
+    for (int r = 0; r < rounds; ++r) {                  // (all threads alike: the maximum goes through shuffles)
+        const bool is_v = kv & 1;
+        RowPlace pl = {-1, 0, 0};
+        if (kv < 2 * rows) pl = place[kv >> 1];
+        const bool live = pl.at >= 0 && works;
+        const int64_t at = (pl.at + h * p.pg.head_stride + col) * C::kBytes, sat = pl.scale + h * p.pg.s_head;
+        if constexpr (kWrite) {
+            if (live && !(direct && r == 0)) load_row(pl.row);
+            char* dst = static_cast<char*>(is_v ? p.v_cache : p.k_cache) + at;
+            float x[kParts][8];
 #pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            const int k = base + u * kGroups + tid / kLanes;
-            live[u] = k < items;
-            const int j = live[u] ? k / p.heads : 0;
-            const int h = live[u] ? k - j * p.heads : 0;
-            const RowPlace pl = place[j >> 1];
-            is_v[u] = j & 1;
-            live[u] = live[u] && pl.at >= 0;
-            at[u] = pl.at + h * p.pg.head_stride + col;
-            sat[u] = pl.scale + h * p.pg.s_head;
-            dense[u] = pl.row * (is_v[u] ? p.v_stride : p.k_stride) + h * D + col;
-            if constexpr (kWrite) {
-                raw[u] = make_uint4(0, 0, 0, 0);
-                if (live[u] && works) raw[u] = ld(reinterpret_cast<const uint4*>((is_v[u] ? p.v : p.k) + dense[u]));
-            } else {
-                if (live[u] && works) {
-                    held[u] = ld(reinterpret_cast<const typename C::Raw*>(static_cast<const char*>(is_v[u] ? p.v_cache : p.k_cache) + at[u] * C::kBytes));
-                    if constexpr (kQuantised<C>) scale[u] = ld((is_v[u] ? p.v_scale : p.k_scale) + sat[u]);
+            for (int c = 0; c < kParts; ++c) Bf16::get(live ? raw[c] : make_uint4(0, 0, 0, 0), x[c]);
+            if constexpr (kQuantised<C>) {
+                uint32_t big = 0;                       // the largest pattern: infinities and NaN are above the finite ones
+#pragma unroll
+                for (int c = 0; c < kParts; ++c)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) big = max(big, __float_as_uint(x[c][e]) & 0x7fffffffu);
+#pragma unroll
+                for (int o = kLanes / 2; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(kFull, big, o, kLanes));
+                const bool fine = big < 0x7f800000u;
+                const float s = fine ? C::scale_of(bits_f(big)) : bits_f(0x7fc00000u);
+                if (live) {
+#pragma unroll
+                    for (int c = 0; c < kParts; ++c) {
+                        if (fine) C::put(dst + c * kApart, x[c], s);
+                        else *reinterpret_cast<uint2*>(dst + c * kApart) = make_uint2(0, 0);
+                    }
+                    if (lane == 0) (is_v ? p.v_scale : p.k_scale)[sat] = s;
                 }
+            } else if (live) {
+#pragma unroll
+                for (int c = 0; c < kParts; ++c) C::put(dst + c * kApart * C::kBytes, x[c]);
+            }
+        } else if (live) {
+            const char* src = static_cast<const char*>(is_v ? p.v_cache : p.k_cache) + at;
+#pragma unroll
+            for (int c = 0; c < kParts; ++c) raw[c] = ld(reinterpret_cast<const Raw*>(src + c * kApart * C::kBytes));
+            if constexpr (kQuantised<C>) scale = ld((is_v ? p.v_scale : p.k_scale) + sat);
+            char* dst = static_cast<char*>(is_v ? p.v_rows : p.k_rows) + (pl.row * (is_v ? p.v_stride : p.k_stride) + h * D + col) * Row::kBytes;
+#pragma unroll
+            for (int c = 0; c < kParts; ++c) {
+                float x[8];
+                C::get(raw[c], x);
+                if constexpr (kQuantised<C>) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] *= scale;
+                }
+                Row::put(dst + c * kApart * Row::kBytes, x);
             }
         }
-#pragma unroll
-        for (int u = 0; u < kAhead; ++u) {
-            float x[8];
-            if constexpr (kWrite) {
-                char* dst = static_cast<char*>(is_v[u] ? p.v_cache : p.k_cache) + at[u] * C::kBytes;
-                if constexpr (kQuantised<C>) {
-                    Bf16::get(raw[u], x);
-                    float a = 0.f;
-                    uint32_t big = 0;                   // the largest pattern: infinities and NaN are above the finite ones
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) big = max(big, __float_as_uint(x[e]) & 0x7fffffffu);
-#pragma unroll
-                    for (int o = kLanes / 2; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(kFull, big, o, kLanes));
-                    a = bits_f(big);
-                    const bool fine = big < 0x7f800000u;
-                    const float s = fine ? C::scale_of(a) : bits_f(0x7fc00000u);
-                    if (live[u] && works) {
-                        if (fine) C::put(dst, x, s);
-                        else *reinterpret_cast<uint2*>(dst) = make_uint2(0, 0);
-                        if (lane == 0) (is_v[u] ? p.v_scale : p.k_scale)[sat[u]] = s;
-                    }
-                } else if constexpr (C::kBytes == 2) {
-                    if (live[u] && works) {
-                        Bf16::get(raw[u], x);
-                        C::put(dst, x);
-                    }
-                }
-            } else {
-                if (live[u] && works) {
-                    C::get(held[u], x);
-                    if constexpr (kQuantised<C>) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] *= scale[u];
-                    }
-                    Row::put(static_cast<char*>(is_v[u] ? p.v_rows : p.k_rows) + dense[u] * Row::kBytes, x);
-                }
-            }
+        kv += dkv;
+        h += dh;
+        if (h >= p.heads) {
+            h -= p.heads;
+            ++kv;
         }
     }
 }
@@ -287,11 +308,11 @@ __global__ void __launch_bounds__(kRThreads) gdn_kv_rows_kernel(const RowsParams
 template <typename C, typename Row, int D, bool kWrite>
 cudaError_t launch_rows(const RowsParams& p, cudaStream_t stream) {
     const int sms = sm_count() ? sm_count() : 148;
-    // rows a CTA: about four rounds of its groups, fewer where that leaves SMs without a CTA
-    const int groups = kRThreads / (D == 192 ? 32 : D / 8);
-    int tile = max(1, 4 * 4 * groups / (2 * p.heads));
-    tile = min(tile, max(1, (p.num_tokens + 2 * sms - 1) / (2 * sms)));
-    tile = min(tile, kMaxTile);
+    // rows a CTA: few rows go to as many CTAs as run at once, more in whole waves of them
+    const int64_t most = std::min(kMaxTile, std::max(1, kRounds * Group<D>::kNum / (2 * p.heads)));
+    const int64_t wave = static_cast<int64_t>(sms) * kRCtas;
+    const int64_t waves = (p.num_tokens + wave * most - 1) / (wave * most);
+    const int tile = static_cast<int>((p.num_tokens + wave * waves - 1) / (wave * waves));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>((p.num_tokens + tile - 1) / tile), 1, 1);
     cfg.blockDim = dim3(kRThreads, 1, 1);
