@@ -40,12 +40,21 @@ __device__ __forceinline__ void make_span(const AttnParams& p, int past, int n, 
     s.len = s.blocks + G::kCost;
 }
 
-// Sequence i's part of the line (blocks 0: nothing to do), and a flag for bad data.
+// A sequence's data (several are loaded before the first is looked at: their latency shows once)
+struct Given {
+    int a, e, past;
+};
+__device__ __forceinline__ Given given(const AttnParams& p, int i) {
+    if (i >= p.batch) return {0, 0, 0};
+    return {ld(p.cu + i), ld(p.cu + i + 1), ld(p.kv_lens + i)};
+}
+
+// A sequence's part of the line (blocks 0: nothing to do), and a flag for bad data; `end` is the last offset.
 template <typename G>
-__device__ __forceinline__ int span_of(const AttnParams& p, int i, Span& s) {
+__device__ __forceinline__ int span_of(const AttnParams& p, const Given& v, int end, Span& s) {
     s.blocks = 0;
-    const int a = ld(p.cu + i), e = ld(p.cu + i + 1), end = ld(p.cu + p.batch);
-    const int64_t past = ld(p.kv_lens + i);
+    const int a = v.a, e = v.e;
+    const int64_t past = v.past;
     if (e <= a) return 0;
     if (a < 0 || e > end || e > p.num_tokens) return GDN_FLAG_TOKEN_ROW;
     const int n = e - a;
@@ -67,7 +76,6 @@ __device__ __forceinline__ int span_of(const AttnParams& p, int i, Span& s) {
 template <typename G>
 struct Line {
     static constexpr int kT = G::kThreads * G::kPer;
-    int64_t total;                      // blocks of the whole line
     int64_t base;                       // blocks in front of the chunk
     int chunk;                          // first sequence of the chunk
     int64_t before[kT + 1];             // in front of each of its sequences, from base on
@@ -103,18 +111,19 @@ template <typename G>
 __device__ __forceinline__ void scan_chunk(const AttnParams& p, Line<G>& L, int first, int64_t base, bool tell) {
     const int tid = threadIdx.x, lane = tid & 31;
     int64_t v[G::kPer], sum = 0;
+    Given of[G::kPer];
+#pragma unroll
+    for (int k = 0; k < G::kPer; ++k) of[k] = given(p, first + tid * G::kPer + k);
+    const int end = ld(p.cu + p.batch);
 #pragma unroll
     for (int k = 0; k < G::kPer; ++k) {
-        const int i = first + tid * G::kPer + k;
+        Span s;
+        const int flag = span_of<G>(p, of[k], end, s);
+        if (flag && tell) raise(p.status, flag);
         v[k] = 0;
-        if (i < p.batch) {
-            Span s;
-            const int flag = span_of<G>(p, i, s);
-            if (flag && tell) raise(p.status, flag);
-            if (s.blocks > 0) {
-                v[k] = static_cast<int64_t>(s.len) * s.tiles * p.groups;
-                L.keep(tid * G::kPer + k, s);
-            }
+        if (s.blocks > 0) {
+            v[k] = static_cast<int64_t>(s.len) * s.tiles * p.groups;
+            L.keep(tid * G::kPer + k, s);
         }
         sum += v[k];
     }
@@ -146,21 +155,32 @@ __device__ __forceinline__ void scan_chunk(const AttnParams& p, Line<G>& L, int 
 
 // The whole line's length; the first chunk is scanned on the way.
 template <typename G>
-__device__ __forceinline__ void begin_line(const AttnParams& p, Line<G>& L) {
+__device__ __forceinline__ int64_t begin_line(const AttnParams& p, Line<G>& L) {
     constexpr int kT = Line<G>::kT;
     scan_chunk<G>(p, L, 0, 0, blockIdx.x == 0);
     int64_t more = 0;
     if (p.batch > kT) {
+        const int end = ld(p.cu + p.batch);
         for (int i = kT + threadIdx.x; i < p.batch; i += G::kThreads) {
             Span s;
-            const int flag = span_of<G>(p, i, s);
+            const int flag = span_of<G>(p, given(p, i), end, s);
             if (flag && blockIdx.x == 0) raise(p.status, flag);
             if (s.blocks > 0) more += static_cast<int64_t>(s.len) * s.tiles * p.groups;
         }
         more = block_sum<G>(L, more);
     }
-    if (threadIdx.x == 0) L.total = L.before[kT] + more;
-    __syncthreads();
+    return L.before[kT] + more;
+}
+
+// The last sequence of the chunk that begins at or before block w of the line (it has blocks); a whole warp
+template <typename G>
+__device__ __forceinline__ int in_chunk(const Line<G>& L, int64_t w) {
+    constexpr int kStep = Line<G>::kT / 32;
+    static_assert(Line<G>::kT % 32 == 0 && kStep <= 32, "two looks");
+    const int lane = threadIdx.x & 31;
+    const int64_t x = w - L.base;
+    const int near = kStep * (__popc(__ballot_sync(kFull, L.before[kStep * lane] <= x)) - 1);
+    return near + __popc(__ballot_sync(kFull, lane < kStep && L.before[near + min(lane, kStep - 1)] <= x)) - 1;
 }
 
 // The sequence whose blocks contain block w of the line (0 <= w < total), chunks moving on.
@@ -173,12 +193,7 @@ __device__ __forceinline__ int sequence_at(const AttnParams& p, Line<G>& L, int6
         __syncthreads();
         scan_chunk<G>(p, L, first, base, false);
     }
-    int lo = 0, hi = min(kT, p.batch - L.chunk) - 1;    // the last one that begins at or before w: it has blocks
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (L.base + L.before[mid] <= w) lo = mid; else hi = mid - 1;
-    }
-    return lo;
+    return in_chunk(L, w);
 }
 
 // The same by one warp.
@@ -191,16 +206,15 @@ __device__ __forceinline__ int sequence_at_warp(const AttnParams& p, Line<G>& L,
         const int first = L.chunk + kT;
         __syncwarp();
         int64_t run = 0;
+        const int end = ld(p.cu + p.batch);
         for (int k = 0; k < kT / 32; ++k) {
             const int i = first + 32 * k + lane;
             int64_t sum = 0;
             Span s;
-            if (i < p.batch) {
-                span_of<G>(p, i, s);
-                if (s.blocks > 0) {
-                    sum = static_cast<int64_t>(s.len) * s.tiles * p.groups;
-                    L.keep(32 * k + lane, s);
-                }
+            span_of<G>(p, given(p, i), end, s);
+            if (s.blocks > 0) {
+                sum = static_cast<int64_t>(s.len) * s.tiles * p.groups;
+                L.keep(32 * k + lane, s);
             }
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -217,12 +231,7 @@ __device__ __forceinline__ int sequence_at_warp(const AttnParams& p, Line<G>& L,
         }
         __syncwarp();
     }
-    int lo = 0, hi = min(kT, p.batch - L.chunk) - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (L.base + L.before[mid] <= w) lo = mid; else hi = mid - 1;
-    }
-    return lo;
+    return in_chunk(L, w);
 }
 
 // CTAs (of one member of the groups of heads) that share the line: no more than leave each `least` blocks
@@ -253,7 +262,7 @@ __device__ __forceinline__ Piece piece_at(const AttnParams& p, const Line<G>& L,
     d.b1 = max(at + d.places - G::kCost, 0);
     d.blocks = s.blocks;
     d.u0 = w - at + G::kCost;
-    const int group = unit / s.tiles;
+    const int group = s.tiles == 1 ? unit : static_cast<int>(static_cast<uint32_t>(unit) / static_cast<uint32_t>(s.tiles));
     d.head = group * p.side + member;
     d.tile = unit - group * s.tiles;
     d.rows = min(G::kRows, s.n * p.ratio - d.tile * G::kRows);

@@ -346,13 +346,12 @@ __global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(saddr(&ms.tmem)), "n"(512));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     }
-    begin_line<G>(p, ms.line);
+    const int64_t total = begin_line<G>(p, ms.line);
     dep_launch();
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tm = ms.tmem;
-    const int64_t total = ms.line.total;
     const int ctas = ctas_of(total, gridDim.x / p.side, 1 + G::kCost);
     const int cta = blockIdx.x, place = cta / p.side, member = cta - place * p.side;
     volatile int* const abort = &ms.abort;

@@ -175,9 +175,8 @@ __global__ void __launch_bounds__(kThreads, Shape<kKind, D, kOct>::kCtas) gdn_at
     unsigned char* const ring0 = smem + S::kQ;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, tq = lane & 3;
     dep_wait();
-    begin_line<G>(p, line);
+    const int64_t total = begin_line<G>(p, line);
     dep_launch();
-    const int64_t total = line.total;
     const int ctas = ctas_of(total, gridDim.x / p.side, 1 + G::kCost);
     const int cta = blockIdx.x, place = cta / p.side, member = cta - place * p.side;
     int32_t* const meta = p.meta + static_cast<int64_t>(cta) * kMetaInts;
@@ -588,43 +587,51 @@ __global__ void __launch_bounds__(kThreads, Shape<kKind, D, kOct>::kCtas) gdn_at
             }
         __syncthreads();                                    // (every warp has read its ring)
         float* const ow = reinterpret_cast<float*>(ring0);  // [warp][row][D]
-        {
+        auto top_of = [&](int row) {
+            float top = row_m[0][row];
 #pragma unroll
-            for (int n = 0; n < kOct; ++n)
+            for (int w2 = 1; w2 < kWarps; ++w2) top = fmaxf(top, row_m[w2][row]);
+            return top;
+        };
+        if (tid < kRowsU) {
+            const float top = top_of(tid);
+            float sum = 0.f;
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int row = 8 * n + 2 * tq + e;
-                    float top = row_m[0][row];
+            for (int w2 = 0; w2 < kWarps; ++w2) sum += ex2(row_m[w2][tid] - top) * row_l[w2][tid];
+            row_inv[tid] = part >= 0 ? 1.f : sum == 0.f ? 0.f : 1.0f / sum;
+            if (part >= 0) {
+                float* ml = p.ws + static_cast<int64_t>(2 * gridDim.x) * kRowsU * D + static_cast<int64_t>(part) * 2 * kRowsU;
+                ml[tid] = top;
+                ml[kRowsU + tid] = sum;
+            }
+        }
+        float a[kOct][2];
 #pragma unroll
-                    for (int w2 = 1; w2 < kWarps; ++w2) top = fmaxf(top, row_m[w2][row]);
-                    float a = ex2(m[n][e] - top);
-                    if (warp == 0 && g == 0) {
-                        float sum = 0.f;
+        for (int n = 0; n < kOct; ++n)
 #pragma unroll
-                        for (int w2 = 0; w2 < kWarps; ++w2) sum += ex2(row_m[w2][row] - top) * row_l[w2][row];
-                        row_inv[row] = part >= 0 ? 1.f : sum == 0.f ? 0.f : 1.0f / sum;
-                        if (part >= 0) {
-                            float* ml = p.ws + static_cast<int64_t>(2 * gridDim.x) * kRowsU * D + static_cast<int64_t>(part) * 2 * kRowsU;
-                            ml[row] = top;
-                            ml[kRowsU + row] = sum;
-                        }
-                    }
-                    if constexpr (kQuantised) a *= __uint_as_float(static_cast<uint32_t>(unit_e) << 23);
-                    if (row >= d.rows) continue;
-                    float* const to = ow + (warp * kRowsU + row) * D;
+            for (int e = 0; e < 2; ++e) {
+                a[n][e] = ex2(m[n][e] - top_of(8 * n + 2 * tq + e));
+                if constexpr (kQuantised) a[n][e] *= __uint_as_float(static_cast<uint32_t>(unit_e) << 23);
+            }
 #pragma unroll
-                    for (int dn = 0; dn < D / 16; ++dn) {
-                        const float x = o[dn][n][e], y = o[dn][n][e + 2];
-                        // (columns exchanged by the row, so that the rows of a store lie in different banks)
-                        if constexpr (kQuantised)
-                            *reinterpret_cast<float2*>(to + ((16 * dn + 2 * g) ^ ((row & 2) << 3))) = make_float2(a == 0.f ? 0.f : x * a, a == 0.f ? 0.f : y * a);
-                        else {
-                            to[(16 * dn + g) ^ ((row & 6) << 2)] = a == 0.f ? 0.f : x * a;
-                            to[(16 * dn + g + 8) ^ ((row & 6) << 2)] = a == 0.f ? 0.f : y * a;
-                        }
+        for (int n = 0; n < kOct; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = 8 * n + 2 * tq + e;
+                if (row >= d.rows) continue;
+                float* const to = ow + (warp * kRowsU + row) * D;
+#pragma unroll
+                for (int dn = 0; dn < D / 16; ++dn) {
+                    const float x = a[n][e] == 0.f ? 0.f : o[dn][n][e] * a[n][e], y = a[n][e] == 0.f ? 0.f : o[dn][n][e + 2] * a[n][e];
+                    // (columns exchanged by the row, so that the rows of a store lie in different banks)
+                    if constexpr (kQuantised) {
+                        *reinterpret_cast<float2*>(to + ((16 * dn + 2 * g) ^ ((row & 2) << 3))) = make_float2(x, y);
+                    } else {
+                        to[(16 * dn + g) ^ ((row & 6) << 2)] = x;
+                        to[(16 * dn + g + 8) ^ ((row & 6) << 2)] = y;
                     }
                 }
-        }
+            }
         __syncthreads();
 #pragma unroll 1
         for (int id = tid; id < d.rows * (D / 4); id += kThreads) {
