@@ -767,7 +767,9 @@ GDNSPEC_API gdn_status gdn_kv_read(
  * order, so equal calls give equal results; how a sequence is cut depends on the others'
  * lengths, by rounding in FP32.  Bad device data: q_len > max_T sets GDN_FLAG_QLEN, the rest
  * as for gdn_kv_write, except that any row of a sequence outside [0, num_tokens) skips the
- * sequence.  An infinity or NaN in k or v spoils the tokens that see it, in q its own row.
+ * sequence.  An infinity or NaN in k or v spoils the tokens that see it, in q its own row.  (In an
+ * 8-bit cache that is a scale; a GDN_E4M3 code that is NaN, which gdn_kv_write never makes, may spoil
+ * other tokens of its sequence too.)
  * q, z, out 16-byte aligned with strides that are multiples of 8; the caches as above.
  * batch at most 2^20 sequences.
  */

@@ -269,12 +269,12 @@ def test_scales_of_very_different_sizes(cuda_device, kind, wide):
 
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
-@BOTH
-def test_a_token_that_is_no_number_spoils_those_that_see_it(cuda_device, kind, bad, wide):
+@pytest.mark.parametrize("heads", [4, 6, 8, 28])              # of one cache head, by four tokens: units of 16, 24, 32 and 64 rows
+def test_a_token_that_is_no_number_spoils_those_that_see_it(cuda_device, kind, bad, heads):
     """The third of four drafted tokens has a value (16 bit) or a scale (8 bit) that is no number, and so has a row just outside
     another sequence's window: who does not see them is not touched."""
     for which in ("v", "k"):
-        H = 8 * wide
+        H = 2 * heads
         c = Case(cuda_device, [61, 200, 30], [4, 2, 1], H, 2, 64, kind, seed=11)
         cache, scale = (c.v, c.vs) if which == "v" else (c.k, c.ks)
         for i, x in ((0, 63), (1, 100)):
@@ -500,6 +500,19 @@ def test_a_given_workspace_holds_anything(cuda_device, wide):
     c.check()
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("rows", [9, 16, 17, 24, 25, 31, 32, 33, 48])
+def test_units_of_every_size_and_pages_that_sequences_share(cuda_device, kind, D, rows):
+    c = Case(cuda_device, [0, 40, 700, 700, 2500], [1, 1, 1, 1, 1], rows, 1, D, kind, seed=rows)
+    c.table[3, :40] = c.table[2, :40]                # a common prefix
+    c.table[4, 7] = c.table[4, 6]                    # and a page twice
+    for window in (0, 300):
+        c.run(window=window)
+        assert int(c.status) == 0
+        c.check(window=window)
+
+
 @pytest.mark.parametrize("seed", range(48))
 def test_random_batches(cuda_device, seed):
     rng = random.Random(1000 + seed)
@@ -653,6 +666,50 @@ def test_write_rows_of_many_sequences(cuda_device, batch):
     gdn.gdn_kv_read(cache[0], cache[1], table.to(dev), _i32(past, dev), ref.offsets(n).to(dev), *rows)
     assert torch.equal(rows[0][:N], k) and torch.equal(rows[1][:N], -k)
     assert bool((rows[0][N:].view(torch.int16) == SENTINEL).all())
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_captured_reads_and_writes_beside_each_other(cuda_device, kind):
+    """A graph that moves rows from one part of a sequence to another sequence, replayed as both places move, beside another
+    graph's on another stream."""
+    dev, page, G, D, N = cuda_device, 16, 2, 128, 70
+    g = torch.Generator(device=dev).manual_seed(6)
+    jobs = []
+    for j in range(2):
+        table, pages = ref.tables([700, 700], [100, 100], page, j)
+        cache = ref.make_cache(pages, page, G, D, kind, "nhd", dev)
+        _fill(cache[:2], cache[2:], table, [800, 800], page, kind, g)
+        rows = [torch.zeros(N, G, D, device=dev, dtype=torch.bfloat16) for _ in range(2)]
+        begin, to, cu = _i32([0], dev), _i32([0], dev), _i32([0, N], dev)
+        tables = [table[i:i + 1].to(dev).contiguous() for i in range(2)]
+        scales = dict(k_scale=cache[2], v_scale=cache[3])
+        calls = [gdn.prepare_kv_read(cache[0], cache[1], tables[0], begin, cu, *rows, **scales),
+                 gdn.prepare_kv_write(*rows, cache[0], cache[1], tables[1], to, cu, **scales)]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+            for call in calls:
+                call()
+        jobs.append((cache, table, rows, begin, to, graph, torch.cuda.Stream(), calls))
+    for a, b in ((0, 0), (31, 555), (729, 3)):
+        for cache, table, rows, begin, to, graph, stream, _ in jobs:
+            begin.fill_(a)
+            to.fill_(b)
+        torch.cuda.synchronize()
+        for job in jobs:
+            with torch.cuda.stream(job[6]):
+                job[5].replay()
+        torch.cuda.synchronize()
+        for cache, table, rows, *_ in jobs:
+            for c, s, r in zip(cache[:2], cache[2:], rows):
+                c, s = c.cpu(), None if s is None else s.cpu()
+                x = torch.arange(N) + a
+                want = ref.pick(c, table[0].long()[x // page], x % page)
+                if s is not None:
+                    want = want * s[table[0].long()[x // page], x % page].double()[..., None]
+                assert torch.equal(r.cpu(), want.float().bfloat16())
+                for t in (0, 33, N - 1):
+                    where = ref.place(table, 1, b + t, page, c.shape[0])
+                    assert all(_written(r[t, h].double().cpu(), kind, c, s, where, h) for h in range(G))
 
 
 @pytest.mark.parametrize("what,flag", [("page", 1), ("long", 1), ("negative", 1), ("row", 8), ("offsets", 8), ("none", 0)])
