@@ -1148,6 +1148,7 @@ cudaError_t launch(const AttnParams& p, bool joins, int grid, cudaStream_t strea
     if (!encode_map(k_map, p.k, p, D, kKind, tc.box) || !encode_map(v_map, p.v, p, D, kKind, tc.box)) return cudaErrorInvalidValue;
     err = cudaLaunchKernelEx(&cfg, kernel, p, k_map, v_map, tc);
     if (err != cudaSuccess || !joins) return err;
+    cfg.gridDim = dim3(static_cast<unsigned>(grid * kJSplit<kRowsT>), 1, 1);
     cfg.blockDim = dim3(kJThreads, 1, 1);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, gdn_attn_join_kernel<D, kRowsT>, p, grid);

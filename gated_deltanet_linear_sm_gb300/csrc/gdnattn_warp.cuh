@@ -684,6 +684,7 @@ cudaError_t launch(const AttnParams& p, bool joins, int grid, cudaStream_t strea
     cfg.numAttrs = 1;
     err = cudaLaunchKernelEx(&cfg, gdn_attn_decode_kernel<kKind, D, kOct>, p);
     if (err != cudaSuccess || !joins) return err;
+    cfg.gridDim = dim3(static_cast<unsigned>(grid * kJSplit<8 * kOct>), 1, 1);
     cfg.blockDim = dim3(kJThreads, 1, 1);
     cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, gdn_attn_join_kernel<D, 8 * kOct>, p, grid);
