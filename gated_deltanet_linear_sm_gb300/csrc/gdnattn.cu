@@ -22,14 +22,16 @@ using namespace gdn_kv;
 
 namespace {
 
-// Which kernel: the tcgen05 one pays where the other one would read the cache a second time: from more than 32 query
-// rows on, and for a head dim over 128, where that one's units end at 16 rows, from more than 16.  32 sequences of up to 4096,
-// tcgen05 and other: bf16, head dim 128, 24 rows 60 and 50 us, 32 rows 62 and 59, 48 rows 71 and 94, 64 rows 79 and 97;
-// e4m3, 24 rows 55 and 45, 48 rows 74 and 85; bf16, head dim 256, 16 rows 88 and 70, 24 rows 93 and 109.  (Head dim 64 is a
-// tie at 48 rows; at 64 rows the other one has 63 us, 60 in e4m3, where this one has 75 and 76, but it falls behind
-// as the sequences grow: fp16, 3 of 65535 84 and 81.)  It wants pages of whole groups of 8 positions, and has no int8 products.
+// Which kernel: the tcgen05 one pays where the other one, whose units have up to 32 rows (16 for a head dim over 128), would read
+// the cache a second time; for head dim 64 from the third time on.  32 sequences of up to 4096, tcgen05 and other, in us:
+// bf16, head dim 128, 24 rows 60 and 50, 32 rows 62 and 59, 48 rows 71 and 94, 64 rows 79 and 97; e4m3, 24 rows 55 and 45, 48
+// rows 74 and 85; bf16, head dim 256, 16 rows 88 and 70, 24 rows 93 and 109; head dim 64, 48 rows 63 and 62, 64 rows 75 and 63.
+// (It also depends on the lengths, which the host does not know: 128 sequences, 8 heads of 64, 48 rows, bf16, of 64 positions
+// 68 and 44, of 512 114 and 102, of 2048 236 and 267; head dim 128, of 64 76 and 60, of 128 77 and 82, of 512 116 and 158.)
+// It wants pages of whole groups of 8 positions, and has no int8 products.
 bool on_tc(const AttnParams& p, int D, gdn_dtype type) {
-    return type != GDN_I8 && p.ratio * p.max_T > (D > 128 ? 16 : 32) && p.pg.page % 8 == 0 && p.pg.num_pages < (1ll << 31);
+    const int few = D == 64 ? 64 : D == 128 ? 32 : 16;
+    return type != GDN_I8 && p.ratio * p.max_T > few && p.pg.page % 8 == 0 && p.pg.num_pages < (1ll << 31);
 }
 
 }  // namespace

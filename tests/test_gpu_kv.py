@@ -32,9 +32,9 @@ from tests import kv_ref as ref
 
 pytestmark = pytest.mark.gpu
 KINDS = list(ref.TYPES)
-# few query rows, a few dozen, and more: there are two kernels and units of 8 to 64 rows (int8 caches, and pages that are no
+# few query rows, a few dozen, and more than 64: there are two kernels and units of 8 to 64 rows (int8 caches, and pages that are no
 # whole groups of 8 positions, run on the first with any number of rows)
-BOTH = pytest.mark.parametrize("wide", [1, 7, 11])
+BOTH = pytest.mark.parametrize("wide", [1, 7, 17])
 SENTINEL = 0x7FBF               # a NaN bf16 pattern that no kernel writes
 
 
@@ -398,7 +398,7 @@ FLAGS = [("page", 1), ("long", 1), ("negative", 1), ("q_len", 4), ("row", 8), ("
 @BOTH
 def test_bad_data_skips_the_sequence(cuda_device, what, flag, wide):
     # (20 and 40 rows for a single token: the bound on the tokens is part of which kernel runs)
-    c = Case(cuda_device, [40, 90, 200], [2, 2, 1], {1: 4, 7: 40, 11: 80}[wide], 2, 128, "bf16", gather=what == "row", seed=8)
+    c = Case(cuda_device, [40, 90, 200], [2, 2, 1], {1: 4, 7: 40, 17: 80}[wide], 2, 128, "bf16", gather=what == "row", seed=8)
     skipped = (1,)
     table, past, cu, sti = c.table.clone(), list(c.past), c.cu.clone(), c.sti
     if what == "page":
