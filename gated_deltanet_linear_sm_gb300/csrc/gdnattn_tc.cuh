@@ -21,9 +21,10 @@
 // the products take them (a score is masked; 0 times NaN is not).
 //
 // What bounds it: with few bytes and many rows the softmax (32 sequences of 8192, head dim 128, 64 rows, e4m3:
-// 148 us, 1.9 TB/s; the time stays when the products, the exponentials, the stores or the loads are left out
+// 136 us, 2.1 TB/s; the time stays when the products, the exponentials, the stores or the loads are left out
 // one at a time: it is the chain of a tile's steps in 4 warps a quarter), with more bytes a row
-// the ring's four places and the call's start and end (2 of 65535, head dim 256, 64 rows, bf16: 65 us, 4.1 TB/s).
+// the ring's four places and the call's start and end (2 of 65535, head dim 256, 64 rows, bf16: 62 us, 4.3 TB/s),
+// and with short sequences a unit's own chain (first tile, its edge, output: 11 us with nothing beside it).
 //
 // bf16: weights as two bf16 parts (16 significant bits), two products.  fp16: one.  e4m3: the
 // codes are operands as they are; q is the sum of two e4m3 parts (its 8 bits), a weight times the
