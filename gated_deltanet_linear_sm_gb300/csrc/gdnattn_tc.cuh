@@ -846,21 +846,9 @@ __global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(
                         y[4 * h + 3] = __float_as_uint(hi2(b));
                     }
                     if (!plain) {
-                        if constexpr (kQ8) {
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                if (unseen(c0 + e)) y[e] = 0xff800000u;
-                        } else {
-                            // Token t sees x where t >= x - past and t < x - past + window: a range of rows.  (With each row's
-                            // bounds read from shared memory a unit's first tile takes 10000 cycles, 6000 so; for e4m3 the
-                            // other way about counts more: this form costs the plain tiles 10 %, 151 us instead of 136.)
-                            const int ahead = x - d.past, skip = d.tile * kRowsT + c0;
-                            const int row0 = ahead > 0 ? ahead * p.ratio - skip : 0;
-                            const int row1 = !live ? 0 : p.window > 0 ? min(ahead + p.window, p.max_T) * p.ratio - skip : kRowsT;
-#pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                if (e < row0 || e >= row1) y[e] = 0xff800000u;
-                        }
+                        for (int e = 0; e < 8; ++e)
+                            if (unseen(c0 + e)) y[e] = 0xff800000u;
                     }
                 };
                 const int ex = kQ8 ? static_cast<int>(__float_as_uint(vs) >> 23) & 0xff : 0;
