@@ -763,10 +763,10 @@ __global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(
             if (lane == 0) bar_arrive(&ms.u_free[u % kUnits]);
         }
         if (more && ok) weigh(t - 1);
-        if (!ok) {                                  // products still in flight: nothing else waits for them
-            commit_to(&ms.drain, lead);
-            if (!__all_sync(kFull, wait(&ms.drain, 0, 0)) && lane == 0) raise(p.status, GDN_FLAG_DRAIN);
-        }
+        // Products still in flight: after a timeout of any warp's nothing else waits for them (a softmax warp may have
+        // given up on the output while this warp's own waits all ended); else the wait is over at once.
+        commit_to(&ms.drain, lead);
+        if (!__all_sync(kFull, wait(&ms.drain, 0, 0)) && lane == 0) raise(p.status, GDN_FLAG_DRAIN);
     } else if (warp < 4 * parts) {
         // ---- weights and outputs: this thread's key of a tile, chunks of 8 rows ----
         const int quad = warp & 3, part = warp >> 2, key = quad * 32 + lane;
