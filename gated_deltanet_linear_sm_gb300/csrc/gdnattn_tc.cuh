@@ -412,6 +412,7 @@ __global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(
             }
             return ok;
         };
+        int begun = 0;                              // blocks loaded of an edge tile's V whose others are not yet
         const int boxes = kTile >> tc.box_log2;     // of a tile and 128-byte column; lane b has box b's place
         Desc d = {};
         const int32_t* table = nullptr;
@@ -469,7 +470,10 @@ __global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(
                         tma_load(dst + col * kTile * 128 + b * tc.box * 128, is_k ? &k_map : &v_map, block * 128 + col * 64, row, is_k ? k_head : v_head, pg, bar);
                 }
                 ++it;
-                if (to_fix && block == L::kBlocks - 1) ++edges;
+                if (to_fix) {
+                    begun = block + 1 < L::kBlocks ? block + 1 : 0;
+                    if (begun == 0) ++edges;
+                }
             }
             if (!more) break;
             v_page = k_page;
@@ -479,6 +483,13 @@ __global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(
             v_edge = is_edge(x0 - kTile, d.key1, p.window > 0 ? max(0, d.past + d.n - p.window) : 0, d.past + 1);
             ++j;
             ++t;
+        }
+        // (given up between an edge tile's blocks: its barrier is told not to expect the others, so that what was loaded
+        // can be waited for like the rest)
+        if (begun > 0) {
+            if (lane == 0)
+                for (int k = begun; k < L::kBlocks; ++k) bar_arrive(&ms.edge_full[edges & 7]);
+            ++edges;
         }
     } else if (warp >= kSoft && warp < kSoft + kHelp) {
         // ---- what goes with a tile: its keys' presence and scales (a thread each), q of its unit, and its values where

@@ -43,3 +43,10 @@ def _sweep(dev, kind, D, window):
 @pytest.mark.parametrize("D", [64, 128])
 def test_a_wait_that_runs_out_anywhere(cuda_device, kind, D):
     _sweep(cuda_device, kind, D, 0)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f16", "e4m3"])
+@pytest.mark.parametrize("D,window", [(192, 0), (256, 0), (256, 100)])
+def test_a_wait_that_runs_out_between_the_blocks_of_a_head_dim(cuda_device, kind, D, window):
+    """Head dims of two blocks: the values of a tile at a sequence's end (with a window: of every tile) are two loads on one barrier."""
+    _sweep(cuda_device, kind, D, window)
