@@ -309,6 +309,32 @@ __device__ __forceinline__ uint32_t pack_b(float a, float b) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// ---- the products of weights and values' scales (8-bit caches) -----------------------------------------
+//
+// With P_j = 2^(s_j - m - e) |scale_j| / unit, o = sum P_j code_j and l = sum 2^(s_j - m - e), the output is
+// unit o / l for any m and e of the row.  P_j goes into an operand of fp16's range, so e is kept such
+// that the row's largest P is 2^kLift or more and stays below 2^(kSlack + 1): e moves as m does, by the
+// products alone.  m and e are not one number: beside scores of 2^24 and more, e would be lost in it.  l is
+// FP32 and needs no care: a scale counts as 2^-kFloor units at least, so 2^(s_j - m - e) stays below 2^(kFloor + kSlack),
+// and scales up to 2^128 leave it 2^-104 or more.  unit = 2^16 puts the scales that have all bits at 2^-74 to 2^128
+// (2^-94: half of them).
+struct Product {
+    static constexpr float kUnitLog2 = 16.f, kUnit = 0x1p16f, kUnitInv = 0x1p-16f, kFloor = 90.f;
+    // log2 of a scale in units, rounded down (one that is no number moves nothing: it spoils the rows that see it as it is)
+    __device__ __forceinline__ static float size_of(float scale) {
+        const int e = static_cast<int>(__float_as_uint(scale) >> 23) & 0xff;
+        return e == 255 ? -kFloor : fmaxf(static_cast<float>(e - 127) - kUnitLog2, -kFloor);
+    }
+    // The reference (m, e) moved to (now, ...), for products of at most 2^top beside now: the factor of what was
+    // added up with the old one.
+    __device__ __forceinline__ static float move(float& m, float& e, float now, float top, float lift, float slack) {
+        const float old = e + (m - now), next = top > old + slack ? top - lift : old;
+        m = now;
+        e = next;
+        return old == next ? 1.f : ex2(old - next);
+    }
+};
+
 __device__ __forceinline__ int64_t token_row(const AttnParams& p, int i) { return p.sti ? ld(p.sti + i) : i; }
 
 // four columns of a row, weighed: to the output, through the gate z

@@ -75,7 +75,7 @@ struct Cut {                            // (gdnattn.cuh)
 };
 
 // weights are 2^(s - m) with m = (largest score when it was set) - kLift; m moves when a weight would
-// pass 2^kSlack (times a value's scale below 2 units that stays in fp16)
+// pass 2^kSlack.  8 bits: 2^(s - m - e), and e keeps weight times scale there (gdnattn.cuh: Product)
 constexpr float kLift = 8.f, kSlack = 14.f;
 constexpr float kUnset = -1e30f;        // m of a row without a score yet
 
@@ -127,12 +127,13 @@ struct Misc {
     uint32_t live[kKeyRing][4];                // per tile and quarter: keys that are there
     float2 scales[kKeyRing][kTile];            // of keys and values (8 bits)
     alignas(16) float q_scale[kUnits][kRowsT];
-    alignas(16) float ref[2][kRowsT];      // minus the references
+    alignas(16) float ref[2][kRowsT];      // minus the references m
+    alignas(16) float shift[2][kRowsT];    // minus their e (8 bits)
     alignas(16) float alpha[kRowsT], zero[kRowsT];
-    float col[4][kRowsT], inv[kRowsT];
+    alignas(16) float col[4][kRowsT], size[4][kRowsT];
+    float inv[kRowsT];
     int first[kRowsT], last[kRowsT];
     int64_t out_at[kRowsT], z_at[kRowsT];
-    int warp_e[16];
     uint32_t tmem;
     int abort;
 };
@@ -798,7 +799,8 @@ __global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(
             if (d.tiles == 0) break;
             if (tid < kRowsT) {
                 const int rr = d.tile * kRowsT + tid, tok = min(rr / p.ratio, d.n - 1);
-                ms.ref[0][tid] = tid < d.rows ? -kUnset : 0.f;      // (rows that are not there score 0)
+                ms.ref[0][tid] = tid < d.rows ? -kUnset : kUnset;   // (rows that are not there score 0: no weight)
+                ms.shift[0][tid] = 0.f;
                 ms.last[tid] = d.past + tok;
                 ms.first[tid] = p.window > 0 ? max(0, d.past + tok - p.window + 1) : 0;
                 if (tid < d.rows) {
@@ -819,8 +821,7 @@ __global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(
             for (int i = 0; i < kMine; ++i)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) l[i][e] = 0;
-            int cur = 0;                            // which of the two ref arrays
-            int unit_e = 1;
+            int cur = 0;                            // which of the two ref (and shift) arrays
             bool stop = false;
             for (int j = 0; j < d.tiles; ++j, ++t) {
                 need(&ms.s_full[t & 1], t / 2);     // (and what the helpers know of the keys)
@@ -840,7 +841,7 @@ __global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(
                 // scores (in units of log2 e) less the references of `ref`; those that a row does not see are -infinity
                 auto unseen = [&](int c) { return !live || x < ms.first[c] || x > ms.last[c]; };
                 uint32_t s[kMine][8];
-                auto score = [&](uint32_t (&y)[8], int c0, const float* ref) {      // one chunk, in place
+                auto score = [&](uint32_t (&y)[8], int c0, const float* ref, const float* shift) {      // one chunk, in place
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const float4 r = *reinterpret_cast<const float4*>(ref + c0 + 4 * h);
@@ -849,8 +850,13 @@ __global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(
                         u64 f0 = dup2(p.scale), f1 = f0;
                         if constexpr (!kB) f0 = pk2(f.x, f.y), f1 = pk2(f.z, f.w);
                         if constexpr (kQ8) f0 = fmul2(f0, dup2(ks)), f1 = fmul2(f1, dup2(ks));
-                        const u64 a = ffma2(raw2(y[4 * h], y[4 * h + 1]), f0, pk2(r.x, r.y));
-                        const u64 b = ffma2(raw2(y[4 * h + 2], y[4 * h + 3]), f1, pk2(r.z, r.w));
+                        u64 a = ffma2(raw2(y[4 * h], y[4 * h + 1]), f0, pk2(r.x, r.y));
+                        u64 b = ffma2(raw2(y[4 * h + 2], y[4 * h + 3]), f1, pk2(r.z, r.w));
+                        if constexpr (kQ8) {
+                            const float4 e4 = *reinterpret_cast<const float4*>(shift + c0 + 4 * h);
+                            a = add2(a, pk2(e4.x, e4.y));
+                            b = add2(b, pk2(e4.z, e4.w));
+                        }
                         y[4 * h] = __float_as_uint(lo2(a));
                         y[4 * h + 1] = __float_as_uint(hi2(a));
                         y[4 * h + 2] = __float_as_uint(lo2(b));
@@ -862,20 +868,20 @@ __global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(
                             if (unseen(c0 + e)) y[e] = 0xff800000u;
                     }
                 };
-                const int ex = kQ8 ? static_cast<int>(__float_as_uint(vs) >> 23) & 0xff : 0;
+                const float size = kQ8 ? Product::size_of(vs) : 0.f;
                 // 0: scores less the references, and whether one has to move; 1: the scores themselves, for new references;
                 // 2: scores less those.  (In a loop, so that the instructions are there once.)
                 int mode = j == 0 ? 1 : 0;
-                float b = 1.f;
                 for (;; ++mode) {
                     const float* const ref = mode == 1 ? ms.zero : ms.ref[cur];
+                    const float* const shift = mode == 1 ? ms.zero : ms.shift[cur];
 #pragma unroll
                     for (int i = 0; i < kMine; ++i)
                         if (i < chunks) tm_ld8(S + 8 * (parts * i + part), s[i]);
                     tm_wait_ld();
 #pragma unroll
                     for (int i = 0; i < kMine; ++i)
-                        if (i < chunks) score(s[i], 8 * (parts * i + part), ref);
+                        if (i < chunks) score(s[i], 8 * (parts * i + part), ref, shift);
                     if (mode == 0) {
                         float most[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -884,40 +890,50 @@ __global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(
 #pragma unroll
                                 for (int e = 0; e < 8; ++e) most[e & 3] = fmaxf(most[e & 3], __uint_as_float(s[i][e]));
                             }
-                        bool grow = fail || fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) > kSlack;
-                        if constexpr (kQ8) grow = grow || (ex != 255 && min(ex, 253) > unit_e);
+                        const bool grow = fail || fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3])) + size > kSlack;
                         if (!soft_any(grow, parts)) break;
                         if (soft_any(fail, parts)) {
                             stop = true;
                             break;
                         }
                     } else if (mode == 1) {
-                        // each row's largest score over the tile's keys, and the largest scale of its values
+                        // each row's largest score over the tile's keys, and its largest product beside that
                         float v[8 * kMine];
 #pragma unroll
                         for (int e = 0; e < 8 * kMine; ++e) v[e] = __uint_as_float(s[e >> 3][e & 7]);
                         const float mx = over_lanes(v, lane, [](float x, float y) { return fmaxf(x, y); });
                         if ((lane >> 3) < chunks) ms.col[quad][8 * (parts * (lane >> 3) + part) + (lane & 7)] = mx;
                         if constexpr (kQ8) {
-                            const int e = __reduce_max_sync(kFull, ex == 255 ? 0 : min(ex, 253));
-                            if (lane == 0) ms.warp_e[warp] = e;
+                            __syncwarp();
+#pragma unroll
+                            for (int i = 0; i < kMine; ++i)
+                                if (i < chunks) {
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e)
+                                        v[8 * i + e] = __uint_as_float(s[i][e]) - ms.col[quad][8 * (parts * i + part) + e] + size;
+                                }
+                            const float top = over_lanes(v, lane, [](float x, float y) { return fmaxf(x, y); });
+                            if ((lane >> 3) < chunks) ms.size[quad][8 * (parts * (lane >> 3) + part) + (lane & 7)] = top;
                         }
                         soft_sync(parts);
                         if (tid < kRowsT) {
                             const float m = -ms.ref[cur][tid];
                             float mx = -INFINITY;
                             if (tid < d.rows) mx = fmaxf(fmaxf(ms.col[0][tid], ms.col[1][tid]), fmaxf(ms.col[2][tid], ms.col[3][tid]));
-                            const float now = mx > m + kSlack ? mx - kLift : m;
-                            ms.ref[cur ^ 1][tid] = -now;
-                            ms.alpha[tid] = now == m ? 1.f : ex2(m - now);
-                        }
-                        if constexpr (kQ8) {
-                            int e = unit_e;
+                            if constexpr (kQ8) {
+                                float m2 = m, e2 = -ms.shift[cur][tid], top = -INFINITY;
+                                const float now = fmaxf(m, mx);
 #pragma unroll
-                            for (int k = 0; k < kSoft; ++k)
-                                if (k < 4 * parts) e = max(e, ms.warp_e[k]);
-                            if (e > unit_e) b = e - unit_e > 126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 - (e - unit_e)) << 23);
-                            unit_e = e;
+                                for (int k = 0; k < 4; ++k)
+                                    if (tid < d.rows && ms.col[k][tid] > -INFINITY) top = fmaxf(top, ms.size[k][tid] + (ms.col[k][tid] - now));
+                                ms.alpha[tid] = Product::move(m2, e2, now, top, kLift, kSlack);
+                                ms.ref[cur ^ 1][tid] = -m2;
+                                ms.shift[cur ^ 1][tid] = -e2;
+                            } else {
+                                const float now = mx > m + kSlack ? mx - kLift : m;
+                                ms.ref[cur ^ 1][tid] = -now;
+                                ms.alpha[tid] = now == m ? 1.f : ex2(m - now);
+                            }
                         }
                         soft_sync(parts);
                         cur ^= 1;
@@ -945,7 +961,7 @@ __global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(
                                 tm_ld8(o, y);
                                 tm_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 8; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * (ms.alpha[c0 + e] * b));
+                                for (int e = 0; e < 8; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * ms.alpha[c0 + e]);
                                 tm_st8(o, y);
                             }
                         }
@@ -962,7 +978,7 @@ __global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(
                 }
                 // weights
                 u64 vu = dup2(1.f);
-                if constexpr (kQ8) vu = dup2(vs * __uint_as_float(static_cast<uint32_t>(254 - unit_e) << 23));
+                if constexpr (kQ8) vu = dup2(vs * Product::kUnitInv);
                 uint32_t w[kMine][4], w2[kMine][4];
 #pragma unroll
                 for (int i = 0; i < kMine; ++i)
@@ -1030,9 +1046,9 @@ __global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(
             need(&ms.o_full[ob], u / L::kOs);
             if (soft_any(fail, parts)) break;
             fence_after();
-            const float unit = kQ8 ? __uint_as_float(static_cast<uint32_t>(unit_e) << 23) : 1.f;
             if (tid < kRowsT) {
-                const float sum = ms.col[0][tid] + ms.col[1][tid] + ms.col[2][tid] + ms.col[3][tid];
+                const float of_e = kQ8 ? ex2(-ms.shift[cur][tid]) : 1.f;        // (sums relative to m alone)
+                const float sum = (ms.col[0][tid] + ms.col[1][tid] + ms.col[2][tid] + ms.col[3][tid]) * of_e, unit = kQ8 ? of_e * Product::kUnit : 1.f;
                 ms.inv[tid] = d.part >= 0 ? unit : sum == 0.f ? 0.f : unit / sum;
                 if (d.part >= 0 && tid < d.rows) {
                     float* ml = p.ws + static_cast<int64_t>(2 * gridDim.x) * kRowsT * D + static_cast<int64_t>(d.part) * 2 * kRowsT;

@@ -21,8 +21,10 @@
 // far from the end of fp16's range.
 //
 // fp16 and 8-bit caches run on fp16 operands: codes are exact in fp16, a key's scale multiplies its score
-// and a value's scale its weight.  So that weight times scale fits fp16, scales count in units of a power
-// of two that a warp keeps for all its values, the largest yet.  q becomes fp16 by a power of two of its
+// and a value's scale its weight.  What has to fit fp16 is then weight times scale, so an 8-bit row has its
+// reference in two parts: m, its largest score when it moved, and e (gdnattn.cuh: Product), from the largest product
+// of a weight and a scale among the keys that the row itself sees.  A scale that other rows see, or that has
+// no weight, takes no bits from a row's other products.  q becomes fp16 by a power of two of its
 // row, which goes into the row's scale.  A bf16 cache runs on bf16 operands, and a weight is the sum of two
 // bf16 parts: one has 8 bits only.
 #pragma once
@@ -353,15 +355,15 @@ __global__ void __launch_bounds__(kThreads, Shape<kKind, D, kOct>::kCtas) gdn_at
 #pragma unroll
                 for (int ks = 0; ks < kSteps; ++ks) q_frag(n, ks, qf[n][ks][0], qf[n][ks][1]);
         }
-        // this thread's rows 8 n + 2 tq and the next: their scale, reference and sum
-        float qs[kOct][2], m[kOct][2], l[kOct][2];
+        // this thread's rows 8 n + 2 tq and the next: their scale, reference (pe: e of the products) and sum
+        float qs[kOct][2], m[kOct][2], pe[kOct][2], l[kOct][2];
 #pragma unroll
         for (int n = 0; n < kOct; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 qs[n][e] = q_scale[8 * n + 2 * tq + e];
-                m[n][e] = 8 * n + 2 * tq + e < d.rows ? kUnset : 0.f;       // (rows that are not there score 0)
-                l[n][e] = 0.f;
+                m[n][e] = 8 * n + 2 * tq + e < d.rows ? kUnset : -kUnset;   // (rows that are not there score 0: no weight)
+                pe[n][e] = l[n][e] = 0.f;
             }
         const int all_lo = p.window > 0 ? max(0, d.past + d.n - p.window) : 0, all_hi = d.past + 1;     // seen by every row
         float o[D / 16][kOct][4];
@@ -371,7 +373,6 @@ __global__ void __launch_bounds__(kThreads, Shape<kKind, D, kOct>::kCtas) gdn_at
             for (int n = 0; n < kOct; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[dn][n][e] = 0.f;
-        int unit_e = 1;                             // exponent (biased) of the values' scale unit
 
         // ---- the keys ----
 #pragma unroll 1
@@ -449,29 +450,31 @@ __global__ void __launch_bounds__(kThreads, Shape<kKind, D, kOct>::kCtas) gdn_at
             __syncwarp();
             issue();
             // ---- the softmax's references and weights ----
-            float f[2] = {1.f, 1.f};
-            int ex = 0;
+            float f[2] = {1.f, 1.f}, size[2] = {0.f, 0.f};
             if constexpr (kQuantised) {
                 f[0] = lds(vs0 + kKeys * S::kRow + 4 * g);
                 f[1] = lds(vs0 + kKeys * S::kRow + 4 * g + 32);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int e = static_cast<int>(__float_as_uint(f[h]) >> 23) & 0xff;
-                    ex = max(ex, e == 255 ? 0 : min(e, 253));
-                }
+                size[0] = Product::size_of(f[0]);
+                size[1] = Product::size_of(f[1]);
             }
-            bool grow = kQuantised && ex > unit_e;
+            float y[kOct][4];                       // scores less their references
+            auto less = [&]() {
+#pragma unroll
+                for (int n = 0; n < kOct; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        y[n][e] = s[n][e] - m[n][e & 1];
+                        if constexpr (kQuantised) y[n][e] -= pe[n][e & 1];
+                    }
+            };
+            less();
+            bool grow = false;
 #pragma unroll
             for (int n = 0; n < kOct; ++n)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) grow = grow || fmaxf(s[n][e], s[n][e + 2]) > m[n][e] + kSlack;
+                for (int e = 0; e < 2; ++e)
+                    grow = grow || (kQuantised ? fmaxf(y[n][e] + size[0], y[n][e + 2] + size[1]) : fmaxf(y[n][e], y[n][e + 2])) > kSlack;
             if (__any_sync(kFull, grow)) {
-                float b = 1.f;
-                if constexpr (kQuantised) {
-                    ex = max(unit_e, __reduce_max_sync(kFull, ex));
-                    if (ex > unit_e) b = ex - unit_e > 126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 - (ex - unit_e)) << 23);
-                    unit_e = ex;
-                }
 #pragma unroll
                 for (int n = 0; n < kOct; ++n) {
                     float a[2];
@@ -480,21 +483,29 @@ __global__ void __launch_bounds__(kThreads, Shape<kKind, D, kOct>::kCtas) gdn_at
                         float mx = fmaxf(s[n][e], s[n][e + 2]);
 #pragma unroll
                         for (int q = 4; q < 32; q <<= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, q));
-                        const float now = mx > m[n][e] + kSlack ? mx - kLift : m[n][e];
-                        a[e] = m[n][e] == now ? 1.f : ex2(m[n][e] - now);
-                        m[n][e] = now;
+                        if constexpr (kQuantised) {
+                            const float now = fmaxf(m[n][e], mx);
+                            float top = fmaxf(s[n][e] - now + size[0], s[n][e + 2] - now + size[1]);
+#pragma unroll
+                            for (int q = 4; q < 32; q <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, q));
+                            a[e] = Product::move(m[n][e], pe[n][e], now, top, kLift, kSlack);
+                        } else {
+                            const float now = mx > m[n][e] + kSlack ? mx - kLift : m[n][e];
+                            a[e] = m[n][e] == now ? 1.f : ex2(m[n][e] - now);
+                            m[n][e] = now;
+                        }
                         l[n][e] *= a[e];
                     }
 #pragma unroll
                     for (int dn = 0; dn < D / 16; ++dn)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) o[dn][n][e] *= a[e & 1] * b;
+                        for (int e = 0; e < 4; ++e) o[dn][n][e] *= a[e & 1];
                 }
+                less();
             }
             if constexpr (kQuantised) {
-                const float unit_inv = __uint_as_float(static_cast<uint32_t>(254 - unit_e) << 23);
-                f[0] *= unit_inv;
-                f[1] *= unit_inv;
+                f[0] *= Product::kUnitInv;
+                f[1] *= Product::kUnitInv;
             }
             uint32_t pf[kOct][2], pl[kOct][2];      // right operand: k is the key, n the row
 #pragma unroll
@@ -504,12 +515,11 @@ __global__ void __launch_bounds__(kThreads, Shape<kKind, D, kOct>::kCtas) gdn_at
                     float w2[2];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float sc = s[n][2 * h + e];
-                        w2[e] = ex2(sc - m[n][e]);
+                        w2[e] = ex2(y[n][2 * h + e]);
                         l[n][e] += w2[e];
                         if constexpr (kQuantised) {                 // (a value that a row does not see may have the scale NaN)
                             w2[e] *= f[h];
-                            if (!plain) w2[e] = sc == -INFINITY ? 0.f : w2[e];
+                            if (!plain) w2[e] = s[n][2 * h + e] == -INFINITY ? 0.f : w2[e];
                         }
                     }
                     if constexpr (kB) {
@@ -585,6 +595,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kKind, D, kOct>::kCtas) gdn_at
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
                 for (int q = 4; q < 32; q <<= 1) l[n][e] += __shfl_xor_sync(kFull, l[n][e], q);
+                if constexpr (kQuantised) l[n][e] *= ex2(pe[n][e]);         // (relative to m alone)
                 if (g == 0) {
                     row_m[warp][8 * n + 2 * tq + e] = m[n][e];
                     row_l[warp][8 * n + 2 * tq + e] = l[n][e];
@@ -615,8 +626,9 @@ __global__ void __launch_bounds__(kThreads, Shape<kKind, D, kOct>::kCtas) gdn_at
         for (int n = 0; n < kOct; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                a[n][e] = ex2(m[n][e] - top_of(8 * n + 2 * tq + e));
-                if constexpr (kQuantised) a[n][e] *= __uint_as_float(static_cast<uint32_t>(unit_e) << 23);
+                a[n][e] = m[n][e] - top_of(8 * n + 2 * tq + e);
+                if constexpr (kQuantised) a[n][e] += pe[n][e] + Product::kUnitLog2;
+                a[n][e] = ex2(a[n][e]);
             }
 #pragma unroll
         for (int n = 0; n < kOct; ++n)

@@ -1,0 +1,172 @@
+"""gdn_attn_decode where sizes differ by many powers of two: values' scales that
+a row does not see or hardly weighs, loud elements of q, scores of any finite
+size, weights far below the largest.  Against the definition in 64 bits.
+
+The bound, elementwise, with p_j the softmax's weights and A = sum_j p_j |v_j|:
+  2^-8 |o|                  the output's rounding to bf16, half a step
+  sum_j p_j d_j (|v_j| + A) an error d_j of score j acts on the sum and on its divisor:
+      D 2^-22 B_j               products of the head dim added up in FP32 (B_j = sum |q k| scale)
+      2^-21 (1 + |s_j| + |s|)   its rounding and its difference from the reference (s: the row's largest score)
+      2^-31 Q K_j               q's elements below 2^-24 of its largest, Q; K_j = sum |k| scale
+  2 A (w + (L / 8 + 64) 2^-22)  a weight's rounding: w = 2^-16 for two bf16 parts, 2^-11 for fp16; FP32 sums over L
+                            positions in parts
+  1.25 2^-31 T C            weights times scales have a step of 2^-22 at most (half of it is off, and 2^-25 before that) where
+                            the row's largest, T = max p_j |scale_j|, is 2^8, or 2^-24 where it is 2^6; C = sum_j |code_j|
+  A 2^-19                   the gate's exponential and division, the division by the sum
+"""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+import gated_deltanet_linear_sm_gb300 as gdn
+from tests import kv_ref as ref
+from tests.test_gpu_kv import BOTH, KINDS, Case
+
+pytestmark = pytest.mark.gpu
+SMALL = ["e4m3", "int8"]
+
+
+def _places(c, i):
+    """Pages and rows of all positions of sequence i."""
+    x = torch.arange(c.past[i] + c.n[i])
+    return c.table[i].long()[x // c.page].to(c.dev), (x % c.page).to(c.dev)
+
+
+def _bits(t):
+    return t.view(torch.int8) if t.dtype.itemsize == 1 else t
+
+
+def _put(c, which, i, x, value):
+    """Row(s) at position(s) x of sequence i become `value` (codes of an 8-bit cache)."""
+    pg, row = _places(c, i)
+    cache = {"k": c.k, "v": c.v}[which]
+    _bits(cache)[pg[x], row[x]] = _bits(value.to(cache.dtype))
+
+
+def check(c, window=0, scale=None):
+    D = c.q.shape[2]
+    scale = D ** -0.5 if scale is None else scale
+    w = 2.0 ** -16 if c.kind == "bf16" else 2.0 ** -11
+    G = c.k.shape[2]
+    worst = 0.0
+    for i, (p, m) in enumerate(zip(c.past, c.n)):
+        pg, row = (t.cpu() for t in _places(c, i))
+        k, code = ref.pick(c.k.cpu(), pg, row), ref.pick(c.v.cpu(), pg, row)
+        f = torch.ones(k.shape[:2], dtype=torch.float64)
+        if c.ks is not None:
+            k, f = k * c.ks.cpu()[pg, row].double()[..., None], c.vs.cpu()[pg, row].double()
+        for t in range(m):
+            r = c.rows[int(c.cu[i]) + t]
+            x = torch.arange(p + m)
+            seen = (x <= p + t) & (x > p + t - window if window else x >= 0)
+            kk, cc, ff = k[seen], code[seen], f[seen]
+            q = c.q[r].double().cpu().view(G, -1, D)
+            s = torch.einsum("grd,lgd->grl", q, kk) * scale
+            B = torch.einsum("grd,lgd->grl", q.abs(), kk.abs()) * scale
+            K = kk.abs().sum(-1).t()[:, None] * scale
+            d = D * 2.0 ** -22 * B + 2.0 ** -21 * (1 + s.abs() + s.amax(-1, keepdim=True).abs()) + 2.0 ** -31 * q.abs().amax(-1, keepdim=True) * K
+            pr = torch.softmax(s, -1)
+            v = cc * ff[..., None]
+            want, A = torch.einsum("grl,lgd->grd", pr, v), torch.einsum("grl,lgd->grd", pr, v.abs())
+            bound = torch.einsum("grl,lgd->grd", pr * d, v.abs()) + A * ((pr * d).sum(-1, keepdim=True) + 2 * w + (len(kk) / 8 + 64) * 2.0 ** -21)
+            if c.kind != "bf16":
+                top = (pr * ff.abs().t()[:, None]).amax(-1, keepdim=True)
+                bound = bound + 1.25 * 2.0 ** -31 * top * cc.abs().sum(0)[:, None]
+            gate = torch.sigmoid(c.z[r].double().cpu()).view(want.shape) if c.z is not None else 1.0
+            want, bound = want * gate, (bound + 2.0 ** -19 * A) * gate
+            bound = bound + 2.0 ** -8 * want.abs() + 2.0 ** -133
+            off = (c.out[r].double().cpu().view(want.shape) - want).abs() / bound
+            assert bool((off <= 1).all()), (i, t, float(off.nan_to_num(math.inf).max()))
+            worst = max(worst, float(off.max()))
+    return worst
+
+
+def _even_scales(c, size=2.0 ** -5):
+    """Values' scales within a factor of two, wherever there is one."""
+    live = ~torch.isnan(c.vs)
+    g = torch.Generator(device=c.dev).manual_seed(3)
+    c.vs[live] = size * (1 + torch.rand(int(live.sum()), generator=g, device=c.dev))
+
+
+# ---- values' scales that a row does not see, or hardly weighs ------------------------------------
+
+
+@pytest.mark.parametrize("kind", SMALL)
+@pytest.mark.parametrize("log2", [20, 32, 60, 120])
+@BOTH
+def test_a_huge_value_that_a_row_does_not_see(cuda_device, kind, log2, wide):
+    """The last drafted token's value, one just below a window, and one that the window leaves to the first token alone."""
+    window = 101
+    c = Case(cuda_device, [61, 200, 300, 0], [4, 3, 2, 2], 8 * wide, 2, 128, kind, page=16, seed=log2)
+    _even_scales(c)
+    for i, x in ((0, 64), (1, 98), (2, 200), (3, 1)):
+        pg, row = _places(c, i)
+        c.vs[pg[x], row[x]] *= 2.0 ** log2
+    c.run(window=window)
+    assert int(c.status) == 0
+    check(c, window)
+
+
+def _along(c, size):
+    """Scores `size` [positions] (natural units) for every row: q of ones, equal elements in a key."""
+    D = c.q.shape[2]
+    c.q.fill_(1.0)
+    for i in range(len(c.n)):
+        pg, row = _places(c, i)
+        k = size[:len(pg)].to(c.dev)[:, None].expand(-1, c.k.shape[2]) / D ** 0.5
+        if c.ks is None:
+            c.k[pg, row] = k[..., None].expand(-1, -1, D).to(c.k.dtype)
+        else:
+            _bits(c.k)[pg, row] = _bits((k.sign() * 64)[..., None].expand(-1, -1, D).to(c.k.dtype))
+            c.ks[pg, row] = (k.abs() / 64).float()
+
+
+@pytest.mark.parametrize("kind", SMALL)
+@pytest.mark.parametrize("order", ["first", "middle", "rising"])
+@BOTH
+def test_huge_values_of_no_weight(cuda_device, kind, order, wide):
+    """Values 2^40 times the others under weights of e^-60, and values 2^60 times the others from where scores have risen by hundreds."""
+    L = 700
+    c = Case(cuda_device, [L - 1, 90], [1, 2], 8 * wide, 2, 128, kind, page=16, seed=1)
+    _even_scales(c)
+    size = torch.zeros(L + 1)
+    if order == "rising":
+        size = torch.linspace(0, 400, L + 1)
+    else:
+        size[5 if order == "first" else 77] = -60.0
+    _along(c, size)
+    for i in range(2):
+        pg, row = _places(c, i)
+        for x in [5] if order == "first" else [77] if order == "middle" else range(0, 16):
+            c.vs[pg[x], row[x]] *= 2.0 ** (60 if order == "rising" else 40)
+    c.run()
+    check(c)
+
+
+@pytest.mark.parametrize("kind", SMALL)
+@pytest.mark.parametrize("size", [2.0 ** -70, 2.0 ** -30, 2.0 ** 30, 2.0 ** 100])
+@BOTH
+def test_values_of_any_size(cuda_device, kind, size, wide):
+    c = Case(cuda_device, [300, 4000], [2, 1], 8 * wide, 2, 128, kind, page=16, seed=2)
+    _even_scales(c, size)
+    c.run()
+    check(c)
+
+
+@pytest.mark.parametrize("kind", SMALL)
+@BOTH
+def test_rows_of_zeros_before_values(cuda_device, kind, wide):
+    """Zeros have the least scale, 2^-100; values of ordinary and of large scales follow, with less weight and with more."""
+    for rise in (0.0, 30.0, -30.0):
+        c = Case(cuda_device, [900], [2], 8 * wide, 2, 128, kind, page=16, seed=4)
+        _even_scales(c)
+        _along(c, torch.cat([torch.zeros(300), torch.full((602,), rise)]))
+        pg, row = _places(c, 0)
+        _bits(c.v)[pg[:300], row[:300]] = 0
+        c.vs[pg[:300], row[:300]] = 2.0 ** -100
+        c.vs[pg[600:], row[600:]] *= 2.0 ** 20
+        c.run()
+        check(c)
