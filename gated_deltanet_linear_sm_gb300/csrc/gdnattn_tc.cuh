@@ -28,8 +28,9 @@
 //
 // bf16: weights as two bf16 parts (16 significant bits), two products.  fp16: one.  e4m3: the
 // codes are operands as they are; q is the sum of two e4m3 parts (its 8 bits), a weight times the
-// value's scale is an fp16 number cut into four e5m2 ones (3 bits each, exactly), two of them in
-// the columns of one product.
+// value's scale is an fp16 number cut into four e5m2 ones of 3 bits each.  e5m2 has fp16's largest value, but no
+// bits below 2^-16: the third and fourth part are of 64 times the rest, in columns of their own that
+// the output adds up divided by that, so the four hold the number up to 2^-23, 2^-31 of the row's largest.
 #pragma once
 
 #include <cuda.h>
@@ -237,11 +238,17 @@ __device__ __forceinline__ void arrive_when_copied(unsigned long long* b) {
 // 16-byte chunk c of row r of a tile of 128-byte rows (SWIZZLE_128B)
 __device__ __forceinline__ uint32_t unit16(int r, int c) { return static_cast<uint32_t>(r * 128 + ((c ^ (r & 7)) << 4)); }
 
-// fp16 pairs as e5m2 parts: the upper byte of an fp16 number is the e5m2 one below it
+// fp16 pairs as e5m2 parts: the upper byte of an fp16 number is the e5m2 one below it (towards zero).  Of a number
+// below 2^15 two parts leave less than 2^9, which times 64 is below 2^15 again.
+constexpr float kUp = 64.f;
 __device__ __forceinline__ uint32_t upper_bytes(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7531); }
 __device__ __forceinline__ uint32_t rest_of(uint32_t h) {               // exact
     const uint32_t hi = h & 0xff00ff00u;
     const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&hi));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t times_up(uint32_t h) {              // exact
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&h), __floats2half2_rn(kUp, kUp));
     return *reinterpret_cast<const uint32_t*>(&r);
 }
 
@@ -1019,12 +1026,18 @@ __global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(
                             if constexpr (kB) st16(a + kTile * 128, w2[i][0], w2[i][1], w2[i][2], w2[i][3]);
                         } else {
 #pragma unroll
-                            for (int b8 = 0; b8 < 4; ++b8) {        // the four parts in columns 0 | 1, then 2 | 3
-                                st8(pbuf + (b8 >> 1) * kTile * 128 + unit16(key, 4 * (b8 & 1) + (c >> 1)) + 8 * (c & 1), upper_bytes(w[i][0], w[i][1]),
+                            for (int b8 = 0; b8 < 4; ++b8) {        // the four parts in columns 0 | 2, then 1 | 3
+                                st8(pbuf + (b8 & 1) * kTile * 128 + unit16(key, 4 * (b8 >> 1) + (c >> 1)) + 8 * (c & 1), upper_bytes(w[i][0], w[i][1]),
                                     upper_bytes(w[i][2], w[i][3]));
                                 if (b8 < 3)
 #pragma unroll
                                     for (int e = 0; e < 4; ++e) w[i][e] = rest_of(w[i][e]);
+                                if (b8 == 1)
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) w[i][e] = times_up(w[i][e]);
+                                if (b8 == 2)                        // (the last one is rounded: half of its last bit)
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) w[i][e] += 0x00800080u;
                             }
                         }
                     }
@@ -1070,7 +1083,7 @@ __global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(
                 tm_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    y[e] = kQ8 ? __uint_as_float(y1[e]) + __uint_as_float(y2[e]) : __uint_as_float(y1[e]);
+                    y[e] = kQ8 ? fmaf(__uint_as_float(y2[e]), 1.f / kUp, __uint_as_float(y1[e])) : __uint_as_float(y1[e]);
                     y[e] *= ms.inv[c0 + e];
                 }
                 if (dcol >= D) continue;

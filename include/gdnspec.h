@@ -763,11 +763,12 @@ GDNSPEC_API gdn_status gdn_kv_read(
  *
  * Scores, the softmax's maximum and sum, and the output are held in FP32; the weights are
  * rounded to 16 significant bits for a bf16 cache (two bf16 parts) and to 11 for the others
- * (fp16), in an 8-bit cache weight times scale of the value: a row's largest product with the
- * values that it sees sets the range, and scales of 2^-74 and more have all bits.  The positions of a batch are cut evenly among the CTAs and the parts joined in
- * order, so equal calls give equal results; how a sequence is cut depends on the others'
- * lengths, by rounding in FP32.  Bad device data: q_len > max_T sets GDN_FLAG_QLEN, the rest
- * as for gdn_kv_write, except that any row of a sequence outside [0, num_tokens) skips the
+ * (fp16), or to half of 2^-30 of the row's largest where that is more.  In an 8-bit cache that
+ * is weight times scale of the value (scales of 2^-74 and more have all bits).  The positions of
+ * a batch are cut evenly among the CTAs and the parts joined in order, so equal calls give equal
+ * results; how a sequence is cut depends on the others' lengths, by rounding in FP32.  Bad device
+ * data: q_len > max_T sets GDN_FLAG_QLEN, the rest as for gdn_kv_write, except that any row of a
+ * sequence outside [0, num_tokens) skips the
  * sequence.  An infinity or NaN in k or v spoils the tokens that see it, in q its own row.  (In an
  * 8-bit cache that is a scale; a GDN_E4M3 code that is NaN, which gdn_kv_write never makes, may spoil
  * other tokens of its sequence too.)

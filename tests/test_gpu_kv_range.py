@@ -170,3 +170,25 @@ def test_rows_of_zeros_before_values(cuda_device, kind, wide):
         c.vs[pg[600:], row[600:]] *= 2.0 ** 20
         c.run()
         check(c)
+
+
+# ---- weights far below the largest ---------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("L,share", [(8192, 0.9), (8192, 0.98), (100003, 0.9)])
+@BOTH
+def test_many_small_weights_beside_a_large_one(cuda_device, kind, L, share, wide):
+    """One position with a value of zeros takes most of the weight; all others share the rest, their values of one sign."""
+    c = Case(cuda_device, [L - 1], [1], 8 * wide, 2, 128, kind, page=64, seed=5)
+    if c.vs is not None:
+        c.vs[~torch.isnan(c.vs)] = 2.0 ** -5
+    size = torch.zeros(L)
+    size[20] = math.log(share / (1 - share) * (L - 1))
+    _along(c, size)
+    pg, row = _places(c, 0)
+    live = _bits(c.v)[pg, row]
+    _bits(c.v)[pg, row] = live.abs() if c.vs is None else live & 0x7F if kind == "e4m3" else live.abs()
+    _bits(c.v)[pg[20], row[20]] = 0
+    c.run()
+    check(c)
