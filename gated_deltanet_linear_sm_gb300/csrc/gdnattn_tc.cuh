@@ -27,7 +27,8 @@
 // and with short sequences a unit's own chain (first tile, its edge, output: 11 us with nothing beside it).
 //
 // bf16: weights as two bf16 parts (16 significant bits), two products.  fp16: one.  e4m3: the
-// codes are operands as they are; q is the sum of two e4m3 parts (its 8 bits), a weight times the
+// codes are operands as they are; q is the sum of three e5m2 parts (3 bits each, with its signs its 8 bits; the row's
+// largest element is 2^14 to 2^15, so elements down to 2^-24 of it are exact), a weight times the
 // value's scale is an fp16 number cut into four e5m2 ones of 3 bits each.  e5m2 has fp16's largest value, but no
 // bits below 2^-16: the third and fourth part are of 64 times the rest, in columns of their own that
 // the output adds up divided by that, so the four hold the number up to 2^-23, 2^-31 of the row's largest.
@@ -90,9 +91,9 @@ struct Lay {
     static constexpr int kPAtoms = kKind == kF16 ? 1 : 2;
     static constexpr int kP = kPAtoms * kTile * 128;
     static constexpr int kQTerm = (kQuantised ? (D + 127) / 128 : D / 64) * kRowsT * 128;
-    static constexpr int kQ = kQTerm * (kQuantised ? 2 : 1);
+    static constexpr int kQ = kQTerm * (kQuantised ? 3 : 1);
     static constexpr int kBudget = 198 * 1024;
-    static constexpr int kQs = kQ <= 16 * 1024 ? 2 : 1;                     // buffers of q
+    static constexpr int kQs = kQTerm <= (kQuantised ? 8 : 16) * 1024 ? 2 : 1;  // buffers of q
     static constexpr int kRing0 = (kBudget - kP - kQs * kQ) / kItem;
     static constexpr int kRing = kRing0 > 9 ? 9 : kRing0;
     // (the weights behind the ring: the products of a head dim of 64 read 64 rows of V^T more than there are, the next item's)
@@ -542,7 +543,8 @@ __global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(
                 }
             }
             if (more && j == 0) {
-                // q: bf16 as it is; else its row's largest element becomes 1 to 2 (fp16), 128 to 256 (e4m3 parts)
+                // q: bf16 as it is; else its row's largest element becomes 2^14 to 2^15 (in fp16 elements down to 2^-31
+                // of that are exact, in e5m2 parts to 2^-24)
                 const int rr = d.tile * kRowsT + qr, tok = rr / p.ratio;
                 const bool has = qr < d.rows;
                 const uint4* src = reinterpret_cast<const uint4*>(p.q);
@@ -563,13 +565,13 @@ __global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(
                         for (int e = 0; e < 4; ++e) big = max(big, max(w4[e] & 0x7fffu, (w4[e] >> 16) & 0x7fffu));
                     }
                     big = max(big, __shfl_xor_sync(kFull, big, 1));
-                    constexpr int kTop = kQ8 ? 7 : 0;
-                    const int e = min(max(static_cast<int>(big >> 7), 1 + kTop), kTop ? 254 : 253);
+                    constexpr int kTop = 14;
+                    const int e = max(static_cast<int>(big >> 7), 1 + kTop);
                     if ((big >> 7) != 255) {
                         down = __uint_as_float(static_cast<uint32_t>(254 + kTop - e) << 23);
                         up = __uint_as_float(static_cast<uint32_t>(e - kTop) << 23);
                     } else if constexpr (kQ8) {
-                        up = __uint_as_float(0x7fc00000u);      // (e4m3 has no infinity: the row's scores are NaN)
+                        up = __uint_as_float(0x7fc00000u);      // (the parts saturate: the row's scores are NaN)
                     }
                 }
                 const int qb = (u - 1) % L::kQs;
@@ -592,20 +594,22 @@ __global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(
                         if constexpr (kKind == kF16) {
                             st16(q0 + (c >> 3) * kRowsT * 128 + unit16(qr, c & 7), pack_h(f[0], f[1]), pack_h(f[2], f[3]), pack_h(f[4], f[5]), pack_h(f[6], f[7]));
                         } else {
-                            // two parts: the nearest e4m3 value and that of what is left
-                            uint32_t hi[2] = {0, 0}, lo[2] = {0, 0};
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * e], f[2 * e + 1]), __NV_SATFINITE, __NV_E4M3);
-                                const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3);
-                                const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-                                const __nv_fp8x2_storage_t l = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * e] - hf.x, f[2 * e + 1] - hf.y), __NV_SATFINITE, __NV_E4M3);
-                                hi[e >> 1] |= static_cast<uint32_t>(h) << (16 * (e & 1));
-                                lo[e >> 1] |= static_cast<uint32_t>(l) << (16 * (e & 1));
-                            }
+                            // three parts, each the nearest e5m2 value of what is left
                             const uint32_t a = q0 + (c >> 4) * kRowsT * 128 + unit16(qr, (c >> 1) & 7) + 8 * (c & 1);
-                            st8(a, hi[0], hi[1]);
-                            st8(a + L::kQTerm, lo[0], lo[1]);
+#pragma unroll
+                            for (int term = 0; term < 3; ++term) {
+                                uint32_t part[2] = {0, 0};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * e], f[2 * e + 1]), __NV_SATFINITE, __NV_E5M2);
+                                    const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(h, __NV_E5M2);
+                                    const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+                                    f[2 * e] -= hf.x;
+                                    f[2 * e + 1] -= hf.y;
+                                    part[e >> 1] |= static_cast<uint32_t>(h) << (16 * (e & 1));
+                                }
+                                st8(a + term * L::kQTerm, part[0], part[1]);
+                            }
                         }
                     }
                 }
@@ -704,7 +708,7 @@ __global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(
         };
         constexpr uint32_t kS16 = (1u << 4) | (kB ? (1u << 7) | (1u << 10) : 0u) | (static_cast<uint32_t>(kRowsT >> 3) << 17) | (8u << 24);
         constexpr uint32_t kMn = (1u << 15) | (1u << 16);
-        constexpr uint32_t kIS = kQ8 ? (1u << 4) | (static_cast<uint32_t>(kRowsT >> 3) << 17) | (8u << 24) : kS16;
+        constexpr uint32_t kIS = kQ8 ? (1u << 4) | (1u << 10) | (static_cast<uint32_t>(kRowsT >> 3) << 17) | (8u << 24) : kS16;
         constexpr uint32_t kIO = kQ8 ? (1u << 4) | (1u << 10) | kMn | (16u << 17) | (8u << 24) : kS16 | kMn;
         int t = 0, fixes = 0;
         int pv_unit = 0;
@@ -757,7 +761,7 @@ __global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(
                     const uint32_t k = ring + slot * L::kItem, q = qbuf + qb * L::kQ + b * L::kAtoms * kRowsT * 128;
                     const int steps = (min(128, D - 128 * b)) * L::kBytes / 32;
 #pragma unroll
-                    for (int term = 0; term < (kQ8 ? 2 : 1); ++term)
+                    for (int term = 0; term < (kQ8 ? 3 : 1); ++term)
 #pragma unroll
                         for (int ks = 0; ks < steps; ++ks)
                             mma_ss<kQ8>(s, desc_sw128(k + (ks >> 2) * kTile * 128 + (ks & 3) * 32),

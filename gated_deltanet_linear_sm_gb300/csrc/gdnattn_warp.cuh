@@ -304,10 +304,12 @@ __global__ void __launch_bounds__(kThreads, Shape<kKind, D, kOct>::kCtas) gdn_at
             if constexpr (!kB) {
 #pragma unroll
                 for (int o = kPer / 2; o > 0; o >>= 1) big = max(big, __shfl_xor_sync(kFull, big, o, kPer));
-                const int e = min(max(static_cast<int>(big >> 7), 1), 253);     // exponent: the row's largest becomes 1 to 2
+                // exponent: the row's largest becomes 2^14 to 2^15, so that elements down to 2^-31 of it are exact
+                constexpr int kTop = 14;
+                const int e = max(static_cast<int>(big >> 7), 1 + kTop);
                 if ((big >> 7) != 255) {                                        // (an infinity or NaN stays what it is)
-                    down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
-                    up = __uint_as_float(static_cast<uint32_t>(e) << 23);
+                    down = __uint_as_float(static_cast<uint32_t>(254 + kTop - e) << 23);
+                    up = __uint_as_float(static_cast<uint32_t>(e - kTop) << 23);
                 }
             }
             if (j == 0 && in) {

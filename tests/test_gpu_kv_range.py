@@ -192,3 +192,20 @@ def test_many_small_weights_beside_a_large_one(cuda_device, kind, L, share, wide
     _bits(c.v)[pg[20], row[20]] = 0
     c.run()
     check(c)
+
+
+# ---- q ---------------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("log2", [7, 11, 16, 22])
+@BOTH
+def test_a_loud_element_of_q(cuda_device, kind, log2, wide):
+    """One element of each query is 2^7 to 2^22 times the others, where the keys have nothing."""
+    c = Case(cuda_device, [61, 500], [2, 3], 8 * wide, 2, 128, kind, page=16, seed=log2)
+    c.q[..., 3] = 2.0 ** log2 * 1.5
+    for i in range(2):
+        pg, row = _places(c, i)
+        _bits(c.k)[pg, row, :, 3] = 0
+    c.run()
+    check(c)
