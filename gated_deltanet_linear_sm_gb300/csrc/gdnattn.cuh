@@ -5,6 +5,8 @@
 
 #include <cuda_fp8.h>
 
+#include <cfloat>
+
 #include "gdnkv.h"
 
 namespace gdn_attn {
@@ -12,6 +14,9 @@ namespace gdn_attn {
 using namespace gdn_common;
 using namespace gdn_kv;
 
+// The reference of a row without a score yet: every finite score is above it or equal, and it is a
+// reference like any other for one that is equal.
+constexpr float kUnset = -FLT_MAX;
 constexpr int kKeys = 16;               // a sequence's first position is rounded down to a multiple of this
 
 // What a kernel cuts by: G::kThreads that scan, G::kPer sequences each at a time, G::kBlock keys of the line,

@@ -79,7 +79,6 @@ struct Cut {                            // (gdnattn.cuh)
 // weights are 2^(s - m) with m = (largest score when it was set) - kLift; m moves when a weight would
 // pass 2^kSlack.  8 bits: 2^(s - m - e), and e keeps weight times scale there (gdnattn.cuh: Product)
 constexpr float kLift = 8.f, kSlack = 14.f;
-constexpr float kUnset = -1e30f;        // m of a row without a score yet
 
 template <int kKind, int D>
 struct Lay {
@@ -827,6 +826,8 @@ __global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(
             const int chunks = tc.chunks;
             const int all_lo = p.window > 0 ? max(0, d.past + d.n - p.window) : 0, all_hi = d.past + 1;
             const float* const qs = ms.q_scale[u % kUnits];
+            // (a zero that the compiler does not know: it makes one instruction of a product and a sum on pairs)
+            const u64 nothing = *reinterpret_cast<const u64*>(ms.zero);
             u64 l[kMine][4];
 #pragma unroll
             for (int i = 0; i < kMine; ++i)
@@ -861,8 +862,10 @@ __global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(
                         u64 f0 = dup2(p.scale), f1 = f0;
                         if constexpr (!kB) f0 = pk2(f.x, f.y), f1 = pk2(f.z, f.w);
                         if constexpr (kQ8) f0 = fmul2(f0, dup2(ks)), f1 = fmul2(f1, dup2(ks));
-                        u64 a = ffma2(raw2(y[4 * h], y[4 * h + 1]), f0, pk2(r.x, r.y));
-                        u64 b = ffma2(raw2(y[4 * h + 2], y[4 * h + 3]), f1, pk2(r.z, r.w));
+                        // (the product rounds before the reference is taken off: that came from such products, and one step
+                        // would leave half a last bit of the score between the two, 2^32 for a score of 10^9)
+                        u64 a = add2(ffma2(raw2(y[4 * h], y[4 * h + 1]), f0, nothing), pk2(r.x, r.y));
+                        u64 b = add2(ffma2(raw2(y[4 * h + 2], y[4 * h + 3]), f1, nothing), pk2(r.z, r.w));
                         if constexpr (kQ8) {
                             const float4 e4 = *reinterpret_cast<const float4*>(shift + c0 + 4 * h);
                             a = add2(a, pk2(e4.x, e4.y));

@@ -16,7 +16,7 @@
 // warps of an SM that the accumulators leave room for (64 x 3 tokens x window 1024, 18 rows, int8 38 us: 950 instructions for
 // 16 keys, 0.4 a cycle and scheduler); with short sequences a unit's chain of start and end, about 2.5 us.
 //
-// A row's reference m is -1e30 until it has a score; it moves when a score passes it by more than
+// A row's reference m is kUnset until it has a score; it moves when a score passes it by more than
 // 2^kSlack, and only then do the lanes compare: a block's vote is one instruction.  kLift keeps weights
 // far from the end of fp16's range.
 //
@@ -37,7 +37,7 @@ using namespace gdn_attn;
 
 enum Kind { kBf16, kF16, kE4m3, kI8 };
 
-constexpr float kLift = 6.f, kSlack = 14.f, kUnset = -1e30f;
+constexpr float kLift = 6.f, kSlack = 14.f;
 
 // ---- instructions -----------------------------------------------------------------------------
 
@@ -431,8 +431,9 @@ __global__ void __launch_bounds__(kThreads, Shape<kKind, D, kOct>::kCtas) gdn_at
                 for (int n = 0; n < kOct; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const float x = (c0[n][e] + c1[n][e]) * qs[n][e & 1];
-                        s[n][e] = kQuantised ? x * f[e >> 1] : x;
+                        // (rounded before the reference is taken off, which comes from such scores)
+                        const float x = __fmul_rn(c0[n][e] + c1[n][e], qs[n][e & 1]);
+                        s[n][e] = kQuantised ? __fmul_rn(x, f[e >> 1]) : x;
                     }
             }
             const int x0 = d.key0 + (warp + (i >> 1) * kWarps) * kKeys;

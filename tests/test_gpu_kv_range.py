@@ -209,3 +209,38 @@ def test_a_loud_element_of_q(cuda_device, kind, log2, wide):
         _bits(c.k)[pg, row, :, 3] = 0
     c.run()
     check(c)
+
+
+# ---- scores --------------------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("score", [-1e34, -3e31, -1e9, 1e9, 1e34])
+@BOTH
+def test_scores_of_any_size(cuda_device, kind, score, wide):
+    """Equal scores, far below or above zero: the output is the mean of the values, whatever their scales."""
+    D = 128
+    for factor in (1.0, 2.0 ** 20):
+        c = Case(cuda_device, [0, 40, 300], [1, 3, 1], 8 * wide, 2, D, kind, page=16, seed=6)
+        if c.vs is not None:
+            _even_scales(c, factor * 2.0 ** -5)
+        size = 32768.0
+        c.q.fill_(score / size / D ** 0.5)
+        for i in range(3):
+            pg, row = _places(c, i)
+            if c.ks is None:
+                c.k[pg, row] = size
+            else:
+                _bits(c.k)[pg, row] = _bits(torch.full((1,), 64.0, device=c.dev).to(c.k.dtype))
+                c.ks[pg, row] = size / 64
+        c.run()
+        for i, (p, n) in enumerate(zip(c.past, c.n)):
+            pg, row = (t.cpu() for t in _places(c, i))
+            v = ref.pick(c.v.cpu(), pg, row)
+            if c.vs is not None:
+                v = v * c.vs.cpu()[pg, row].double()[..., None]
+            for t in range(n):
+                want, A = v[:p + t + 1].mean(0), v[:p + t + 1].abs().mean(0)
+                got = c.out[int(c.cu[i]) + t].double().cpu().view(2, -1, D)
+                # (a weight's rounding twice over; FP32 sums; the output's half step)
+                assert bool(((got - want[:, None]).abs() <= 2.0 ** -8 * want.abs()[:, None] + 2.0 ** -9 * A[:, None]).all()), (i, t)
