@@ -423,8 +423,8 @@ __global__ void __launch_bounds__(kJThreads) gdn_attn_join_kernel(const AttnPara
 #pragma unroll
                         for (int e = 0; e < kV; e += 2) {
                             const float2 y = ld(reinterpret_cast<const float2*>(src + 32 * e + 2 * lane));
-                            x[e] += aq == 0.f ? 0.f : aq * y.x;
-                            x[e + 1] += aq == 0.f ? 0.f : aq * y.y;
+                            x[e] += aq * y.x;                       // (a factor of 0 too: what is no number stays none)
+                            x[e + 1] += aq * y.y;
                         }
                     }
                 }

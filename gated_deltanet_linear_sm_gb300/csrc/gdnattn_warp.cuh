@@ -642,7 +642,8 @@ __global__ void __launch_bounds__(kThreads, Shape<kKind, D, kOct>::kCtas) gdn_at
                 float* const to = ow + (warp * kRowsU + row) * D;
 #pragma unroll
                 for (int dn = 0; dn < D / 16; ++dn) {
-                    const float x = a[n][e] == 0.f ? 0.f : o[dn][n][e] * a[n][e], y = a[n][e] == 0.f ? 0.f : o[dn][n][e + 2] * a[n][e];
+                    // (a factor of 0 is a product too: what is no number stays none, whichever warp took it)
+                    const float x = o[dn][n][e] * a[n][e], y = o[dn][n][e + 2] * a[n][e];
                     // (columns exchanged by the row, so that the rows of a store lie in different banks)
                     if constexpr (kQuantised) {
                         *reinterpret_cast<float2*>(to + ((16 * dn + 2 * g) ^ ((row & 2) << 3))) = make_float2(x, y);

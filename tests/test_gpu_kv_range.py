@@ -244,3 +244,30 @@ def test_scores_of_any_size(cuda_device, kind, score, wide):
                 got = c.out[int(c.cu[i]) + t].double().cpu().view(2, -1, D)
                 # (a weight's rounding twice over; FP32 sums; the output's half step)
                 assert bool(((got - want[:, None]).abs() <= 2.0 ** -8 * want.abs()[:, None] + 2.0 ** -9 * A[:, None]).all()), (i, t)
+
+
+# ---- what is no number, where its weight is 0 in FP32 ----------------------------------------------------
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+@pytest.mark.parametrize("x", [0, 21, 700, 2000])
+@BOTH
+def test_a_value_that_is_no_number_at_scores_far_below(cuda_device, kind, bad, x, wide):
+    """Scores rise by 900 along the sequence; whoever sees the value is spoiled, whichever warp or CTA took it."""
+    L = 6000
+    c = Case(cuda_device, [L, 300], [1, 2], 8 * wide, 2, 128, kind, page=16, seed=8)
+    _along(c, torch.linspace(0, 900, L + 2))
+    clean = c.run().double().cpu()
+    pg, row = _places(c, 0)
+    if c.vs is None:
+        c.v[pg[x], row[x], 1, 5] = bad
+    else:
+        c.vs[pg[x], row[x], 1] = bad
+    spoiled = torch.zeros(3, 8 * wide, 128, dtype=torch.bool)
+    spoiled[0, 4 * wide:, slice(5, 6) if c.vs is None else slice(None)] = True
+    out = c.run().double().cpu()
+    if c.vs is not None and math.isinf(bad):         # (an infinite scale times a code of 0 is NaN, times others an infinity)
+        assert not bool(torch.isfinite(out[spoiled]).any())
+    assert torch.equal(~torch.isfinite(out), spoiled)
+    assert torch.equal(out[~spoiled], clean[~spoiled])
