@@ -338,7 +338,26 @@ struct Product {
         e = next;
         return old == next ? 1.f : ex2(old - next);
     }
+    // A part's sums, kept with (m, e), are joined relative to a new m: the one that makes l 1 (as far as m's own last bit
+    // allows), whatever l is, since weights of values that are almost zero may be far above the products' reference.
+    __device__ __forceinline__ static void settle(float& m, float& e, float l) {
+        const float above = e + __log2f(l);
+        if (above > 0.f) {
+            const float now = m + above;
+            e -= now - m;
+            m = now;
+        }
+    }
+    // The factors of l and of o then, both with 2^-16, so that sums of values up to the largest FP32 number do not
+    // overflow (the joined output divides them); o's makes up for the unit.
+    __device__ __forceinline__ static float of_l(float e) { return ex2(e - kUnitLog2); }
+    __device__ __forceinline__ static float of_o(float e) { return ex2(e); }
 };
+
+// Lift and slack of the references of a bf16 cache: its weights have FP32's range, and this far below 1 sums
+// of values up to the largest stay below infinity (4 million of them in the worst case; values down to 2^-90 keep
+// their bits).
+constexpr float kLiftBf = -36.f, kSlackBf = -22.f;
 
 __device__ __forceinline__ int64_t token_row(const AttnParams& p, int i) { return p.sti ? ld(p.sti + i) : i; }
 

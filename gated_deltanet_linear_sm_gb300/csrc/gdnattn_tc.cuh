@@ -78,7 +78,7 @@ struct Cut {                            // (gdnattn.cuh)
 
 // weights are 2^(s - m) with m = (largest score when it was set) - kLift; m moves when a weight would
 // pass 2^kSlack.  8 bits: 2^(s - m - e), and e keeps weight times scale there (gdnattn.cuh: Product)
-constexpr float kLift = 8.f, kSlack = 14.f;
+constexpr float kLiftH = 8.f, kSlackH = 14.f;
 
 template <int kKind, int D>
 struct Lay {
@@ -312,6 +312,7 @@ __global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(
     constexpr int kSoft = Warps<kKind>::kSoft, kLoadWarp = Warps<kKind>::kLoad, kMmaWarp = Warps<kKind>::kMma, kLineWarp = Warps<kKind>::kLine;
     constexpr int kMine = Warps<kKind>::kMine;
     constexpr bool kQ8 = L::kQuantised, kB = kKind == kBf16;
+    constexpr float kLift = kB ? kLiftBf : kLiftH, kSlack = kB ? kSlackBf : kSlackH;
     extern __shared__ unsigned char raw_smem[];
     unsigned char* const sm = raw_smem + ((1024 - (saddr(raw_smem) & 1023)) & 1023);
     Misc<kKind>& ms = *reinterpret_cast<Misc<kKind>*>(sm + L::kOMisc);
@@ -1067,13 +1068,17 @@ __global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(
             if (soft_any(fail, parts)) break;
             fence_after();
             if (tid < kRowsT) {
-                const float of_e = kQ8 ? ex2(-ms.shift[cur][tid]) : 1.f;        // (sums relative to m alone)
-                const float sum = (ms.col[0][tid] + ms.col[1][tid] + ms.col[2][tid] + ms.col[3][tid]) * of_e, unit = kQ8 ? of_e * Product::kUnit : 1.f;
-                ms.inv[tid] = d.part >= 0 ? unit : sum == 0.f ? 0.f : unit / sum;
-                if (d.part >= 0 && tid < d.rows) {
-                    float* ml = p.ws + static_cast<int64_t>(2 * gridDim.x) * kRowsT * D + static_cast<int64_t>(d.part) * 2 * kRowsT;
-                    ml[tid] = -ms.ref[cur][tid];
-                    ml[kRowsT + tid] = sum;
+                const float sum = ms.col[0][tid] + ms.col[1][tid] + ms.col[2][tid] + ms.col[3][tid];
+                ms.inv[tid] = sum == 0.f ? 0.f : (kQ8 ? Product::kUnit : 1.f) / sum;
+                if (d.part >= 0) {
+                    float m = -ms.ref[cur][tid], e = -ms.shift[cur][tid];
+                    if constexpr (kQ8) Product::settle(m, e, sum);
+                    ms.inv[tid] = kQ8 ? Product::of_o(e) : 1.f;
+                    if (tid < d.rows) {
+                        float* ml = p.ws + static_cast<int64_t>(2 * gridDim.x) * kRowsT * D + static_cast<int64_t>(d.part) * 2 * kRowsT;
+                        ml[tid] = m;
+                        ml[kRowsT + tid] = kQ8 ? sum * Product::of_l(e) : sum;
+                    }
                 }
             }
             soft_sync(parts);

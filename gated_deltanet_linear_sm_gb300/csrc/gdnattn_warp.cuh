@@ -18,7 +18,7 @@
 //
 // A row's reference m is kUnset until it has a score; it moves when a score passes it by more than
 // 2^kSlack, and only then do the lanes compare: a block's vote is one instruction.  kLift keeps weights
-// far from the end of fp16's range.
+// far from the end of fp16's range (bf16: gdnattn.cuh).
 //
 // fp16 and 8-bit caches run on fp16 operands: codes are exact in fp16, a key's scale multiplies its score
 // and a value's scale its weight.  What has to fit fp16 is then weight times scale, so an 8-bit row has its
@@ -37,7 +37,7 @@ using namespace gdn_attn;
 
 enum Kind { kBf16, kF16, kE4m3, kI8 };
 
-constexpr float kLift = 6.f, kSlack = 14.f;
+constexpr float kLiftH = 6.f, kSlackH = 14.f;
 
 // ---- instructions -----------------------------------------------------------------------------
 
@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kKind, D, kOct>::kCtas) gdn_at
     constexpr int kRowsU = 8 * kOct;
     constexpr bool kQuantised = S::kBytes == 1;
     constexpr bool kB = kKind == kBf16;
+    constexpr float kLift = kB ? kLiftBf : kLiftH, kSlack = kB ? kSlackBf : kSlackH;
     constexpr int kSteps = D / 16;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ Line<G> line;
@@ -598,7 +599,10 @@ __global__ void __launch_bounds__(kThreads, Shape<kKind, D, kOct>::kCtas) gdn_at
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
                 for (int q = 4; q < 32; q <<= 1) l[n][e] += __shfl_xor_sync(kFull, l[n][e], q);
-                if constexpr (kQuantised) l[n][e] *= ex2(pe[n][e]);         // (relative to m alone)
+                if constexpr (kQuantised) {
+                    Product::settle(m[n][e], pe[n][e], l[n][e]);
+                    l[n][e] *= Product::of_l(pe[n][e]);
+                }
                 if (g == 0) {
                     row_m[warp][8 * n + 2 * tq + e] = m[n][e];
                     row_l[warp][8 * n + 2 * tq + e] = l[n][e];
@@ -630,8 +634,7 @@ __global__ void __launch_bounds__(kThreads, Shape<kKind, D, kOct>::kCtas) gdn_at
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 a[n][e] = m[n][e] - top_of(8 * n + 2 * tq + e);
-                if constexpr (kQuantised) a[n][e] += pe[n][e] + Product::kUnitLog2;
-                a[n][e] = ex2(a[n][e]);
+                a[n][e] = kQuantised ? Product::of_o(a[n][e] + pe[n][e]) : ex2(a[n][e]);
             }
 #pragma unroll
         for (int n = 0; n < kOct; ++n)

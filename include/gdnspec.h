@@ -764,7 +764,8 @@ GDNSPEC_API gdn_status gdn_kv_read(
  * Scores, the softmax's maximum and sum, and the output are held in FP32; the weights are
  * rounded to 16 significant bits for a bf16 cache (two bf16 parts) and to 11 for the others
  * (fp16), or to half of 2^-30 of the row's largest where that is more.  In an 8-bit cache that
- * is weight times scale of the value (scales of 2^-74 and more have all bits).  q is exact, its
+ * is weight times scale of the value (scales of 2^-74 and more have all bits).  Values may be as
+ * large as FP32 and bf16 are (those of a bf16 cache below 2^-90 lose bits).  q is exact, its
  * elements below 2^-24 of a head's largest to 2^-31 of that.  The positions of
  * a batch are cut evenly among the CTAs and the parts joined in order, so equal calls give equal
  * results; how a sequence is cut depends on the others' lengths, by rounding in FP32.  Bad device

@@ -271,3 +271,25 @@ def test_a_value_that_is_no_number_at_scores_far_below(cuda_device, kind, bad, x
         assert not bool(torch.isfinite(out[spoiled]).any())
     assert torch.equal(~torch.isfinite(out), spoiled)
     assert torch.equal(out[~spoiled], clean[~spoiled])
+
+
+# ---- values up to the largest ------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "int8"])
+@BOTH
+def test_values_up_to_the_largest(cuda_device, kind, wide):
+    """Rows of values up to 3e38 through gdn_kv_write, attended to alone, a few and many of them."""
+    dev, H, G, D, page = cuda_device, 8 * wide, 2, 128, 16
+    past, n = [0, 2, 700], [1, 2, 1]
+    c = Case(dev, past, n, H, G, D, kind, page=page, seed=9)
+    g = torch.Generator(device=dev).manual_seed(1)
+    full = [p + m for p, m in zip(past, n)]
+    N = sum(full)
+    k = torch.randn(N, G, D, generator=g, device=dev).bfloat16()
+    v = ((torch.rand(N, G, D, generator=g, device=dev) * 0.5 + 0.45) * 3e38).bfloat16()
+    v[..., ::3] = -v[..., ::3]
+    gdn.gdn_kv_write(k, v, c.k, c.v, c.table.to(dev), torch.zeros(3, dtype=torch.int32, device=dev), ref.offsets(full).to(dev),
+                     k_scale=c.ks, v_scale=c.vs)
+    c.run()
+    check(c)
