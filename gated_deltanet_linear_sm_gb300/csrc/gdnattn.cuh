@@ -361,6 +361,13 @@ constexpr float kLiftBf = -36.f, kSlackBf = -22.f;
 
 __device__ __forceinline__ int64_t token_row(const AttnParams& p, int i) { return p.sti ? ld(p.sti + i) : i; }
 
+// x sigmoid(z) without a denominator that overflows: with u = e^-|z| it is x / (1 + u) or x u / (1 + u), u in two
+// factors, which are normal numbers wherever the product is one
+__device__ __forceinline__ float gated(float x, float z) {
+    const float h = __expf(-0.5f * fabsf(z));
+    return __fdividef(z < 0.f ? x * h * h : x, fmaf(h, h, 1.0f));
+}
+
 // four columns of a row, weighed: to the output, through the gate z
 __device__ __forceinline__ void put_out(const AttnParams& p, int64_t at, int64_t z_at, const float (&o)[4]) {
     float x[4] = {o[0], o[1], o[2], o[3]};
@@ -368,7 +375,7 @@ __device__ __forceinline__ void put_out(const AttnParams& p, int64_t at, int64_t
         const uint2 raw = ld(reinterpret_cast<const uint2*>(p.z + z_at));
         const float z[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u), __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u)};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = __fdividef(x[e], 1.0f + __expf(-z[e]));
+        for (int e = 0; e < 4; ++e) x[e] = gated(x[e], z[e]);
     }
     *reinterpret_cast<uint2*>(p.out + at) = make_uint2(pack_b(x[0], x[1]), pack_b(x[2], x[3]));
 }

@@ -1108,7 +1108,7 @@ __global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(
                     if (p.z) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            if (c0 + e < d.rows) y[e] = __fdividef(y[e], 1.0f + __expf(-__bfloat162float(ld(p.z + ms.z_at[c0 + e] + dcol))));
+                            if (c0 + e < d.rows) y[e] = gated(y[e], __bfloat162float(ld(p.z + ms.z_at[c0 + e] + dcol)));
                     }
 #pragma unroll
                     for (int e = 0; e < 8; ++e)

@@ -293,3 +293,18 @@ def test_values_up_to_the_largest(cuda_device, kind, wide):
                      k_scale=c.ks, v_scale=c.vs)
     c.run()
     check(c)
+
+
+# ---- the gate ------------------------------------------------------------------------------------------------
+
+
+@BOTH
+def test_gates_far_below_zero(cuda_device, wide):
+    """Large values through a gate of e^-60 to e^-100 (an output that is a number as long as bf16 has one)."""
+    c = Case(cuda_device, [3, 900], [2, 1], 8 * wide, 2, 128, "bf16", page=16, seed=10, gate=True)
+    for i in range(2):
+        pg, row = _places(c, i)
+        c.v[pg, row] = (c.v[pg, row].float() * 1e30).bfloat16()
+    c.z[:] = torch.linspace(-100, -60, 128, device=c.dev).bfloat16()
+    c.run()
+    check(c)
