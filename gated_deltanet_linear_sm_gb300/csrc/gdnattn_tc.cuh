@@ -78,7 +78,8 @@ struct Cut {                            // (gdnattn.cuh)
 
 // weights are 2^(s - m) with m = (largest score when it was set) - kLift; m moves when a weight would
 // pass 2^kSlack.  8 bits: 2^(s - m - e), and e keeps weight times scale there (gdnattn.cuh: Product)
-constexpr float kLiftH = 8.f, kSlackH = 14.f;
+// (fp16: beside a score of 2^27, whose last bit is 16, m is rounded, and 8 below it would be 16)
+constexpr float kLiftH = 7.f, kLiftQ = 8.f, kSlackH = 14.f;
 
 template <int kKind, int D>
 struct Lay {
@@ -312,7 +313,7 @@ __global__ void __launch_bounds__(Warps<kKind>::kThreads, 1) gdn_attn_tc_kernel(
     constexpr int kSoft = Warps<kKind>::kSoft, kLoadWarp = Warps<kKind>::kLoad, kMmaWarp = Warps<kKind>::kMma, kLineWarp = Warps<kKind>::kLine;
     constexpr int kMine = Warps<kKind>::kMine;
     constexpr bool kQ8 = L::kQuantised, kB = kKind == kBf16;
-    constexpr float kLift = kB ? kLiftBf : kLiftH, kSlack = kB ? kSlackBf : kSlackH;
+    constexpr float kLift = kB ? kLiftBf : kQ8 ? kLiftQ : kLiftH, kSlack = kB ? kSlackBf : kSlackH;
     extern __shared__ unsigned char raw_smem[];
     unsigned char* const sm = raw_smem + ((1024 - (saddr(raw_smem) & 1023)) & 1023);
     Misc<kKind>& ms = *reinterpret_cast<Misc<kKind>*>(sm + L::kOMisc);

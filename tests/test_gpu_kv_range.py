@@ -308,3 +308,27 @@ def test_gates_far_below_zero(cuda_device, wide):
     c.z[:] = torch.linspace(-100, -60, 128, device=c.dev).bfloat16()
     c.run()
     check(c)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@BOTH
+def test_scores_beside_which_a_reference_is_rounded(cuda_device, kind, wide):
+    """A single position: its value, whatever the score's size (2^20 to 2^36 in steps of a third of a power)."""
+    D = 128
+    c = Case(cuda_device, [0], [1], 8 * wide, 2, D, kind, page=16, seed=6)
+    if c.vs is not None:
+        _even_scales(c)
+    pg, row = _places(c, 0)
+    if c.ks is None:
+        c.k[pg, row] = 32768.0
+    else:
+        _bits(c.k)[pg, row] = _bits(torch.full((1,), 64.0, device=c.dev).to(c.k.dtype))
+        c.ks[pg, row] = 512.0
+    v = ref.pick(c.v.cpu(), pg.cpu(), row.cpu())[0]
+    if c.vs is not None:
+        v = v * c.vs.cpu()[pg.cpu(), row.cpu()].double()[0][:, None]
+    for log2 in range(60, 109):
+        for sign in (1, -1):
+            c.q.fill_(sign * 2.0 ** (log2 / 3) / 32768.0 / D ** 0.5)
+            got = c.run()[0].double().cpu().view(2, -1, D)
+            assert bool(((got - v[:, None]).abs() <= (2.0 ** -8 + 2.0 ** -11) * v.abs()[:, None]).all()), (log2, sign)
