@@ -23,11 +23,11 @@ using namespace gdn_kv;
 namespace {
 
 // Which kernel: the tcgen05 one pays where the other one, whose units have up to 32 rows (16 for a head dim over 128), would read
-// the cache a second time; for head dim 64 from the third time on.  32 sequences of up to 4096, tcgen05 and other, in us:
-// bf16, head dim 128, 24 rows 60 and 50, 32 rows 62 and 59, 48 rows 71 and 94, 64 rows 79 and 97; e4m3, 24 rows 55 and 45, 48
-// rows 74 and 85; bf16, head dim 256, 16 rows 88 and 70, 24 rows 93 and 109; head dim 64, 48 rows 63 and 62, 64 rows 75 and 63.
-// (It also depends on the lengths, which the host does not know: 128 sequences, 8 heads of 64, 48 rows, bf16, of 64 positions
-// 68 and 44, of 512 114 and 102, of 2048 236 and 267; head dim 128, of 64 76 and 60, of 128 77 and 82, of 512 116 and 158.)
+// the cache a second time; for head dim 64 from the third time on.  32 sequences of up to 4096, 4 heads, tcgen05 and other, in us:
+// bf16, head dim 128, 24 rows 54 and 43, 32 rows 54 and 51, 48 rows 58 and 70, 64 rows 62 and 71; e4m3, 24 rows 51 and 40, 32 rows
+// 55 and 50, 48 rows 68 and 70; bf16, head dim 256, 16 rows 84 and 65, 24 rows 86 and 87; head dim 64, 48 rows 53 and 45, 64 rows
+// 59 and 45.  (It also depends on the lengths, which the host does not know: 128 sequences, 8 heads of 64, 48 rows, bf16, of 64
+// positions 68 and 44, of 512 102 and 102, of 2048 224 and 264; head dim 128, of 64 75 and 60, of 128 76 and 82, of 512 108 and 158.)
 // It wants pages of whole groups of 8 positions, and has no int8 products.
 bool on_tc(const AttnParams& p, int D, gdn_dtype type) {
     const int few = D == 64 ? 64 : D == 128 ? 32 : 16;

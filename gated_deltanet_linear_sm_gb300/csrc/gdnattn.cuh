@@ -1,6 +1,6 @@
-// Internal to libgdnspec: what the two attention kernels (gdnattn.cu, gdnattn_tc.cu) share: how a
-// batch's keys are laid on one line and cut among the CTAs, loads, outputs, and the launch that
-// joins the parts of units that several CTAs worked on.
+// Internal to libgdnspec: what the two attention kernels (gdnattn_warp.cuh, gdnattn_tc.cuh) share: how a
+// batch's keys are laid on one line and cut among the CTAs, loads, the references of 8-bit rows, outputs, and
+// the launch that joins the parts of units that several CTAs worked on.
 #pragma once
 
 #include <cuda_fp8.h>
@@ -385,7 +385,7 @@ __device__ __forceinline__ void put_out(const AttnParams& p, int64_t at, int64_t
 // Each of the CTAs that share a unit joins some of its rows: the one at place c of c0 .. c1 of the line those whose
 // number is c - c0 modulo their count, up to 16 of them to a CTA of this launch: the time is a row's chain of loads, and
 // more rows than warps repeat it (units of 64 rows, 32 sequences of 8192, e4m3: the call 151 us with all rows of a CTA here,
-// 143 with 32, 138 with 16, 142 with 8).  A row's parts are summed by the warps that are left over for it.
+// 143 with 32, 138 with 16, 142 with 8, when the first launch took 10 us less).  A row's parts are summed by the warps that are left over for it.
 
 constexpr int kJThreads = 256, kJWarps = 8;
 template <int kTileRows>

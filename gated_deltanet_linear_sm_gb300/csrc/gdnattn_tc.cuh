@@ -21,9 +21,9 @@
 // the products take them (a score is masked; 0 times NaN is not).
 //
 // What bounds it: with few bytes and many rows the softmax (32 sequences of 8192, head dim 128, 64 rows, e4m3:
-// 136 us, 2.1 TB/s; the time stays when the products, the exponentials, the stores or the loads are left out
+// 149 us, 1.9 TB/s; the time stays when the products, the exponentials, the stores or the loads are left out
 // one at a time: it is the chain of a tile's steps in 4 warps a quarter), with more bytes a row
-// the ring's four places and the call's start and end (2 of 65535, head dim 256, 64 rows, bf16: 62 us, 4.3 TB/s),
+// the ring's four places (beside q and weights laid out for 64 rows, whatever the call has) and the call's start and end (2 of 65535, head dim 256, 64 rows, bf16: 62 us, 4.3 TB/s),
 // and with short sequences a unit's own chain (first tile, its edge, output: 11 us with nothing beside it).
 //
 // bf16: weights as two bf16 parts (16 significant bits), two products.  fp16: one.  e4m3: the
@@ -58,8 +58,8 @@ constexpr int kKeyRing = 8;             // tiles whose keys' scales and presence
 constexpr int kHelp = 4;
 
 // Roles by warp: softmax and output, helpers, loads, products, the line.  16 softmax warps of at most two chunks of 8
-// rows do better than 8 of four where a weight takes most work (32 sequences of 8192, head dim 128, 64 rows, e4m3: 148 us and
-// 158), 8 with twice the registers where it takes less (16 of up to 16384, head dim 256, 32 rows, bf16: 76 and 72).
+// rows do better than 8 of four where a weight takes most work (32 sequences of 8192, head dim 128, 64 rows, e4m3: 6 % less
+// time), 8 with twice the registers where it takes less (16 of up to 16384, head dim 256, 32 rows, bf16: 5 % less).
 template <int kKind>
 struct Warps {
     static constexpr int kSoft = kKind == kE4m3 ? 16 : 8;

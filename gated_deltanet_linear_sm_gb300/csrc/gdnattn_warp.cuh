@@ -12,9 +12,9 @@
 // transposed for the second product; movmatrix turns them.
 //
 // What bounds it: with 8 rows or fewer the bytes (32 of up to 4096, head dim 128, bf16 64 us, 5.4 TB/s; 4 of
-// 131072, e4m3 184 us, 6.0 TB/s); with more rows the instructions of the widening and the softmax in the 8
-// warps of an SM that the accumulators leave room for (64 x 3 tokens x window 1024, 18 rows, int8 38 us: 950 instructions for
-// 16 keys, 0.4 a cycle and scheduler); with short sequences a unit's chain of start and end, about 2.5 us.
+// 131072, e4m3 185 us, 6.0 TB/s); with more rows the instructions of the widening and the softmax in the 8
+// warps of an SM that the accumulators leave room for (64 x 3 tokens x window 1024, 18 rows, int8 38.5 us: 1000 instructions for
+// 16 keys with a unit's start and end, 0.45 a cycle and scheduler); with short sequences a unit's chain of start and end, about 2.5 us.
 //
 // A row's reference m is kUnset until it has a score; it moves when a score passes it by more than
 // 2^kSlack, and only then do the lanes compare: a block's vote is one instruction.  kLift keeps weights
@@ -101,7 +101,7 @@ struct Shape {
     static constexpr int kRow = D * kBytes;                     // bytes of a key
     static constexpr int kItem = kKeys * kRow + (kBytes == 1 ? 4 * kKeys : 0);      // K or V of 16 keys, with their scales
     // CTAs of an SM: short rows (64 x 16 bits, 128 x 8) leave room for three with long rings, whose units' starts and
-    // ends overlap (256 sequences of up to 500, head dim 64: 59 us with two or four, 49 with three); with more bytes a
+    // ends overlap (256 sequences of up to 500, head dim 64: 59 us with two or four, 49 with three, 45 as it is now); with more bytes a
     // row two long rings do better than four short ones (32 of up to 4096, head dim 128, bf16: 64 us, 69 with three, 78 with four)
     static constexpr int kCtas = kRow <= 128 && kOct == 1 ? 3 : 2;
     static constexpr int kQ = 8 * kOct * D * 2;

@@ -1,7 +1,7 @@
 // libgdnspec: the paged key-value cache of the attention layers beside the recurrent
 // ones: rows into it (gdn_kv_write), quantised where it has 8 bits, and back out of it
 // (gdn_kv_read), with the C entry points of the cache and of the attention over it
-// (gdnattn.cu).  Declared in include/gdnspec.h.
+// (launched in gdnattn.cu).  Declared in include/gdnspec.h.
 #include <cuda_fp8.h>
 
 #include <algorithm>

@@ -1,6 +1,7 @@
 // Internal to libgdnspec: the kernel parameters of the paged key-value cache and
 // of the attention over it, shared by the cache's kernels with the C entry points
-// (gdnkv.cu) and the attention kernels (gdnattn.cu).
+// (gdnkv.cu), the choice of the attention kernel (gdnattn.cu) and the kernels (gdnattn_warp.cuh,
+// gdnattn_tc.cuh).
 #pragma once
 
 #include "gdn_common.h"
@@ -83,7 +84,7 @@ struct AttnParams {
 constexpr int kMaxCtas = 1024;      // of an attention launch
 constexpr int kMetaInts = 16;       // of a CTA: two records of 8
 
-// Workspace in bytes on the current device, and the launch (gdnattn.cu).
+// Workspace in bytes on the current device, and the launch (gdnattn.cu chooses the kernel).
 int64_t attn_workspace(const AttnParams& p, int D, gdn_dtype type);
 cudaError_t launch_attn(const AttnParams& p, int D, gdn_dtype type, void* workspace, cudaStream_t stream);
 

@@ -103,8 +103,8 @@ class PreparedOp:
 
 
 class PreparedScan(PreparedOp):
-    """A prepared gdn_ssm_prefill whose caller gave no workspace: each launch
-    takes one from the memory of the stream that it runs on, where nothing else
+    """A prepared gdn_ssm_prefill or gdn_attn_decode whose caller gave no
+    workspace: each launch takes one from the memory of the stream that it runs on, where nothing else
     can be given it before the launch has run.  So one such call may run on
     several streams at once and be dropped while it runs, and a graph that
     captures it (through torch.cuda.graph, whose memory that is; a capture

@@ -733,7 +733,7 @@ GDNSPEC_API gdn_status gdn_kv_write(
  * attention over a cached prefix, or to move a sequence.
  *
  *   k, v         row_type (GDN_F32, GDN_BF16 or GDN_F16) [num_tokens, H_kv, D], rows k_stride,
- *                v_stride apart; each element code * scale rounded once
+ *                v_stride apart; each element code * scale in FP32, rounded to the type
  *   kv_begin     int32 [batch], or NULL;  everything else as for gdn_kv_write
  *
  * Rows of no sequence, of a skipped sequence and of positions without a page are left as
@@ -764,13 +764,13 @@ GDNSPEC_API gdn_status gdn_kv_read(
  * Scores, the softmax's maximum and sum, and the output are held in FP32; the weights are
  * rounded to 16 significant bits for a bf16 cache (two bf16 parts) and to 11 for the others
  * (fp16), or to half of 2^-30 of the row's largest where that is more.  In an 8-bit cache that
- * is weight times scale of the value (scales of 2^-74 and more have all bits).  Values may be as
- * large as FP32 and bf16 are (those of a bf16 cache below 2^-90 lose bits).  q is exact, its
- * elements below 2^-24 of a head's largest to 2^-31 of that.  The positions of
- * a batch are cut evenly among the CTAs and the parts joined in order, so equal calls give equal
- * results; how a sequence is cut depends on the others' lengths, by rounding in FP32.  Bad device
- * data: q_len > max_T sets GDN_FLAG_QLEN, the rest as for gdn_kv_write, except that any row of a
- * sequence outside [0, num_tokens) skips the
+ * is weight times scale of the value (all bits where a row's largest product is 2^-74 or more,
+ * its largest weight being 1).  Values may be as large as FP32 and bf16 are (those of a bf16 cache
+ * below 2^-90 lose bits).  q is exact, its elements below 2^-24 of a head's largest to 2^-31 of
+ * that.  The positions of a batch are cut evenly among the CTAs and the parts joined in order, so
+ * equal calls give equal results; how a sequence is cut depends on the others' lengths, by rounding
+ * in FP32.  Bad device data: q_len > max_T sets GDN_FLAG_QLEN, the rest as for gdn_kv_write, except
+ * that any row of a sequence outside [0, num_tokens) skips the
  * sequence.  An infinity or NaN in k or v spoils the tokens that see it, in q its own row.  (In an
  * 8-bit cache that is a scale; a GDN_E4M3 code that is NaN, which gdn_kv_write never makes, may spoil
  * other tokens of its sequence too.)
